@@ -193,6 +193,26 @@ __device__ __forceinline__ void block_reduce(double& ss, uint32_t& bad) {
 }
 
 // ---------------------------------------------------------------------------
+// AdamW of one element in binary32, one IEEE operation an operator (the
+// order is zf_step.hip's arithmetic contract).
+struct Coef {
+  float gs, dec, b1, c1, b2, c2, bc1, bc2, lrf, ef;
+};
+
+__device__ __forceinline__ void adamw1(const Coef& c, float acc, float& p, float& m, float& v) {
+  const float g = acc * c.gs;
+  float pp = p * c.dec;
+  const float mm = c.b1 * m + c.c1 * g;
+  const float vv = c.b2 * v + c.c2 * (g * g);
+  const float d = sqrtf(vv / c.bc2) + c.ef;
+  const float mh = mm / c.bc1;
+  pp = pp - c.lrf * (mh / d);
+  p = pp;
+  m = mm;
+  v = vv;
+}
+
+// ---------------------------------------------------------------------------
 // Argument checks shared by the entry points.
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

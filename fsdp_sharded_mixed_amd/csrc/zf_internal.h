@@ -181,6 +181,8 @@ struct zf_plan {
   zf_plan_summary summary;
   std::vector<zf_unit_info> units;
   std::vector<zf_group_info> groups;
+  std::vector<zf_segment> segs; // the parameters, in model order
+  std::vector<int64_t> seg_at;  // each one's first element in the padded flat
   int32_t unr1;                 // tile steps of pass 1 per thread
   int32_t pass1_map;            // pass-1 tile walk (0 shared window, 1 XCD-contiguous)
   int64_t pass1_tiles;          // pass-1 blocks = squared-norm partials

@@ -1,0 +1,87 @@
+// zf_ortho.h -- the Newton-Schulz engine shared by zf_orthogonalize and the
+// Muon step: the work layout of a batch of matrices in a device workspace,
+// and the sequence of launches over it.
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+#include <vector>
+
+#include "zf.h"
+#include "zf_internal.h"
+
+namespace zf {
+namespace ns {
+
+// The work layout.  A matrix of R x C is iterated on its short side: X is
+// m x n with m = min(R, C), n = max(R, C), the transpose of the matrix when
+// R > C ("tall").  Both sides are padded with zeros to multiples of kPad, so
+// that no load of the products needs a range check along the summed axis.
+constexpr int kPad = 64;
+
+// One matrix: where its data come from and where its buffers lie (byte
+// offsets into the workspace).
+struct Mat {
+  const void* src;        // zf_orthogonalize: the matrix, row stride src_ld
+  void* dst;              // zf_orthogonalize: the result, row stride dst_ld
+  int64_t src_ld, dst_ld; // the Muon step: both = cols
+  int64_t flat;           // the Muon step: offset in the padded flat arrays
+  int64_t x;              // fp32 [mp][np]: X (before the first step: not yet normalised)
+  int64_t h;              // fp16 [mp][np]: X * 2^10 rounded
+  int64_t t[2];           // fp16 [np][mp]: its transpose, two buffers in turn
+  int64_t a, b;           // fp16 [mp][mp]: A and B off the diagonal, * 2^10
+  int64_t da, db;         // fp32 [mp]: their diagonals
+  int64_t lo_x, lo_s;     // bytes from a 16-bit buffer to the one that holds
+                          // what its rounding left (three products)
+  int64_t part;           // its first squared-norm partial
+  int32_t m, n, mp, np;
+  int32_t tall, slot;     // slot: its place in the array of inverse norms
+  float rate;             // the Muon step: lr * scale
+  int32_t load0, tri0, app0;  // its first block in the launches of its group
+};
+
+// Launches of one group of matrices [first, first + count).
+struct Group {
+  int32_t first, count;
+  int32_t load_blocks, tri_blocks, app_blocks;
+};
+
+struct Layout {
+  std::vector<Mat> mats;
+  std::vector<Group> groups;
+  int64_t table = 0, inv = 0, partials = 0;  // byte offsets
+  int64_t bytes = 0;
+};
+
+struct Shape {
+  int64_t rows, cols;
+};
+
+// Plans the buffers of `count` matrices; products: 1, or 3 with the second
+// 16-bit halves.  false: a size out of range.
+bool layout(const Shape* shapes, int64_t count, int products, Layout& out);
+
+// Products a call computes: the caller's choice, or by the result's type.
+int products_of(const zf_ns_params& p, int32_t dst_dtype);
+// ZF_OK, or ZF_EINVAL for parameters out of range.
+int check_params(const zf_ns_params& p);
+zf_ns_params defaults();
+
+// What the Muon step reads and writes beside the products.
+struct MuonIo {
+  const float* sums;
+  float* master;
+  float* momentum;
+  void* params;           // or NULL
+  const DevState* st;
+  float mu, dec;
+  int32_t nesterov, param_dtype;
+};
+
+// Enqueues the orthogonalisation of every matrix of `l` on `s`.  io == NULL:
+// from Mat.src (src_dtype) to Mat.dst (dst_dtype); else the Muon update.
+int enqueue(const Layout& l, const zf_ns_params& p, int products, int32_t src_dtype,
+            int32_t dst_dtype, const MuonIo* io, char* ws, hipStream_t s);
+
+}  // namespace ns
+}  // namespace zf

@@ -76,6 +76,7 @@ extern "C" int zf_plan_flat(const zf_segment* segs, int64_t nseg, int32_t n_rank
   const int64_t kLimit = int64_t(1) << 62;
   int64_t lam = 0;
   int32_t cur = -1;
+  std::vector<int64_t> seg_unit;
   try {
     for (int64_t i = 0; i < nseg; ++i) {
       const int32_t uid = (layout == ZF_GLOBAL_FLAT) ? 0 : segs[i].unit;
@@ -110,6 +111,10 @@ extern "C" int zf_plan_flat(const zf_segment* segs, int64_t nseg, int32_t n_rank
       }
       p->groups.back().n_units = (int64_t)p->units.size() - p->groups.back().first_unit;
       p->groups.back().numel += segs[i].numel;
+      p->segs.push_back(segs[i]);
+      // relative to its unit for now (the units' places follow below)
+      p->seg_at.push_back(lam - p->units.back().lam);
+      seg_unit.push_back((int64_t)p->units.size() - 1);
       lam += segs[i].numel;
     }
   } catch (const std::bad_alloc&) {
@@ -128,6 +133,7 @@ extern "C" int zf_plan_flat(const zf_segment* segs, int64_t nseg, int32_t n_rank
     if (u.P > max_pad) max_pad = u.P;
     if (off >= kLimit) { delete p; return ZF_ESIZE; }
   }
+  for (size_t i = 0; i < seg_unit.size(); ++i) p->seg_at[i] += p->units[seg_unit[i]].O;
   int64_t max_group = 0;
   for (zf_group_info& g : p->groups) {
     for (int64_t k = 0; k < g.n_units; ++k) g.padded += p->units[g.first_unit + k].P;

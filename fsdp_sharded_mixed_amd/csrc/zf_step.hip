@@ -332,23 +332,6 @@ struct Pass2Args {
   int32_t reverse;  // MAT: 1 if block b takes tile gridDim.x - 1 - b (cached sums first)
 };
 
-struct Coef {
-  float gs, dec, b1, c1, b2, c2, bc1, bc2, lrf, ef;
-};
-
-__device__ __forceinline__ void adamw1(const Coef& c, float acc, float& p, float& m, float& v) {
-  const float g = acc * c.gs;
-  float pp = p * c.dec;
-  const float mm = c.b1 * m + c.c1 * g;
-  const float vv = c.b2 * v + c.c2 * (g * g);
-  const float d = sqrtf(vv / c.bc2) + c.ef;
-  const float mh = mm / c.bc1;
-  pp = pp - c.lrf * (mh / d);
-  p = pp;
-  m = mm;
-  v = vv;
-}
-
 template <int NR, int GDT, int PDT, bool MAT, int Q, bool OUT16>
 __global__ __launch_bounds__(zf::kThreadsPass2Mat) void zf_pass2(Pass2Args a) {
   constexpr int T = zf::threads_pass2(MAT);  // the block size

@@ -94,6 +94,21 @@ class OffloadArgs(C.Structure):
                 ("phase_events", C.POINTER(C.c_void_p))]
 
 
+class NsParams(C.Structure):
+    _fields_ = [("steps", C.c_int32), ("products", C.c_int32), ("a", C.c_double),
+                ("b", C.c_double), ("c", C.c_double), ("eps", C.c_double)]
+
+
+class Matrix(C.Structure):
+    _fields_ = [("src", C.c_void_p), ("dst", C.c_void_p), ("rows", C.c_int64),
+                ("cols", C.c_int64), ("src_stride", C.c_int64), ("dst_stride", C.c_int64)]
+
+
+class MuonHparams(C.Structure):
+    _fields_ = [("lr", C.c_double), ("momentum", C.c_double), ("weight_decay", C.c_double),
+                ("nesterov", C.c_int32), ("scale_rule", C.c_int32), ("ns", NsParams)]
+
+
 # Every function declared in include/zf.h, with its ctypes signature.
 _SIGNATURES = {
     "zf_plan_flat": (C.c_int, [C.POINTER(Segment), C.c_int64, C.c_int32, C.c_int32, C.c_int32,
@@ -128,6 +143,16 @@ _SIGNATURES = {
                                   C.c_void_p, C.POINTER(StepResult)]),
     "zf_reshard": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p,
                              C.c_int64, C.c_int32, C.c_void_p]),
+    "zf_orthogonalize_bytes": (C.c_int64, [C.POINTER(Matrix), C.c_int64, C.c_int32,
+                                           C.POINTER(NsParams)]),
+    "zf_orthogonalize": (C.c_int, [C.POINTER(Matrix), C.c_int64, C.c_int32, C.c_int32,
+                                   C.POINTER(NsParams), C.c_void_p, C.c_int64, C.c_void_p]),
+    "zf_muon_plan": (C.c_int, [C.c_void_p, C.POINTER(C.c_int64), C.c_int64,
+                               C.POINTER(C.c_void_p)]),
+    "zf_muon_free": (None, [C.c_void_p]),
+    "zf_muon_workspace_bytes": (C.c_int64, [C.c_void_p, C.POINTER(NsParams)]),
+    "zf_muon_step": (C.c_int, [C.c_void_p, C.POINTER(Hparams), C.POINTER(MuonHparams),
+                               C.POINTER(StepArgs), C.c_void_p]),
     "zf_strerror": (C.c_char_p, [C.c_int]),
     "zf_hip_error_name": (C.c_char_p, []),
 }
@@ -465,3 +490,132 @@ def reshard(plan_from, plan_to, src, dst, stream=None, elem_bytes=None, src_nume
     dn = dst_numel if dst_numel is not None else _default_numel([dst], "zf_reshard")
     _check(lib.zf_reshard(_handle(plan_from), _handle(plan_to), _ptr(src), int(sn), _ptr(dst),
                           int(dn), int(eb), _stream(stream)), "zf_reshard")
+
+
+# ---- Muon --------------------------------------------------------------------
+
+MUON_SCALE_ROWS, MUON_SCALE_RMS = 0, 1
+
+
+def ns_params(steps=5, products=0, a=3.4445, b=-4.7750, c=2.0315, eps=1e-7):
+    """The Newton-Schulz iteration of zf_orthogonalize and zf_muon_step."""
+    return NsParams(int(steps), int(products), a, b, c, eps)
+
+
+def _ns(params):
+    return None if params is None else C.byref(params)
+
+
+@dataclass
+class OrthoBatch:
+    """The matrices of zf_orthogonalize calls: their addresses, shapes and
+    types.  Holds the tensors, so the addresses stay good."""
+    mats: object
+    count: int
+    src_dtype: int
+    dst_dtype: int
+    device: object
+    tensors: tuple
+
+
+def _dtype_of(t):
+    import torch
+    code = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}.get(t.dtype)
+    if code is None:
+        raise ValueError(f"zf_orthogonalize: unsupported dtype {t.dtype}")
+    return code
+
+
+def ortho_batch(mats, outs):
+    """The batch of zf_orthogonalize: outs[i] receives mats[i] orthogonalised.
+    2-D tensors on one GPU with contiguous rows (any row stride), all mats of
+    one dtype and all outs of one dtype; outs[i] may be mats[i]."""
+    mats, outs = tuple(mats), tuple(outs)
+    if len(mats) != len(outs):
+        raise ValueError("zf_orthogonalize: as many outs as mats")
+    arr = (Matrix * len(mats))()
+    for i, (x, y) in enumerate(zip(mats, outs)):
+        if x.dim() != 2 or x.shape != y.shape:
+            raise ValueError("zf_orthogonalize: 2-D tensors, outs shaped as mats")
+        for t in (x, y):
+            if t.shape[1] > 1 and t.stride(1) != 1:
+                raise ValueError("zf_orthogonalize: rows must be contiguous")
+            if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+                raise ValueError("zf_orthogonalize: rows must not overlap")
+            if t.device != mats[0].device:
+                raise ValueError("zf_orthogonalize: tensors on one device")
+        if x.dtype != mats[0].dtype or y.dtype != outs[0].dtype:
+            raise ValueError("zf_orthogonalize: one dtype for all mats and one for all outs")
+        rows, cols = x.shape
+        arr[i] = Matrix(_ptr(x), _ptr(y), rows, cols, max(x.stride(0), cols),
+                        max(y.stride(0), cols))
+    return OrthoBatch(arr, len(mats), _dtype_of(mats[0]) if mats else BF16,
+                      _dtype_of(outs[0]) if outs else BF16,
+                      mats[0].device if mats else None, mats + outs)
+
+
+def orthogonalize_bytes(batch, ns=None):
+    """zf_orthogonalize_bytes of a batch."""
+    n = lib.zf_orthogonalize_bytes(batch.mats, batch.count, batch.dst_dtype, _ns(ns))
+    if n < 0:
+        raise ZfError(n, "zf_orthogonalize_bytes")
+    return n
+
+
+def orthogonalize(batch, workspace, ns=None, stream=None, workspace_size=None):
+    """zf_orthogonalize of a batch (ortho_batch); ns: None or ns_params()."""
+    _check(lib.zf_orthogonalize(batch.mats, batch.count, batch.src_dtype, batch.dst_dtype,
+                                _ns(ns), _ptr(workspace), _nbytes(workspace, workspace_size),
+                                _stream(stream)), "zf_orthogonalize")
+
+
+@dataclass
+class Muon:
+    """Which parameters of a plan Muon updates (owns the C zf_muon)."""
+    handle: int
+
+    def __del__(self, _free=lib.zf_muon_free):
+        h, self.handle = self.handle, None
+        if h:
+            _free(h)
+
+
+def muon_plan(plan, segments):
+    """zf_muon_plan: the segments (indices) that Muon updates; the rest is
+    AdamW's."""
+    n = len(segments)
+    arr = (C.c_int64 * n)(*[int(i) for i in segments])
+    h = C.c_void_p()
+    _check(lib.zf_muon_plan(_handle(plan), arr, n, C.byref(h)), "zf_muon_plan")
+    return Muon(h.value)
+
+
+def muon_workspace_bytes(muon, ns=None):
+    n = lib.zf_muon_workspace_bytes(muon.handle, _ns(ns))
+    if n < 0:
+        raise ZfError(n, "zf_muon_workspace_bytes")
+    return n
+
+
+def muon_hparams(lr, momentum=0.95, weight_decay=0.01, nesterov=True,
+                 scale_rule=MUON_SCALE_RMS, ns=None):
+    return MuonHparams(lr, momentum, weight_decay, int(nesterov), int(scale_rule),
+                       ns if ns is not None else ns_params())
+
+
+def muon_step(muon, hp, mhp, grad_dtype, param_dtype, grads, master, exp_avg, exp_avg_sq, params,
+              workspace, state, stream=None, phase_events=None, numel=None,
+              workspace_size=None, grad_shards=None, grads_reduced=False):
+    """zf_muon_step; the arguments after mhp are shard_step's.  workspace:
+    muon_workspace_bytes(muon, mhp.ns) bytes."""
+    gp = _ptr_array(grads) if grads is not None else None
+    ev = (C.c_void_p * 4)(*phase_events) if phase_events is not None else None
+    if numel is None:
+        numel = _default_numel(list(grads or []) + [master, exp_avg, exp_avg_sq, params,
+                                                    grad_shards], "zf_muon_step")
+    args = StepArgs(int(grad_dtype), int(param_dtype), gp, _ptr(master), _ptr(exp_avg),
+                    _ptr(exp_avg_sq), _ptr(params), _ptr(grad_shards), int(bool(grads_reduced)),
+                    0, int(numel), _ptr(workspace), _nbytes(workspace, workspace_size),
+                    _ptr(state), ev)
+    _check(lib.zf_muon_step(muon.handle, C.byref(hp), C.byref(mhp), C.byref(args),
+                            _stream(stream)), "zf_muon_step")

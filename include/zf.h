@@ -53,8 +53,8 @@
  *   - No call aborts or throws.
  *   - HIP graphs: zf_shard_step, zf_shard_step_noalloc (after its first
  *     call on the device), zf_reduce_scatter, zf_gather, zf_gather_cast,
- *     zf_bucket_reduce_scatter, zf_accumulate and
- *     zf_state_init enqueue kernels only (no memset, copy, allocation or
+ *     zf_bucket_reduce_scatter, zf_accumulate, zf_orthogonalize,
+ *     zf_muon_step and zf_state_init enqueue kernels only (no memset, copy, allocation or
  *     synchronisation; every pointer travels by value in the kernel
  *     arguments), so a caller may capture them on a stream and replay the
  *     graph.  The state block carries t, the loss scale and the skip
@@ -521,6 +521,132 @@ typedef struct {
  * ZF_EINVAL, ZF_EALIGN, ZF_EDTYPE, ZF_ESIZE, ZF_EHIP, ZF_EUNSUP. */
 int zf_offload_step(const zf_plan* plan, const zf_hparams* hp, const zf_offload_args* args,
                     void* stream, zf_step_result* result);
+
+/* ---- Muon ---------------------------------------------------------------
+ * Muon updates a weight matrix along the orthogonalised direction of its
+ * momentum instead of AdamW's element-wise ratio; vectors, embeddings and
+ * the output head stay with AdamW.  zf_orthogonalize is the operation alone,
+ * for optimizers of the caller's own; zf_muon_step is zf_shard_step with
+ * Muon for the matrices that the caller names.  Both may be captured in a
+ * HIP graph (kernels only; pointers, sizes and hyperparameters are those of
+ * the capture). */
+
+/* The Newton-Schulz iteration.  With X0 = G / (|G|_F + eps), transposed if G
+ * has more rows than columns, each step is
+ *   A = X X^T,   X <- a X + (b A + c A A) X
+ * and the result is the last X, transposed back.  NULL in place of the
+ * struct selects steps = 5, products = 0, a = 3.4445, b = -4.7750,
+ * c = 2.0315, eps = 1e-7.
+ * products: how exactly the matrix products are computed.  1: operands are
+ * rounded to 11 bits (fp16 with a common power-of-two factor; sums, the
+ * linear term and the diagonals of A and of its polynomial in binary32); the
+ * result is within about 1e-3 of the exact one (|error|_F / |X|_F), below
+ * bf16's own rounding.  3: operands are sums of two fp16 numbers, about 22
+ * bits, for three times the work; the result is within about 1e-5.  0: 1 for
+ * a ZF_BF16 result and for zf_muon_step, else 3.
+ * The operands' range bounds the coefficients: singular values, and the
+ * entries of A and b A + c A A, must stay below 64 (they stay below 8 for
+ * the default ones). */
+#define ZF_NS_MAX_STEPS 32
+typedef struct {
+  int32_t steps;     /* 1 .. ZF_NS_MAX_STEPS */
+  int32_t products;  /* 0, 1 or 3 */
+  double a, b, c;    /* finite */
+  double eps;        /* >= 0 */
+} zf_ns_params;
+
+/* One matrix of a batch, row-major: element (i, j) at src[i * src_stride +
+ * j] and dst[i * dst_stride + j], strides in elements (ignored for a single
+ * row). */
+typedef struct {
+  const void* src;
+  void* dst;
+  int64_t rows, cols;
+  int64_t src_stride, dst_stride;
+} zf_matrix;
+
+#define ZF_ORTHO_MAX_MATRICES (1 << 20)
+
+/* Device workspace that zf_orthogonalize needs for these shapes (src, dst
+ * and the strides are not looked at), result type and parameters.  < 0 on
+ * error. */
+int64_t zf_orthogonalize_bytes(const zf_matrix* mats, int64_t count, int32_t dst_dtype,
+                               const zf_ns_params* params);
+
+/* Orthogonalise `count` matrices (0 is allowed): dst = the Newton-Schulz
+ * result for src.  src_dtype and dst_dtype: ZF_F16, ZF_BF16 or ZF_F32, the
+ * same for the whole batch; src and dst aligned to their element size.  The
+ * shapes may differ; every side is at most 2^20.  dst may be the matrix's
+ * own src (same place, stride and type); nothing else may overlap a dst.
+ * Elements between the rows of a strided dst are left as they are.
+ * A matrix of zeros gives zeros (eps > 0); one that holds an infinity or a
+ * NaN gives NaN throughout, and no other matrix of the batch is touched by
+ * it.  Sums are taken in a fixed order: the same call gives the same bits.
+ * workspace: device memory of workspace_size >= zf_orthogonalize_bytes,
+ * 16-byte aligned; calls that may overlap in time (two streams, two graphs)
+ * need workspaces of their own.
+ * Errors: ZF_EINVAL (NULL, count < 0, a side < 1, a stride < cols, params
+ * out of range), ZF_EALIGN, ZF_EDTYPE, ZF_ESIZE (workspace too small, a side
+ * above 2^20, more than ZF_ORTHO_MAX_MATRICES matrices), ZF_ENOMEM,
+ * ZF_EHIP. */
+int zf_orthogonalize(const zf_matrix* mats, int64_t count, int32_t src_dtype, int32_t dst_dtype,
+                     const zf_ns_params* params, void* workspace, int64_t workspace_size,
+                     void* stream);
+
+/* Which parameters of a plan Muon updates; opaque, immutable once made,
+ * holding its own copy of the plan. */
+typedef struct zf_muon zf_muon;
+
+/* segments: n indices into the plan's segments, each a matrix (dim0 >= 1
+ * dividing numel: dim0 rows of numel / dim0), none twice.  Every other
+ * parameter, and all padding, is updated by AdamW.  Any layout: the ranks'
+ * shards of a matrix lie side by side in the padded flat arrays, so its
+ * rows are whole there (on N GPUs they would be gathered first).  Host only;
+ * release with zf_muon_free.  Errors: ZF_EINVAL, ZF_ESIZE (a side above
+ * 2^20), ZF_ENOMEM. */
+int zf_muon_plan(const zf_plan* plan, const int64_t* segments, int64_t n, zf_muon** out);
+
+/* Release a zf_muon (NULL is allowed), after the stream has passed every
+ * call that used it. */
+void zf_muon_free(zf_muon* muon);
+
+/* Device workspace of zf_muon_step: zf_workspace_bytes of the plan, the fp32
+ * sums unless the layout has gradient shards of its own, and the iteration's
+ * buffers.  params: NULL or the step's zf_muon_hparams.ns.  < 0 on error. */
+int64_t zf_muon_workspace_bytes(const zf_muon* muon, const zf_ns_params* params);
+
+/* Muon's factor on the learning rate for an R x C matrix: */
+enum zf_muon_scale {
+  ZF_MUON_SCALE_ROWS = 0, /* sqrt(max(1, R / C)) */
+  ZF_MUON_SCALE_RMS = 1   /* 0.2 * sqrt(max(R, C)): updates as large as AdamW's */
+};
+
+typedef struct {
+  double lr;            /* of the matrices */
+  double momentum;      /* in [0, 1) */
+  double weight_decay;  /* decoupled: W <- W (1 - lr * weight_decay) first */
+  int32_t nesterov;     /* 0 or 1 */
+  int32_t scale_rule;   /* zf_muon_scale */
+  zf_ns_params ns;
+} zf_muon_hparams;
+
+/* One emulated step for all N ranks with Muon: the sums, the overflow check,
+ * the clip coefficient, the skip and the loss scale are zf_shard_step's (the
+ * norm is taken over all parameters), then unless skipped, in binary32,
+ *   matrices: g = sum * gs;  M = momentum * M + g;  U = g + momentum * M
+ *             (nesterov) or M;  O = U orthogonalised as above;
+ *             W = W * (1 - lr * weight_decay) - lr * scale * O
+ *   the rest: AdamW, with `hp`, bit for bit as zf_shard_step
+ * and the 16-bit parameters RNE16(W).  args: as zf_shard_step; exp_avg holds
+ * M for the matrices' elements, exp_avg_sq is not touched there; grad_shards
+ * as zf_shard_step (NULL: the sums go through the workspace); workspace_size
+ * must be >= zf_muon_workspace_bytes(muon, &mhp->ns).  mhp->ns.products = 0
+ * selects 1.  phase_events: before pass 1, after pass 1, after the norm
+ * reduction and finish, after the updates.  The state block is
+ * zf_shard_step's: t counts applied steps of both.  Errors: as
+ * zf_shard_step, plus ZF_EINVAL (mhp out of range) and ZF_ENOMEM. */
+int zf_muon_step(const zf_muon* muon, const zf_hparams* hp, const zf_muon_hparams* mhp,
+                 const zf_step_args* args, void* stream);
 
 /* Text for a status code (static storage). */
 const char* zf_strerror(int status);
