@@ -26,24 +26,23 @@ struct Mat {
   void* dst;              // zf_orthogonalize: the result, row stride dst_ld
   int64_t src_ld, dst_ld; // the Muon step: both = cols
   int64_t flat;           // the Muon step: offset in the padded flat arrays
-  int64_t x;              // fp32 [mp][np]: X (before the first step: not yet normalised)
-  int64_t h;              // fp16 [mp][np]: X * 2^10 rounded
-  int64_t t[2];           // fp16 [np][mp]: its transpose, two buffers in turn
-  int64_t a, b;           // fp16 [mp][mp]: A and B off the diagonal, * 2^10
-  int64_t da, db;         // fp32 [mp]: their diagonals
-  int64_t lo_x, lo_s;     // bytes from a 16-bit buffer to the one that holds
-                          // what its rounding left (three products)
+  int64_t h[2], l[2];     // fp16 [mp][np]: X * 2^10 rounded, and what the
+                          // rounding left; two buffers in turn
+  int64_t s[3], sl[3];    // fp16 [mp][mp]: symmetric matrices off the
+                          // diagonal, rounded, and what that left
+  int64_t d[3];           // fp32 [mp]: their diagonals
   int64_t part;           // its first squared-norm partial
   int32_t m, n, mp, np;
   int32_t tall, slot;     // slot: its place in the array of inverse norms
   float rate;             // the Muon step: lr * scale
-  int32_t load0, tri0, app0;  // its first block in the launches of its group
+  int32_t load0;          // its first block in the launches of its group,
+  int32_t tri0[2], app0[2];  // by tile size
 };
 
 // Launches of one group of matrices [first, first + count).
 struct Group {
   int32_t first, count;
-  int32_t load_blocks, tri_blocks, app_blocks;
+  int32_t load_blocks, tri_blocks[2], app_blocks[2];
 };
 
 struct Layout {

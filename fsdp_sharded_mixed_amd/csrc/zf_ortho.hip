@@ -81,15 +81,18 @@ __global__ __launch_bounds__(64) void zf_ns_table(TableArgs a) {
 
 // The matrix whose blocks hold block b: the last one that starts at or
 // before it.
-template <int32_t Mat::*FIRST>
-__device__ __forceinline__ const Mat* find(const Mat* table, int count, int b) {
+template <typename F>
+__device__ __forceinline__ const Mat* find(const Mat* table, int count, int b, F first) {
   int lo = 0, hi = count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (table[mid].*FIRST <= b) lo = mid;
+    if (first(table[mid]) <= b) lo = mid;
     else hi = mid - 1;
   }
   return table + lo;
+}
+__device__ __forceinline__ const Mat* find_load(const Mat* table, int count, int b) {
+  return find(table, count, b, [](const Mat& m) { return m.load0; });
 }
 
 struct Common {
@@ -107,8 +110,8 @@ __device__ __forceinline__ T* at(const Common& c, int64_t offset) {
 }
 
 // ---------------------------------------------------------------------------
-// Load: the matrix (or the Muon step's momentum update) into X in 32 bits,
-// with zero padding, and one squared-norm partial (64 bits) per 64 x 64 tile.
+// The squared norm, one partial (64 bits) per 64 x 64 tile; the Muon step's
+// momentum update on the way.
 constexpr int kTile = 64;
 
 struct LoadArgs {
@@ -116,14 +119,20 @@ struct LoadArgs {
   MuonIo io;
 };
 
-template <int SRC>  // ZF_F16, ZF_BF16, ZF_F32, or 0: the Muon step
+// Element (r, c) of the matrix; SRC: ZF_F16, ZF_BF16, ZF_F32, or 0: the Muon
+// step's U, from the momentum that it updates first (FIRST) or has updated.
+template <int SRC, bool FIRST>
 __device__ __forceinline__ float load1(const LoadArgs& a, const Mat& m, float gs, int64_t r,
                                        int64_t c) {
   if constexpr (SRC == 0) {
     const int64_t p = m.flat + r * m.src_ld + c;
+    float mm = a.io.momentum[p];
+    if (!FIRST && !a.io.nesterov) return mm;
     const float g = a.io.sums[p] * gs;
-    const float mm = a.io.mu * a.io.momentum[p] + g;
-    a.io.momentum[p] = mm;
+    if constexpr (FIRST) {
+      mm = a.io.mu * mm + g;
+      a.io.momentum[p] = mm;
+    }
     return a.io.nesterov ? g + a.io.mu * mm : mm;
   } else if constexpr (SRC == ZF_F32) {
     return static_cast<const float*>(m.src)[r * m.src_ld + c];
@@ -132,33 +141,26 @@ __device__ __forceinline__ float load1(const LoadArgs& a, const Mat& m, float gs
   }
 }
 
+// A wave reads 64 elements along the source's rows; tile (i0, j0) of X.
 template <int SRC>
 __global__ __launch_bounds__(kThreads) void zf_ns_load(LoadArgs a) {
   if (a.c.st && a.c.st->skipped) return;
-  const Mat& m = *find<&Mat::load0>(a.c.table, a.c.count, blockIdx.x);
+  const Mat& m = *find_load(a.c.table, a.c.count, blockIdx.x);
   const int tile = blockIdx.x - m.load0, tiles_n = m.np / kTile;
   const int i0 = tile / tiles_n * kTile, j0 = tile % tiles_n * kTile;
   const float gs = SRC == 0 ? a.c.st->gs : 0.0f;
-  __shared__ float s[kTile][kTile + 1];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   double ss = 0.0;
 #pragma unroll 4
   for (int k = wave; k < kTile; k += kThreads / 64) {
-    // a wave reads 64 elements along the source's rows
     const int i = m.tall ? i0 + lane : i0 + k, j = m.tall ? j0 + k : j0 + lane;
-    float v = 0.0f;
-    if (i < m.m && j < m.n) v = load1<SRC>(a, m, gs, m.tall ? j : i, m.tall ? i : j);
+    if (i >= m.m || j >= m.n) continue;
+    const float v = load1<SRC, true>(a, m, gs, m.tall ? j : i, m.tall ? i : j);
     ss += (double)v * (double)v;
-    if (m.tall) s[lane][k] = v;
-    else s[k][lane] = v;
   }
   uint32_t unused = 0;
-  block_reduce(ss, unused);  // synchronises: the tile is whole
+  block_reduce(ss, unused);
   if (threadIdx.x == 0) a.c.partials[m.part + tile] = ss;
-  float* x = at<float>(a.c, m.x);
-#pragma unroll 4
-  for (int k = wave; k < kTile; k += kThreads / 64)
-    x[(int64_t)(i0 + k) * m.np + j0 + lane] = s[k][lane];
 }
 
 // The inverse norm of every matrix of the group: its partials in a fixed
@@ -180,63 +182,464 @@ __global__ __launch_bounds__(kThreads) void zf_ns_norm(NormArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// The 16-bit operands of the first step from X and the inverse norm.
-template <int PRODUCTS>
-__global__ __launch_bounds__(kThreads) void zf_ns_prep(Common c) {
-  if (c.st && c.st->skipped) return;
-  const Mat& m = *find<&Mat::load0>(c.table, c.count, blockIdx.x);
+// X in 16-bit halves from the matrix and its inverse norm, transposed if the
+// matrix is tall, with zero padding.
+template <int SRC>
+__global__ __launch_bounds__(kThreads) void zf_ns_prep(LoadArgs a) {
+  if (a.c.st && a.c.st->skipped) return;
+  const Mat& m = *find_load(a.c.table, a.c.count, blockIdx.x);
   const int tile = blockIdx.x - m.load0, tiles_n = m.np / kTile;
   const int i0 = tile / tiles_n * kTile, j0 = tile % tiles_n * kTile;
-  const double inv = c.inv[m.slot];
+  const float gs = SRC == 0 ? a.c.st->gs : 0.0f;
+  const double inv = a.c.inv[m.slot];
   __shared__ float s[kTile][kTile + 1];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const float* x = at<float>(c, m.x);
-  f16* h = at<f16>(c, m.h);
-  f16* t = at<f16>(c, m.t[0]);
-  f16* hl = at<f16>(c, m.h + m.lo_x);
-  f16* tl = at<f16>(c, m.t[0] + m.lo_x);
+  f16* h = at<f16>(a.c, m.h[0]);
+  f16* l = at<f16>(a.c, m.l[0]);
+  if (m.tall) {
 #pragma unroll 4
-  for (int k = wave; k < kTile; k += kThreads / 64) {
-    const int64_t p = (int64_t)(i0 + k) * m.np + j0 + lane;
-    const float v = (float)((double)x[p] * inv);
-    s[k][lane] = v;
-    h[p] = hi_of(v);
-    if constexpr (PRODUCTS == 3) hl[p] = lo_of(v, hi_of(v));
+    for (int k = wave; k < kTile; k += kThreads / 64) {
+      const int i = i0 + lane, j = j0 + k;
+      s[lane][k] = i < m.m && j < m.n ? load1<SRC, false>(a, m, gs, j, i) : 0.0f;
+    }
+    __syncthreads();
   }
-  __syncthreads();
 #pragma unroll 4
   for (int k = wave; k < kTile; k += kThreads / 64) {
-    const int64_t p = (int64_t)(j0 + k) * m.mp + i0 + lane;
-    const float v = s[lane][k];
-    t[p] = hi_of(v);
-    if constexpr (PRODUCTS == 3) tl[p] = lo_of(v, hi_of(v));
+    const int i = i0 + k, j = j0 + lane;
+    float u = 0.0f;
+    if (m.tall) u = s[k][lane];
+    else if (i < m.m && j < m.n) u = load1<SRC, false>(a, m, gs, i, j);
+    const float v = i < m.m && j < m.n ? (float)((double)u * inv) : 0.0f;
+    const int64_t p = (int64_t)i * m.np + j;
+    const f16 hi = hi_of(v);
+    h[p] = hi;
+    l[p] = lo_of(v, hi);
   }
 }
 
 // ---------------------------------------------------------------------------
-// The products.  One kernel, four uses; every operand is stored with the
-// summed axis contiguous (a symmetric matrix is its own transpose, and X is
-// kept in both orientations), so C_ij = sum_k P[i][k] Q[j][k]:
-//   kGram   A = X X^T         P = Q = X,       lower tiles, mirrored
-//   kPoly   B = b A + c A A   P = Q = A,       lower tiles, mirrored
-//   kApply  X <- a X + B X    P = B, Q = X^T
-//   kLast   the same, written to the destination
-enum Mode { kGram, kPoly, kApply, kLast };
+// The products.
+//
+// C_ij = sum_k P[i][k] Q(k, j) over a BM x BN tile by WI x WJ waves, 64 of
+// the summed axis a step.  P is stored with the summed axis contiguous; so
+// is Q where it is a symmetric matrix or X^T (X itself, read by rows); where
+// Q is X (the application), its rows run along j and the fragments are
+// transposed on their way out of shared memory (ds_read_b64_tr_b16).
+//
+// What bounds it: the matrix cores, if they are fed.  A 256 x 256 tile needs
+// 32 bytes a cycle of a CU from the second-level cache at their full rate
+// (128 x 128: 64), and its 8 waves of 128 x 64 read 48 KiB of shared memory
+// per 1024 cycles.  Loads go from global to shared memory directly (no
+// registers), into two buffers of 64 KiB in turn; a step's barrier stands
+// between its two halves, so that the fragments of the next half are read
+// while the matrix cores work on this one, and a buffer's loads are on their
+// way for a whole step.  The 16-byte pieces of a row lie permuted by the row
+// number, which keeps every read free of bank conflicts (counter
+// SQ_LDS_BANK_CONFLICT: 0).  fp16 operands, 16x16x32 instructions.
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+#define ZF_LDS __attribute__((address_space(3)))
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+
+constexpr int kBK = 64;
+
+// A buffer of n bytes; loads past its end return nothing.
+__device__ __forceinline__ uint32_t extent(int64_t bytes) {
+  return bytes <= 0 ? 0u : bytes > 0x7FFFFFFFll ? 0x7FFFFFFFu : (uint32_t)bytes;
+}
+__device__ __forceinline__ Rsrc rsrc(const f16* base, uint32_t n) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<f16*>(base), 0, n, 0x00020000);
+}
+
+template <int BM_, int BN_, int WI, int WJ>
+struct Tile {
+  static constexpr int BM = BM_, BN = BN_, kWaves = WI * WJ, kThreads = kWaves * 64;
+  static constexpr int TI = BM / WI, TJ = BN / WJ, FI = TI / 16, FJ = TJ / 16;
+  static constexpr int kWavesJ = WJ;
+  static constexpr int kPBytes = BM * kBK * 2, kQBytes = BN * kBK * 2;
+  static constexpr int kBuf = (BM + BN) * kBK;  // elements of one buffer
+  static constexpr int kRows = kThreads / 8;    // rows that a load of all threads covers
+  static constexpr int kChunks = BN / 8;        // 16-byte pieces of a row of X
+  static constexpr int kRowsX = kThreads / kChunks;
+  static_assert(BM % kRows == 0 && BN % kRows == 0 && kRows % 8 == 0 && kRowsX == 16, "tile");
+};
+
+// The operands of one tile.  XQ: Q is X, rows along j.
+template <typename T, bool XQ>
+struct Operands {
+  Rsrc p, q;
+  uint32_t np, nq;
+  const f16* x;     // XQ: X at column j0
+  int64_t ld;       // elements of a row of P, Q or X
+  int64_t ldp;
+  int64_t skip;     // XQ: columns of X before j0
+  int k_len, vp, vq, rowp, rowq;
+  int rp, rq[T::FJ];  // shared-memory byte offsets of this lane's fragments
+
+  // rows_p, rows_q: rows of P and Q from this tile's first on (XQ: rows_q is
+  // the tile's first column j0)
+  __device__ __forceinline__ Operands(const f16* pp, int64_t p_ld, int rows_p, const f16* qq,
+                                      int64_t q_ld, int rows_q, int len) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int wi = wave / T::kWavesJ * T::TI, wj = wave % T::kWavesJ * T::TJ;
+    const int l = lane & 15, g = lane >> 4;
+    k_len = len;
+    ldp = p_ld;
+    ld = q_ld;
+    np = extent(rows_p * ldp * 2);
+    p = rsrc(pp, np);
+    const int r = tid >> 3, c = (tid & 7) ^ (r & 7);
+    vp = (int)(r * ldp * 2) + c * 16;
+    rowp = (int)(T::kRows * ldp * 2);
+    rp = (wi + l) * (kBK * 2) + ((g ^ (l & 7)) * 16);
+    if constexpr (XQ) {
+      x = qq;
+      skip = rows_q;
+      const int rx = tid / T::kChunks, cx = (tid % T::kChunks) ^ (2 * turn(rx));
+      vq = (int)(rx * ld * 2) + cx * 16;
+      rowq = (int)(T::kRowsX * ld * 2);
+      const int row = 8 * g + (l >> 2);
+#pragma unroll
+      for (int f = 0; f < T::FJ; ++f)
+        rq[f] = T::kPBytes + row * (T::BN * 2) +
+                ((((wj + 16 * f) / 8 + ((l & 3) >> 1)) ^ (2 * turn(row))) * 16) + (l & 1) * 8;
+    } else {
+      nq = extent(rows_q * ld * 2);
+      q = rsrc(qq, nq);
+      vq = (int)(r * ld * 2) + c * 16;
+      rowq = (int)(T::kRows * ld * 2);
+      rq[0] = T::kPBytes + (wj + l) * (kBK * 2) + ((g ^ (l & 7)) * 16);
+    }
+  }
+  // the permutation of a row of X
+  static __device__ __forceinline__ int turn(int r) { return (r & 3) | ((r >> 1) & 4); }
+};
+
+template <typename T>
+struct Frags {
+  f16x8 p[T::FI], q[T::FJ];
+};
+
+// One load of 16 bytes a lane from global to shared memory, at byte
+// lane_at + at of a buffer of n bytes.  The hardware compares lane_at with
+// n - at, which must not wrap.  (The compiler's
+// pass over the host code does not know the 16-byte form.)
+__device__ __forceinline__ void to_shared(Rsrc from, uint32_t n, ZF_LDS char* to, int lane_at,
+                                          uint32_t at) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (ZF_LDS void*)to, 16, lane_at, min(at, n), 0, 0);
+#endif
+}
+
+// Loads of step k into `buf`.  Past the end of the summed axis they read
+// other rows of the operand, or (past its end) nothing; no one uses them.
+template <typename T, bool XQ>
+__device__ __forceinline__ void fetch(const Operands<T, XQ>& o, int k, f16* __restrict buf) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  ZF_LDS char* b = (ZF_LDS char*)(buf) + wave * 1024;
+#pragma unroll
+  for (int h = 0; h < T::BM / T::kRows; ++h)
+    to_shared(o.p, o.np, b + h * T::kThreads * 16, o.vp, k * (kBK * 2) + h * o.rowp);
+  b += T::kPBytes;
+  if constexpr (XQ) {
+    // 64 rows of X; the last column tile may end past the row, inside the
+    // next one or (in the last row) past the 64 rows, which reads nothing
+    const int k0 = k * kBK;
+    const uint32_t n = k0 < o.k_len ? extent((kBK * o.ld - o.skip) * 2) : 0;
+    const Rsrc q = rsrc(o.x + k0 * o.ld, n);
+#pragma unroll
+    for (int h = 0; h < kBK / T::kRowsX; ++h)
+      to_shared(q, n, b + h * T::kThreads * 16, o.vq, h * o.rowq);
+  } else {
+#pragma unroll
+    for (int h = 0; h < T::BN / T::kRows; ++h)
+      to_shared(o.q, o.nq, b + h * T::kThreads * 16, o.vq, k * (kBK * 2) + h * o.rowq);
+  }
+}
+
+// Fragments of half kk of a step.
+template <typename T, bool XQ>
+__device__ __forceinline__ void read(const Operands<T, XQ>& o, const f16* __restrict buf,
+                                     Frags<T>& f, int kk) {
+  const char* b = reinterpret_cast<const char*>(buf);
+  if constexpr (XQ) {
+#pragma unroll
+    for (int j = 0; j < T::FJ; ++j) {
+      const ZF_LDS char* q = (const ZF_LDS char*)(b) + o.rq[j] + kk * 32 * T::BN * 2;
+      s16x4 half[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        half[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ZF_LDS s16x4*)(q + e * 4 * T::BN * 2));
+      f.q[j] = __builtin_bit_cast(
+          f16x8, __builtin_shufflevector(half[0], half[1], 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < T::FJ; ++j)
+      f.q[j] = *reinterpret_cast<const f16x8*>(b + (o.rq[0] ^ (kk * 64)) + j * 16 * kBK * 2);
+  }
+#pragma unroll
+  for (int i = 0; i < T::FI; ++i)
+    f.p[i] = *reinterpret_cast<const f16x8*>(b + (o.rp ^ (kk * 64)) + i * 16 * kBK * 2);
+}
+
+// acc[i][j] holds 4 consecutive i for one j (XQ: 4 consecutive j for one i).
+template <typename T, bool XQ>
+__device__ __forceinline__ void multiply(const Frags<T>& f, f32x4 (&acc)[T::FI][T::FJ]) {
+#pragma unroll
+  for (int i = 0; i < T::FI; ++i)
+#pragma unroll
+    for (int j = 0; j < T::FJ; ++j)
+      acc[i][j] = XQ ? __builtin_amdgcn_mfma_f32_16x16x32_f16(f.q[j], f.p[i], acc[i][j], 0, 0, 0)
+                     : __builtin_amdgcn_mfma_f32_16x16x32_f16(f.p[i], f.q[j], acc[i][j], 0, 0, 0);
+}
+
+// The order within a half: one shared-memory read, one load, then a share of
+// the matrix instructions, again and again (8192^2 x 4096: 1117 TFLOP/s; the
+// compiler's own order 1012, reads first 1106).
+template <typename T, bool XQ, int LOADS>
+__device__ __forceinline__ void interleave() {
+  constexpr int reads = T::FI + (XQ ? 2 : 1) * T::FJ, mma = T::FI * T::FJ;
+#pragma unroll
+  for (int k = 0; k < reads; ++k) {
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    if (k < LOADS) __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x8, mma / reads, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x8, mma % reads, 0);
+}
+
+template <typename T, bool XQ>
+__device__ __forceinline__ void half0(const Operands<T, XQ>& o, const f16* __restrict cur,
+                                      Frags<T>& a, Frags<T>& b, f32x4 (&acc)[T::FI][T::FJ]) {
+  read(o, cur, b, 1);
+  multiply<T, XQ>(a, acc);
+  interleave<T, XQ, 0>();
+}
+
+template <typename T, bool XQ>
+__device__ __forceinline__ void half1(const Operands<T, XQ>& o, int k, f16* __restrict cur,
+                                      const f16* __restrict nxt, Frags<T>& a, Frags<T>& b,
+                                      f32x4 (&acc)[T::FI][T::FJ]) {
+  fetch(o, k, cur);
+  read(o, nxt, a, 0);
+  multiply<T, XQ>(b, acc);
+  interleave<T, XQ, T::BM / T::kRows + (XQ ? kBK / T::kRowsX : T::BN / T::kRows)>();
+}
+
+// Every load to shared memory has arrived and every read of it is done, for
+// all waves (the barrier alone does not wait for loads to shared memory).
+__device__ __forceinline__ void arrive() {
+  __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+  __syncthreads();
+}
+
+template <typename T, bool XQ>
+__device__ __forceinline__ void product(const Operands<T, XQ>& o, f16* s0, f16* s1,
+                                        f32x4 (&acc)[T::FI][T::FJ]) {
+  const int steps = o.k_len / kBK;
+  Frags<T> a, b;
+  fetch(o, 0, s0);
+  arrive();
+  fetch(o, 1, s1);
+  read(o, s0, a, 0);
+  int t = 0;
+  for (; t + 2 <= steps; t += 2) {
+    half0(o, s0, a, b, acc);
+    arrive();
+    half1(o, t + 2, s0, s1, a, b, acc);
+    half0(o, s1, a, b, acc);
+    arrive();
+    half1(o, t + 3, s1, s0, a, b, acc);
+  }
+  if (t < steps) {
+    half0(o, s0, a, b, acc);
+    multiply<T, XQ>(b, acc);
+  }
+  arrive();  // shared memory is free again
+}
 
 struct GemmArgs {
   Common c;
   MuonIo io;
-  float ca, cb, cc;
-  int32_t turn;      // which transpose buffer holds X
-  int32_t first;     // X is not normalised yet
+  float ca, cb, cc;   // kPoly: ca I + cb S + cc S S
+  int32_t in0, in1, out;  // symmetric matrices (kApply: in0)
+  int32_t turn;       // which X
 };
 
-constexpr int kBM = 128, kBK = 64;
-constexpr int kLd = kBK + 8;  // LDS row stride in elements
+// Blocks go to the 8 XCDs in turn; each XCD takes runs of kRun consecutive
+// tiles, which share rows of their operands in its cache.
+constexpr int kRun = 8;
+__device__ __forceinline__ int tile_index() {
+  const int b = blockIdx.x, whole = gridDim.x / (8 * kRun) * (8 * kRun);
+  if (b >= whole) return b;
+  const int x = b & 7, k = b >> 3;
+  return (k / kRun * 8 + x) * kRun + k % kRun;
+}
 
+constexpr int kBig = 0, kSmall = 1;  // places of the tile sizes in the tables
+typedef Tile<256, 256, 2, 4> Big;
+typedef Tile<128, 128, 2, 2> Small;
+
+__device__ __forceinline__ f16x4 halves(const float (&v)[4]) {
+  return (f16x4){hi_of(v[0]), hi_of(v[1]), hi_of(v[2]), hi_of(v[3])};
+}
+__device__ __forceinline__ f16x4 rests(const float (&v)[4], f16x4 h) {
+  return (f16x4){lo_of(v[0], h[0]), lo_of(v[1], h[1]), lo_of(v[2], h[2]), lo_of(v[3], h[3])};
+}
+
+// Three products instead of one: hi lo + lo hi, scaled down, + hi hi.
+template <typename T, bool XQ, int PRODUCTS, typename F>
+__device__ __forceinline__ void products(F operands, f16* s0, f16* s1,
+                                         f32x4 (&acc)[T::FI][T::FJ]) {
+#pragma unroll
+  for (int i = 0; i < T::FI; ++i)
+#pragma unroll
+    for (int j = 0; j < T::FJ; ++j) acc[i][j] = (f32x4){0, 0, 0, 0};
+#pragma unroll 1
+  for (int pass = 0; pass < PRODUCTS; ++pass) {
+    if (PRODUCTS == 3 && pass == 2) {
+#pragma unroll
+      for (int i = 0; i < T::FI; ++i)
+#pragma unroll
+        for (int j = 0; j < T::FJ; ++j) acc[i][j] = acc[i][j] * (1.0f / kLo);
+    }
+    product(operands(PRODUCTS == 3 && pass == 1, PRODUCTS == 3 && pass == 0), s0, s1, acc);
+  }
+}
+
+// Symmetric results, lower tiles only, written to both places:
+//   kGram  S_out = X X^T
+//   kPoly  S_out = ca I + cb S + cc S S, S = S_in0
+//   kMul   S_out = S_in0 S_in1 (which commute: polynomials of one matrix)
+// A symmetric matrix is diag(D) + O, with O in 16 bits.
+enum Mode { kGram, kPoly, kMul };
+
+template <typename T, int SIZE, int MODE, int PRODUCTS>
+__global__ __launch_bounds__(T::kThreads) void zf_ns_sym(GemmArgs a) {
+  if (a.c.st && a.c.st->skipped) return;
+  __shared__ __align__(16) f16 s0[T::kBuf];
+  __shared__ __align__(16) f16 s1[T::kBuf];
+  const int w = tile_index();
+  const Mat& m = *find(a.c.table, a.c.count, w, [](const Mat& x) { return x.tri0[SIZE]; });
+  const int b = w - m.tri0[SIZE];
+  int ti = (int)((sqrtf(8.0f * (float)b + 1.0f) - 1.0f) * 0.5f);
+  while ((ti + 1) * (ti + 2) / 2 <= b) ++ti;
+  while (ti * (ti + 1) / 2 > b) --ti;
+  const int tj = b - ti * (ti + 1) / 2;
+  const int mp = m.mp, i0 = ti * T::BM, j0 = tj * T::BN;
+  const int64_t ld = MODE == kGram ? m.np : mp;
+
+  f32x4 acc[T::FI][T::FJ];
+  products<T, false, PRODUCTS>(
+      [&](bool lo_p, bool lo_q) {
+        const int64_t p = MODE == kGram ? (lo_p ? m.l[a.turn] : m.h[a.turn])
+                                        : (lo_p ? m.sl[a.in0] : m.s[a.in0]);
+        const int64_t q = MODE == kGram ? (lo_q ? m.l[a.turn] : m.h[a.turn])
+                                        : (lo_q ? m.sl[a.in1] : m.s[a.in1]);
+        return Operands<T, false>(at<f16>(a.c, p) + i0 * ld, ld, mp - i0,
+                                  at<f16>(a.c, q) + j0 * ld, ld, mp - j0, (int)ld);
+      },
+      s0, s1, acc);
+
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane & 15, g = lane >> 4;
+  const int wi = i0 + wave / T::kWavesJ * T::TI, wj = j0 + wave % T::kWavesJ * T::TJ;
+  const f16* o0 = at<f16>(a.c, m.s[a.in0]);
+  const f16* o1 = at<f16>(a.c, m.s[a.in1]);
+  const f16* r0 = at<f16>(a.c, m.sl[a.in0]);
+  const f16* r1 = at<f16>(a.c, m.sl[a.in1]);
+  const float* d0 = at<float>(a.c, m.d[a.in0]);
+  const float* d1 = at<float>(a.c, m.d[a.in1]);
+  f16* out = at<f16>(a.c, m.s[a.out]);
+  f16* rest = at<f16>(a.c, m.sl[a.out]);
+  float* diag = at<float>(a.c, m.d[a.out]);
+  // a wave's own 64 x 64 values, 16 bits each, on the way to the mirrored
+  // place: 8-byte pieces of a row permuted by the row number
+  static_assert(T::TJ == 64 && T::TI % 64 == 0, "staged in squares of 64");
+  ZF_LDS char* stage = (ZF_LDS char*)(s0) + wave * 8192;
+#pragma unroll
+  for (int half = 0; half < (PRODUCTS == 3 ? 2 : 1); ++half) {
+#pragma unroll
+    for (int q = 0; q < T::FI / 4; ++q) {
+#pragma unroll
+      for (int fi = q * 4; fi < q * 4 + 4; ++fi) {
+        const int i = wi + fi * 16 + 4 * g;
+        if (wi + fi * 16 >= mp) continue;
+#pragma unroll
+        for (int fj = 0; fj < T::FJ; ++fj) {
+          const int j = wj + fj * 16 + l;
+          if (wj + fj * 16 >= mp) continue;
+          const int64_t p = (int64_t)j * mp + i;  // (j, i..i+3): the mirrored place
+          float v[4];
+          if (half == 0) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = acc[fi][fj][r] * kUnscale2;
+            if constexpr (MODE != kGram) {
+              const f16x4 x0 = *reinterpret_cast<const f16x4*>(o0 + p);
+              const f32x4 di = *reinterpret_cast<const f32x4*>(d0 + i);
+              const float dj = d1[j];
+              f16x4 x1 = x0, y0 = {0, 0, 0, 0}, y1 = {0, 0, 0, 0};
+              if constexpr (MODE == kMul) x1 = *reinterpret_cast<const f16x4*>(o1 + p);
+              if constexpr (PRODUCTS == 3) {
+                y0 = *reinterpret_cast<const f16x4*>(r0 + p);
+                y1 = MODE == kMul ? *reinterpret_cast<const f16x4*>(r1 + p) : y0;
+              }
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const float e0 = value_of(x0[r], y0[r]), e1 = value_of(x1[r], y1[r]);
+                const bool on = i + r == j;
+                float w2 = v[r] + (on ? di[r] * dj : di[r] * e1 + e0 * dj);
+                if constexpr (MODE == kPoly)
+                  w2 = a.cb * (on ? dj : e0) + a.cc * w2 + (on ? a.ca : 0.0f);
+                v[r] = w2;
+              }
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              if (i + r == j) {
+                diag[j] = v[r];
+                v[r] = 0.0f;
+              }
+              acc[fi][fj][r] = v[r];  // kept for the second halves
+            }
+          } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = acc[fi][fj][r];
+          }
+          f16x4 x = halves(v);
+          if (half == 1) x = rests(v, x);
+          *reinterpret_cast<f16x4*>((half ? rest : out) + p) = x;
+          const int jj = fj * 16 + l, turn = ((jj & 3) << 2) | ((jj >> 2) & 3);
+          *(ZF_LDS f16x4*)(stage + jj * 128 + (((fi & 3) * 4 + g) ^ turn) * 8) = x;
+        }
+      }
+      if (ti == tj) continue;  // both places lie in this tile
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int fi = q * 4; fi < q * 4 + 4; ++fi) {
+        if (wi + fi * 16 >= mp) continue;
+#pragma unroll
+        for (int fj = 0; fj < T::FJ; ++fj) {
+          if (wj + fj * 16 >= mp) continue;
+          // source lane (row e, piece k) of each 16 hands over 4 values along
+          // i; lane l receives those of i = l along j
+          const int jj = fj * 16 + 4 * g + (l >> 2), turn = ((jj & 3) << 2) | ((jj >> 2) & 3);
+          const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (ZF_LDS s16x4*)(stage + jj * 128 + (((fi & 3) * 4 + (l & 3)) ^ turn) * 8));
+          const int64_t p = (int64_t)(wi + fi * 16 + l) * mp + wj + fj * 16 + 4 * g;
+          *reinterpret_cast<s16x4*>((half ? rest : out) + p) = x;
+        }
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    }
+  }
+}
+
+// X <- S X with S = S_in0: D_i X_ij from both halves of X, and O X.
 template <int DST>
-__device__ __forceinline__ void store1(const GemmArgs& a, const Mat& m, int64_t r, int64_t c,
-                                       float o) {
+__device__ __forceinline__ void store1(const Mat& m, int64_t r, int64_t c, float o) {
   if constexpr (DST == ZF_F32) {
     static_cast<float*>(m.dst)[r * m.dst_ld + c] = o;
   } else {
@@ -254,208 +657,156 @@ __device__ __forceinline__ void update1(const GemmArgs& a, const Mat& m, int64_t
   if constexpr (PDT != 0) static_cast<uint16_t*>(a.io.params)[p] = narrow1<PDT>(w);
 }
 
-template <int MODE, int PRODUCTS, int DST, bool MUON>
-__global__ __launch_bounds__(kThreads) void zf_ns_gemm(GemmArgs a) {
+template <typename T, int SIZE, bool LAST, int PRODUCTS, int DST, bool MUON>
+__global__ __launch_bounds__(T::kThreads) void zf_ns_apply(GemmArgs a) {
   if (a.c.st && a.c.st->skipped) return;
-  constexpr bool SYM = MODE == kGram || MODE == kPoly;
-  const Mat& m = SYM ? *find<&Mat::tri0>(a.c.table, a.c.count, blockIdx.x)
-                     : *find<&Mat::app0>(a.c.table, a.c.count, blockIdx.x);
-  int ti, tj;
-  if constexpr (SYM) {
-    const int b = blockIdx.x - m.tri0;
-    ti = (int)((sqrtf(8.0f * (float)b + 1.0f) - 1.0f) * 0.5f);
-    while ((ti + 1) * (ti + 2) / 2 <= b) ++ti;
-    while (ti * (ti + 1) / 2 > b) --ti;
-    tj = b - ti * (ti + 1) / 2;
-  } else {
-    const int b = blockIdx.x - m.app0, tiles_m = (m.mp + kBM - 1) / kBM;
-    ti = b % tiles_m;
-    tj = b / tiles_m;
-  }
-  const int mp = m.mp, np = m.np;
-  const int64_t k_len = MODE == kGram ? np : mp;
-  const int rows_p = mp, rows_q = SYM ? mp : np;
-  const int64_t off_p = MODE == kGram ? m.h : MODE == kPoly ? m.a : m.b;
-  const int64_t off_q = SYM ? off_p : m.t[a.turn];
-  const int64_t lo_p = MODE == kGram ? m.lo_x : m.lo_s;
-  const int64_t lo_q = MODE == kPoly ? m.lo_s : m.lo_x;
-  const int i0 = ti * kBM, j0 = tj * kBM;
+  __shared__ __align__(16) f16 s0[T::kBuf];
+  __shared__ __align__(16) f16 s1[T::kBuf];
+  const int w = tile_index();
+  const Mat& m = *find(a.c.table, a.c.count, w, [](const Mat& x) { return x.app0[SIZE]; });
+  const int b = w - m.app0[SIZE], tiles_m = (m.mp + T::BM - 1) / T::BM;
+  const int ti = b % tiles_m, tj = b / tiles_m;
+  const int mp = m.mp, np = m.np, i0 = ti * T::BM, j0 = tj * T::BN;
 
-  __shared__ union {
-    f16 k[2][kBM][kLd];
-    float c[kBM][kBM + 1];
-  } s;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int wi = (wave >> 1) * 64, wj = (wave & 1) * 64;
-  f32x4 acc[4][4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = (f32x4){0, 0, 0, 0};
+  f32x4 acc[T::FI][T::FJ];
+  products<T, true, PRODUCTS>(
+      [&](bool lo_p, bool lo_q) {
+        const int64_t p = lo_p ? m.sl[a.in0] : m.s[a.in0];
+        const int64_t q = lo_q ? m.l[a.turn] : m.h[a.turn];
+        return Operands<T, true>(at<f16>(a.c, p) + (int64_t)i0 * mp, mp, mp - i0,
+                                 at<f16>(a.c, q) + j0, np, j0, mp);
+      },
+      s0, s1, acc);
 
-  // a thread copies 4 pieces of 8 elements of each operand per step; rows
-  // past the padding are read from the last one and never stored
-  const int lr = threadIdx.x >> 3, lc = (threadIdx.x & 7) * 8;
-#pragma unroll 1
-  for (int pass = 0; pass < PRODUCTS; ++pass) {
-    // three products: hi lo, lo hi, (scaled down), hi hi
-    const int64_t dp = (PRODUCTS == 3 && pass == 1) ? lo_p : 0;
-    const int64_t dq = (PRODUCTS == 3 && pass == 0) ? lo_q : 0;
-    const f16* p = at<f16>(a.c, off_p + dp);
-    const f16* q = at<f16>(a.c, off_q + dq);
-    if (PRODUCTS == 3 && pass == 2) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane & 15, g = lane >> 4;
+  const int wi = i0 + wave / T::kWavesJ * T::TI, wj = j0 + wave % T::kWavesJ * T::TJ;
+  const f16* h = at<f16>(a.c, m.h[a.turn]);
+  const f16* lo = at<f16>(a.c, m.l[a.turn]);
+  f16* h1 = at<f16>(a.c, m.h[a.turn ^ 1]);
+  f16* lo1 = at<f16>(a.c, m.l[a.turn ^ 1]);
+  const float* d = at<float>(a.c, m.d[a.in0]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+  for (int fi = 0; fi < T::FI; ++fi) {
+    const int i = wi + fi * 16 + l;
+    if (wi + fi * 16 >= mp) continue;
+    const float di = d[i];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = acc[i][j] * (1.0f / kLo);
-    }
-    for (int64_t k0 = 0; k0 < k_len; k0 += kBK) {
-      f16x8 vp[4], vq[4];
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        const int64_t rp = min(i0 + lr + h * 32, rows_p - 1);
-        const int64_t rq = min(j0 + lr + h * 32, rows_q - 1);
-        vp[h] = *reinterpret_cast<const f16x8*>(p + rp * k_len + k0 + lc);
-        vq[h] = *reinterpret_cast<const f16x8*>(q + rq * k_len + k0 + lc);
-      }
-      __syncthreads();
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        *reinterpret_cast<f16x8*>(&s.k[0][lr + h * 32][lc]) = vp[h];
-        *reinterpret_cast<f16x8*>(&s.k[1][lr + h * 32][lc]) = vq[h];
-      }
-      __syncthreads();
-#pragma unroll
-      for (int kk = 0; kk < kBK; kk += 32) {
-        f16x8 fp[4], fq[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          fp[i] = *reinterpret_cast<f16x8*>(&s.k[0][wi + i * 16 + (lane & 15)][kk + (lane >> 4) * 8]);
-          fq[i] = *reinterpret_cast<f16x8*>(&s.k[1][wj + i * 16 + (lane & 15)][kk + (lane >> 4) * 8]);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fp[i], fq[j], acc[i][j], 0, 0, 0);
-      }
-    }
-  }
-
-  // the tile into shared memory: the result goes out along either axis
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        s.c[wi + i * 16 + (lane >> 4) * 4 + r][wj + j * 16 + (lane & 15)] = acc[i][j][r] * kUnscale2;
-  __syncthreads();
-
-  const int col = threadIdx.x & (kBM - 1), row0 = threadIdx.x / kBM;
-  constexpr int kRows = kThreads / kBM;
-  if constexpr (SYM) {
-    const f16* o = at<f16>(a.c, m.a);
-    const f16* ol = at<f16>(a.c, m.a + m.lo_s);
-    const float* da = at<float>(a.c, m.da);
-    f16* out = at<f16>(a.c, MODE == kGram ? m.a : m.b);
-    f16* outl = at<f16>(a.c, (MODE == kGram ? m.a : m.b) + m.lo_s);
-    float* diag = at<float>(a.c, MODE == kGram ? m.da : m.db);
-    for (int r = row0; r < kBM; r += kRows) {
-      const int i = i0 + r, j = j0 + col;
-      if (i >= mp || j >= mp) continue;
-      const int64_t p = (int64_t)i * mp + j;
-      float v = s.c[r][col];
-      if constexpr (MODE == kPoly) {
-        if (i == j) {
-          const float d = da[i];
-          v = a.cb * d + a.cc * (v + d * d);
-        } else {
-          const float x = value_of(o[p], PRODUCTS == 3 ? ol[p] : (f16)0);
-          v = a.cb * x + a.cc * (v + (da[i] + da[j]) * x);
-        }
-      }
-      if (i == j) {
-        diag[i] = v;
-        v = 0.0f;
-      }
-      s.c[r][col] = v;
-      out[p] = hi_of(v);
-      if constexpr (PRODUCTS == 3) outl[p] = lo_of(v, hi_of(v));
-    }
-    if (ti == tj) return;
-    __syncthreads();
-    for (int r = row0; r < kBM; r += kRows) {
-      const int i = j0 + r, j = i0 + col;  // the mirrored tile
-      if (i >= mp || j >= mp) continue;
-      const int64_t p = (int64_t)i * mp + j;
-      const float v = s.c[col][r];
-      out[p] = hi_of(v);
-      if constexpr (PRODUCTS == 3) outl[p] = lo_of(v, hi_of(v));
-    }
-  } else {
-    float* x = at<float>(a.c, m.x);
-    const float* db = at<float>(a.c, m.db);
-    const double inv = a.first ? a.c.inv[m.slot] : 1.0;
-    f16* h = at<f16>(a.c, m.h);
-    f16* hl = at<f16>(a.c, m.h + m.lo_x);
-    f16* t = at<f16>(a.c, m.t[a.turn ^ 1]);
-    f16* tl = at<f16>(a.c, m.t[a.turn ^ 1] + m.lo_x);
-    for (int r = row0; r < kBM; r += kRows) {
-      const int i = i0 + r, j = j0 + col;
-      if (i >= mp || j >= np) continue;
+    for (int fj = 0; fj < T::FJ; ++fj) {
+      const int j = wj + fj * 16 + 4 * g;
+      if (wj + fj * 16 >= np) continue;
       const int64_t p = (int64_t)i * np + j;
-      const float v = (a.ca + db[i]) * (float)((double)x[p] * inv) + s.c[r][col];
-      s.c[r][col] = v;
-      if constexpr (MODE == kApply) {
-        x[p] = v;
-        h[p] = hi_of(v);
-        if constexpr (PRODUCTS == 3) hl[p] = lo_of(v, hi_of(v));
-      } else if (!m.tall && i < m.m && j < m.n) {
-        if constexpr (MUON) update1<DST>(a, m, i, j, v);
-        else store1<DST>(a, m, i, j, v);
-      }
-    }
-    if (MODE == kLast && !m.tall) return;
-    __syncthreads();
-    for (int r = row0; r < kBM; r += kRows) {
-      const int j = j0 + r, i = i0 + col;
-      if (i >= mp || j >= np) continue;
-      const float v = s.c[col][r];
-      if constexpr (MODE == kApply) {
-        const int64_t p = (int64_t)j * mp + i;
-        t[p] = hi_of(v);
-        if constexpr (PRODUCTS == 3) tl[p] = lo_of(v, hi_of(v));
-      } else if (i < m.m && j < m.n) {
-        if constexpr (MUON) update1<DST>(a, m, j, i, v);
-        else store1<DST>(a, m, j, i, v);
+      const f16x4 x = *reinterpret_cast<const f16x4*>(h + p);
+      const f16x4 y = *reinterpret_cast<const f16x4*>(lo + p);
+      float v[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = di * value_of(x[r], y[r]) + acc[fi][fj][r] * kUnscale2;
+      if constexpr (!LAST) {
+        const f16x4 z = halves(v);
+        *reinterpret_cast<f16x4*>(h1 + p) = z;
+        *reinterpret_cast<f16x4*>(lo1 + p) = rests(v, z);
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if (i >= m.m || j + r >= m.n) continue;
+          const int64_t row = m.tall ? j + r : i, col = m.tall ? i : j + r;
+          if constexpr (MUON) update1<DST>(a, m, row, col, v[r]);
+          else store1<DST>(m, row, col, v[r]);
+        }
       }
     }
   }
 }
 
 template <int MODE, int PRODUCTS>
-void launch_inner(int blocks, hipStream_t s, const GemmArgs& a) {
-  hipLaunchKernelGGL((zf_ns_gemm<MODE, PRODUCTS, 0, false>), dim3(blocks), dim3(kThreads), 0, s, a);
+void launch_sym(const Group& g, int size, hipStream_t s, const GemmArgs& a) {
+  if (size == kBig)
+    hipLaunchKernelGGL((zf_ns_sym<Big, kBig, MODE, PRODUCTS>), dim3(g.tri_blocks[kBig]),
+                       dim3(Big::kThreads), 0, s, a);
+  else
+    hipLaunchKernelGGL((zf_ns_sym<Small, kSmall, MODE, PRODUCTS>), dim3(g.tri_blocks[kSmall]),
+                       dim3(Small::kThreads), 0, s, a);
+}
+
+template <bool LAST, int PRODUCTS, int DST, bool MUON>
+void launch_apply(const Group& g, int size, hipStream_t s, const GemmArgs& a) {
+  if (size == kBig)
+    hipLaunchKernelGGL((zf_ns_apply<Big, kBig, LAST, PRODUCTS, DST, MUON>),
+                       dim3(g.app_blocks[kBig]), dim3(Big::kThreads), 0, s, a);
+  else
+    hipLaunchKernelGGL((zf_ns_apply<Small, kSmall, LAST, PRODUCTS, DST, MUON>),
+                       dim3(g.app_blocks[kSmall]), dim3(Small::kThreads), 0, s, a);
 }
 
 template <int PRODUCTS>
-void launch_last(int blocks, hipStream_t s, int32_t dst, bool muon, const GemmArgs& a) {
-#define ZF_LAST(D, MU) \
-  hipLaunchKernelGGL((zf_ns_gemm<kLast, PRODUCTS, D, MU>), dim3(blocks), dim3(kThreads), 0, s, a)
+void launch_last(const Group& g, int size, hipStream_t s, int32_t dst, bool muon,
+                 const GemmArgs& a) {
   if (muon) {
-    if (!a.io.params) ZF_LAST(0, true);
-    else if (dst == ZF_BF16) ZF_LAST(ZF_BF16, true);
-    else ZF_LAST(ZF_F16, true);
+    if (!a.io.params) launch_apply<true, PRODUCTS, 0, true>(g, size, s, a);
+    else if (dst == ZF_BF16) launch_apply<true, PRODUCTS, ZF_BF16, true>(g, size, s, a);
+    else launch_apply<true, PRODUCTS, ZF_F16, true>(g, size, s, a);
   } else if (dst == ZF_BF16) {
-    ZF_LAST(ZF_BF16, false);
+    launch_apply<true, PRODUCTS, ZF_BF16, false>(g, size, s, a);
   } else if (dst == ZF_F16) {
-    ZF_LAST(ZF_F16, false);
+    launch_apply<true, PRODUCTS, ZF_F16, false>(g, size, s, a);
   } else {
-    ZF_LAST(ZF_F32, false);
+    launch_apply<true, PRODUCTS, ZF_F32, false>(g, size, s, a);
   }
-#undef ZF_LAST
+}
+
+// The iteration of one group.  Steps run on X, or in pairs on the m x m side
+// (X_2 = Q_2 Q_1 X with A_2 = Q_1 A Q_1), which touches the long side once
+// for two steps and costs no more products when n = m: 20 m^3 + 9 m^2 (n-m)
+// instead of 20 m^3 + 15 m^2 (n-m) for five.  Pairs and single steps take
+// turns (2, 1, 2): longer stretches lose the small singular values, whose
+// squares vanish in A's rounding (error 1.3e-3 at most for 2, 1, 2; 3e-3 for
+// 3, 2; 0.2 for all five).
+template <int PRODUCTS>
+int iterate(const Group& g, const zf_ns_params& p, int sym, int app, int32_t dst, bool muon,
+            hipStream_t s, GemmArgs a) {
+  a.turn = 0;
+  bool pair = p.steps > 1;
+  for (int k = 0; k < p.steps;) {
+    const int n = pair && k + 2 <= p.steps ? 2 : 1;
+    pair = !pair;
+    a.ca = (float)p.a;
+    a.cb = (float)p.b;
+    a.cc = (float)p.c;
+    auto op = [&](int in0, int in1, int out) {
+      a.in0 = in0;
+      a.in1 = in1;
+      a.out = out;
+    };
+    op(0, 0, 0);
+    launch_sym<kGram, PRODUCTS>(g, sym, s, a);  // 0 = A
+    op(0, 0, 1);
+    launch_sym<kPoly, PRODUCTS>(g, sym, s, a);  // 1 = Q
+    if (n == 2) {
+      op(1, 0, 2);
+      launch_sym<kMul, PRODUCTS>(g, sym, s, a);   // 2 = Q A
+      op(1, 2, 0);
+      launch_sym<kMul, PRODUCTS>(g, sym, s, a);   // 0 = Q Q A: the next A
+      op(0, 0, 2);
+      launch_sym<kPoly, PRODUCTS>(g, sym, s, a);  // 2 = the next Q
+      op(2, 1, 0);
+      launch_sym<kMul, PRODUCTS>(g, sym, s, a);   // 0 = their product
+    }
+    a.in0 = n == 2 ? 0 : 1;
+    k += n;
+    if (k == p.steps) launch_last<PRODUCTS>(g, app, s, dst, muon, a);
+    else launch_apply<false, PRODUCTS, ZF_F32, false>(g, app, s, a);
+    a.turn ^= 1;
+    if (!hip_ok(hipGetLastError())) return ZF_EHIP;
+  }
+  return ZF_OK;
+}
+
+// The tile size for a launch of `big` tiles of 256 x 256 (one block a CU) or
+// `small` ones of 128 x 128 (two a CU, at 0.85 of the rate): whichever takes
+// fewer rounds over the 256 CUs, weighted by its tile's time.
+int tile_size(int64_t big, int64_t small) {
+  const double b = 4.0 * (double)((big + 255) / 256);
+  const double sm = 2.0 / 0.85 * (double)((small + 511) / 512);
+  return b <= sm ? kBig : kSmall;
 }
 
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
@@ -496,17 +847,21 @@ bool zf::ns::layout(const Shape* shapes, int64_t count, int products, Layout& ou
   out.mats.resize((size_t)count);
   out.groups.clear();
   int64_t partials = 0, region = 0, used = 0, elements = 0;
-  Group g{0, 0, 0, 0, 0};
-  int64_t load = 0, tri = 0, app = 0;
-  const int halves = products == 3 ? 2 : 1;
+  Group g{};
+  int64_t load = 0, tri[2] = {0, 0}, app[2] = {0, 0};
   auto close = [&]() {
     g.load_blocks = (int32_t)load;
-    g.tri_blocks = (int32_t)tri;
-    g.app_blocks = (int32_t)app;
+    for (int z = 0; z < 2; ++z) {
+      g.tri_blocks[z] = (int32_t)tri[z];
+      g.app_blocks[z] = (int32_t)app[z];
+      tri[z] = app[z] = 0;
+    }
     out.groups.push_back(g);
     region = std::max(region, used);
-    g = Group{g.first + g.count, 0, 0, 0, 0};
-    used = elements = load = tri = app = 0;
+    const int32_t next = g.first + g.count;
+    g = Group{};
+    g.first = next;
+    used = elements = load = 0;
   };
   auto take = [&](int64_t bytes) {
     const int64_t o = used;
@@ -527,26 +882,30 @@ bool zf::ns::layout(const Shape* shapes, int64_t count, int products, Layout& ou
     if (g.count > 0 && elements + mn > kGroupElements) close();
     m.slot = (int32_t)k;
     m.src_ld = m.dst_ld = cols;
-    m.lo_x = round_up(mn * 2, 256);
-    m.lo_s = round_up(mm * 2, 256);
-    m.x = take(mn * 4);
-    m.h = take(m.lo_x * halves);
-    m.t[0] = take(m.lo_x * halves);
-    m.t[1] = take(m.lo_x * halves);
-    m.a = take(m.lo_s * halves);
-    m.b = take(m.lo_s * halves);
-    m.da = take((int64_t)m.mp * 4);
-    m.db = take((int64_t)m.mp * 4);
-    const int64_t tm = (m.mp + kBM - 1) / kBM, tn = (m.np + kBM - 1) / kBM;
+    // what the rounding left of X: an operand of the products if there are
+    // three, else used by its own tile alone, in place
+    for (int z = 0; z < 2; ++z) {
+      m.h[z] = take(mn * 2);
+      m.l[z] = z == 0 || products == 3 ? take(mn * 2) : m.l[0];
+    }
+    for (int z = 0; z < 3; ++z) {
+      m.s[z] = take(mm * 2);
+      m.sl[z] = products == 3 ? take(mm * 2) : m.s[z];
+      m.d[z] = take((int64_t)m.mp * 4);
+    }
     const int64_t tiles = (int64_t)(m.mp / kTile) * (m.np / kTile);
     m.part = partials;
     partials += tiles;
     m.load0 = (int32_t)load;
-    m.tri0 = (int32_t)tri;
-    m.app0 = (int32_t)app;
     load += tiles;
-    tri += tm * (tm + 1) / 2;
-    app += tm * tn;
+    const int side[2] = {Big::BM, Small::BM};
+    for (int z = 0; z < 2; ++z) {
+      const int64_t tm = (m.mp + side[z] - 1) / side[z], tn = (m.np + side[z] - 1) / side[z];
+      m.tri0[z] = (int32_t)tri[z];
+      m.app0[z] = (int32_t)app[z];
+      tri[z] += tm * (tm + 1) / 2;
+      app[z] += tm * tn;
+    }
     if (load > 0x7FFFFFFF) return false;
     elements += mn;
     ++g.count;
@@ -559,8 +918,10 @@ bool zf::ns::layout(const Shape* shapes, int64_t count, int products, Layout& ou
   at += round_up(count * 8, 256);
   out.partials = at;
   at += round_up(partials * 8, 256);
-  for (Mat& m : out.mats)
-    for (int64_t* o : {&m.x, &m.h, &m.t[0], &m.t[1], &m.a, &m.b, &m.da, &m.db}) *o += at;
+  for (Mat& m : out.mats) {
+    for (int z = 0; z < 2; ++z) m.h[z] += at, m.l[z] += at;
+    for (int z = 0; z < 3; ++z) m.s[z] += at, m.sl[z] += at, m.d[z] += at;
+  }
   out.bytes = at + region;
   return true;
 }
@@ -577,55 +938,40 @@ int zf::ns::enqueue(const Layout& l, const zf_ns_params& p, int products, int32_
     if (!hip_ok(hipGetLastError())) return ZF_EHIP;
   }
   for (const Group& g : l.groups) {
-    Common c;
+    LoadArgs la;
+    Common& c = la.c;
     c.ws = ws;
     c.table = table + g.first;
     c.count = g.count;
     c.st = io ? io->st : nullptr;
     c.inv = reinterpret_cast<double*>(ws + l.inv);
     c.partials = reinterpret_cast<double*>(ws + l.partials);
-
-    LoadArgs la;
-    la.c = c;
     la.io = io ? *io : MuonIo{};
     const dim3 load(g.load_blocks), block(kThreads);
-    if (io) hipLaunchKernelGGL(zf_ns_load<0>, load, block, 0, s, la);
-    else if (src_dtype == ZF_F32) hipLaunchKernelGGL(zf_ns_load<ZF_F32>, load, block, 0, s, la);
-    else if (src_dtype == ZF_BF16) hipLaunchKernelGGL(zf_ns_load<ZF_BF16>, load, block, 0, s, la);
+    const int32_t src = io ? 0 : src_dtype;
+    if (src == 0) hipLaunchKernelGGL(zf_ns_load<0>, load, block, 0, s, la);
+    else if (src == ZF_F32) hipLaunchKernelGGL(zf_ns_load<ZF_F32>, load, block, 0, s, la);
+    else if (src == ZF_BF16) hipLaunchKernelGGL(zf_ns_load<ZF_BF16>, load, block, 0, s, la);
     else hipLaunchKernelGGL(zf_ns_load<ZF_F16>, load, block, 0, s, la);
-    if (!hip_ok(hipGetLastError())) return ZF_EHIP;
     NormArgs na;
     na.c = c;
     na.eps = p.eps;
     hipLaunchKernelGGL(zf_ns_norm, dim3(g.count), block, 0, s, na);
-    if (!hip_ok(hipGetLastError())) return ZF_EHIP;
-    if (products == 3) hipLaunchKernelGGL(zf_ns_prep<3>, load, block, 0, s, c);
-    else hipLaunchKernelGGL(zf_ns_prep<1>, load, block, 0, s, c);
+    if (src == 0) hipLaunchKernelGGL(zf_ns_prep<0>, load, block, 0, s, la);
+    else if (src == ZF_F32) hipLaunchKernelGGL(zf_ns_prep<ZF_F32>, load, block, 0, s, la);
+    else if (src == ZF_BF16) hipLaunchKernelGGL(zf_ns_prep<ZF_BF16>, load, block, 0, s, la);
+    else hipLaunchKernelGGL(zf_ns_prep<ZF_F16>, load, block, 0, s, la);
     if (!hip_ok(hipGetLastError())) return ZF_EHIP;
 
     GemmArgs ga;
     ga.c = c;
     ga.io = la.io;
-    ga.ca = (float)p.a;
-    ga.cb = (float)p.b;
-    ga.cc = (float)p.c;
-    for (int k = 0; k < p.steps; ++k) {
-      ga.turn = k & 1;
-      ga.first = k == 0;
-      const bool last = k + 1 == p.steps;
-      if (products == 3) {
-        launch_inner<kGram, 3>(g.tri_blocks, s, ga);
-        launch_inner<kPoly, 3>(g.tri_blocks, s, ga);
-        if (last) launch_last<3>(g.app_blocks, s, dst_dtype, io != nullptr, ga);
-        else launch_inner<kApply, 3>(g.app_blocks, s, ga);
-      } else {
-        launch_inner<kGram, 1>(g.tri_blocks, s, ga);
-        launch_inner<kPoly, 1>(g.tri_blocks, s, ga);
-        if (last) launch_last<1>(g.app_blocks, s, dst_dtype, io != nullptr, ga);
-        else launch_inner<kApply, 1>(g.app_blocks, s, ga);
-      }
-      if (!hip_ok(hipGetLastError())) return ZF_EHIP;
-    }
+    const int sym = tile_size(g.tri_blocks[kBig], g.tri_blocks[kSmall]);
+    const int app = tile_size(g.app_blocks[kBig], g.app_blocks[kSmall]);
+    const int rc = products == 3
+                       ? iterate<3>(g, p, sym, app, dst_dtype, io != nullptr, s, ga)
+                       : iterate<1>(g, p, sym, app, dst_dtype, io != nullptr, s, ga);
+    if (rc != ZF_OK) return rc;
   }
   return ZF_OK;
 }
