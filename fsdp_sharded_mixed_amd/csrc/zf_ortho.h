@@ -26,13 +26,14 @@ struct Mat {
   void* dst;              // zf_orthogonalize: the result, row stride dst_ld
   int64_t src_ld, dst_ld; // the Muon step: both = cols
   int64_t flat;           // the Muon step: offset in the padded flat arrays
-  int64_t h[2], l[2];     // fp16 [mp][np]: X * 2^10 rounded, and what the
+  int64_t h[2], l[2];     // fp16 [mp][ldx]: X * 2^10 rounded, and what the
                           // rounding left; two buffers in turn
-  int64_t s[3], sl[3];    // fp16 [mp][mp]: symmetric matrices off the
+  int64_t s[3], sl[3];    // fp16 [mp][lds]: symmetric matrices off the
                           // diagonal, rounded, and what that left
   int64_t d[3];           // fp32 [mp]: their diagonals
   int64_t part;           // its first squared-norm partial
   int32_t m, n, mp, np;
+  int32_t ldx, lds;       // row strides of X and of the symmetric matrices
   int32_t tall, slot;     // slot: its place in the array of inverse norms
   float rate;             // the Muon step: lr * scale
   int32_t load0;          // its first block in the launches of its group,

@@ -110,57 +110,133 @@ __device__ __forceinline__ T* at(const Common& c, int64_t offset) {
 }
 
 // ---------------------------------------------------------------------------
-// The squared norm, one partial (64 bits) per 64 x 64 tile; the Muon step's
-// momentum update on the way.
-constexpr int kTile = 64;
+// The squared norm, one partial (64 bits) per block; the Muon step's momentum
+// update on the way.
+constexpr int kTile = 64, kLoadTiles = 4;
 
 struct LoadArgs {
   Common c;
   MuonIo io;
 };
 
-// Element (r, c) of the matrix; SRC: ZF_F16, ZF_BF16, ZF_F32, or 0: the Muon
-// step's U, from the momentum that it updates first (FIRST) or has updated.
+// Whether 8 elements at a multiple of 8 of any row lie at a multiple of 16
+// bytes.
+template <int SRC>
+__device__ __forceinline__ bool wide_loads(const Mat& m) {
+  if constexpr (SRC == 0) return ((m.flat | m.src_ld) & 3) == 0;
+  else if constexpr (SRC == ZF_F32)
+    return ((reinterpret_cast<uintptr_t>(m.src) | (uintptr_t)(m.src_ld * 4)) & 15) == 0;
+  else return ((reinterpret_cast<uintptr_t>(m.src) | (uintptr_t)(m.src_ld * 2)) & 15) == 0;
+}
+
+// Elements (r, c .. c + 7) of the matrix, zeros past its last column.  SRC:
+// ZF_F16, ZF_BF16, ZF_F32, or 0: the Muon step's U, from the momentum that it
+// updates first (FIRST) or has updated.
 template <int SRC, bool FIRST>
-__device__ __forceinline__ float load1(const LoadArgs& a, const Mat& m, float gs, int64_t r,
-                                       int64_t c) {
+__device__ __forceinline__ void load8(const LoadArgs& a, const Mat& m, float gs, bool wide,
+                                      int64_t r, int c, int cols, float (&v)[8]) {
+  const int64_t p = r * m.src_ld + c;
+  const int n = cols - c;
   if constexpr (SRC == 0) {
-    const int64_t p = m.flat + r * m.src_ld + c;
-    float mm = a.io.momentum[p];
-    if (!FIRST && !a.io.nesterov) return mm;
-    const float g = a.io.sums[p] * gs;
-    if constexpr (FIRST) {
-      mm = a.io.mu * mm + g;
-      a.io.momentum[p] = mm;
+    float* mom = a.io.momentum + m.flat + p;
+    const float* sums = a.io.sums + m.flat + p;
+    const bool with_g = FIRST || a.io.nesterov;
+    float g[8];
+    if (wide && n >= 8) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const f32x4 x = reinterpret_cast<const f32x4*>(mom)[h];
+        f32x4 y = {0, 0, 0, 0};
+        if (with_g) y = reinterpret_cast<const f32x4*>(sums)[h];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[h * 4 + e] = x[e], g[h * 4 + e] = y[e];
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[e] = e < n ? mom[e] : 0.0f;
+        g[e] = e < n && with_g ? sums[e] : 0.0f;
+      }
     }
-    return a.io.nesterov ? g + a.io.mu * mm : mm;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      g[e] = g[e] * gs;
+      if constexpr (FIRST) v[e] = a.io.mu * v[e] + g[e];
+    }
+    if constexpr (FIRST) {
+      if (wide && n >= 8) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          reinterpret_cast<f32x4*>(mom)[h] =
+              (f32x4){v[h * 4], v[h * 4 + 1], v[h * 4 + 2], v[h * 4 + 3]};
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (e < n) mom[e] = v[e];
+      }
+    }
+    if (a.io.nesterov) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = g[e] + a.io.mu * v[e];
+    }
   } else if constexpr (SRC == ZF_F32) {
-    return static_cast<const float*>(m.src)[r * m.src_ld + c];
+    const float* x = static_cast<const float*>(m.src) + p;
+    if (wide && n >= 8) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const f32x4 y = reinterpret_cast<const f32x4*>(x)[h];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[h * 4 + e] = y[e];
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = e < n ? x[e] : 0.0f;
+    }
   } else {
-    return widen1<SRC>(static_cast<const uint16_t*>(m.src)[r * m.src_ld + c]);
+    const uint16_t* x = static_cast<const uint16_t*>(m.src) + p;
+    if (wide && n >= 8) {
+      typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+      const u32x4 y = *reinterpret_cast<const u32x4*>(x);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[2 * e] = lo16<SRC>(y[e]), v[2 * e + 1] = hi16<SRC>(y[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = e < n ? widen1<SRC>(x[e]) : 0.0f;
+    }
   }
 }
 
-// A wave reads 64 elements along the source's rows; tile (i0, j0) of X.
+// A block takes kLoadTiles tiles of 64 x 64; a thread 8 neighbours along the
+// source's rows at a time.
 template <int SRC>
 __global__ __launch_bounds__(kThreads) void zf_ns_load(LoadArgs a) {
   if (a.c.st && a.c.st->skipped) return;
   const Mat& m = *find_load(a.c.table, a.c.count, blockIdx.x);
-  const int tile = blockIdx.x - m.load0, tiles_n = m.np / kTile;
-  const int i0 = tile / tiles_n * kTile, j0 = tile % tiles_n * kTile;
+  const int block = blockIdx.x - m.load0, tiles_n = m.np / kTile;
+  const int tiles = m.mp / kTile * tiles_n;
   const float gs = SRC == 0 ? a.c.st->gs : 0.0f;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const bool wide = wide_loads<SRC>(m);
+  const int rows = m.tall ? m.n : m.m, cols = m.tall ? m.m : m.n;
   double ss = 0.0;
-#pragma unroll 4
-  for (int k = wave; k < kTile; k += kThreads / 64) {
-    const int i = m.tall ? i0 + lane : i0 + k, j = m.tall ? j0 + k : j0 + lane;
-    if (i >= m.m || j >= m.n) continue;
-    const float v = load1<SRC, true>(a, m, gs, m.tall ? j : i, m.tall ? i : j);
-    ss += (double)v * (double)v;
+#pragma unroll
+  for (int t = 0; t < kLoadTiles; ++t) {
+    const int tile = block * kLoadTiles + t;
+    if (tile >= tiles) break;
+    const int i0 = tile / tiles_n * kTile, j0 = tile % tiles_n * kTile;
+    const int r0 = m.tall ? j0 : i0, c0 = m.tall ? i0 : j0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = threadIdx.x + h * kThreads, r = r0 + k / 8, c = c0 + k % 8 * 8;
+      if (r >= rows || c >= cols) continue;
+      float v[8];
+      load8<SRC, true>(a, m, gs, wide, r, c, cols, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss += (double)v[e] * (double)v[e];
+    }
   }
   uint32_t unused = 0;
   block_reduce(ss, unused);
-  if (threadIdx.x == 0) a.c.partials[m.part + tile] = ss;
+  if (threadIdx.x == 0) a.c.partials[m.part + block] = ss;
 }
 
 // The inverse norm of every matrix of the group: its partials in a fixed
@@ -174,8 +250,9 @@ __global__ __launch_bounds__(kThreads) void zf_ns_norm(NormArgs a) {
   if (a.c.st && a.c.st->skipped) return;
   const Mat& m = a.c.table[blockIdx.x];
   const int64_t tiles = (int64_t)(m.mp / kTile) * (m.np / kTile);
+  const int64_t parts = (tiles + kLoadTiles - 1) / kLoadTiles;
   double ss = 0.0;
-  for (int64_t i = threadIdx.x; i < tiles; i += kThreads) ss += a.c.partials[m.part + i];
+  for (int64_t i = threadIdx.x; i < parts; i += kThreads) ss += a.c.partials[m.part + i];
   uint32_t unused = 0;
   block_reduce(ss, unused);
   if (threadIdx.x == 0) a.c.inv[m.slot] = 1.0 / (sqrt(ss) + a.eps);
@@ -188,33 +265,59 @@ template <int SRC>
 __global__ __launch_bounds__(kThreads) void zf_ns_prep(LoadArgs a) {
   if (a.c.st && a.c.st->skipped) return;
   const Mat& m = *find_load(a.c.table, a.c.count, blockIdx.x);
-  const int tile = blockIdx.x - m.load0, tiles_n = m.np / kTile;
-  const int i0 = tile / tiles_n * kTile, j0 = tile % tiles_n * kTile;
+  const int block = blockIdx.x - m.load0, tiles_n = m.np / kTile;
+  const int tiles = m.mp / kTile * tiles_n;
   const float gs = SRC == 0 ? a.c.st->gs : 0.0f;
   const double inv = a.c.inv[m.slot];
+  const bool wide = wide_loads<SRC>(m);
+  const int rows = m.tall ? m.n : m.m, cols = m.tall ? m.m : m.n;
   __shared__ float s[kTile][kTile + 1];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  f16* h = at<f16>(a.c, m.h[0]);
-  f16* l = at<f16>(a.c, m.l[0]);
-  if (m.tall) {
-#pragma unroll 4
-    for (int k = wave; k < kTile; k += kThreads / 64) {
-      const int i = i0 + lane, j = j0 + k;
-      s[lane][k] = i < m.m && j < m.n ? load1<SRC, false>(a, m, gs, j, i) : 0.0f;
+  f16* hp = at<f16>(a.c, m.h[0]);
+  f16* lp = at<f16>(a.c, m.l[0]);
+#pragma unroll 1
+  for (int t = 0; t < kLoadTiles; ++t) {
+    const int tile = block * kLoadTiles + t;
+    if (tile >= tiles) break;
+    const int i0 = tile / tiles_n * kTile, j0 = tile % tiles_n * kTile;
+    const int r0 = m.tall ? j0 : i0, c0 = m.tall ? i0 : j0;
+    float v[2][8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = threadIdx.x + h * kThreads, r = r0 + k / 8, c = c0 + k % 8 * 8;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[h][e] = 0.0f;
+      if (r < rows && c < cols) load8<SRC, false>(a, m, gs, wide, r, c, cols, v[h]);
     }
-    __syncthreads();
-  }
-#pragma unroll 4
-  for (int k = wave; k < kTile; k += kThreads / 64) {
-    const int i = i0 + k, j = j0 + lane;
-    float u = 0.0f;
-    if (m.tall) u = s[k][lane];
-    else if (i < m.m && j < m.n) u = load1<SRC, false>(a, m, gs, i, j);
-    const float v = i < m.m && j < m.n ? (float)((double)u * inv) : 0.0f;
-    const int64_t p = (int64_t)i * m.np + j;
-    const f16 hi = hi_of(v);
-    h[p] = hi;
-    l[p] = lo_of(v, hi);
+    if (m.tall) {
+      __syncthreads();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int k = threadIdx.x + h * kThreads;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[k % 8 * 8 + e][k / 8] = v[h][e];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int k = threadIdx.x + h * kThreads;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[h][e] = s[k / 8][k % 8 * 8 + e];
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = threadIdx.x + h * kThreads, i = i0 + k / 8, j = j0 + k % 8 * 8;
+      f16x8 hi, lo;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x = i < m.m && j + e < m.n ? (float)((double)v[h][e] * inv) : 0.0f;
+        hi[e] = hi_of(x);
+        lo[e] = lo_of(x, hi[e]);
+      }
+      const int64_t p = (int64_t)i * m.ldx + j;
+      *reinterpret_cast<f16x8*>(hp + p) = hi;
+      *reinterpret_cast<f16x8*>(lp + p) = lo;
+    }
   }
 }
 
@@ -528,7 +631,8 @@ __global__ __launch_bounds__(T::kThreads) void zf_ns_sym(GemmArgs a) {
   while (ti * (ti + 1) / 2 > b) --ti;
   const int tj = b - ti * (ti + 1) / 2;
   const int mp = m.mp, i0 = ti * T::BM, j0 = tj * T::BN;
-  const int64_t ld = MODE == kGram ? m.np : mp;
+  const int64_t ld = MODE == kGram ? m.ldx : m.lds;
+  const int len = MODE == kGram ? m.np : mp;
 
   f32x4 acc[T::FI][T::FJ];
   products<T, false, PRODUCTS>(
@@ -538,11 +642,12 @@ __global__ __launch_bounds__(T::kThreads) void zf_ns_sym(GemmArgs a) {
         const int64_t q = MODE == kGram ? (lo_q ? m.l[a.turn] : m.h[a.turn])
                                         : (lo_q ? m.sl[a.in1] : m.s[a.in1]);
         return Operands<T, false>(at<f16>(a.c, p) + i0 * ld, ld, mp - i0,
-                                  at<f16>(a.c, q) + j0 * ld, ld, mp - j0, (int)ld);
+                                  at<f16>(a.c, q) + j0 * ld, ld, mp - j0, len);
       },
       s0, s1, acc);
 
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wi = i0 + wave / T::kWavesJ * T::TI, wj = j0 + wave % T::kWavesJ * T::TJ;
   const f16* o0 = at<f16>(a.c, m.s[a.in0]);
   const f16* o1 = at<f16>(a.c, m.s[a.in1]);
@@ -556,39 +661,69 @@ __global__ __launch_bounds__(T::kThreads) void zf_ns_sym(GemmArgs a) {
   // a wave's own 64 x 64 values, 16 bits each, on the way to the mirrored
   // place: 8-byte pieces of a row permuted by the row number
   static_assert(T::TJ == 64 && T::TI % 64 == 0, "staged in squares of 64");
+  float dv[T::FJ];
+  if constexpr (MODE != kGram) {
+#pragma unroll
+    for (int fj = 0; fj < T::FJ; ++fj) {
+      const int j = wj + fj * 16 + l;
+      dv[fj] = j < mp ? d1[j] : 0.0f;
+    }
+  }
   ZF_LDS char* stage = (ZF_LDS char*)(s0) + wave * 8192;
 #pragma unroll
   for (int half = 0; half < (PRODUCTS == 3 ? 2 : 1); ++half) {
 #pragma unroll
     for (int q = 0; q < T::FI / 4; ++q) {
+      // every load of 4 rows of fragments before the first store, which the
+      // compiler could not move them past
+      f16x4 x0[4][T::FJ], x1[4][T::FJ], y0[4][T::FJ], y1[4][T::FJ];
+      f32x4 di[4];
+      if constexpr (MODE != kGram) {
+        if (half == 0) {
+#pragma unroll
+          for (int f = 0; f < 4; ++f) {
+            const int i = wi + (q * 4 + f) * 16 + 4 * g;
+            if (wi + (q * 4 + f) * 16 >= mp) continue;
+            di[f] = *reinterpret_cast<const f32x4*>(d0 + i);
+#pragma unroll
+            for (int fj = 0; fj < T::FJ; ++fj) {
+              const int j = wj + fj * 16 + l;
+              if (wj + fj * 16 >= mp) continue;
+              const int64_t p = (int64_t)j * m.lds + i;
+              x0[f][fj] = *reinterpret_cast<const f16x4*>(o0 + p);
+              if constexpr (MODE == kMul) x1[f][fj] = *reinterpret_cast<const f16x4*>(o1 + p);
+              if constexpr (PRODUCTS == 3) {
+                y0[f][fj] = *reinterpret_cast<const f16x4*>(r0 + p);
+                if constexpr (MODE == kMul) y1[f][fj] = *reinterpret_cast<const f16x4*>(r1 + p);
+              }
+            }
+          }
+        }
+      }
 #pragma unroll
       for (int fi = q * 4; fi < q * 4 + 4; ++fi) {
-        const int i = wi + fi * 16 + 4 * g;
+        const int i = wi + fi * 16 + 4 * g, f = fi & 3;
         if (wi + fi * 16 >= mp) continue;
 #pragma unroll
         for (int fj = 0; fj < T::FJ; ++fj) {
           const int j = wj + fj * 16 + l;
           if (wj + fj * 16 >= mp) continue;
-          const int64_t p = (int64_t)j * mp + i;  // (j, i..i+3): the mirrored place
+          const int64_t p = (int64_t)j * m.lds + i;  // (j, i..i+3): the mirrored place
           float v[4];
           if (half == 0) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) v[r] = acc[fi][fj][r] * kUnscale2;
             if constexpr (MODE != kGram) {
-              const f16x4 x0 = *reinterpret_cast<const f16x4*>(o0 + p);
-              const f32x4 di = *reinterpret_cast<const f32x4*>(d0 + i);
-              const float dj = d1[j];
-              f16x4 x1 = x0, y0 = {0, 0, 0, 0}, y1 = {0, 0, 0, 0};
-              if constexpr (MODE == kMul) x1 = *reinterpret_cast<const f16x4*>(o1 + p);
-              if constexpr (PRODUCTS == 3) {
-                y0 = *reinterpret_cast<const f16x4*>(r0 + p);
-                y1 = MODE == kMul ? *reinterpret_cast<const f16x4*>(r1 + p) : y0;
-              }
+              const float dj = dv[fj];
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
-                const float e0 = value_of(x0[r], y0[r]), e1 = value_of(x1[r], y1[r]);
+                const f16 none = 0;
+                const float e0 = value_of(x0[f][fj][r], PRODUCTS == 3 ? y0[f][fj][r] : none);
+                const float e1 = MODE == kMul
+                                     ? value_of(x1[f][fj][r], PRODUCTS == 3 ? y1[f][fj][r] : none)
+                                     : e0;
                 const bool on = i + r == j;
-                float w2 = v[r] + (on ? di[r] * dj : di[r] * e1 + e0 * dj);
+                float w2 = v[r] + (on ? di[f][r] * dj : di[f][r] * e1 + e0 * dj);
                 if constexpr (MODE == kPoly)
                   w2 = a.cb * (on ? dj : e0) + a.cc * w2 + (on ? a.ca : 0.0f);
                 v[r] = w2;
@@ -627,7 +762,7 @@ __global__ __launch_bounds__(T::kThreads) void zf_ns_sym(GemmArgs a) {
           const int jj = fj * 16 + 4 * g + (l >> 2), turn = ((jj & 3) << 2) | ((jj >> 2) & 3);
           const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
               (ZF_LDS s16x4*)(stage + jj * 128 + (((fi & 3) * 4 + (l & 3)) ^ turn) * 8));
-          const int64_t p = (int64_t)(wi + fi * 16 + l) * mp + wj + fj * 16 + 4 * g;
+          const int64_t p = (int64_t)(wi + fi * 16 + l) * m.lds + wj + fj * 16 + 4 * g;
           *reinterpret_cast<s16x4*>((half ? rest : out) + p) = x;
         }
       }
@@ -637,26 +772,47 @@ __global__ __launch_bounds__(T::kThreads) void zf_ns_sym(GemmArgs a) {
   }
 }
 
-// X <- S X with S = S_in0: D_i X_ij from both halves of X, and O X.
-template <int DST>
-__device__ __forceinline__ void store1(const Mat& m, int64_t r, int64_t c, float o) {
-  if constexpr (DST == ZF_F32) {
-    static_cast<float*>(m.dst)[r * m.dst_ld + c] = o;
-  } else {
-    static_cast<uint16_t*>(m.dst)[r * m.dst_ld + c] = narrow1<DST>(o);
+// A wave's 64 x 64 results at (i0, j0) of X, from shared memory (laid out as
+// in zf_ns_apply), to the destination, whose rows run along j, or for a
+// tall matrix along i: 64 neighbours an instruction, at any alignment.
+// DST is the result's type; MUON: W <- W dec - rate (result), and the 16-bit
+// parameters of type DST (0: none).
+template <int DST, bool MUON>
+__device__ __forceinline__ void write_square(const GemmArgs& a, const Mat& m,
+                                             const ZF_LDS float* square, int i0, int j0) {
+  const int lane = threadIdx.x & 63;
+  const int rows = m.tall ? m.n - j0 : m.m - i0, cols = m.tall ? m.m - i0 : m.n - j0;
+  const int64_t at = (int64_t)(m.tall ? j0 : i0) * m.dst_ld + (m.tall ? i0 : j0) + lane;
+  if (lane >= cols) return;
+  constexpr int kBatch = 8;  // rows whose loads are on their way together
+  for (int k = 0; k < min(rows, 64); k += kBatch) {
+    float v[kBatch], w[kBatch];
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      const int i = m.tall ? lane : k + e, j = m.tall ? k + e : lane;
+      v[e] = square[i * 64 + (j ^ (i & 31))];
+      if constexpr (MUON)
+        w[e] = k + e < rows ? a.io.master[m.flat + at + (k + e) * m.dst_ld] : 0.0f;
+    }
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      if (k + e >= rows) break;
+      const int64_t p = at + (k + e) * m.dst_ld;
+      if constexpr (MUON) {
+        const float x = w[e] * a.io.dec - m.rate * v[e];
+        a.io.master[m.flat + p] = x;
+        if constexpr (DST != 0) static_cast<uint16_t*>(a.io.params)[m.flat + p] = narrow1<DST>(x);
+      } else if constexpr (DST == ZF_F32) {
+        static_cast<float*>(m.dst)[p] = v[e];
+      } else {
+        static_cast<uint16_t*>(m.dst)[p] = narrow1<DST>(v[e]);
+      }
+    }
   }
 }
 
-// W <- W dec - rate O and the 16-bit parameter.
-template <int PDT>  // 0: no 16-bit copy
-__device__ __forceinline__ void update1(const GemmArgs& a, const Mat& m, int64_t r, int64_t c,
-                                        float o) {
-  const int64_t p = m.flat + r * m.dst_ld + c;
-  const float w = a.io.master[p] * a.io.dec - m.rate * o;
-  a.io.master[p] = w;
-  if constexpr (PDT != 0) static_cast<uint16_t*>(a.io.params)[p] = narrow1<PDT>(w);
-}
-
+// X <- S X with S = S_in0: D_i X_ij from both halves of X, and O X; LAST:
+// into the destination, or W <- W dec - rate (S X).
 template <typename T, int SIZE, bool LAST, int PRODUCTS, int DST, bool MUON>
 __global__ __launch_bounds__(T::kThreads) void zf_ns_apply(GemmArgs a) {
   if (a.c.st && a.c.st->skipped) return;
@@ -673,46 +829,74 @@ __global__ __launch_bounds__(T::kThreads) void zf_ns_apply(GemmArgs a) {
       [&](bool lo_p, bool lo_q) {
         const int64_t p = lo_p ? m.sl[a.in0] : m.s[a.in0];
         const int64_t q = lo_q ? m.l[a.turn] : m.h[a.turn];
-        return Operands<T, true>(at<f16>(a.c, p) + (int64_t)i0 * mp, mp, mp - i0,
-                                 at<f16>(a.c, q) + j0, np, j0, mp);
+        return Operands<T, true>(at<f16>(a.c, p) + (int64_t)i0 * m.lds, m.lds, mp - i0,
+                                 at<f16>(a.c, q) + j0, m.ldx, j0, mp);
       },
       s0, s1, acc);
 
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wi = i0 + wave / T::kWavesJ * T::TI, wj = j0 + wave % T::kWavesJ * T::TJ;
   const f16* h = at<f16>(a.c, m.h[a.turn]);
   const f16* lo = at<f16>(a.c, m.l[a.turn]);
   f16* h1 = at<f16>(a.c, m.h[a.turn ^ 1]);
   f16* lo1 = at<f16>(a.c, m.l[a.turn ^ 1]);
   const float* d = at<float>(a.c, m.d[a.in0]);
+  ZF_LDS float* square = (ZF_LDS float*)(wave < T::kWaves / 2 ? s0 : s1) +
+                         wave % (T::kWaves / 2) * 4096;
+  static_assert(T::kBuf * 2 >= T::kWaves / 2 * 16384, "squares of 64 fit");
 #pragma unroll
-  for (int fi = 0; fi < T::FI; ++fi) {
-    const int i = wi + fi * 16 + l;
-    if (wi + fi * 16 >= mp) continue;
-    const float di = d[i];
+  for (int q = 0; q < T::FI / 4; ++q) {
+    // 64 x 64 of O X to shared memory, and back by rows of whole 128-byte
+    // lines: element (i, j) at i * 64 + (j ^ (i & 31)), so that rows and
+    // columns both read without conflicts
+    if (wi + q * 64 >= mp || wj >= np) continue;
+    const int row = lane >> 3, c = (lane & 7) * 8;
+    const int64_t p0 = (int64_t)(wi + q * 64 + row) * m.ldx + wj + c;
+    f16x8 x[8], y[8];
+    float di[8];
 #pragma unroll
-    for (int fj = 0; fj < T::FJ; ++fj) {
-      const int j = wj + fj * 16 + 4 * g;
-      if (wj + fj * 16 >= np) continue;
-      const int64_t p = (int64_t)i * np + j;
-      const f16x4 x = *reinterpret_cast<const f16x4*>(h + p);
-      const f16x4 y = *reinterpret_cast<const f16x4*>(lo + p);
-      float v[4];
+    for (int e = 0; e < 8; ++e) {
+      x[e] = *reinterpret_cast<const f16x8*>(h + p0 + (int64_t)e * 8 * m.ldx);
+      y[e] = *reinterpret_cast<const f16x8*>(lo + p0 + (int64_t)e * 8 * m.ldx);
+      di[e] = d[wi + q * 64 + e * 8 + row];
+    }
 #pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] = di * value_of(x[r], y[r]) + acc[fi][fj][r] * kUnscale2;
-      if constexpr (!LAST) {
-        const f16x4 z = halves(v);
-        *reinterpret_cast<f16x4*>(h1 + p) = z;
-        *reinterpret_cast<f16x4*>(lo1 + p) = rests(v, z);
-      } else {
+    for (int f = 0; f < 4; ++f)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          if (i >= m.m || j + r >= m.n) continue;
-          const int64_t row = m.tall ? j + r : i, col = m.tall ? i : j + r;
-          if constexpr (MUON) update1<DST>(a, m, row, col, v[r]);
-          else store1<DST>(m, row, col, v[r]);
+      for (int fj = 0; fj < T::FJ; ++fj)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          square[(f * 16 + l) * 64 + ((fj * 16 + 4 * g + r) ^ ((f * 16 + l) & 31))] =
+              acc[q * 4 + f][fj][r];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int i = e * 8 + row;
+      f16x8 hi, rest;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        ZF_LDS float* s = square + i * 64 + ((c + r) ^ (i & 31));
+        const float v = di[e] * value_of(x[e][r], y[e][r]) + *s * kUnscale2;
+        if constexpr (LAST) {
+          *s = v;
+        } else {
+          hi[r] = hi_of(v);
+          rest[r] = lo_of(v, hi[r]);
         }
       }
+      if constexpr (!LAST) {
+        *reinterpret_cast<f16x8*>(h1 + p0 + (int64_t)e * 8 * m.ldx) = hi;
+        *reinterpret_cast<f16x8*>(lo1 + p0 + (int64_t)e * 8 * m.ldx) = rest;
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if constexpr (LAST) {
+      write_square<DST, MUON>(a, m, square, wi + q * 64, wj);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
     }
   }
 }
@@ -817,6 +1001,8 @@ int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 constexpr int64_t kGroupElements = 1ll << 28;
 constexpr int64_t kMaxSide = 1ll << 20;
 
+int32_t stride_of(int32_t side) { return side; }
+
 }  // namespace
 
 zf_ns_params zf::ns::defaults() {
@@ -878,7 +1064,9 @@ bool zf::ns::layout(const Shape* shapes, int64_t count, int products, Layout& ou
     m.n = (int32_t)std::max(rows, cols);
     m.mp = (int32_t)round_up(m.m, kPad);
     m.np = (int32_t)round_up(m.n, kPad);
-    const int64_t mn = (int64_t)m.mp * m.np, mm = (int64_t)m.mp * m.mp;
+    m.ldx = stride_of(m.np);
+    m.lds = stride_of(m.mp);
+    const int64_t mn = (int64_t)m.mp * m.ldx, mm = (int64_t)m.mp * m.lds;
     if (g.count > 0 && elements + mn > kGroupElements) close();
     m.slot = (int32_t)k;
     m.src_ld = m.dst_ld = cols;
@@ -894,10 +1082,12 @@ bool zf::ns::layout(const Shape* shapes, int64_t count, int products, Layout& ou
       m.d[z] = take((int64_t)m.mp * 4);
     }
     const int64_t tiles = (int64_t)(m.mp / kTile) * (m.np / kTile);
+    const int64_t blocks = (tiles + kLoadTiles - 1) / kLoadTiles;
+    if (tiles > 0x7FFFFFFF) return false;
     m.part = partials;
-    partials += tiles;
+    partials += blocks;
     m.load0 = (int32_t)load;
-    load += tiles;
+    load += blocks;
     const int side[2] = {Big::BM, Small::BM};
     for (int z = 0; z < 2; ++z) {
       const int64_t tm = (m.mp + side[z] - 1) / side[z], tn = (m.np + side[z] - 1) / side[z];
