@@ -268,13 +268,13 @@ extern "C" int zf_muon_step(const zf_muon* muon, const zf_hparams* hp,
     rc = zf::step_enqueue(&muon->plan, hp, &front, stream, false, false);
     if (rc != ZF_OK) return rc;
 
-    for (size_t k = 0; k < l.mats.size(); ++k) {
-      const zf::ns::Shape& sh = muon->shapes[k];
+    for (zf::ns::Mat& m : l.mats) {
+      const zf::ns::Shape& sh = muon->shapes[m.slot];
       const double scale = mhp->scale_rule == ZF_MUON_SCALE_RMS
                                ? 0.2 * std::sqrt((double)std::max(sh.rows, sh.cols))
                                : std::sqrt(std::max(1.0, (double)sh.rows / (double)sh.cols));
-      l.mats[k].flat = muon->flat[k];
-      l.mats[k].rate = (float)(mhp->lr * scale);
+      m.flat = muon->flat[m.slot];
+      m.rate = (float)(mhp->lr * scale);
     }
     zf::ns::MuonIo io;
     io.sums = front.grad_shards;
@@ -286,7 +286,10 @@ extern "C" int zf_muon_step(const zf_muon* muon, const zf_hparams* hp,
     io.dec = (float)(1.0 - mhp->lr * mhp->weight_decay);
     io.nesterov = mhp->nesterov;
     io.param_dtype = args->param_dtype;
-    rc = zf::ns::enqueue(l, p, products, ZF_F32, args->param_dtype, &io, ws + at.engine, s);
+    // matrices held in shared memory take three products unless the caller
+    // chose: a launch's latency either way
+    rc = zf::ns::enqueue(l, p, products, p.products ? p.products : 3, ZF_F32, args->param_dtype,
+                         &io, ws + at.engine, s);
     if (rc != ZF_OK) return rc;
     rc = enqueue_rest(muon, hp, args, front.grad_shards, s);
     if (rc != ZF_OK) return rc;

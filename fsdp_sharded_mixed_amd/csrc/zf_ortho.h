@@ -34,7 +34,7 @@ struct Mat {
   int64_t part;           // its first squared-norm partial
   int32_t m, n, mp, np;
   int32_t ldx, lds;       // row strides of X and of the symmetric matrices
-  int32_t tall, slot;     // slot: its place in the array of inverse norms
+  int32_t tall, slot;     // slot: its place in the call
   float rate;             // the Muon step: lr * scale
   int32_t load0;          // its first block in the launches of its group,
   int32_t tri0[2], app0[2];  // by tile size
@@ -47,8 +47,10 @@ struct Group {
 };
 
 struct Layout {
-  std::vector<Mat> mats;
+  std::vector<Mat> mats;      // Mat.slot: the matrix's place in the call
   std::vector<Group> groups;
+  int32_t small_first = 0, small_count = 0;  // matrices held in shared memory,
+  int32_t small_tiles = 0;                   // and the most tiles of a wave
   int64_t table = 0, inv = 0, partials = 0;  // byte offsets
   int64_t bytes = 0;
 };
@@ -80,8 +82,9 @@ struct MuonIo {
 
 // Enqueues the orthogonalisation of every matrix of `l` on `s`.  io == NULL:
 // from Mat.src (src_dtype) to Mat.dst (dst_dtype); else the Muon update.
-int enqueue(const Layout& l, const zf_ns_params& p, int products, int32_t src_dtype,
-            int32_t dst_dtype, const MuonIo* io, char* ws, hipStream_t s);
+// small_products: of the matrices held in shared memory.
+int enqueue(const Layout& l, const zf_ns_params& p, int products, int small_products,
+            int32_t src_dtype, int32_t dst_dtype, const MuonIo* io, char* ws, hipStream_t s);
 
 }  // namespace ns
 }  // namespace zf

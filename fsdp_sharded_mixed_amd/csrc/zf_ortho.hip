@@ -993,6 +993,322 @@ int tile_size(int64_t big, int64_t small) {
   return b <= sm ? kBig : kSmall;
 }
 
+// ---------------------------------------------------------------------------
+// Small matrices: the whole iteration in one block, X and one symmetric
+// matrix in shared memory, one launch for all of them.  Such a matrix would
+// spend its time in launches (128 x 128: 20 of them, 190 us); here a step is
+// three products between barriers.  Each of the 8 waves takes a block of 2 x
+// CJ tiles of 16 x 16 of X (2 x 4 of S, both triangles: cheaper than
+// mirroring one), so that a fragment read from shared memory serves several
+// tiles; tiles past the last one are computed again (no branches) and not
+// stored.  Bound by shared memory's latency and the barriers.
+constexpr int kSmallPad = 32;              // sides padded to this
+constexpr int kSmallThreads = 512, kSmallWaves = 8;
+constexpr int kSmallShared = 147456;       // bytes of X and S
+constexpr int kSmallSide = 128;            // longest short side
+constexpr int kSmallByValue = 12;          // matrices that travel as arguments
+
+struct SmallArgs {
+  Common c;                 // c.table NULL: the matrices are m[]
+  MuonIo io;
+  float ca, cb, cc;
+  double eps;
+  int32_t steps, src, dst;  // types; src 0: the Muon step
+  Mat m[kSmallByValue];
+};
+
+// Waves along the short side (each takes 2 tiles of it), the rest along the
+// long one.
+__host__ __device__ inline int small_waves_i(int mp) { return mp <= 32 ? 1 : mp <= 64 ? 2 : 4; }
+
+__device__ __forceinline__ float small_load(const SmallArgs& a, const Mat& m, int64_t p) {
+  if (a.src == ZF_F32) return static_cast<const float*>(m.src)[p];
+  const uint16_t x = static_cast<const uint16_t*>(m.src)[p];
+  return a.src == ZF_BF16 ? widen1<ZF_BF16>(x) : widen1<ZF_F16>(x);
+}
+
+// Every element of the matrix, 8 of a thread's at a time with their loads on
+// their way together: use(r, c, value).  FIRST: the Muon step's momentum
+// update on the way.
+template <bool FIRST, typename F>
+__device__ __forceinline__ void small_walk(const SmallArgs& a, const Mat& m, int rows, int cols,
+                                           F use) {
+  constexpr int kBatch = 8;
+  const float gs = a.src == 0 ? a.c.st->gs : 0.0f;
+  const int dr = kSmallThreads / cols, dc = kSmallThreads % cols;
+  int r = threadIdx.x / cols, c = threadIdx.x % cols;
+  while (r < rows) {
+    float v[kBatch], g[kBatch];
+    int rr[kBatch], cc[kBatch];
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      rr[e] = r;
+      cc[e] = c;
+      const int64_t p = min(r, rows - 1) * m.src_ld + c;
+      if (a.src == 0) {
+        v[e] = a.io.momentum[m.flat + p];
+        g[e] = a.io.sums[m.flat + p];
+      } else {
+        v[e] = small_load(a, m, p);
+      }
+      r += dr;
+      c += dc;
+      if (c >= cols) c -= cols, ++r;
+    }
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      if (rr[e] >= rows) continue;
+      if (a.src == 0) {
+        g[e] = g[e] * gs;
+        if constexpr (FIRST) {
+          v[e] = a.io.mu * v[e] + g[e];
+          a.io.momentum[m.flat + rr[e] * m.src_ld + cc[e]] = v[e];
+        }
+        if (a.io.nesterov) v[e] = g[e] + a.io.mu * v[e];
+      }
+      use(rr[e], cc[e], v[e]);
+    }
+  }
+}
+
+__device__ __forceinline__ void small_store(const SmallArgs& a, const Mat& m, int64_t r, int64_t c,
+                                            float v) {
+  const int64_t p = r * m.dst_ld + c;
+  void* out = m.dst;
+  int64_t q = p;
+  if (a.src == 0) {
+    q = m.flat + p;
+    v = a.io.master[q] * a.io.dec - m.rate * v;
+    a.io.master[q] = v;
+    out = a.io.params;
+    if (!out) return;
+  }
+  if (a.dst == ZF_F32) static_cast<float*>(out)[q] = v;
+  else static_cast<uint16_t*>(out)[q] = a.dst == ZF_BF16 ? narrow1<ZF_BF16>(v) : narrow1<ZF_F16>(v);
+}
+
+template <int CJ, int PRODUCTS>
+__global__ __launch_bounds__(kSmallThreads) void zf_ns_small(SmallArgs a) {
+  if (a.c.st && a.c.st->skipped) return;
+  const Mat& m = a.c.table ? a.c.table[blockIdx.x] : a.m[blockIdx.x];
+  const int mp = (m.m + kSmallPad - 1) / kSmallPad * kSmallPad;
+  const int np = (m.n + kSmallPad - 1) / kSmallPad * kSmallPad;
+  // row strides that put 16 rows' pieces in different banks
+  const int lx = np + 8, ls = mp + 8;
+  __shared__ __align__(16) f16 shared[kSmallShared / 2];
+  __shared__ float diag[kSmallSide];
+  __shared__ double sum[kSmallWaves];
+  f16* xh = shared;
+  f16* xl = xh + mp * lx;
+  f16* sh = xl + mp * lx;
+  f16* sl = sh + mp * ls;
+  const int tid = threadIdx.x, lane = tid & 63, l = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int rows = m.tall ? m.n : m.m, cols = m.tall ? m.m : m.n;
+
+  for (int k = tid; k < mp * lx; k += kSmallThreads) reinterpret_cast<uint32_t*>(xh)[k] = 0;
+  double ss = 0.0;
+  small_walk<true>(a, m, rows, cols, [&](int, int, float v) { ss += (double)v * (double)v; });
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) ss = ss + __shfl_xor(ss, off, 64);
+  if (lane == 0) sum[wave] = ss;
+  __syncthreads();
+  ss = sum[0];
+#pragma unroll
+  for (int w = 1; w < kSmallWaves; ++w) ss = ss + sum[w];
+  const double inv = 1.0 / (sqrt(ss) + a.eps);
+  small_walk<false>(a, m, rows, cols, [&](int r, int c, float u) {
+    const float v = (float)((double)u * inv);
+    const int p = m.tall ? c * lx + r : r * lx + c;
+    const f16 h = hi_of(v);
+    xh[p] = h;
+    xl[p] = lo_of(v, h);
+  });
+  __syncthreads();
+
+  const int tm = mp / 16, tn = np / 16, waves_i = small_waves_i(mp);
+  const int i0 = wave % waves_i * 2, js = wave / waves_i * 4, jx = wave / waves_i * CJ;
+
+  // S = P P^T for P of `len` columns and row stride ld, through f(i, j, v)
+  auto symmetric = [&](const f16* ph, const f16* pl, int ld, int len, auto f) {
+    f32x4 acc[2][4], low[2][4];
+    int pi[2], pj[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) pi[i] = (min(i0 + i, tm - 1) * 16 + l) * ld + 8 * g;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) pj[j] = (min(js + j, tm - 1) * 16 + l) * ld + 8 * g;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = low[i][j] = (f32x4){0, 0, 0, 0};
+#pragma unroll 2
+    for (int k = 0; k < len; k += 32) {
+      f16x8 x[2], y[4], xr[2], yr[4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        x[i] = *reinterpret_cast<const f16x8*>(ph + pi[i] + k);
+        if constexpr (PRODUCTS == 3) xr[i] = *reinterpret_cast<const f16x8*>(pl + pi[i] + k);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        y[j] = *reinterpret_cast<const f16x8*>(ph + pj[j] + k);
+        if constexpr (PRODUCTS == 3) yr[j] = *reinterpret_cast<const f16x8*>(pl + pj[j] + k);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[i], y[j], acc[i][j], 0, 0, 0);
+          if constexpr (PRODUCTS == 3) {
+            low[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[i], yr[j], low[i][j], 0, 0, 0);
+            low[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xr[i], y[j], low[i][j], 0, 0, 0);
+          }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (i0 + i >= tm || js + j >= tm) continue;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          acc[i][j][r] = f((i0 + i) * 16 + 4 * g + r, (js + j) * 16 + l,
+                           (acc[i][j][r] + low[i][j][r] * (1.0f / kLo)) * kUnscale2);
+      }
+    __syncthreads();  // every read of the old S is done
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (i0 + i >= tm || js + j >= tm) continue;
+        // (i, j) goes to (j, i): S is symmetric, and this way in one piece
+        const int ii = (i0 + i) * 16 + 4 * g, jj = (js + j) * 16 + l;
+        float v[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          v[r] = acc[i][j][r];
+          if (ii + r == jj) {
+            diag[jj] = v[r];
+            v[r] = 0.0f;
+          }
+        }
+        const f16x4 h = halves(v);
+        *reinterpret_cast<f16x4*>(sh + jj * ls + ii) = h;
+        if constexpr (PRODUCTS == 3) *reinterpret_cast<f16x4*>(sl + jj * ls + ii) = rests(v, h);
+      }
+    __syncthreads();
+  };
+
+#pragma unroll 1
+  for (int step = 0; step < a.steps; ++step) {
+    symmetric(xh, xl, lx, np, [&](int, int, float v) { return v; });
+    symmetric(sh, sl, ls, mp, [&](int i, int j, float v) {
+      const float di = diag[i], dj = diag[j];
+      const float e = value_of(sh[j * ls + i], PRODUCTS == 3 ? sl[j * ls + i] : (f16)0);
+      const bool on = i == j;
+      const float s2 = v + (on ? di * dj : (di + dj) * e);
+      return a.cb * (on ? dj : e) + a.cc * s2 + (on ? a.ca : 0.0f);
+    });
+    const bool last = step + 1 == a.steps;
+    f32x4 acc[2][CJ], low[2][CJ];
+    int pi[2], pj[CJ];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) pi[i] = (min(i0 + i, tm - 1) * 16 + l) * ls + 8 * g;
+#pragma unroll
+    for (int j = 0; j < CJ; ++j)
+      pj[j] = (8 * g + (l >> 2)) * lx + min(jx + j, tn - 1) * 16 + 4 * (l & 3);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < CJ; ++j) acc[i][j] = low[i][j] = (f32x4){0, 0, 0, 0};
+    auto turned = [&](const f16* x) {
+      const s16x4 h0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ZF_LDS s16x4*)(x));
+      const s16x4 h1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ZF_LDS s16x4*)(x + 4 * lx));
+      return __builtin_bit_cast(f16x8, __builtin_shufflevector(h0, h1, 0, 1, 2, 3, 4, 5, 6, 7));
+    };
+#pragma unroll 2
+    for (int k = 0; k < mp; k += 32) {
+      f16x8 x[CJ], xr[CJ], y[2], yr[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        y[i] = *reinterpret_cast<const f16x8*>(sh + pi[i] + k);
+        if constexpr (PRODUCTS == 3) yr[i] = *reinterpret_cast<const f16x8*>(sl + pi[i] + k);
+      }
+#pragma unroll
+      for (int j = 0; j < CJ; ++j) {
+        x[j] = turned(xh + pj[j] + k * lx);
+        if constexpr (PRODUCTS == 3) xr[j] = turned(xl + pj[j] + k * lx);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < CJ; ++j) {
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[j], y[i], acc[i][j], 0, 0, 0);
+          if constexpr (PRODUCTS == 3) {
+            low[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[j], yr[i], low[i][j], 0, 0, 0);
+            low[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xr[j], y[i], low[i][j], 0, 0, 0);
+          }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int ii = min(i0 + i, tm - 1) * 16 + l;
+      const float di = diag[ii];
+#pragma unroll
+      for (int j = 0; j < CJ; ++j) {
+        const int p = ii * lx + min(jx + j, tn - 1) * 16 + 4 * g;
+        const f16x4 h = *reinterpret_cast<const f16x4*>(xh + p);
+        const f16x4 w = *reinterpret_cast<const f16x4*>(xl + p);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          acc[i][j][r] = di * value_of(h[r], w[r]) +
+                         (acc[i][j][r] + low[i][j][r] * (1.0f / kLo)) * kUnscale2;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < CJ; ++j) {
+        if (i0 + i >= tm || jx + j >= tn) continue;
+        const int ii = (i0 + i) * 16 + l, jj = (jx + j) * 16 + 4 * g;
+        const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+        if (last) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (ii < m.m && jj + r < m.n)
+              small_store(a, m, m.tall ? jj + r : ii, m.tall ? ii : jj + r, v[r]);
+        } else {
+          const f16x4 h = halves(v);
+          *reinterpret_cast<f16x4*>(xh + ii * lx + jj) = h;
+          *reinterpret_cast<f16x4*>(xl + ii * lx + jj) = rests(v, h);
+        }
+      }
+    __syncthreads();
+  }
+}
+
+// Tiles along the long side that each wave would take, or 0 for a matrix too
+// large for a block.
+int small_tiles(int64_t m, int64_t n) {
+  if (m > kSmallSide || n > 4096) return 0;
+  const int64_t mp = (m + kSmallPad - 1) / kSmallPad * kSmallPad;
+  const int64_t np = (n + kSmallPad - 1) / kSmallPad * kSmallPad;
+  if (mp * (np + 8 + mp + 8) * 4 > kSmallShared) return 0;
+  const int64_t along = kSmallWaves / small_waves_i((int)mp);
+  const int64_t tiles = (np / 16 + along - 1) / along;
+  return tiles <= 8 ? (int)tiles : 0;
+}
+
+template <int PRODUCTS>
+void launch_small(const Layout& l, hipStream_t s, const SmallArgs& a) {
+  const dim3 grid(l.small_count), block(kSmallThreads);
+  if (l.small_tiles <= 1) hipLaunchKernelGGL((zf_ns_small<1, PRODUCTS>), grid, block, 0, s, a);
+  else if (l.small_tiles <= 4)
+    hipLaunchKernelGGL((zf_ns_small<4, PRODUCTS>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((zf_ns_small<8, PRODUCTS>), grid, block, 0, s, a);
+}
+
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
 // Matrices are worked on in groups whose buffers share one region, so that
@@ -1002,6 +1318,10 @@ constexpr int64_t kGroupElements = 1ll << 28;
 constexpr int64_t kMaxSide = 1ll << 20;
 
 int32_t stride_of(int32_t side) { return side; }
+
+int small_tiles_of(const zf::ns::Shape& s) {
+  return small_tiles(std::min(s.rows, s.cols), std::max(s.rows, s.cols));
+}
 
 }  // namespace
 
@@ -1054,22 +1374,35 @@ bool zf::ns::layout(const Shape* shapes, int64_t count, int products, Layout& ou
     used += round_up(bytes, 256);
     return o;
   };
+  int64_t large = 0;
+  for (int64_t k = 0; k < count; ++k) {
+    if (shapes[k].rows > kMaxSide || shapes[k].cols > kMaxSide) return false;
+    large += small_tiles_of(shapes[k]) == 0;
+  }
+  out.small_first = (int32_t)large;
+  out.small_count = (int32_t)(count - large);
+  out.small_tiles = 0;
+  int64_t place[2] = {0, large};  // the next large and the next small one
   for (int64_t k = 0; k < count; ++k) {
     const int64_t rows = shapes[k].rows, cols = shapes[k].cols;
-    if (rows > kMaxSide || cols > kMaxSide) return false;
-    Mat& m = out.mats[(size_t)k];
+    const int tiles_held = small_tiles_of(shapes[k]);
+    Mat& m = out.mats[(size_t)place[tiles_held > 0]++];
     m = Mat{};
+    m.slot = (int32_t)k;
+    m.src_ld = m.dst_ld = cols;
     m.tall = rows > cols;
     m.m = (int32_t)std::min(rows, cols);
     m.n = (int32_t)std::max(rows, cols);
     m.mp = (int32_t)round_up(m.m, kPad);
     m.np = (int32_t)round_up(m.n, kPad);
+    if (tiles_held > 0) {
+      out.small_tiles = std::max(out.small_tiles, tiles_held);
+      continue;
+    }
     m.ldx = stride_of(m.np);
     m.lds = stride_of(m.mp);
     const int64_t mn = (int64_t)m.mp * m.ldx, mm = (int64_t)m.mp * m.lds;
     if (g.count > 0 && elements + mn > kGroupElements) close();
-    m.slot = (int32_t)k;
-    m.src_ld = m.dst_ld = cols;
     // what the rounding left of X: an operand of the products if there are
     // three, else used by its own tile alone, in place
     for (int z = 0; z < 2; ++z) {
@@ -1116,15 +1449,39 @@ bool zf::ns::layout(const Shape* shapes, int64_t count, int products, Layout& ou
   return true;
 }
 
-int zf::ns::enqueue(const Layout& l, const zf_ns_params& p, int products, int32_t src_dtype,
-                    int32_t dst_dtype, const MuonIo* io, char* ws, hipStream_t s) {
+int zf::ns::enqueue(const Layout& l, const zf_ns_params& p, int products, int small_products,
+                    int32_t src_dtype, int32_t dst_dtype, const MuonIo* io, char* ws,
+                    hipStream_t s) {
   Mat* table = reinterpret_cast<Mat*>(ws + l.table);
-  for (size_t k = 0; k < l.mats.size(); k += kTableChunk) {
+  // a few small matrices go as arguments and need no table
+  const bool by_value = l.small_count <= kSmallByValue;
+  const size_t tabled = l.mats.size() - (by_value ? l.small_count : 0);
+  for (size_t k = 0; k < tabled; k += kTableChunk) {
     TableArgs t;
     t.to = table + k;
-    t.count = (int32_t)std::min<size_t>(kTableChunk, l.mats.size() - k);
+    t.count = (int32_t)std::min<size_t>(kTableChunk, tabled - k);
     for (int i = 0; i < t.count; ++i) t.m[i] = l.mats[k + i];
     hipLaunchKernelGGL(zf_ns_table, dim3(1), dim3(64), 0, s, t);
+    if (!hip_ok(hipGetLastError())) return ZF_EHIP;
+  }
+  if (l.small_count > 0) {
+    SmallArgs a;
+    a.c.ws = ws;
+    a.c.table = by_value ? nullptr : table + l.small_first;
+    for (int k = 0; by_value && k < l.small_count; ++k) a.m[k] = l.mats[l.small_first + k];
+    a.c.count = l.small_count;
+    a.c.st = io ? io->st : nullptr;
+    a.c.inv = a.c.partials = nullptr;
+    a.io = io ? *io : MuonIo{};
+    a.ca = (float)p.a;
+    a.cb = (float)p.b;
+    a.cc = (float)p.c;
+    a.eps = p.eps;
+    a.steps = p.steps;
+    a.src = io ? 0 : src_dtype;
+    a.dst = dst_dtype;
+    if (small_products == 3) launch_small<3>(l, s, a);
+    else launch_small<1>(l, s, a);
     if (!hip_ok(hipGetLastError())) return ZF_EHIP;
   }
   for (const Group& g : l.groups) {
@@ -1224,7 +1581,9 @@ extern "C" int zf_orthogonalize(const zf_matrix* mats, int64_t count, int32_t sr
       if (!z.src || !z.dst) return ZF_EINVAL;
       if (z.rows > 1 && (z.src_stride < z.cols || z.dst_stride < z.cols)) return ZF_EINVAL;
       if (!aligned(z.src, src_dtype) || !aligned(z.dst, dst_dtype)) return ZF_EALIGN;
-      Mat& m = l.mats[(size_t)k];
+    }
+    for (Mat& m : l.mats) {
+      const zf_matrix& z = mats[m.slot];
       m.src = z.src;
       m.dst = z.dst;
       m.src_ld = z.src_stride;
@@ -1235,7 +1594,7 @@ extern "C" int zf_orthogonalize(const zf_matrix* mats, int64_t count, int32_t sr
     if ((reinterpret_cast<uintptr_t>(workspace) & 15u) != 0) return ZF_EALIGN;
     if (workspace_size < l.bytes) return ZF_ESIZE;
     (void)hipGetLastError();
-    return zf::ns::enqueue(l, p, products, src_dtype, dst_dtype, nullptr,
+    return zf::ns::enqueue(l, p, products, products, src_dtype, dst_dtype, nullptr,
                            static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
   } catch (const std::bad_alloc&) {
     return ZF_ENOMEM;

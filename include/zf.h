@@ -543,7 +543,9 @@ int zf_offload_step(const zf_plan* plan, const zf_hparams* hp, const zf_offload_
  * result is within about 1e-3 of the exact one (|error|_F / |X|_F), below
  * bf16's own rounding.  3: operands are sums of two fp16 numbers, about 22
  * bits, for three times the work; the result is within about 1e-5.  0: 1 for
- * a ZF_BF16 result and for zf_muon_step, else 3.
+ * a ZF_BF16 result, else 3; in zf_muon_step 1, and 3 for matrices that fit
+ * in a compute unit's shared memory (up to 128 x 128), where they cost
+ * little.
  * The operands' range bounds the coefficients: singular values, and the
  * entries of A and b A + c A A, must stay below 64 (they stay below 8 for
  * the default ones). */
@@ -640,8 +642,7 @@ typedef struct {
  * and the 16-bit parameters RNE16(W).  args: as zf_shard_step; exp_avg holds
  * M for the matrices' elements, exp_avg_sq is not touched there; grad_shards
  * as zf_shard_step (NULL: the sums go through the workspace); workspace_size
- * must be >= zf_muon_workspace_bytes(muon, &mhp->ns).  mhp->ns.products = 0
- * selects 1.  phase_events: before pass 1, after pass 1, after the norm
+ * must be >= zf_muon_workspace_bytes(muon, &mhp->ns).  phase_events: before pass 1, after pass 1, after the norm
  * reduction and finish, after the updates.  The state block is
  * zf_shard_step's: t counts applied steps of both.  Errors: as
  * zf_shard_step, plus ZF_EINVAL (mhp out of range) and ZF_ENOMEM. */

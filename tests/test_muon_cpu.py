@@ -108,7 +108,8 @@ def test_ortho_batch_refuses(zf):
         zf.ortho_batch([x.double()], [x.double()])
 
 
-SEGS = [(24, 0, 0, 4), (6, 0, 0, 0), (35, 1, 0, 7), (35, 1, 0, 0)]
+# the first matrix is too large for shared memory, the second is held there
+SEGS = [(400 * 600, 0, 0, 400), (6, 0, 0, 0), (35, 1, 0, 7), (35, 1, 0, 0)]
 
 
 def plan(zf, layout=W.PER_UNIT, n=3):
