@@ -49,17 +49,17 @@ typedef _Float16 f16;
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 
-constexpr float kScale = 1024.0f;           // of every 16-bit operand
-constexpr float kUnscale2 = 1.0f / (1024.0f * 1024.0f);
+// Everything between the load and the result is in units of 2^-10 ("scaled"):
+// a 16-bit operand holds the scaled value rounded, products of two need one
+// factor 2^-10.  Multiplications by powers of two are exact, so the factors
+// go wherever they cost least; the vector unit, at 4 cycles an instruction,
+// is what an epilogue waits for.
+constexpr float kScale = 1024.0f, kUnscale = 1.0f / 1024.0f;
 constexpr float kLo = 2048.0f;              // lo halves: 2^11 more
 
-// hi and lo halves of x.
-__device__ __forceinline__ f16 hi_of(float x) { return (f16)(x * kScale); }
-__device__ __forceinline__ f16 lo_of(float x, f16 hi) {
-  return (f16)((x * kScale - (float)hi) * kLo);
-}
-__device__ __forceinline__ float value_of(f16 hi, f16 lo) {
-  return ((float)hi + (float)lo * (1.0f / kLo)) * (1.0f / kScale);
+__device__ __forceinline__ f16 rest_of(float x, f16 hi) { return (f16)((x - (float)hi) * kLo); }
+__device__ __forceinline__ float join(f16 hi, f16 lo) {
+  return __builtin_fmaf((float)lo, 1.0f / kLo, (float)hi);
 }
 
 // ---------------------------------------------------------------------------
@@ -268,7 +268,7 @@ __global__ __launch_bounds__(kThreads) void zf_ns_prep(LoadArgs a) {
   const int block = blockIdx.x - m.load0, tiles_n = m.np / kTile;
   const int tiles = m.mp / kTile * tiles_n;
   const float gs = SRC == 0 ? a.c.st->gs : 0.0f;
-  const double inv = a.c.inv[m.slot];
+  const double inv = a.c.inv[m.slot] * kScale;
   const bool wide = wide_loads<SRC>(m);
   const int rows = m.tall ? m.n : m.m, cols = m.tall ? m.m : m.n;
   __shared__ float s[kTile][kTile + 1];
@@ -311,8 +311,8 @@ __global__ __launch_bounds__(kThreads) void zf_ns_prep(LoadArgs a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float x = i < m.m && j + e < m.n ? (float)((double)v[h][e] * inv) : 0.0f;
-        hi[e] = hi_of(x);
-        lo[e] = lo_of(x, hi[e]);
+        hi[e] = (f16)x;
+        lo[e] = rest_of(x, hi[e]);
       }
       const int64_t p = (int64_t)i * m.ldx + j;
       *reinterpret_cast<f16x8*>(hp + p) = hi;
@@ -585,10 +585,27 @@ typedef Tile<256, 256, 2, 4> Big;
 typedef Tile<128, 128, 2, 2> Small;
 
 __device__ __forceinline__ f16x4 halves(const float (&v)[4]) {
-  return (f16x4){hi_of(v[0]), hi_of(v[1]), hi_of(v[2]), hi_of(v[3])};
+  return (f16x4){(f16)v[0], (f16)v[1], (f16)v[2], (f16)v[3]};
 }
 __device__ __forceinline__ f16x4 rests(const float (&v)[4], f16x4 h) {
-  return (f16x4){lo_of(v[0], h[0]), lo_of(v[1], h[1]), lo_of(v[2], h[2]), lo_of(v[3], h[3])};
+  return (f16x4){rest_of(v[0], h[0]), rest_of(v[1], h[1]), rest_of(v[2], h[2]),
+                 rest_of(v[3], h[3])};
+}
+
+// Entry (i, j) of a product of two symmetric matrices diag(D) + O, from the
+// sum over the 16-bit parts (times 2^20), the scaled parts o0, o1 of either,
+// and their diagonals: D0_i O1_ij + O0_ij D1_j + sum, scaled; on the diagonal
+// D0_i D1_i + sum.  POLY (both the same matrix S): ca I + cb S + cc S S.
+template <bool POLY>
+__device__ __forceinline__ float combine(float sum, float o0, float o1, float d0i, float d1j,
+                                         bool on, float ca, float cb, float cc) {
+  if constexpr (POLY) {
+    if (on) return (ca + d1j * (cb + cc * d1j)) * kScale + cc * kUnscale * sum;
+    return __builtin_fmaf(o0, __builtin_fmaf(cc, d0i + d1j, cb), cc * kUnscale * sum);
+  } else {
+    if (on) return __builtin_fmaf(d0i * d1j, kScale, sum * kUnscale);
+    return __builtin_fmaf(d0i, o1, __builtin_fmaf(o0, d1j, sum * kUnscale));
+  }
 }
 
 // Three products instead of one: hi lo + lo hi, scaled down, + hi hi.
@@ -619,7 +636,7 @@ __device__ __forceinline__ void products(F operands, f16* s0, f16* s1,
 enum Mode { kGram, kPoly, kMul };
 
 template <typename T, int SIZE, int MODE, int PRODUCTS>
-__global__ __launch_bounds__(T::kThreads) void zf_ns_sym(GemmArgs a) {
+__global__ __launch_bounds__(T::kThreads, 2) void zf_ns_sym(GemmArgs a) {
   if (a.c.st && a.c.st->skipped) return;
   __shared__ __align__(16) f16 s0[T::kBuf];
   __shared__ __align__(16) f16 s1[T::kBuf];
@@ -712,30 +729,33 @@ __global__ __launch_bounds__(T::kThreads) void zf_ns_sym(GemmArgs a) {
           float v[4];
           if (half == 0) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] = acc[fi][fj][r] * kUnscale2;
-            if constexpr (MODE != kGram) {
-              const float dj = dv[fj];
-#pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                const f16 none = 0;
-                const float e0 = value_of(x0[f][fj][r], PRODUCTS == 3 ? y0[f][fj][r] : none);
-                const float e1 = MODE == kMul
-                                     ? value_of(x1[f][fj][r], PRODUCTS == 3 ? y1[f][fj][r] : none)
-                                     : e0;
-                const bool on = i + r == j;
-                float w2 = v[r] + (on ? di[f][r] * dj : di[f][r] * e1 + e0 * dj);
-                if constexpr (MODE == kPoly)
-                  w2 = a.cb * (on ? dj : e0) + a.cc * w2 + (on ? a.ca : 0.0f);
-                v[r] = w2;
+            for (int r = 0; r < 4; ++r) {
+              if constexpr (MODE == kGram) {
+                v[r] = acc[fi][fj][r] * kUnscale;
+              } else {
+                const float e0 = PRODUCTS == 3 ? join(x0[f][fj][r], y0[f][fj][r])
+                                               : (float)x0[f][fj][r];
+                float e1 = e0;
+                if constexpr (MODE == kMul)
+                  e1 = PRODUCTS == 3 ? join(x1[f][fj][r], y1[f][fj][r]) : (float)x1[f][fj][r];
+                v[r] = combine<MODE == kPoly>(acc[fi][fj][r], e0, e1, di[f][r], dv[fj], false,
+                                              a.ca, a.cb, a.cc);
               }
             }
+            if (wi + fi * 16 == wj + fj * 16) {  // the diagonal runs through it
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              if (i + r == j) {
-                diag[j] = v[r];
+              for (int r = 0; r < 4; ++r) {
+                if (i + r != j) continue;
+                if constexpr (MODE != kGram)
+                  v[r] = combine<MODE == kPoly>(acc[fi][fj][r], 0.0f, 0.0f, di[f][r], dv[fj], true,
+                                                a.ca, a.cb, a.cc);
+                diag[j] = v[r] * kUnscale;
                 v[r] = 0.0f;
               }
-              acc[fi][fj][r] = v[r];  // kept for the second halves
+            }
+            if constexpr (PRODUCTS == 3) {
+#pragma unroll
+              for (int r = 0; r < 4; ++r) acc[fi][fj][r] = v[r];  // for the second halves
             }
           } else {
 #pragma unroll
@@ -772,26 +792,38 @@ __global__ __launch_bounds__(T::kThreads) void zf_ns_sym(GemmArgs a) {
   }
 }
 
-// A wave's 64 x 64 results at (i0, j0) of X, from shared memory (laid out as
-// in zf_ns_apply), to the destination, whose rows run along j, or for a
-// tall matrix along i: 64 neighbours an instruction, at any alignment.
+// A wave's 64 x 64 results at (i0, j0) of X, from shared memory (scaled, laid
+// out as in zf_ns_apply), to the destination, whose rows run along j, or for
+// a tall matrix along i: 64 neighbours an instruction, at any alignment.
 // DST is the result's type; MUON: W <- W dec - rate (result), and the 16-bit
 // parameters of type DST (0: none).
 template <int DST, bool MUON>
 __device__ __forceinline__ void write_square(const GemmArgs& a, const Mat& m,
                                              const ZF_LDS float* square, int i0, int j0) {
   const int lane = threadIdx.x & 63;
-  const int rows = m.tall ? m.n - j0 : m.m - i0, cols = m.tall ? m.m - i0 : m.n - j0;
+  const int rows = min(m.tall ? m.n - j0 : m.m - i0, 64);
+  const int cols = m.tall ? m.m - i0 : m.n - j0;
   const int64_t at = (int64_t)(m.tall ? j0 : i0) * m.dst_ld + (m.tall ? i0 : j0) + lane;
   if (lane >= cols) return;
+  const float rate = m.rate * kUnscale;
   constexpr int kBatch = 8;  // rows whose loads are on their way together
-  for (int k = 0; k < min(rows, 64); k += kBatch) {
+  for (int k = 0; k < rows; k += kBatch) {
     float v[kBatch], w[kBatch];
+    if (m.tall) {
 #pragma unroll
-    for (int e = 0; e < kBatch; ++e) {
-      const int i = m.tall ? lane : k + e, j = m.tall ? k + e : lane;
-      v[e] = square[i * 64 + (j ^ (i & 31))];
-      if constexpr (MUON)
+      for (int e = 0; e < kBatch; e += 4) {
+        const f32x4 x = *(const ZF_LDS f32x4*)(square + lane * 64 + (((k + e) / 4) ^ (lane & 7)) * 4);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[e + r] = x[r];
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e)
+        v[e] = square[(k + e) * 64 + ((lane >> 2) ^ e) * 4 + (lane & 3)];
+    }
+    if constexpr (MUON) {
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e)
         w[e] = k + e < rows ? a.io.master[m.flat + at + (k + e) * m.dst_ld] : 0.0f;
     }
 #pragma unroll
@@ -799,13 +831,13 @@ __device__ __forceinline__ void write_square(const GemmArgs& a, const Mat& m,
       if (k + e >= rows) break;
       const int64_t p = at + (k + e) * m.dst_ld;
       if constexpr (MUON) {
-        const float x = w[e] * a.io.dec - m.rate * v[e];
+        const float x = w[e] * a.io.dec - rate * v[e];
         a.io.master[m.flat + p] = x;
         if constexpr (DST != 0) static_cast<uint16_t*>(a.io.params)[m.flat + p] = narrow1<DST>(x);
       } else if constexpr (DST == ZF_F32) {
-        static_cast<float*>(m.dst)[p] = v[e];
+        static_cast<float*>(m.dst)[p] = v[e] * kUnscale;
       } else {
-        static_cast<uint16_t*>(m.dst)[p] = narrow1<DST>(v[e]);
+        static_cast<uint16_t*>(m.dst)[p] = narrow1<DST>(v[e] * kUnscale);
       }
     }
   }
@@ -814,7 +846,7 @@ __device__ __forceinline__ void write_square(const GemmArgs& a, const Mat& m,
 // X <- S X with S = S_in0: D_i X_ij from both halves of X, and O X; LAST:
 // into the destination, or W <- W dec - rate (S X).
 template <typename T, int SIZE, bool LAST, int PRODUCTS, int DST, bool MUON>
-__global__ __launch_bounds__(T::kThreads) void zf_ns_apply(GemmArgs a) {
+__global__ __launch_bounds__(T::kThreads, 2) void zf_ns_apply(GemmArgs a) {
   if (a.c.st && a.c.st->skipped) return;
   __shared__ __align__(16) f16 s0[T::kBuf];
   __shared__ __align__(16) f16 s1[T::kBuf];
@@ -848,11 +880,10 @@ __global__ __launch_bounds__(T::kThreads) void zf_ns_apply(GemmArgs a) {
 #pragma unroll
   for (int q = 0; q < T::FI / 4; ++q) {
     // 64 x 64 of O X to shared memory, and back by rows of whole 128-byte
-    // lines: element (i, j) at i * 64 + (j ^ (i & 31)), so that rows and
-    // columns both read without conflicts
+    // lines: the 16-byte piece c of row i lies at piece c ^ (i & 7)
     if (wi + q * 64 >= mp || wj >= np) continue;
-    const int row = lane >> 3, c = (lane & 7) * 8;
-    const int64_t p0 = (int64_t)(wi + q * 64 + row) * m.ldx + wj + c;
+    const int row = lane >> 3, c = lane & 7;
+    const int64_t p0 = (int64_t)(wi + q * 64 + row) * m.ldx + wj + c * 8;
     f16x8 x[8], y[8];
     float di[8];
 #pragma unroll
@@ -865,26 +896,27 @@ __global__ __launch_bounds__(T::kThreads) void zf_ns_apply(GemmArgs a) {
     for (int f = 0; f < 4; ++f)
 #pragma unroll
       for (int fj = 0; fj < T::FJ; ++fj)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          square[(f * 16 + l) * 64 + ((fj * 16 + 4 * g + r) ^ ((f * 16 + l) & 31))] =
-              acc[q * 4 + f][fj][r];
+        *(ZF_LDS f32x4*)(square + (f * 16 + l) * 64 + ((fj * 4 + g) ^ (l & 7)) * 4) =
+            acc[q * 4 + f][fj];
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int i = e * 8 + row;
+      ZF_LDS float* s = square + (e * 8 + row) * 64;
       f16x8 hi, rest;
 #pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        ZF_LDS float* s = square + i * 64 + ((c + r) ^ (i & 31));
-        const float v = di[e] * value_of(x[e][r], y[e][r]) + *s * kUnscale2;
-        if constexpr (LAST) {
-          *s = v;
-        } else {
-          hi[r] = hi_of(v);
-          rest[r] = lo_of(v, hi[r]);
+      for (int t = 0; t < 2; ++t) {
+        ZF_LDS f32x4* piece = (ZF_LDS f32x4*)(s + ((2 * c + t) ^ row) * 4);
+        f32x4 v = *piece * kUnscale;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          v[r] = __builtin_fmaf(di[e], join(x[e][t * 4 + r], y[e][t * 4 + r]), v[r]);
+          if constexpr (!LAST) {
+            hi[t * 4 + r] = (f16)v[r];
+            rest[t * 4 + r] = rest_of(v[r], hi[t * 4 + r]);
+          }
         }
+        if constexpr (LAST) *piece = v;
       }
       if constexpr (!LAST) {
         *reinterpret_cast<f16x8*>(h1 + p0 + (int64_t)e * 8 * m.ldx) = hi;
@@ -1096,7 +1128,7 @@ __global__ __launch_bounds__(kSmallThreads) void zf_ns_small(SmallArgs a) {
   // row strides that put 16 rows' pieces in different banks
   const int lx = np + 8, ls = mp + 8;
   __shared__ __align__(16) f16 shared[kSmallShared / 2];
-  __shared__ float diag[kSmallSide];
+  __shared__ __align__(16) float diag[kSmallSide];
   __shared__ double sum[kSmallWaves];
   f16* xh = shared;
   f16* xl = xh + mp * lx;
@@ -1116,21 +1148,22 @@ __global__ __launch_bounds__(kSmallThreads) void zf_ns_small(SmallArgs a) {
   ss = sum[0];
 #pragma unroll
   for (int w = 1; w < kSmallWaves; ++w) ss = ss + sum[w];
-  const double inv = 1.0 / (sqrt(ss) + a.eps);
+  const double inv = 1.0 / (sqrt(ss) + a.eps) * kScale;
   small_walk<false>(a, m, rows, cols, [&](int r, int c, float u) {
     const float v = (float)((double)u * inv);
     const int p = m.tall ? c * lx + r : r * lx + c;
-    const f16 h = hi_of(v);
+    const f16 h = (f16)v;
     xh[p] = h;
-    xl[p] = lo_of(v, h);
+    xl[p] = rest_of(v, h);
   });
   __syncthreads();
 
   const int tm = mp / 16, tn = np / 16, waves_i = small_waves_i(mp);
   const int i0 = wave % waves_i * 2, js = wave / waves_i * 4, jx = wave / waves_i * CJ;
 
-  // S = P P^T for P of `len` columns and row stride ld, through f(i, j, v)
-  auto symmetric = [&](const f16* ph, const f16* pl, int ld, int len, auto f) {
+  // S = P P^T for P of `len` columns and row stride ld; finish(i, j, diagonal
+  // tile, sums) turns the sums (times 2^20) of (i .. i + 3, j) into values
+  auto symmetric = [&](const f16* ph, const f16* pl, int ld, int len, auto finish) {
     f32x4 acc[2][4], low[2][4];
     int pi[2], pj[4];
 #pragma unroll
@@ -1141,7 +1174,6 @@ __global__ __launch_bounds__(kSmallThreads) void zf_ns_small(SmallArgs a) {
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = low[i][j] = (f32x4){0, 0, 0, 0};
-#pragma unroll 2
     for (int k = 0; k < len; k += 32) {
       f16x8 x[2], y[4], xr[2], yr[4];
 #pragma unroll
@@ -1170,10 +1202,9 @@ __global__ __launch_bounds__(kSmallThreads) void zf_ns_small(SmallArgs a) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (i0 + i >= tm || js + j >= tm) continue;
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          acc[i][j][r] = f((i0 + i) * 16 + 4 * g + r, (js + j) * 16 + l,
-                           (acc[i][j][r] + low[i][j][r] * (1.0f / kLo)) * kUnscale2);
+        const int ii = (i0 + i) * 16 + 4 * g, jj = (js + j) * 16 + l;
+        if constexpr (PRODUCTS == 3) acc[i][j] = acc[i][j] + low[i][j] * (1.0f / kLo);
+        finish(ii, jj, i0 + i == js + j, acc[i][j]);
       }
     __syncthreads();  // every read of the old S is done
 #pragma unroll
@@ -1183,12 +1214,12 @@ __global__ __launch_bounds__(kSmallThreads) void zf_ns_small(SmallArgs a) {
         if (i0 + i >= tm || js + j >= tm) continue;
         // (i, j) goes to (j, i): S is symmetric, and this way in one piece
         const int ii = (i0 + i) * 16 + 4 * g, jj = (js + j) * 16 + l;
-        float v[4];
+        float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+        if (i0 + i == js + j) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          v[r] = acc[i][j][r];
-          if (ii + r == jj) {
-            diag[jj] = v[r];
+          for (int r = 0; r < 4; ++r) {
+            if (ii + r != jj) continue;
+            diag[jj] = v[r] * kUnscale;
             v[r] = 0.0f;
           }
         }
@@ -1201,13 +1232,20 @@ __global__ __launch_bounds__(kSmallThreads) void zf_ns_small(SmallArgs a) {
 
 #pragma unroll 1
   for (int step = 0; step < a.steps; ++step) {
-    symmetric(xh, xl, lx, np, [&](int, int, float v) { return v; });
-    symmetric(sh, sl, ls, mp, [&](int i, int j, float v) {
-      const float di = diag[i], dj = diag[j];
-      const float e = value_of(sh[j * ls + i], PRODUCTS == 3 ? sl[j * ls + i] : (f16)0);
-      const bool on = i == j;
-      const float s2 = v + (on ? di * dj : (di + dj) * e);
-      return a.cb * (on ? dj : e) + a.cc * s2 + (on ? a.ca : 0.0f);
+    symmetric(xh, xl, lx, np, [&](int, int, bool, f32x4& v) { v = v * kUnscale; });
+    symmetric(sh, sl, ls, mp, [&](int i, int j, bool diagonal, f32x4& v) {
+      const float dj = diag[j];
+      const f32x4 di = *reinterpret_cast<const f32x4*>(diag + i);
+      const f16x4 h = *reinterpret_cast<const f16x4*>(sh + j * ls + i);
+      f16x4 w = h;
+      if constexpr (PRODUCTS == 3) w = *reinterpret_cast<const f16x4*>(sl + j * ls + i);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float e = PRODUCTS == 3 ? join(h[r], w[r]) : (float)h[r];
+        const float x = combine<true>(v[r], e, e, di[r], dj, false, a.ca, a.cb, a.cc);
+        const float y = combine<true>(v[r], e, e, di[r], dj, true, a.ca, a.cb, a.cc);
+        v[r] = diagonal && i + r == j ? y : x;
+      }
     });
     const bool last = step + 1 == a.steps;
     f32x4 acc[2][CJ], low[2][CJ];
@@ -1226,7 +1264,6 @@ __global__ __launch_bounds__(kSmallThreads) void zf_ns_small(SmallArgs a) {
       const s16x4 h1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ZF_LDS s16x4*)(x + 4 * lx));
       return __builtin_bit_cast(f16x8, __builtin_shufflevector(h0, h1, 0, 1, 2, 3, 4, 5, 6, 7));
     };
-#pragma unroll 2
     for (int k = 0; k < mp; k += 32) {
       f16x8 x[CJ], xr[CJ], y[2], yr[2];
 #pragma unroll
@@ -1259,10 +1296,10 @@ __global__ __launch_bounds__(kSmallThreads) void zf_ns_small(SmallArgs a) {
         const int p = ii * lx + min(jx + j, tn - 1) * 16 + 4 * g;
         const f16x4 h = *reinterpret_cast<const f16x4*>(xh + p);
         const f16x4 w = *reinterpret_cast<const f16x4*>(xl + p);
+        if constexpr (PRODUCTS == 3) acc[i][j] = acc[i][j] + low[i][j] * (1.0f / kLo);
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          acc[i][j][r] = di * value_of(h[r], w[r]) +
-                         (acc[i][j][r] + low[i][j][r] * (1.0f / kLo)) * kUnscale2;
+          acc[i][j][r] = __builtin_fmaf(di, join(h[r], w[r]), acc[i][j][r] * kUnscale);
       }
     }
     __syncthreads();
@@ -1277,7 +1314,7 @@ __global__ __launch_bounds__(kSmallThreads) void zf_ns_small(SmallArgs a) {
 #pragma unroll
           for (int r = 0; r < 4; ++r)
             if (ii < m.m && jj + r < m.n)
-              small_store(a, m, m.tall ? jj + r : ii, m.tall ? ii : jj + r, v[r]);
+              small_store(a, m, m.tall ? jj + r : ii, m.tall ? ii : jj + r, v[r] * kUnscale);
         } else {
           const f16x4 h = halves(v);
           *reinterpret_cast<f16x4*>(xh + ii * lx + jj) = h;
