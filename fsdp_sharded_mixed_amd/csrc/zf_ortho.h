@@ -37,13 +37,13 @@ struct Mat {
   int32_t tall, slot;     // slot: its place in the call
   float rate;             // the Muon step: lr * scale
   int32_t load0;          // its first block in the launches of its group,
-  int32_t tri0[2], app0[2];  // by tile size
+  int32_t tri0[3], app0[3];  // by tile size
 };
 
 // Launches of one group of matrices [first, first + count).
 struct Group {
   int32_t first, count;
-  int32_t load_blocks, tri_blocks[2], app_blocks[2];
+  int32_t load_blocks, tri_blocks[3], app_blocks[3];
 };
 
 struct Layout {

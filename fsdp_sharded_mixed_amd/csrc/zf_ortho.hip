@@ -354,17 +354,21 @@ __device__ __forceinline__ Rsrc rsrc(const f16* base, uint32_t n) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<f16*>(base), 0, n, 0x00020000);
 }
 
-template <int BM_, int BN_, int WI, int WJ>
+template <int BM_, int BN_, int WI, int WJ, int BUFFERS>
 struct Tile {
   static constexpr int BM = BM_, BN = BN_, kWaves = WI * WJ, kThreads = kWaves * 64;
   static constexpr int TI = BM / WI, TJ = BN / WJ, FI = TI / 16, FJ = TJ / 16;
-  static constexpr int kWavesJ = WJ;
+  static constexpr int kWavesJ = WJ, kBuffers = BUFFERS;
   static constexpr int kPBytes = BM * kBK * 2, kQBytes = BN * kBK * 2;
   static constexpr int kBuf = (BM + BN) * kBK;  // elements of one buffer
   static constexpr int kRows = kThreads / 8;    // rows that a load of all threads covers
   static constexpr int kChunks = BN / 8;        // 16-byte pieces of a row of X
   static constexpr int kRowsX = kThreads / kChunks;
-  static_assert(BM % kRows == 0 && BN % kRows == 0 && kRows % 8 == 0 && kRowsX == 16, "tile");
+  // a square of 64 x 64 results goes out by one wave, or by the whole block
+  static constexpr int kSquareWaves = TI * TJ >= 4096 ? 1 : 4096 / (TI * TJ);
+  static_assert(BM % kRows == 0 && BN % kRows == 0 && kRows % 8 == 0 && kRowsX % 16 == 0, "tile");
+  static_assert(kSquareWaves == 1 ? TJ == 64 && TI % 64 == 0
+                                  : BM == 64 && BN == 64 && kWaves == kSquareWaves, "squares");
 };
 
 // The operands of one tile.  XQ: Q is X, rows along j.
@@ -414,8 +418,10 @@ struct Operands {
       rq[0] = T::kPBytes + (wj + l) * (kBK * 2) + ((g ^ (l & 7)) * 16);
     }
   }
-  // the permutation of a row of X
-  static __device__ __forceinline__ int turn(int r) { return (r & 3) | ((r >> 1) & 4); }
+  // the permutation of a row of X: pairs of pieces, as many as a row has
+  static __device__ __forceinline__ int turn(int r) {
+    return ((r & 3) | ((r >> 1) & 4)) & (T::kChunks / 2 - 1);
+  }
 };
 
 template <typename T>
@@ -537,27 +543,66 @@ __device__ __forceinline__ void arrive() {
   __syncthreads();
 }
 
+// The same for all but the wave's last N loads.
+template <int N>
+__device__ __forceinline__ void arrive_but() {
+  static_assert(N < 64, "the counter's range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0070);
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 template <typename T, bool XQ>
-__device__ __forceinline__ void product(const Operands<T, XQ>& o, f16* s0, f16* s1,
+__device__ __forceinline__ void one_step(const Operands<T, XQ>& o, int k, f16* __restrict next,
+                                         const f16* __restrict cur,
+                                         f32x4 (&acc)[T::FI][T::FJ]) {
+  Frags<T> a, b;
+  fetch(o, k, next);
+  read(o, cur, a, 0);
+  read(o, cur, b, 1);
+  multiply<T, XQ>(a, acc);
+  multiply<T, XQ>(b, acc);
+}
+
+template <typename T, bool XQ>
+__device__ __forceinline__ void product(const Operands<T, XQ>& o, f16* shared,
                                         f32x4 (&acc)[T::FI][T::FJ]) {
   const int steps = o.k_len / kBK;
-  Frags<T> a, b;
-  fetch(o, 0, s0);
-  arrive();
-  fetch(o, 1, s1);
-  read(o, s0, a, 0);
-  int t = 0;
-  for (; t + 2 <= steps; t += 2) {
-    half0(o, s0, a, b, acc);
+  if constexpr (T::kBuffers == 2) {
+    f16 *s0 = shared, *s1 = shared + T::kBuf;
+    Frags<T> a, b;
+    fetch(o, 0, s0);
     arrive();
-    half1(o, t + 2, s0, s1, a, b, acc);
-    half0(o, s1, a, b, acc);
-    arrive();
-    half1(o, t + 3, s1, s0, a, b, acc);
-  }
-  if (t < steps) {
-    half0(o, s0, a, b, acc);
-    multiply<T, XQ>(b, acc);
+    fetch(o, 1, s1);
+    read(o, s0, a, 0);
+    int t = 0;
+    for (; t + 2 <= steps; t += 2) {
+      half0(o, s0, a, b, acc);
+      arrive();
+      half1(o, t + 2, s0, s1, a, b, acc);
+      half0(o, s1, a, b, acc);
+      arrive();
+      half1(o, t + 3, s1, s0, a, b, acc);
+    }
+    if (t < steps) {
+      half0(o, s0, a, b, acc);
+      multiply<T, XQ>(b, acc);
+    }
+  } else {
+    // few blocks, so latency counts: loads run kBuffers - 1 steps ahead
+    constexpr int ahead = T::kBuffers - 1;
+#pragma unroll
+    for (int t = 0; t < ahead; ++t) fetch(o, t, shared + t * T::kBuf);
+    for (int t = 0; t < steps; t += T::kBuffers) {
+#pragma unroll
+      for (int u = 0; u < T::kBuffers; ++u) {
+        if (t + u >= steps) break;
+        arrive_but<(ahead - 1) * (T::BM / T::kRows + (XQ ? kBK / T::kRowsX : T::BN / T::kRows))>();
+        one_step(o, t + u + ahead, shared + (u + ahead) % T::kBuffers * T::kBuf,
+                 shared + u * T::kBuf, acc);
+      }
+    }
   }
   arrive();  // shared memory is free again
 }
@@ -580,9 +625,21 @@ __device__ __forceinline__ int tile_index() {
   return (k / kRun * 8 + x) * kRun + k % kRun;
 }
 
-constexpr int kBig = 0, kSmall = 1;  // places of the tile sizes in the tables
-typedef Tile<256, 256, 2, 4> Big;
-typedef Tile<128, 128, 2, 2> Small;
+constexpr int kBig = 0, kMiddle = 1, kLittle = 2;  // places of the tile sizes in the tables
+typedef Tile<256, 256, 2, 4, 2> Big;
+typedef Tile<128, 128, 2, 2, 2> Middle;
+typedef Tile<64, 64, 2, 2, 4> Little;
+
+// The waves of a square of results may read what the others wrote.
+template <typename T>
+__device__ __forceinline__ void square_ready() {
+  if constexpr (T::kSquareWaves == 1) {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  } else {
+    __syncthreads();
+  }
+}
 
 __device__ __forceinline__ f16x4 halves(const float (&v)[4]) {
   return (f16x4){(f16)v[0], (f16)v[1], (f16)v[2], (f16)v[3]};
@@ -610,7 +667,7 @@ __device__ __forceinline__ float combine(float sum, float o0, float o1, float d0
 
 // Three products instead of one: hi lo + lo hi, scaled down, + hi hi.
 template <typename T, bool XQ, int PRODUCTS, typename F>
-__device__ __forceinline__ void products(F operands, f16* s0, f16* s1,
+__device__ __forceinline__ void products(F operands, f16* shared,
                                          f32x4 (&acc)[T::FI][T::FJ]) {
 #pragma unroll
   for (int i = 0; i < T::FI; ++i)
@@ -624,7 +681,7 @@ __device__ __forceinline__ void products(F operands, f16* s0, f16* s1,
 #pragma unroll
         for (int j = 0; j < T::FJ; ++j) acc[i][j] = acc[i][j] * (1.0f / kLo);
     }
-    product(operands(PRODUCTS == 3 && pass == 1, PRODUCTS == 3 && pass == 0), s0, s1, acc);
+    product(operands(PRODUCTS == 3 && pass == 1, PRODUCTS == 3 && pass == 0), shared, acc);
   }
 }
 
@@ -638,8 +695,7 @@ enum Mode { kGram, kPoly, kMul };
 template <typename T, int SIZE, int MODE, int PRODUCTS>
 __global__ __launch_bounds__(T::kThreads, 2) void zf_ns_sym(GemmArgs a) {
   if (a.c.st && a.c.st->skipped) return;
-  __shared__ __align__(16) f16 s0[T::kBuf];
-  __shared__ __align__(16) f16 s1[T::kBuf];
+  __shared__ __align__(16) f16 shared[T::kBuf * T::kBuffers];
   const int w = tile_index();
   const Mat& m = *find(a.c.table, a.c.count, w, [](const Mat& x) { return x.tri0[SIZE]; });
   const int b = w - m.tri0[SIZE];
@@ -661,7 +717,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void zf_ns_sym(GemmArgs a) {
         return Operands<T, false>(at<f16>(a.c, p) + i0 * ld, ld, mp - i0,
                                   at<f16>(a.c, q) + j0 * ld, ld, mp - j0, len);
       },
-      s0, s1, acc);
+      shared, acc);
 
   const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -675,9 +731,12 @@ __global__ __launch_bounds__(T::kThreads, 2) void zf_ns_sym(GemmArgs a) {
   f16* out = at<f16>(a.c, m.s[a.out]);
   f16* rest = at<f16>(a.c, m.sl[a.out]);
   float* diag = at<float>(a.c, m.d[a.out]);
-  // a wave's own 64 x 64 values, 16 bits each, on the way to the mirrored
+  // a square of 64 x 64 values, 16 bits each, on the way to the mirrored
   // place: 8-byte pieces of a row permuted by the row number
-  static_assert(T::TJ == 64 && T::TI % 64 == 0, "staged in squares of 64");
+  constexpr int kWaves = T::kSquareWaves;
+  const int part = kWaves == 1 ? 0 : wave;
+  ZF_LDS char* stage = (ZF_LDS char*)(shared) + (kWaves == 1 ? wave * 8192 : 0);
+  const int ri = (wi - i0) % 64, rj = (wj - j0) % 64;  // this wave's place in its square
   float dv[T::FJ];
   if constexpr (MODE != kGram) {
 #pragma unroll
@@ -686,19 +745,19 @@ __global__ __launch_bounds__(T::kThreads, 2) void zf_ns_sym(GemmArgs a) {
       dv[fj] = j < mp ? d1[j] : 0.0f;
     }
   }
-  ZF_LDS char* stage = (ZF_LDS char*)(s0) + wave * 8192;
 #pragma unroll
   for (int half = 0; half < (PRODUCTS == 3 ? 2 : 1); ++half) {
 #pragma unroll
-    for (int q = 0; q < T::FI / 4; ++q) {
+    for (int q = 0; q < (T::FI + 3) / 4; ++q) {
       // every load of 4 rows of fragments before the first store, which the
       // compiler could not move them past
-      f16x4 x0[4][T::FJ], x1[4][T::FJ], y0[4][T::FJ], y1[4][T::FJ];
-      f32x4 di[4];
+      constexpr int F = T::FI < 4 ? T::FI : 4;
+      f16x4 x0[F][T::FJ], x1[F][T::FJ], y0[F][T::FJ], y1[F][T::FJ];
+      f32x4 di[F];
       if constexpr (MODE != kGram) {
         if (half == 0) {
 #pragma unroll
-          for (int f = 0; f < 4; ++f) {
+          for (int f = 0; f < F; ++f) {
             const int i = wi + (q * 4 + f) * 16 + 4 * g;
             if (wi + (q * 4 + f) * 16 >= mp) continue;
             di[f] = *reinterpret_cast<const f32x4*>(d0 + i);
@@ -718,7 +777,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void zf_ns_sym(GemmArgs a) {
         }
       }
 #pragma unroll
-      for (int fi = q * 4; fi < q * 4 + 4; ++fi) {
+      for (int fi = q * 4; fi < q * 4 + F; ++fi) {
         const int i = wi + fi * 16 + 4 * g, f = fi & 3;
         if (wi + fi * 16 >= mp) continue;
 #pragma unroll
@@ -764,30 +823,26 @@ __global__ __launch_bounds__(T::kThreads, 2) void zf_ns_sym(GemmArgs a) {
           f16x4 x = halves(v);
           if (half == 1) x = rests(v, x);
           *reinterpret_cast<f16x4*>((half ? rest : out) + p) = x;
-          const int jj = fj * 16 + l, turn = ((jj & 3) << 2) | ((jj >> 2) & 3);
-          *(ZF_LDS f16x4*)(stage + jj * 128 + (((fi & 3) * 4 + g) ^ turn) * 8) = x;
+          const int jj = rj + fj * 16 + l, turn = ((jj & 3) << 2) | ((jj >> 2) & 3);
+          *(ZF_LDS f16x4*)(stage + jj * 128 + ((ri / 4 + f * 4 + g) ^ turn) * 8) = x;
         }
       }
       if (ti == tj) continue;  // both places lie in this tile
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
+      square_ready<T>();
+      const int si = wi - ri + q * 64, sj = wj - rj;  // the square
 #pragma unroll
-      for (int fi = q * 4; fi < q * 4 + 4; ++fi) {
-        if (wi + fi * 16 >= mp) continue;
-#pragma unroll
-        for (int fj = 0; fj < T::FJ; ++fj) {
-          if (wj + fj * 16 >= mp) continue;
-          // source lane (row e, piece k) of each 16 hands over 4 values along
-          // i; lane l receives those of i = l along j
-          const int jj = fj * 16 + 4 * g + (l >> 2), turn = ((jj & 3) << 2) | ((jj >> 2) & 3);
-          const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (ZF_LDS s16x4*)(stage + jj * 128 + (((fi & 3) * 4 + (l & 3)) ^ turn) * 8));
-          const int64_t p = (int64_t)(wi + fi * 16 + l) * m.lds + wj + fj * 16 + 4 * g;
-          *reinterpret_cast<s16x4*>((half ? rest : out) + p) = x;
-        }
+      for (int k = 0; k < 16 / kWaves; ++k) {
+        // source lane (row e, piece k) of each 16 hands over 4 values along
+        // i; lane l receives those of i = l along j
+        const int fi = part * (4 / kWaves) + k / 4, fj = k % 4;
+        if (si + fi * 16 >= mp || sj + fj * 16 >= mp) continue;
+        const int jj = fj * 16 + 4 * g + (l >> 2), turn = ((jj & 3) << 2) | ((jj >> 2) & 3);
+        const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (ZF_LDS s16x4*)(stage + jj * 128 + ((fi * 4 + (l & 3)) ^ turn) * 8));
+        const int64_t p = (int64_t)(si + fi * 16 + l) * m.lds + sj + fj * 16 + 4 * g;
+        *reinterpret_cast<s16x4*>((half ? rest : out) + p) = x;
       }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
+      square_ready<T>();
     }
   }
 }
@@ -795,11 +850,13 @@ __global__ __launch_bounds__(T::kThreads, 2) void zf_ns_sym(GemmArgs a) {
 // A wave's 64 x 64 results at (i0, j0) of X, from shared memory (scaled, laid
 // out as in zf_ns_apply), to the destination, whose rows run along j, or for
 // a tall matrix along i: 64 neighbours an instruction, at any alignment.
-// DST is the result's type; MUON: W <- W dec - rate (result), and the 16-bit
+// Lines first .. first + count - 1 of it (rows of the destination).  DST is
+// the result's type; MUON: W <- W dec - rate (result), and the 16-bit
 // parameters of type DST (0: none).
 template <int DST, bool MUON>
 __device__ __forceinline__ void write_square(const GemmArgs& a, const Mat& m,
-                                             const ZF_LDS float* square, int i0, int j0) {
+                                             const ZF_LDS float* square, int i0, int j0, int first,
+                                             int count) {
   const int lane = threadIdx.x & 63;
   const int rows = min(m.tall ? m.n - j0 : m.m - i0, 64);
   const int cols = m.tall ? m.m - i0 : m.n - j0;
@@ -807,7 +864,7 @@ __device__ __forceinline__ void write_square(const GemmArgs& a, const Mat& m,
   if (lane >= cols) return;
   const float rate = m.rate * kUnscale;
   constexpr int kBatch = 8;  // rows whose loads are on their way together
-  for (int k = 0; k < rows; k += kBatch) {
+  for (int k = first; k < min(rows, first + count); k += kBatch) {
     float v[kBatch], w[kBatch];
     if (m.tall) {
 #pragma unroll
@@ -819,7 +876,7 @@ __device__ __forceinline__ void write_square(const GemmArgs& a, const Mat& m,
     } else {
 #pragma unroll
       for (int e = 0; e < kBatch; ++e)
-        v[e] = square[(k + e) * 64 + ((lane >> 2) ^ e) * 4 + (lane & 3)];
+        v[e] = square[(k + e) * 64 + ((lane >> 2) ^ e) * 4 + (lane & 3)];  // k: a multiple of 8
     }
     if constexpr (MUON) {
 #pragma unroll
@@ -848,8 +905,7 @@ __device__ __forceinline__ void write_square(const GemmArgs& a, const Mat& m,
 template <typename T, int SIZE, bool LAST, int PRODUCTS, int DST, bool MUON>
 __global__ __launch_bounds__(T::kThreads, 2) void zf_ns_apply(GemmArgs a) {
   if (a.c.st && a.c.st->skipped) return;
-  __shared__ __align__(16) f16 s0[T::kBuf];
-  __shared__ __align__(16) f16 s1[T::kBuf];
+  __shared__ __align__(16) f16 shared[T::kBuf * T::kBuffers];
   const int w = tile_index();
   const Mat& m = *find(a.c.table, a.c.count, w, [](const Mat& x) { return x.app0[SIZE]; });
   const int b = w - m.app0[SIZE], tiles_m = (m.mp + T::BM - 1) / T::BM;
@@ -864,7 +920,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void zf_ns_apply(GemmArgs a) {
         return Operands<T, true>(at<f16>(a.c, p) + (int64_t)i0 * m.lds, m.lds, mp - i0,
                                  at<f16>(a.c, q) + j0, m.ldx, j0, mp);
       },
-      s0, s1, acc);
+      shared, acc);
 
   const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -874,35 +930,37 @@ __global__ __launch_bounds__(T::kThreads, 2) void zf_ns_apply(GemmArgs a) {
   f16* h1 = at<f16>(a.c, m.h[a.turn ^ 1]);
   f16* lo1 = at<f16>(a.c, m.l[a.turn ^ 1]);
   const float* d = at<float>(a.c, m.d[a.in0]);
-  ZF_LDS float* square = (ZF_LDS float*)(wave < T::kWaves / 2 ? s0 : s1) +
-                         wave % (T::kWaves / 2) * 4096;
-  static_assert(T::kBuf * 2 >= T::kWaves / 2 * 16384, "squares of 64 fit");
+  constexpr int kWaves = T::kSquareWaves, E = 8 / kWaves;  // lines of 8 rows a wave takes
+  const int e0 = kWaves == 1 ? 0 : wave * E;
+  ZF_LDS float* square = (ZF_LDS float*)(shared) + (kWaves == 1 ? wave * 4096 : 0);
+  const int ri = (wi - i0) % 64, rj = (wj - j0) % 64;  // this wave's place in its square
+  static_assert(T::kBuf * T::kBuffers * 2 >= T::kWaves / kWaves * 16384, "squares of 64 fit");
 #pragma unroll
-  for (int q = 0; q < T::FI / 4; ++q) {
+  for (int q = 0; q < (T::FI + 3) / 4; ++q) {
     // 64 x 64 of O X to shared memory, and back by rows of whole 128-byte
     // lines: the 16-byte piece c of row i lies at piece c ^ (i & 7)
-    if (wi + q * 64 >= mp || wj >= np) continue;
+    const int si = wi - ri + q * 64, sj = wj - rj;
+    if (si >= mp || sj >= np) continue;
     const int row = lane >> 3, c = lane & 7;
-    const int64_t p0 = (int64_t)(wi + q * 64 + row) * m.ldx + wj + c * 8;
-    f16x8 x[8], y[8];
-    float di[8];
+    const int64_t p0 = (int64_t)(si + e0 * 8 + row) * m.ldx + sj + c * 8;
+    f16x8 x[E], y[E];
+    float di[E];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < E; ++e) {
       x[e] = *reinterpret_cast<const f16x8*>(h + p0 + (int64_t)e * 8 * m.ldx);
       y[e] = *reinterpret_cast<const f16x8*>(lo + p0 + (int64_t)e * 8 * m.ldx);
-      di[e] = d[wi + q * 64 + e * 8 + row];
+      di[e] = d[si + (e0 + e) * 8 + row];
     }
 #pragma unroll
-    for (int f = 0; f < 4; ++f)
+    for (int f = 0; f < (T::FI < 4 ? T::FI : 4); ++f)
 #pragma unroll
       for (int fj = 0; fj < T::FJ; ++fj)
-        *(ZF_LDS f32x4*)(square + (f * 16 + l) * 64 + ((fj * 4 + g) ^ (l & 7)) * 4) =
-            acc[q * 4 + f][fj];
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+        *(ZF_LDS f32x4*)(square + (ri + f * 16 + l) * 64 +
+                         ((rj / 4 + fj * 4 + g) ^ (l & 7)) * 4) = acc[q * 4 + f][fj];
+    square_ready<T>();
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      ZF_LDS float* s = square + (e * 8 + row) * 64;
+    for (int e = 0; e < E; ++e) {
+      ZF_LDS float* s = square + ((e0 + e) * 8 + row) * 64;
       f16x8 hi, rest;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -923,34 +981,39 @@ __global__ __launch_bounds__(T::kThreads, 2) void zf_ns_apply(GemmArgs a) {
         *reinterpret_cast<f16x8*>(lo1 + p0 + (int64_t)e * 8 * m.ldx) = rest;
       }
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    square_ready<T>();
     if constexpr (LAST) {
-      write_square<DST, MUON>(a, m, square, wi + q * 64, wj);
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
+      write_square<DST, MUON>(a, m, square, si, sj, e0 * 8, E * 8);
+      square_ready<T>();
     }
   }
 }
 
 template <int MODE, int PRODUCTS>
 void launch_sym(const Group& g, int size, hipStream_t s, const GemmArgs& a) {
+  const dim3 grid(g.tri_blocks[size]);
   if (size == kBig)
-    hipLaunchKernelGGL((zf_ns_sym<Big, kBig, MODE, PRODUCTS>), dim3(g.tri_blocks[kBig]),
-                       dim3(Big::kThreads), 0, s, a);
+    hipLaunchKernelGGL((zf_ns_sym<Big, kBig, MODE, PRODUCTS>), grid, dim3(Big::kThreads), 0, s, a);
+  else if (size == kMiddle)
+    hipLaunchKernelGGL((zf_ns_sym<Middle, kMiddle, MODE, PRODUCTS>), grid, dim3(Middle::kThreads),
+                       0, s, a);
   else
-    hipLaunchKernelGGL((zf_ns_sym<Small, kSmall, MODE, PRODUCTS>), dim3(g.tri_blocks[kSmall]),
-                       dim3(Small::kThreads), 0, s, a);
+    hipLaunchKernelGGL((zf_ns_sym<Little, kLittle, MODE, PRODUCTS>), grid, dim3(Little::kThreads),
+                       0, s, a);
 }
 
 template <bool LAST, int PRODUCTS, int DST, bool MUON>
 void launch_apply(const Group& g, int size, hipStream_t s, const GemmArgs& a) {
+  const dim3 grid(g.app_blocks[size]);
   if (size == kBig)
-    hipLaunchKernelGGL((zf_ns_apply<Big, kBig, LAST, PRODUCTS, DST, MUON>),
-                       dim3(g.app_blocks[kBig]), dim3(Big::kThreads), 0, s, a);
+    hipLaunchKernelGGL((zf_ns_apply<Big, kBig, LAST, PRODUCTS, DST, MUON>), grid,
+                       dim3(Big::kThreads), 0, s, a);
+  else if (size == kMiddle)
+    hipLaunchKernelGGL((zf_ns_apply<Middle, kMiddle, LAST, PRODUCTS, DST, MUON>), grid,
+                       dim3(Middle::kThreads), 0, s, a);
   else
-    hipLaunchKernelGGL((zf_ns_apply<Small, kSmall, LAST, PRODUCTS, DST, MUON>),
-                       dim3(g.app_blocks[kSmall]), dim3(Small::kThreads), 0, s, a);
+    hipLaunchKernelGGL((zf_ns_apply<Little, kLittle, LAST, PRODUCTS, DST, MUON>), grid,
+                       dim3(Little::kThreads), 0, s, a);
 }
 
 template <int PRODUCTS>
@@ -1016,13 +1079,17 @@ int iterate(const Group& g, const zf_ns_params& p, int sym, int app, int32_t dst
   return ZF_OK;
 }
 
-// The tile size for a launch of `big` tiles of 256 x 256 (one block a CU) or
-// `small` ones of 128 x 128 (two a CU, at 0.85 of the rate): whichever takes
-// fewer rounds over the 256 CUs, weighted by its tile's time.
-int tile_size(int64_t big, int64_t small) {
-  const double b = 4.0 * (double)((big + 255) / 256);
-  const double sm = 2.0 / 0.85 * (double)((small + 511) / 512);
-  return b <= sm ? kBig : kSmall;
+// The tile size for a launch of n[kBig] tiles of 256 x 256 (one block a CU),
+// n[kMiddle] of 128 x 128 or n[kLittle] of 64 x 64 (two a CU): whichever takes
+// the least time, counted in rounds over the 256 CUs, each weighted by its
+// blocks' work at the rate they reach together.
+int tile_size(const int32_t (&n)[3]) {
+  const double cost[3] = {4.0 * ((n[kBig] + 255) / 256), 2.0 / 0.85 * ((n[kMiddle] + 511) / 512),
+                          0.5 / 0.5 * ((n[kLittle] + 511) / 512)};
+  int best = kBig;
+  for (int z = 1; z < 3; ++z)
+    if (cost[z] < cost[best]) best = z;
+  return best;
 }
 
 // ---------------------------------------------------------------------------
@@ -1391,10 +1458,10 @@ bool zf::ns::layout(const Shape* shapes, int64_t count, int products, Layout& ou
   out.groups.clear();
   int64_t partials = 0, region = 0, used = 0, elements = 0;
   Group g{};
-  int64_t load = 0, tri[2] = {0, 0}, app[2] = {0, 0};
+  int64_t load = 0, tri[3] = {}, app[3] = {};
   auto close = [&]() {
     g.load_blocks = (int32_t)load;
-    for (int z = 0; z < 2; ++z) {
+    for (int z = 0; z < 3; ++z) {
       g.tri_blocks[z] = (int32_t)tri[z];
       g.app_blocks[z] = (int32_t)app[z];
       tri[z] = app[z] = 0;
@@ -1458,8 +1525,8 @@ bool zf::ns::layout(const Shape* shapes, int64_t count, int products, Layout& ou
     partials += blocks;
     m.load0 = (int32_t)load;
     load += blocks;
-    const int side[2] = {Big::BM, Small::BM};
-    for (int z = 0; z < 2; ++z) {
+    const int side[3] = {Big::BM, Middle::BM, Little::BM};
+    for (int z = 0; z < 3; ++z) {
       const int64_t tm = (m.mp + side[z] - 1) / side[z], tn = (m.np + side[z] - 1) / side[z];
       m.tri0[z] = (int32_t)tri[z];
       m.app0[z] = (int32_t)app[z];
@@ -1550,8 +1617,7 @@ int zf::ns::enqueue(const Layout& l, const zf_ns_params& p, int products, int sm
     GemmArgs ga;
     ga.c = c;
     ga.io = la.io;
-    const int sym = tile_size(g.tri_blocks[kBig], g.tri_blocks[kSmall]);
-    const int app = tile_size(g.app_blocks[kBig], g.app_blocks[kSmall]);
+    const int sym = tile_size(g.tri_blocks), app = tile_size(g.app_blocks);
     const int rc = products == 3
                        ? iterate<3>(g, p, sym, app, dst_dtype, io != nullptr, s, ga)
                        : iterate<1>(g, p, sym, app, dst_dtype, io != nullptr, s, ga);
