@@ -91,6 +91,26 @@ __device__ __forceinline__ const Mat* find(const Mat* table, int count, int b, F
   }
   return table + lo;
 }
+// The same with the first blocks of up to kFirsts matrices among the
+// arguments: one scalar load instead of a chain of them.
+constexpr int kFirsts = 64;
+struct Firsts {
+  int32_t at[kFirsts];  // INT32_MAX past the last
+};
+template <typename F>
+__device__ __forceinline__ const Mat* find(const Mat* table, int count, int b, const Firsts& f,
+                                           F first) {
+  if (count > kFirsts) return find(table, count, b, first);
+  int k = 0;
+  if (count <= 8) {
+#pragma unroll
+    for (int j = 1; j < 8; ++j) k += f.at[j] <= b ? 1 : 0;
+  } else {
+#pragma unroll
+    for (int j = 1; j < kFirsts; ++j) k += f.at[j] <= b ? 1 : 0;
+  }
+  return table + k;
+}
 __device__ __forceinline__ const Mat* find_load(const Mat* table, int count, int b) {
   return find(table, count, b, [](const Mat& m) { return m.load0; });
 }
@@ -350,6 +370,14 @@ constexpr int kBK = 64;
 __device__ __forceinline__ uint32_t extent(int64_t bytes) {
   return bytes <= 0 ? 0u : bytes > 0x7FFFFFFFll ? 0x7FFFFFFFu : (uint32_t)bytes;
 }
+// An address that is the same for the whole wave, as the compiler must know:
+// a buffer's descriptor otherwise takes a loop over the lanes at every load.
+__device__ __forceinline__ const f16* uniform(const f16* p) {
+  const uint64_t x = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(x >> 32));
+  return reinterpret_cast<const f16*>((uint64_t)hi << 32 | lo);
+}
 __device__ __forceinline__ Rsrc rsrc(const f16* base, uint32_t n) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<f16*>(base), 0, n, 0x00020000);
 }
@@ -390,9 +418,13 @@ struct Operands {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int wi = wave / T::kWavesJ * T::TI, wj = wave % T::kWavesJ * T::TJ;
     const int l = lane & 15, g = lane >> 4;
-    k_len = len;
-    ldp = p_ld;
-    ld = q_ld;
+    pp = uniform(pp);
+    qq = uniform(qq);
+    k_len = __builtin_amdgcn_readfirstlane(len);
+    ldp = __builtin_amdgcn_readfirstlane((int)p_ld);
+    ld = __builtin_amdgcn_readfirstlane((int)q_ld);
+    rows_p = __builtin_amdgcn_readfirstlane(rows_p);
+    rows_q = __builtin_amdgcn_readfirstlane(rows_q);
     np = extent(rows_p * ldp * 2);
     p = rsrc(pp, np);
     const int r = tid >> 3, c = (tid & 7) ^ (r & 7);
@@ -609,6 +641,7 @@ __device__ __forceinline__ void product(const Operands<T, XQ>& o, f16* shared,
 
 struct GemmArgs {
   Common c;
+  Firsts firsts;      // of this launch
   MuonIo io;
   float ca, cb, cc;   // kPoly: ca I + cb S + cc S S
   int32_t in0, in1, out;  // symmetric matrices (kApply: in0)
@@ -697,7 +730,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void zf_ns_sym(GemmArgs a) {
   if (a.c.st && a.c.st->skipped) return;
   __shared__ __align__(16) f16 shared[T::kBuf * T::kBuffers];
   const int w = tile_index();
-  const Mat& m = *find(a.c.table, a.c.count, w, [](const Mat& x) { return x.tri0[SIZE]; });
+  const Mat& m = *find(a.c.table, a.c.count, w, a.firsts, [](const Mat& x) { return x.tri0[SIZE]; });
   const int b = w - m.tri0[SIZE];
   int ti = (int)((sqrtf(8.0f * (float)b + 1.0f) - 1.0f) * 0.5f);
   while ((ti + 1) * (ti + 2) / 2 <= b) ++ti;
@@ -907,7 +940,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void zf_ns_apply(GemmArgs a) {
   if (a.c.st && a.c.st->skipped) return;
   __shared__ __align__(16) f16 shared[T::kBuf * T::kBuffers];
   const int w = tile_index();
-  const Mat& m = *find(a.c.table, a.c.count, w, [](const Mat& x) { return x.app0[SIZE]; });
+  const Mat& m = *find(a.c.table, a.c.count, w, a.firsts, [](const Mat& x) { return x.app0[SIZE]; });
   const int b = w - m.app0[SIZE], tiles_m = (m.mp + T::BM - 1) / T::BM;
   const int ti = b % tiles_m, tj = b / tiles_m;
   const int mp = m.mp, np = m.np, i0 = ti * T::BM, j0 = tj * T::BN;
@@ -1040,8 +1073,13 @@ void launch_last(const Group& g, int size, hipStream_t s, int32_t dst, bool muon
 // squares vanish in A's rounding (error 1.3e-3 at most for 2, 1, 2; 3e-3 for
 // 3, 2; 0.2 for all five).
 template <int PRODUCTS>
-int iterate(const Group& g, const zf_ns_params& p, int sym, int app, int32_t dst, bool muon,
-            hipStream_t s, GemmArgs a) {
+int iterate(const Group& g, const Mat* mats, const zf_ns_params& p, int sym, int app, int32_t dst,
+            bool muon, hipStream_t s, GemmArgs a) {
+  Firsts tri, along;
+  for (int k = 0; k < kFirsts; ++k) {
+    tri.at[k] = k < g.count ? mats[k].tri0[sym] : INT32_MAX;
+    along.at[k] = k < g.count ? mats[k].app0[app] : INT32_MAX;
+  }
   a.turn = 0;
   bool pair = p.steps > 1;
   for (int k = 0; k < p.steps;) {
@@ -1055,6 +1093,7 @@ int iterate(const Group& g, const zf_ns_params& p, int sym, int app, int32_t dst
       a.in1 = in1;
       a.out = out;
     };
+    a.firsts = tri;
     op(0, 0, 0);
     launch_sym<kGram, PRODUCTS>(g, sym, s, a);  // 0 = A
     op(0, 0, 1);
@@ -1070,6 +1109,7 @@ int iterate(const Group& g, const zf_ns_params& p, int sym, int app, int32_t dst
       launch_sym<kMul, PRODUCTS>(g, sym, s, a);   // 0 = their product
     }
     a.in0 = n == 2 ? 0 : 1;
+    a.firsts = along;
     k += n;
     if (k == p.steps) launch_last<PRODUCTS>(g, app, s, dst, muon, a);
     else launch_apply<false, PRODUCTS, ZF_F32, false>(g, app, s, a);
@@ -1619,8 +1659,8 @@ int zf::ns::enqueue(const Layout& l, const zf_ns_params& p, int products, int sm
     ga.io = la.io;
     const int sym = tile_size(g.tri_blocks), app = tile_size(g.app_blocks);
     const int rc = products == 3
-                       ? iterate<3>(g, p, sym, app, dst_dtype, io != nullptr, s, ga)
-                       : iterate<1>(g, p, sym, app, dst_dtype, io != nullptr, s, ga);
+                       ? iterate<3>(g, l.mats.data() + g.first, p, sym, app, dst_dtype, io != nullptr, s, ga)
+                       : iterate<1>(g, l.mats.data() + g.first, p, sym, app, dst_dtype, io != nullptr, s, ga);
     if (rc != ZF_OK) return rc;
   }
   return ZF_OK;
