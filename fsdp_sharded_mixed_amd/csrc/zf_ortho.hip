@@ -392,6 +392,9 @@ struct Tile {
   static constexpr int kRows = kThreads / 8;    // rows that a load of all threads covers
   static constexpr int kChunks = BN / 8;        // 16-byte pieces of a row of X
   static constexpr int kRowsX = kThreads / kChunks;
+  // consecutive symmetric tiles of one XCD, as many as it works on at a time
+  // (a quarter to three percent less time than runs of 8 along the rows)
+  static constexpr int kRun = BM == 256 ? 16 : 32;
   // a square of 64 x 64 results goes out by one wave, or by the whole block
   static constexpr int kSquareWaves = TI * TJ >= 4096 ? 1 : 4096 / (TI * TJ);
   static_assert(BM % kRows == 0 && BN % kRows == 0 && kRows % 8 == 0 && kRowsX % 16 == 0, "tile");
@@ -648,14 +651,39 @@ struct GemmArgs {
   int32_t turn;       // which X
 };
 
-// Blocks go to the 8 XCDs in turn; each XCD takes runs of kRun consecutive
+// Blocks go to the 8 XCDs in turn; each XCD takes runs of `run` consecutive
 // tiles, which share rows of their operands in its cache.
-constexpr int kRun = 8;
-__device__ __forceinline__ int tile_index() {
-  const int b = blockIdx.x, whole = gridDim.x / (8 * kRun) * (8 * kRun);
+__device__ __forceinline__ int tile_index(int run) {
+  const int b = blockIdx.x, whole = gridDim.x / (8 * run) * (8 * run);
   if (b >= whole) return b;
   const int x = b & 7, k = b >> 3;
-  return (k / kRun * 8 + x) * kRun + k % kRun;
+  return (k / run * 8 + x) * run + k % run;
+}
+
+constexpr int kApplyRun = 8;  // of the application: a column of tiles of X
+
+__device__ __forceinline__ int row_of(int b) {  // of place b in a triangle by rows
+  int i = (int)((sqrtf(8.0f * (float)b + 1.0f) - 1.0f) * 0.5f);
+  while ((i + 1) * (i + 2) / 2 <= b) ++i;
+  while (i * (i + 1) / 2 > b) --i;
+  return i;
+}
+
+// Tile b of the lower triangle of rows x rows tiles, in squares of SUPER x
+// SUPER: neighbours share rows and columns.
+template <int SUPER>
+__device__ __forceinline__ void tri_tile(int b, int rows, int& ti, int& tj) {
+  const int i0 = row_of(b) / SUPER * SUPER;  // rows before a row of squares come first
+  const int o = b - i0 * (i0 + 1) / 2, h = min(SUPER, rows - i0), square = o / (h * SUPER);
+  const int r = o - square * h * SUPER;
+  if (square * SUPER < i0) {
+    ti = i0 + r % h;
+    tj = square * SUPER + r / h;
+  } else {
+    const int i = row_of(r);
+    ti = i0 + i;
+    tj = i0 + r - i * (i + 1) / 2;
+  }
 }
 
 constexpr int kBig = 0, kMiddle = 1, kLittle = 2;  // places of the tile sizes in the tables
@@ -729,13 +757,10 @@ template <typename T, int SIZE, int MODE, int PRODUCTS>
 __global__ __launch_bounds__(T::kThreads, 2) void zf_ns_sym(GemmArgs a) {
   if (a.c.st && a.c.st->skipped) return;
   __shared__ __align__(16) f16 shared[T::kBuf * T::kBuffers];
-  const int w = tile_index();
+  const int w = tile_index(T::kRun);
   const Mat& m = *find(a.c.table, a.c.count, w, a.firsts, [](const Mat& x) { return x.tri0[SIZE]; });
-  const int b = w - m.tri0[SIZE];
-  int ti = (int)((sqrtf(8.0f * (float)b + 1.0f) - 1.0f) * 0.5f);
-  while ((ti + 1) * (ti + 2) / 2 <= b) ++ti;
-  while (ti * (ti + 1) / 2 > b) --ti;
-  const int tj = b - ti * (ti + 1) / 2;
+  int ti, tj;
+  tri_tile<4>(w - m.tri0[SIZE], (m.mp + T::BM - 1) / T::BM, ti, tj);
   const int mp = m.mp, i0 = ti * T::BM, j0 = tj * T::BN;
   const int64_t ld = MODE == kGram ? m.ldx : m.lds;
   const int len = MODE == kGram ? m.np : mp;
@@ -764,119 +789,124 @@ __global__ __launch_bounds__(T::kThreads, 2) void zf_ns_sym(GemmArgs a) {
   f16* out = at<f16>(a.c, m.s[a.out]);
   f16* rest = at<f16>(a.c, m.sl[a.out]);
   float* diag = at<float>(a.c, m.d[a.out]);
-  // a square of 64 x 64 values, 16 bits each, on the way to the mirrored
-  // place: 8-byte pieces of a row permuted by the row number
-  constexpr int kWaves = T::kSquareWaves;
-  const int part = kWaves == 1 ? 0 : wave;
-  ZF_LDS char* stage = (ZF_LDS char*)(shared) + (kWaves == 1 ? wave * 8192 : 0);
+  // 64 x 64 sums at a time through shared memory (row j, 16-byte piece c at
+  // c ^ (j & 7)) into values by rows of whole 128-byte lines; the values'
+  // 16-bit halves then take the sums' place (row j, piece c at c ^ 2 (j & 3))
+  // and go out along the other axis, transposed on the way
+  constexpr int kWaves = T::kSquareWaves, E = 8 / kWaves;  // lines of 8 rows a wave takes
+  const int e0 = kWaves == 1 ? 0 : wave * E;
+  ZF_LDS char* square = (ZF_LDS char*)(shared) + (kWaves == 1 ? wave * 16384 : 0);
   const int ri = (wi - i0) % 64, rj = (wj - j0) % 64;  // this wave's place in its square
-  float dv[T::FJ];
-  if constexpr (MODE != kGram) {
+  static_assert(T::kBuf * T::kBuffers * 2 >= T::kWaves / kWaves * 16384, "squares of 64 fit");
+  const int row = lane >> 3, c = lane & 7;
 #pragma unroll
-    for (int fj = 0; fj < T::FJ; ++fj) {
-      const int j = wj + fj * 16 + l;
-      dv[fj] = j < mp ? d1[j] : 0.0f;
+  for (int q = 0; q < (T::FI + 3) / 4; ++q) {
+    const int si = wi - ri + q * 64, sj = wj - rj;  // the square
+    if (si >= mp || sj >= mp) continue;
+    const int64_t p0 = (int64_t)(sj + e0 * 8 + row) * m.lds + si + c * 8;
+    float di[8], dj[E];
+    if constexpr (MODE != kGram) {
+#pragma unroll
+      for (int r = 0; r < 8; ++r) di[r] = d0[si + c * 8 + r];
+#pragma unroll
+      for (int e = 0; e < E; ++e) dj[e] = d1[sj + (e0 + e) * 8 + row];
     }
-  }
 #pragma unroll
-  for (int half = 0; half < (PRODUCTS == 3 ? 2 : 1); ++half) {
+    for (int f = 0; f < (T::FI < 4 ? T::FI : 4); ++f)
 #pragma unroll
-    for (int q = 0; q < (T::FI + 3) / 4; ++q) {
-      // every load of 4 rows of fragments before the first store, which the
-      // compiler could not move them past
-      constexpr int F = T::FI < 4 ? T::FI : 4;
-      f16x4 x0[F][T::FJ], x1[F][T::FJ], y0[F][T::FJ], y1[F][T::FJ];
-      f32x4 di[F];
+      for (int fj = 0; fj < T::FJ; ++fj)
+        *(ZF_LDS f32x4*)(square + (rj + fj * 16 + l) * 256 +
+                         ((ri / 4 + f * 4 + g) ^ (l & 7)) * 16) = acc[q * 4 + f][fj];
+    square_ready<T>();
+    f16x8 low[E];
+    constexpr int kBatch = E < 4 ? E : 4;  // lines whose loads are on their way together
+#pragma unroll
+    for (int eb = 0; eb < E; eb += kBatch) {
+      f16x8 x0[kBatch], x1[kBatch], y0[kBatch], y1[kBatch];
       if constexpr (MODE != kGram) {
-        if (half == 0) {
 #pragma unroll
-          for (int f = 0; f < F; ++f) {
-            const int i = wi + (q * 4 + f) * 16 + 4 * g;
-            if (wi + (q * 4 + f) * 16 >= mp) continue;
-            di[f] = *reinterpret_cast<const f32x4*>(d0 + i);
-#pragma unroll
-            for (int fj = 0; fj < T::FJ; ++fj) {
-              const int j = wj + fj * 16 + l;
-              if (wj + fj * 16 >= mp) continue;
-              const int64_t p = (int64_t)j * m.lds + i;
-              x0[f][fj] = *reinterpret_cast<const f16x4*>(o0 + p);
-              if constexpr (MODE == kMul) x1[f][fj] = *reinterpret_cast<const f16x4*>(o1 + p);
-              if constexpr (PRODUCTS == 3) {
-                y0[f][fj] = *reinterpret_cast<const f16x4*>(r0 + p);
-                if constexpr (MODE == kMul) y1[f][fj] = *reinterpret_cast<const f16x4*>(r1 + p);
-              }
-            }
+        for (int e = 0; e < kBatch; ++e) {
+          const int64_t p = p0 + (int64_t)(eb + e) * 8 * m.lds;
+          x0[e] = *reinterpret_cast<const f16x8*>(o0 + p);
+          if constexpr (MODE == kMul) x1[e] = *reinterpret_cast<const f16x8*>(o1 + p);
+          if constexpr (PRODUCTS == 3) {
+            y0[e] = *reinterpret_cast<const f16x8*>(r0 + p);
+            if constexpr (MODE == kMul) y1[e] = *reinterpret_cast<const f16x8*>(r1 + p);
           }
         }
       }
 #pragma unroll
-      for (int fi = q * 4; fi < q * 4 + F; ++fi) {
-        const int i = wi + fi * 16 + 4 * g, f = fi & 3;
-        if (wi + fi * 16 >= mp) continue;
+      for (int e = 0; e < kBatch; ++e) {
+        const int j = (e0 + eb + e) * 8 + row;  // in the square
+        ZF_LDS char* line = square + j * 256;
+        float v[8];
 #pragma unroll
-        for (int fj = 0; fj < T::FJ; ++fj) {
-          const int j = wj + fj * 16 + l;
-          if (wj + fj * 16 >= mp) continue;
-          const int64_t p = (int64_t)j * m.lds + i;  // (j, i..i+3): the mirrored place
-          float v[4];
-          if (half == 0) {
+        for (int t = 0; t < 2; ++t) {
+          const f32x4 sum = *(const ZF_LDS f32x4*)(line + ((2 * c + t) ^ row) * 16);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              if constexpr (MODE == kGram) {
-                v[r] = acc[fi][fj][r] * kUnscale;
-              } else {
-                const float e0 = PRODUCTS == 3 ? join(x0[f][fj][r], y0[f][fj][r])
-                                               : (float)x0[f][fj][r];
-                float e1 = e0;
-                if constexpr (MODE == kMul)
-                  e1 = PRODUCTS == 3 ? join(x1[f][fj][r], y1[f][fj][r]) : (float)x1[f][fj][r];
-                v[r] = combine<MODE == kPoly>(acc[fi][fj][r], e0, e1, di[f][r], dv[fj], false,
-                                              a.ca, a.cb, a.cc);
-              }
-            }
-            if (wi + fi * 16 == wj + fj * 16) {  // the diagonal runs through it
+          for (int r = 0; r < 4; ++r) v[t * 4 + r] = sum[r];
+        }
+        f16x8 hi;
 #pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                if (i + r != j) continue;
-                if constexpr (MODE != kGram)
-                  v[r] = combine<MODE == kPoly>(acc[fi][fj][r], 0.0f, 0.0f, di[f][r], dv[fj], true,
-                                                a.ca, a.cb, a.cc);
-                diag[j] = v[r] * kUnscale;
-                v[r] = 0.0f;
-              }
-            }
-            if constexpr (PRODUCTS == 3) {
-#pragma unroll
-              for (int r = 0; r < 4; ++r) acc[fi][fj][r] = v[r];  // for the second halves
-            }
+        for (int r = 0; r < 8; ++r) {
+          const float sum = v[r];
+          if constexpr (MODE == kGram) {
+            v[r] = sum * kUnscale;
           } else {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] = acc[fi][fj][r];
+            const float a0 = PRODUCTS == 3 ? join(x0[e][r], y0[e][r]) : (float)x0[e][r];
+            float a1 = a0;
+            if constexpr (MODE == kMul)
+              a1 = PRODUCTS == 3 ? join(x1[e][r], y1[e][r]) : (float)x1[e][r];
+            v[r] = combine<MODE == kPoly>(sum, a0, a1, di[r], dj[eb + e], false, a.ca, a.cb, a.cc);
           }
-          f16x4 x = halves(v);
-          if (half == 1) x = rests(v, x);
-          *reinterpret_cast<f16x4*>((half ? rest : out) + p) = x;
-          const int jj = rj + fj * 16 + l, turn = ((jj & 3) << 2) | ((jj >> 2) & 3);
-          *(ZF_LDS f16x4*)(stage + jj * 128 + ((ri / 4 + f * 4 + g) ^ turn) * 8) = x;
+          if (si == sj && c * 8 + r == j) {  // the diagonal
+            if constexpr (MODE != kGram)
+              v[r] = combine<MODE == kPoly>(sum, 0.0f, 0.0f, di[r], dj[eb + e], true, a.ca, a.cb,
+                                            a.cc);
+            diag[sj + j] = v[r] * kUnscale;
+            v[r] = 0.0f;
+          }
+          hi[r] = (f16)v[r];
+          if constexpr (PRODUCTS == 3) low[eb + e][r] = rest_of(v[r], hi[r]);
         }
+        const int64_t p = p0 + (int64_t)(eb + e) * 8 * m.lds;
+        *reinterpret_cast<f16x8*>(out + p) = hi;
+        if constexpr (PRODUCTS == 3) *reinterpret_cast<f16x8*>(rest + p) = low[eb + e];
+        *(ZF_LDS f16x8*)(line + (c ^ (2 * (row & 3))) * 16) = hi;
       }
-      if (ti == tj) continue;  // both places lie in this tile
-      square_ready<T>();
-      const int si = wi - ri + q * 64, sj = wj - rj;  // the square
-#pragma unroll
-      for (int k = 0; k < 16 / kWaves; ++k) {
-        // source lane (row e, piece k) of each 16 hands over 4 values along
-        // i; lane l receives those of i = l along j
-        const int fi = part * (4 / kWaves) + k / 4, fj = k % 4;
-        if (si + fi * 16 >= mp || sj + fj * 16 >= mp) continue;
-        const int jj = fj * 16 + 4 * g + (l >> 2), turn = ((jj & 3) << 2) | ((jj >> 2) & 3);
-        const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (ZF_LDS s16x4*)(stage + jj * 128 + ((fi * 4 + (l & 3)) ^ turn) * 8));
-        const int64_t p = (int64_t)(si + fi * 16 + l) * m.lds + sj + fj * 16 + 4 * g;
-        *reinterpret_cast<s16x4*>((half ? rest : out) + p) = x;
-      }
-      square_ready<T>();
     }
+    if (ti == tj) {  // both places lie in this tile
+      square_ready<T>();
+      continue;
+    }
+#pragma unroll
+    for (int half = 0; half < (PRODUCTS == 3 ? 2 : 1); ++half) {
+      if (half == 1) {
+        square_ready<T>();
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          *(ZF_LDS f16x8*)(square + ((e0 + e) * 8 + row) * 256 + (c ^ (2 * (row & 3))) * 16) =
+              low[e];
+      }
+      square_ready<T>();
+#pragma unroll
+      for (int k = 0; k < E; ++k) {
+        // 16 lines of 32 values: in each group of 16 lanes, source lane (row
+        // e, piece k) hands over 4 values along i, and lane l receives those
+        // of i = l along j
+        const int ib = (e0 + k) / 2, jb = (e0 + k) % 2 * 32 + 8 * g;
+        s16x4 x[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          x[t] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (ZF_LDS s16x4*)(square + (jb + 4 * t + (l >> 2)) * 256 +
+                              ((ib * 2 + ((l & 3) >> 1)) ^ (2 * (l >> 2))) * 16 + (l & 1) * 8));
+        const int64_t p = (int64_t)(si + ib * 16 + l) * m.lds + sj + jb;
+        *reinterpret_cast<f16x8*>((half ? rest : out) + p) = __builtin_bit_cast(
+            f16x8, __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7));
+      }
+    }
+    square_ready<T>();
   }
 }
 
@@ -939,7 +969,7 @@ template <typename T, int SIZE, bool LAST, int PRODUCTS, int DST, bool MUON>
 __global__ __launch_bounds__(T::kThreads, 2) void zf_ns_apply(GemmArgs a) {
   if (a.c.st && a.c.st->skipped) return;
   __shared__ __align__(16) f16 shared[T::kBuf * T::kBuffers];
-  const int w = tile_index();
+  const int w = tile_index(kApplyRun);
   const Mat& m = *find(a.c.table, a.c.count, w, a.firsts, [](const Mat& x) { return x.app0[SIZE]; });
   const int b = w - m.app0[SIZE], tiles_m = (m.mp + T::BM - 1) / T::BM;
   const int ti = b % tiles_m, tj = b / tiles_m;
@@ -1121,14 +1151,22 @@ int iterate(const Group& g, const Mat* mats, const zf_ns_params& p, int sym, int
 
 // The tile size for a launch of n[kBig] tiles of 256 x 256 (one block a CU),
 // n[kMiddle] of 128 x 128 or n[kLittle] of 64 x 64 (two a CU): whichever takes
-// the least time, counted in rounds over the 256 CUs, each weighted by its
-// blocks' work at the rate they reach together.
+// the least time, counted in rounds over the 256 CUs.  A full round takes 68,
+// 37 and 14 us at 2048 x 2048, 44, 26 and 9.6 at 1024 x 1024; one that is
+// nearly empty about half of that.
 int tile_size(const int32_t (&n)[3]) {
-  const double cost[3] = {4.0 * ((n[kBig] + 255) / 256), 2.0 / 0.85 * ((n[kMiddle] + 511) / 512),
-                          0.5 / 0.5 * ((n[kLittle] + 511) / 512)};
+  const int slots[3] = {256, 512, 512};
+  const double round[3] = {1.76, 1.0, 0.375};
+  double least = 0.0;
   int best = kBig;
-  for (int z = 1; z < 3; ++z)
-    if (cost[z] < cost[best]) best = z;
+  for (int z = 0; z < 3; ++z) {
+    const double part = (double)(n[z] % slots[z]) / slots[z];
+    const double cost = round[z] * (n[z] / slots[z] + (part > 0.0 ? 0.5 + 0.5 * part : 0.0));
+    if (z == 0 || cost < least) {
+      least = cost;
+      best = z;
+    }
+  }
   return best;
 }
 
