@@ -79,50 +79,50 @@ __global__ __launch_bounds__(64) void zf_ns_table(TableArgs a) {
   for (int i = threadIdx.x; i < a.count * (int)(sizeof(Mat) / 8); i += 64) d[i] = s[i];
 }
 
-// The matrix whose blocks hold block b: the last one that starts at or
-// before it.
-template <typename F>
-__device__ __forceinline__ const Mat* find(const Mat* table, int count, int b, F first) {
-  int lo = 0, hi = count - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (first(table[mid]) <= b) lo = mid;
-    else hi = mid - 1;
-  }
-  return table + lo;
-}
-// The same with the first blocks of up to kFirsts matrices among the
-// arguments: one scalar load instead of a chain of them.
-constexpr int kFirsts = 64;
-struct Firsts {
-  int32_t at[kFirsts];  // INT32_MAX past the last
-};
-template <typename F>
-__device__ __forceinline__ const Mat* find(const Mat* table, int count, int b, const Firsts& f,
-                                           F first) {
-  if (count > kFirsts) return find(table, count, b, first);
-  int k = 0;
-  if (count <= 8) {
-#pragma unroll
-    for (int j = 1; j < 8; ++j) k += f.at[j] <= b ? 1 : 0;
-  } else {
-#pragma unroll
-    for (int j = 1; j < kFirsts; ++j) k += f.at[j] <= b ? 1 : 0;
-  }
-  return table + k;
-}
-__device__ __forceinline__ const Mat* find_load(const Mat* table, int count, int b) {
-  return find(table, count, b, [](const Mat& m) { return m.load0; });
-}
-
+// The matrices of a launch: a table in the workspace, and, for a launch of a
+// few, the matrices themselves among the arguments, where they are one scalar
+// load away instead of a chain of them.
+constexpr int kFirsts = 64, kByValue = 8;
 struct Common {
   char* ws;
   const Mat* table;       // the group's matrices
   int32_t count;
+  int32_t load_tiles, own_norm;
   const DevState* st;     // the Muon step's skip flag, or NULL
   double* inv;            // 1 / (|G|_F + eps), by slot
   double* partials;       // squared-norm partials
+  double eps;
+  int32_t firsts[kFirsts];  // each matrix's first block in this launch, INT32_MAX past the last
+  Mat m[kByValue];          // count <= kByValue
 };
+
+// The matrix that holds block b of the launch: the last one that starts at
+// or before it.
+template <typename F>
+__device__ __forceinline__ const Mat& find(const Common& c, int b, F first) {
+  if (c.count <= kByValue) {
+    int k = 0;
+#pragma unroll
+    for (int j = 1; j < kByValue; ++j) k += c.firsts[j] <= b ? 1 : 0;
+    return c.m[k];
+  }
+  if (c.count <= kFirsts) {
+    int k = 0;
+#pragma unroll
+    for (int j = 1; j < kFirsts; ++j) k += c.firsts[j] <= b ? 1 : 0;
+    return c.table[k];
+  }
+  int lo = 0, hi = c.count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (first(c.table[mid]) <= b) lo = mid;
+    else hi = mid - 1;
+  }
+  return c.table[lo];
+}
+__device__ __forceinline__ const Mat& find_load(const Common& c, int b) {
+  return find(c, b, [](const Mat& m) { return m.load0; });
+}
 
 template <typename T>
 __device__ __forceinline__ T* at(const Common& c, int64_t offset) {
@@ -132,7 +132,7 @@ __device__ __forceinline__ T* at(const Common& c, int64_t offset) {
 // ---------------------------------------------------------------------------
 // The squared norm, one partial (64 bits) per block; the Muon step's momentum
 // update on the way.
-constexpr int kTile = 64, kLoadTiles = 4;
+constexpr int kTile = 64, kLoadTiles = 4;  // tiles of a block, if there are many
 
 struct LoadArgs {
   Common c;
@@ -231,7 +231,7 @@ __device__ __forceinline__ void load8(const LoadArgs& a, const Mat& m, float gs,
 template <int SRC>
 __global__ __launch_bounds__(kThreads) void zf_ns_load(LoadArgs a) {
   if (a.c.st && a.c.st->skipped) return;
-  const Mat& m = *find_load(a.c.table, a.c.count, blockIdx.x);
+  const Mat& m = find_load(a.c, blockIdx.x);
   const int block = blockIdx.x - m.load0, tiles_n = m.np / kTile;
   const int tiles = m.mp / kTile * tiles_n;
   const float gs = SRC == 0 ? a.c.st->gs : 0.0f;
@@ -240,8 +240,8 @@ __global__ __launch_bounds__(kThreads) void zf_ns_load(LoadArgs a) {
   double ss = 0.0;
 #pragma unroll
   for (int t = 0; t < kLoadTiles; ++t) {
-    const int tile = block * kLoadTiles + t;
-    if (tile >= tiles) break;
+    const int tile = block * a.c.load_tiles + t;
+    if (t >= a.c.load_tiles || tile >= tiles) break;
     const int i0 = tile / tiles_n * kTile, j0 = tile % tiles_n * kTile;
     const int r0 = m.tall ? j0 : i0, c0 = m.tall ? i0 : j0;
 #pragma unroll
@@ -259,44 +259,48 @@ __global__ __launch_bounds__(kThreads) void zf_ns_load(LoadArgs a) {
   if (threadIdx.x == 0) a.c.partials[m.part + block] = ss;
 }
 
-// The inverse norm of every matrix of the group: its partials in a fixed
-// order, one block a matrix.
-struct NormArgs {
-  Common c;
-  double eps;
-};
-
-__global__ __launch_bounds__(kThreads) void zf_ns_norm(NormArgs a) {
-  if (a.c.st && a.c.st->skipped) return;
-  const Mat& m = a.c.table[blockIdx.x];
+// The inverse norm of a matrix from its partials, in an order that depends on
+// its shape alone; valid in every thread.
+__device__ __forceinline__ double inverse_norm(const Common& c, const Mat& m) {
   const int64_t tiles = (int64_t)(m.mp / kTile) * (m.np / kTile);
-  const int64_t parts = (tiles + kLoadTiles - 1) / kLoadTiles;
+  const int64_t parts = (tiles + c.load_tiles - 1) / c.load_tiles;
   double ss = 0.0;
-  for (int64_t i = threadIdx.x; i < parts; i += kThreads) ss += a.c.partials[m.part + i];
+  for (int64_t i = threadIdx.x; i < parts; i += kThreads) ss += c.partials[m.part + i];
   uint32_t unused = 0;
   block_reduce(ss, unused);
-  if (threadIdx.x == 0) a.c.inv[m.slot] = 1.0 / (sqrt(ss) + a.eps);
+  __shared__ double total;
+  if (threadIdx.x == 0) total = 1.0 / (sqrt(ss) + c.eps);
+  __syncthreads();
+  return total;
 }
 
-// ---------------------------------------------------------------------------
+// The inverse norm of every matrix of the group, one block a matrix, unless
+// the blocks of the next launch take it themselves (own_norm).
+__global__ __launch_bounds__(kThreads) void zf_ns_norm(Common c) {
+  if (c.st && c.st->skipped) return;
+  const Mat& m = c.count <= kByValue ? c.m[blockIdx.x] : c.table[blockIdx.x];
+  const double inv = inverse_norm(c, m);
+  if (threadIdx.x == 0) c.inv[m.slot] = inv;
+}
+
 // X in 16-bit halves from the matrix and its inverse norm, transposed if the
 // matrix is tall, with zero padding.
 template <int SRC>
 __global__ __launch_bounds__(kThreads) void zf_ns_prep(LoadArgs a) {
   if (a.c.st && a.c.st->skipped) return;
-  const Mat& m = *find_load(a.c.table, a.c.count, blockIdx.x);
+  const Mat& m = find_load(a.c, blockIdx.x);
   const int block = blockIdx.x - m.load0, tiles_n = m.np / kTile;
   const int tiles = m.mp / kTile * tiles_n;
   const float gs = SRC == 0 ? a.c.st->gs : 0.0f;
-  const double inv = a.c.inv[m.slot] * kScale;
+  const double inv = (a.c.own_norm ? inverse_norm(a.c, m) : a.c.inv[m.slot]) * kScale;
   const bool wide = wide_loads<SRC>(m);
   const int rows = m.tall ? m.n : m.m, cols = m.tall ? m.m : m.n;
   __shared__ float s[kTile][kTile + 1];
   f16* hp = at<f16>(a.c, m.h[0]);
   f16* lp = at<f16>(a.c, m.l[0]);
 #pragma unroll 1
-  for (int t = 0; t < kLoadTiles; ++t) {
-    const int tile = block * kLoadTiles + t;
+  for (int t = 0; t < a.c.load_tiles; ++t) {
+    const int tile = block * a.c.load_tiles + t;
     if (tile >= tiles) break;
     const int i0 = tile / tiles_n * kTile, j0 = tile % tiles_n * kTile;
     const int r0 = m.tall ? j0 : i0, c0 = m.tall ? i0 : j0;
@@ -644,7 +648,6 @@ __device__ __forceinline__ void product(const Operands<T, XQ>& o, f16* shared,
 
 struct GemmArgs {
   Common c;
-  Firsts firsts;      // of this launch
   MuonIo io;
   float ca, cb, cc;   // kPoly: ca I + cb S + cc S S
   int32_t in0, in1, out;  // symmetric matrices (kApply: in0)
@@ -758,7 +761,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void zf_ns_sym(GemmArgs a) {
   if (a.c.st && a.c.st->skipped) return;
   __shared__ __align__(16) f16 shared[T::kBuf * T::kBuffers];
   const int w = tile_index(T::kRun);
-  const Mat& m = *find(a.c.table, a.c.count, w, a.firsts, [](const Mat& x) { return x.tri0[SIZE]; });
+  const Mat& m = find(a.c, w, [](const Mat& x) { return x.tri0[SIZE]; });
   int ti, tj;
   tri_tile<4>(w - m.tri0[SIZE], (m.mp + T::BM - 1) / T::BM, ti, tj);
   const int mp = m.mp, i0 = ti * T::BM, j0 = tj * T::BN;
@@ -970,7 +973,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void zf_ns_apply(GemmArgs a) {
   if (a.c.st && a.c.st->skipped) return;
   __shared__ __align__(16) f16 shared[T::kBuf * T::kBuffers];
   const int w = tile_index(kApplyRun);
-  const Mat& m = *find(a.c.table, a.c.count, w, a.firsts, [](const Mat& x) { return x.app0[SIZE]; });
+  const Mat& m = find(a.c, w, [](const Mat& x) { return x.app0[SIZE]; });
   const int b = w - m.app0[SIZE], tiles_m = (m.mp + T::BM - 1) / T::BM;
   const int ti = b % tiles_m, tj = b / tiles_m;
   const int mp = m.mp, np = m.np, i0 = ti * T::BM, j0 = tj * T::BN;
@@ -1105,11 +1108,11 @@ void launch_last(const Group& g, int size, hipStream_t s, int32_t dst, bool muon
 template <int PRODUCTS>
 int iterate(const Group& g, const Mat* mats, const zf_ns_params& p, int sym, int app, int32_t dst,
             bool muon, hipStream_t s, GemmArgs a) {
-  Firsts tri, along;
-  for (int k = 0; k < kFirsts; ++k) {
-    tri.at[k] = k < g.count ? mats[k].tri0[sym] : INT32_MAX;
-    along.at[k] = k < g.count ? mats[k].app0[app] : INT32_MAX;
-  }
+  auto firsts = [&](int32_t (*of)(const Mat&, int), int size) {
+    for (int k = 0; k < kFirsts; ++k) a.c.firsts[k] = k < g.count ? of(mats[k], size) : INT32_MAX;
+  };
+  const auto tri = [](const Mat& m, int size) { return m.tri0[size]; };
+  const auto along = [](const Mat& m, int size) { return m.app0[size]; };
   a.turn = 0;
   bool pair = p.steps > 1;
   for (int k = 0; k < p.steps;) {
@@ -1123,7 +1126,7 @@ int iterate(const Group& g, const Mat* mats, const zf_ns_params& p, int sym, int
       a.in1 = in1;
       a.out = out;
     };
-    a.firsts = tri;
+    firsts(tri, sym);
     op(0, 0, 0);
     launch_sym<kGram, PRODUCTS>(g, sym, s, a);  // 0 = A
     op(0, 0, 1);
@@ -1139,7 +1142,7 @@ int iterate(const Group& g, const Mat* mats, const zf_ns_params& p, int sym, int
       launch_sym<kMul, PRODUCTS>(g, sym, s, a);   // 0 = their product
     }
     a.in0 = n == 2 ? 0 : 1;
-    a.firsts = along;
+    firsts(along, app);
     k += n;
     if (k == p.steps) launch_last<PRODUCTS>(g, app, s, dst, muon, a);
     else launch_apply<false, PRODUCTS, ZF_F32, false>(g, app, s, a);
@@ -1186,7 +1189,8 @@ constexpr int kSmallSide = 128;            // longest short side
 constexpr int kSmallByValue = 12;          // matrices that travel as arguments
 
 struct SmallArgs {
-  Common c;                 // c.table NULL: the matrices are m[]
+  const Mat* table;         // or NULL: the matrices are m[]
+  const DevState* st;       // the Muon step's skip flag, or NULL
   MuonIo io;
   float ca, cb, cc;
   double eps;
@@ -1198,54 +1202,67 @@ struct SmallArgs {
 // long one.
 __host__ __device__ inline int small_waves_i(int mp) { return mp <= 32 ? 1 : mp <= 64 ? 2 : 4; }
 
-__device__ __forceinline__ float small_load(const SmallArgs& a, const Mat& m, int64_t p) {
-  if (a.src == ZF_F32) return static_cast<const float*>(m.src)[p];
-  const uint16_t x = static_cast<const uint16_t*>(m.src)[p];
-  return a.src == ZF_BF16 ? widen1<ZF_BF16>(x) : widen1<ZF_F16>(x);
+// A thread's elements k = tid, tid + 512, ... of the matrix, walked by row
+// and column.
+struct SmallWalk {
+  int r, c, dr, dc, cols;
+  __device__ __forceinline__ explicit SmallWalk(int columns) : cols(columns) {
+    r = threadIdx.x / cols;
+    c = threadIdx.x % cols;
+    dr = kSmallThreads / cols;
+    dc = kSmallThreads % cols;
+  }
+  __device__ __forceinline__ void next() {
+    r += dr;
+    c += dc;
+    if (c >= cols) c -= cols, ++r;
+  }
+  __device__ __forceinline__ void skip();  // kSmallBatch elements
+};
+constexpr int kSmallBatch = 32;  // elements of a thread whose loads are on their way together
+
+__device__ __forceinline__ void SmallWalk::skip() {
+  const int k = r * cols + c + kSmallBatch * kSmallThreads;
+  r = k / cols;
+  c = k % cols;
 }
 
-// Every element of the matrix, 8 of a thread's at a time with their loads on
-// their way together: use(r, c, value).  FIRST: the Muon step's momentum
-// update on the way.
-template <bool FIRST, typename F>
-__device__ __forceinline__ void small_walk(const SmallArgs& a, const Mat& m, int rows, int cols,
-                                           F use) {
-  constexpr int kBatch = 8;
-  const float gs = a.src == 0 ? a.c.st->gs : 0.0f;
-  const int dr = kSmallThreads / cols, dc = kSmallThreads % cols;
-  int r = threadIdx.x / cols, c = threadIdx.x % cols;
-  while (r < rows) {
-    float v[kBatch], g[kBatch];
-    int rr[kBatch], cc[kBatch];
+// The next kSmallBatch elements of the walk, from memory (the type decides
+// outside the loop, so that the loads do not wait for each other); FIRST: the
+// Muon step's momentum update on the way.  Zeros past the last row.
+template <bool FIRST>
+__device__ __forceinline__ void small_batch(const SmallArgs& a, const Mat& m, SmallWalk w,
+                                            int rows, float (&v)[kSmallBatch]) {
+  auto each = [&](auto f) {
+    SmallWalk at = w;
 #pragma unroll
-    for (int e = 0; e < kBatch; ++e) {
-      rr[e] = r;
-      cc[e] = c;
-      const int64_t p = min(r, rows - 1) * m.src_ld + c;
-      if (a.src == 0) {
-        v[e] = a.io.momentum[m.flat + p];
-        g[e] = a.io.sums[m.flat + p];
-      } else {
-        v[e] = small_load(a, m, p);
+    for (int e = 0; e < kSmallBatch; ++e, at.next())
+      f(e, min(at.r, rows - 1) * m.src_ld + at.c, at.r < rows);
+  };
+  if (a.src == 0) {
+    const float gs = a.st->gs;
+    const float* sums = a.io.sums + m.flat;
+    float* momentum = a.io.momentum + m.flat;
+    float g[kSmallBatch];
+    each([&](int e, int64_t p, bool) { v[e] = momentum[p], g[e] = sums[p]; });
+    each([&](int e, int64_t p, bool in) {
+      g[e] = g[e] * gs;
+      if constexpr (FIRST) {
+        v[e] = a.io.mu * v[e] + g[e];
+        if (in) momentum[p] = v[e];
       }
-      r += dr;
-      c += dc;
-      if (c >= cols) c -= cols, ++r;
-    }
+      if (a.io.nesterov) v[e] = g[e] + a.io.mu * v[e];
+    });
+  } else if (a.src == ZF_F32) {
+    each([&](int e, int64_t p, bool) { v[e] = static_cast<const float*>(m.src)[p]; });
+  } else {
+    uint16_t x[kSmallBatch];
+    each([&](int e, int64_t p, bool) { x[e] = static_cast<const uint16_t*>(m.src)[p]; });
 #pragma unroll
-    for (int e = 0; e < kBatch; ++e) {
-      if (rr[e] >= rows) continue;
-      if (a.src == 0) {
-        g[e] = g[e] * gs;
-        if constexpr (FIRST) {
-          v[e] = a.io.mu * v[e] + g[e];
-          a.io.momentum[m.flat + rr[e] * m.src_ld + cc[e]] = v[e];
-        }
-        if (a.io.nesterov) v[e] = g[e] + a.io.mu * v[e];
-      }
-      use(rr[e], cc[e], v[e]);
-    }
+    for (int e = 0; e < kSmallBatch; ++e)
+      v[e] = a.src == ZF_BF16 ? widen1<ZF_BF16>(x[e]) : widen1<ZF_F16>(x[e]);
   }
+  each([&](int e, int64_t, bool in) { v[e] = in ? v[e] : 0.0f; });
 }
 
 __device__ __forceinline__ void small_store(const SmallArgs& a, const Mat& m, int64_t r, int64_t c,
@@ -1266,8 +1283,8 @@ __device__ __forceinline__ void small_store(const SmallArgs& a, const Mat& m, in
 
 template <int CJ, int PRODUCTS>
 __global__ __launch_bounds__(kSmallThreads) void zf_ns_small(SmallArgs a) {
-  if (a.c.st && a.c.st->skipped) return;
-  const Mat& m = a.c.table ? a.c.table[blockIdx.x] : a.m[blockIdx.x];
+  if (a.st && a.st->skipped) return;
+  const Mat& m = a.table ? a.table[blockIdx.x] : a.m[blockIdx.x];
   const int mp = (m.m + kSmallPad - 1) / kSmallPad * kSmallPad;
   const int np = (m.n + kSmallPad - 1) / kSmallPad * kSmallPad;
   // row strides that put 16 rows' pieces in different banks
@@ -1283,9 +1300,18 @@ __global__ __launch_bounds__(kSmallThreads) void zf_ns_small(SmallArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int rows = m.tall ? m.n : m.m, cols = m.tall ? m.m : m.n;
 
-  for (int k = tid; k < mp * lx; k += kSmallThreads) reinterpret_cast<uint32_t*>(xh)[k] = 0;
+  // one batch of a thread's elements stays in registers until the norm is
+  // known; a matrix of more is read twice
+  float v[kSmallBatch];
+  const SmallWalk start(cols);
   double ss = 0.0;
-  small_walk<true>(a, m, rows, cols, [&](int, int, float v) { ss += (double)v * (double)v; });
+  for (SmallWalk w = start; w.r < rows; w.skip()) {
+    small_batch<true>(a, m, w, rows, v);
+#pragma unroll
+    for (int e = 0; e < kSmallBatch; ++e) ss += (double)v[e] * (double)v[e];
+  }
+  for (int k = tid; k < mp * lx / 4; k += kSmallThreads)
+    reinterpret_cast<f32x4*>(xh)[k] = (f32x4){0, 0, 0, 0};
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) ss = ss + __shfl_xor(ss, off, 64);
   if (lane == 0) sum[wave] = ss;
@@ -1294,13 +1320,20 @@ __global__ __launch_bounds__(kSmallThreads) void zf_ns_small(SmallArgs a) {
 #pragma unroll
   for (int w = 1; w < kSmallWaves; ++w) ss = ss + sum[w];
   const double inv = 1.0 / (sqrt(ss) + a.eps) * kScale;
-  small_walk<false>(a, m, rows, cols, [&](int r, int c, float u) {
-    const float v = (float)((double)u * inv);
-    const int p = m.tall ? c * lx + r : r * lx + c;
-    const f16 h = (f16)v;
-    xh[p] = h;
-    xl[p] = rest_of(v, h);
-  });
+  const bool once = rows * cols <= kSmallBatch * kSmallThreads;
+  for (SmallWalk w = start; w.r < rows; w.skip()) {
+    if (!once) small_batch<false>(a, m, w, rows, v);
+    SmallWalk to = w;
+#pragma unroll
+    for (int e = 0; e < kSmallBatch; ++e, to.next()) {
+      if (to.r >= rows) continue;
+      const float x = (float)((double)v[e] * inv);
+      const int p = m.tall ? to.c * lx + to.r : to.r * lx + to.c;
+      const f16 h = (f16)x;
+      xh[p] = h;
+      xl[p] = rest_of(x, h);
+    }
+  }
   __syncthreads();
 
   const int tm = mp / 16, tn = np / 16, waves_i = small_waves_i(mp);
@@ -1387,9 +1420,10 @@ __global__ __launch_bounds__(kSmallThreads) void zf_ns_small(SmallArgs a) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const float e = PRODUCTS == 3 ? join(h[r], w[r]) : (float)h[r];
-        const float x = combine<true>(v[r], e, e, di[r], dj, false, a.ca, a.cb, a.cc);
-        const float y = combine<true>(v[r], e, e, di[r], dj, true, a.ca, a.cb, a.cc);
-        v[r] = diagonal && i + r == j ? y : x;
+        const float sum2 = v[r];
+        v[r] = combine<true>(sum2, e, e, di[r], dj, false, a.ca, a.cb, a.cc);
+        if (diagonal && i + r == j)
+          v[r] = combine<true>(sum2, e, e, di[r], dj, true, a.ca, a.cb, a.cc);
       }
     });
     const bool last = step + 1 == a.steps;
@@ -1498,6 +1532,9 @@ int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 // padded elements.
 constexpr int64_t kGroupElements = 1ll << 28;
 constexpr int64_t kMaxSide = 1ll << 20;
+// Partials that every block of the next launch sums by itself: two a thread,
+// a microsecond, against four for a launch of their own.
+constexpr int64_t kOwnNorm = 512;
 
 int32_t stride_of(int32_t side) { return side; }
 
@@ -1538,7 +1575,21 @@ bool zf::ns::layout(const Shape* shapes, int64_t count, int products, Layout& ou
   Group g{};
   int64_t load = 0, tri[3] = {}, app[3] = {};
   auto close = [&]() {
-    g.load_blocks = (int32_t)load;
+    // tiles a block takes: one while that leaves CUs without a block
+    g.load_tiles = load >= 4096 ? kLoadTiles : 1;
+    g.own_norm = 1;
+    int64_t blocks = 0;
+    for (int32_t k = g.first; k < g.first + g.count; ++k) {
+      Mat& m = out.mats[(size_t)k];
+      const int64_t tiles = (int64_t)(m.mp / kTile) * (m.np / kTile);
+      const int64_t parts = (tiles + g.load_tiles - 1) / g.load_tiles;
+      if (parts > kOwnNorm) g.own_norm = 0;
+      m.part = partials;
+      partials += parts;
+      m.load0 = (int32_t)blocks;
+      blocks += parts;
+    }
+    g.load_blocks = (int32_t)blocks;
     for (int z = 0; z < 3; ++z) {
       g.tri_blocks[z] = (int32_t)tri[z];
       g.app_blocks[z] = (int32_t)app[z];
@@ -1597,12 +1648,8 @@ bool zf::ns::layout(const Shape* shapes, int64_t count, int products, Layout& ou
       m.d[z] = take((int64_t)m.mp * 4);
     }
     const int64_t tiles = (int64_t)(m.mp / kTile) * (m.np / kTile);
-    const int64_t blocks = (tiles + kLoadTiles - 1) / kLoadTiles;
     if (tiles > 0x7FFFFFFF) return false;
-    m.part = partials;
-    partials += blocks;
-    m.load0 = (int32_t)load;
-    load += blocks;
+    load += tiles;  // blocks follow when the group is whole
     const int side[3] = {Big::BM, Middle::BM, Little::BM};
     for (int z = 0; z < 3; ++z) {
       const int64_t tm = (m.mp + side[z] - 1) / side[z], tn = (m.np + side[z] - 1) / side[z];
@@ -1635,9 +1682,11 @@ int zf::ns::enqueue(const Layout& l, const zf_ns_params& p, int products, int sm
                     int32_t src_dtype, int32_t dst_dtype, const MuonIo* io, char* ws,
                     hipStream_t s) {
   Mat* table = reinterpret_cast<Mat*>(ws + l.table);
-  // a few small matrices go as arguments and need no table
+  // a few small matrices, and a few large ones, go as arguments and need no
+  // table
   const bool by_value = l.small_count <= kSmallByValue;
-  const size_t tabled = l.mats.size() - (by_value ? l.small_count : 0);
+  size_t tabled = l.mats.size() - (by_value ? l.small_count : 0);
+  if (by_value && tabled <= kByValue) tabled = 0;
   for (size_t k = 0; k < tabled; k += kTableChunk) {
     TableArgs t;
     t.to = table + k;
@@ -1648,12 +1697,9 @@ int zf::ns::enqueue(const Layout& l, const zf_ns_params& p, int products, int sm
   }
   if (l.small_count > 0) {
     SmallArgs a;
-    a.c.ws = ws;
-    a.c.table = by_value ? nullptr : table + l.small_first;
+    a.table = by_value ? nullptr : table + l.small_first;
     for (int k = 0; by_value && k < l.small_count; ++k) a.m[k] = l.mats[l.small_first + k];
-    a.c.count = l.small_count;
-    a.c.st = io ? io->st : nullptr;
-    a.c.inv = a.c.partials = nullptr;
+    a.st = io ? io->st : nullptr;
     a.io = io ? *io : MuonIo{};
     a.ca = (float)p.a;
     a.cb = (float)p.b;
@@ -1672,9 +1718,15 @@ int zf::ns::enqueue(const Layout& l, const zf_ns_params& p, int products, int sm
     c.ws = ws;
     c.table = table + g.first;
     c.count = g.count;
+    c.load_tiles = g.load_tiles;
+    c.own_norm = g.own_norm;
     c.st = io ? io->st : nullptr;
     c.inv = reinterpret_cast<double*>(ws + l.inv);
     c.partials = reinterpret_cast<double*>(ws + l.partials);
+    c.eps = p.eps;
+    for (int k = 0; k < kFirsts; ++k)
+      c.firsts[k] = k < g.count ? l.mats[g.first + k].load0 : INT32_MAX;
+    for (int k = 0; k < kByValue && k < g.count; ++k) c.m[k] = l.mats[g.first + k];
     la.io = io ? *io : MuonIo{};
     const dim3 load(g.load_blocks), block(kThreads);
     const int32_t src = io ? 0 : src_dtype;
@@ -1682,10 +1734,7 @@ int zf::ns::enqueue(const Layout& l, const zf_ns_params& p, int products, int sm
     else if (src == ZF_F32) hipLaunchKernelGGL(zf_ns_load<ZF_F32>, load, block, 0, s, la);
     else if (src == ZF_BF16) hipLaunchKernelGGL(zf_ns_load<ZF_BF16>, load, block, 0, s, la);
     else hipLaunchKernelGGL(zf_ns_load<ZF_F16>, load, block, 0, s, la);
-    NormArgs na;
-    na.c = c;
-    na.eps = p.eps;
-    hipLaunchKernelGGL(zf_ns_norm, dim3(g.count), block, 0, s, na);
+    if (!g.own_norm) hipLaunchKernelGGL(zf_ns_norm, dim3(g.count), block, 0, s, c);
     if (src == 0) hipLaunchKernelGGL(zf_ns_prep<0>, load, block, 0, s, la);
     else if (src == ZF_F32) hipLaunchKernelGGL(zf_ns_prep<ZF_F32>, load, block, 0, s, la);
     else if (src == ZF_BF16) hipLaunchKernelGGL(zf_ns_prep<ZF_BF16>, load, block, 0, s, la);
