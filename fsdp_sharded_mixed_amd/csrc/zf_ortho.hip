@@ -130,7 +130,7 @@ __device__ __forceinline__ T* at(const Common& c, int64_t offset) {
 }
 
 // ---------------------------------------------------------------------------
-// The squared norm, one partial (64 bits) per block; the Muon step's momentum
+// The squared norm, one partial (64 bits) a block; the Muon step's momentum
 // update on the way.
 constexpr int kTile = 64, kLoadTiles = 4;  // tiles of a block, if there are many
 
@@ -226,33 +226,45 @@ __device__ __forceinline__ void load8(const LoadArgs& a, const Mat& m, float gs,
   }
 }
 
-// A block takes kLoadTiles tiles of 64 x 64; a thread 8 neighbours along the
-// source's rows at a time.
+// A block takes load_tiles * 4096 elements of the rows one after another
+// (padded to multiples of 64), a thread 8 neighbours at a time: this walks
+// them, 2048 elements of the block a step.
+struct Walk {
+  int64_t r;
+  int c, width;
+  __device__ __forceinline__ Walk(int64_t first, int padded) : width(padded) {
+    r = first / width;  // the same for the block
+    c = (int)(first - r * width) + threadIdx.x * 8;
+    wrap();
+  }
+  __device__ __forceinline__ void wrap() {
+    while (c >= width) c -= width, ++r;
+  }
+  __device__ __forceinline__ void next() {
+    c += kThreads * 8;
+    wrap();
+  }
+};
+
 template <int SRC>
 __global__ __launch_bounds__(kThreads) void zf_ns_load(LoadArgs a) {
   if (a.c.st && a.c.st->skipped) return;
   const Mat& m = find_load(a.c, blockIdx.x);
-  const int block = blockIdx.x - m.load0, tiles_n = m.np / kTile;
-  const int tiles = m.mp / kTile * tiles_n;
+  const int block = blockIdx.x - m.load0;
   const float gs = SRC == 0 ? a.c.st->gs : 0.0f;
   const bool wide = wide_loads<SRC>(m);
   const int rows = m.tall ? m.n : m.m, cols = m.tall ? m.m : m.n;
+  const int steps = a.c.load_tiles * 2;
+  Walk w((int64_t)block * a.c.load_tiles * 4096, m.tall ? m.mp : m.np);
   double ss = 0.0;
 #pragma unroll
-  for (int t = 0; t < kLoadTiles; ++t) {
-    const int tile = block * a.c.load_tiles + t;
-    if (t >= a.c.load_tiles || tile >= tiles) break;
-    const int i0 = tile / tiles_n * kTile, j0 = tile % tiles_n * kTile;
-    const int r0 = m.tall ? j0 : i0, c0 = m.tall ? i0 : j0;
+  for (int t = 0; t < kLoadTiles * 2; ++t, w.next()) {
+    if (t >= steps) break;
+    if (w.r >= rows || w.c >= cols) continue;
+    float v[8];
+    load8<SRC, true>(a, m, gs, wide, w.r, w.c, cols, v);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int k = threadIdx.x + h * kThreads, r = r0 + k / 8, c = c0 + k % 8 * 8;
-      if (r >= rows || c >= cols) continue;
-      float v[8];
-      load8<SRC, true>(a, m, gs, wide, r, c, cols, v);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss += (double)v[e] * (double)v[e];
-    }
+    for (int e = 0; e < 8; ++e) ss += (double)v[e] * (double)v[e];
   }
   uint32_t unused = 0;
   block_reduce(ss, unused);
@@ -284,65 +296,88 @@ __global__ __launch_bounds__(kThreads) void zf_ns_norm(Common c) {
 }
 
 // X in 16-bit halves from the matrix and its inverse norm, transposed if the
-// matrix is tall, with zero padding.
-template <int SRC>
+// matrix is tall (by tiles of 64 x 64), with zero padding.  Non-temporal
+// stores: 143 -> 85 us for a layer of hidden 2048.
+template <int SRC, bool OWN_NORM>
 __global__ __launch_bounds__(kThreads) void zf_ns_prep(LoadArgs a) {
   if (a.c.st && a.c.st->skipped) return;
   const Mat& m = find_load(a.c, blockIdx.x);
   const int block = blockIdx.x - m.load0, tiles_n = m.np / kTile;
   const int tiles = m.mp / kTile * tiles_n;
   const float gs = SRC == 0 ? a.c.st->gs : 0.0f;
-  const double inv = (a.c.own_norm ? inverse_norm(a.c, m) : a.c.inv[m.slot]) * kScale;
+  double inv = kScale;
+  if constexpr (OWN_NORM) inv *= inverse_norm(a.c, m);
+  else inv *= a.c.inv[m.slot];
   const bool wide = wide_loads<SRC>(m);
-  const int rows = m.tall ? m.n : m.m, cols = m.tall ? m.m : m.n;
-  __shared__ float s[kTile][kTile + 1];
   f16* hp = at<f16>(a.c, m.h[0]);
   f16* lp = at<f16>(a.c, m.l[0]);
+  // 8 values at (i, j) in whole lines that this kernel does not read back
+  auto put = [&](int64_t i, int j, const float (&v)[8]) {
+    f16x8 hi, lo;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float x = i < m.m && j + e < m.n ? (float)((double)v[e] * inv) : 0.0f;
+      hi[e] = (f16)x;
+      lo[e] = rest_of(x, hi[e]);
+    }
+    const int64_t p = i * m.ldx + j;
+    __builtin_nontemporal_store(hi, reinterpret_cast<f16x8*>(hp + p));
+    __builtin_nontemporal_store(lo, reinterpret_cast<f16x8*>(lp + p));
+  };
+  if (!m.tall) {
+    Walk w((int64_t)block * a.c.load_tiles * 4096, m.np);
+#pragma unroll 2
+    for (int t = 0; t < a.c.load_tiles * 2; ++t, w.next()) {
+      if (w.r >= m.mp) break;
+      float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      if (w.r < m.m && w.c < m.n) load8<SRC, false>(a, m, gs, wide, w.r, w.c, m.n, v);
+      put(w.r, w.c, v);
+    }
+    return;
+  }
+  __shared__ float s[kTile][kTile + 1];
 #pragma unroll 1
   for (int t = 0; t < a.c.load_tiles; ++t) {
     const int tile = block * a.c.load_tiles + t;
     if (tile >= tiles) break;
     const int i0 = tile / tiles_n * kTile, j0 = tile % tiles_n * kTile;
-    const int r0 = m.tall ? j0 : i0, c0 = m.tall ? i0 : j0;
     float v[2][8];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int k = threadIdx.x + h * kThreads, r = r0 + k / 8, c = c0 + k % 8 * 8;
+      const int k = threadIdx.x + h * kThreads, r = j0 + k / 8, c = i0 + k % 8 * 8;
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[h][e] = 0.0f;
-      if (r < rows && c < cols) load8<SRC, false>(a, m, gs, wide, r, c, cols, v[h]);
+      if (r < m.n && c < m.m) load8<SRC, false>(a, m, gs, wide, r, c, m.m, v[h]);
     }
-    if (m.tall) {
-      __syncthreads();
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int k = threadIdx.x + h * kThreads;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s[k % 8 * 8 + e][k / 8] = v[h][e];
-      }
-      __syncthreads();
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int k = threadIdx.x + h * kThreads;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[h][e] = s[k / 8][k % 8 * 8 + e];
-      }
-    }
+    __syncthreads();
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int k = threadIdx.x + h * kThreads, i = i0 + k / 8, j = j0 + k % 8 * 8;
-      f16x8 hi, lo;
+      const int k = threadIdx.x + h * kThreads;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float x = i < m.m && j + e < m.n ? (float)((double)v[h][e] * inv) : 0.0f;
-        hi[e] = (f16)x;
-        lo[e] = rest_of(x, hi[e]);
-      }
-      const int64_t p = (int64_t)i * m.ldx + j;
-      *reinterpret_cast<f16x8*>(hp + p) = hi;
-      *reinterpret_cast<f16x8*>(lp + p) = lo;
+      for (int e = 0; e < 8; ++e) s[k % 8 * 8 + e][k / 8] = v[h][e];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = threadIdx.x + h * kThreads;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[h][e] = s[k / 8][k % 8 * 8 + e];
+      put(i0 + k / 8, j0 + k % 8 * 8, v[h]);
     }
   }
+}
+
+void launch_prep(int32_t src, bool own_norm, dim3 grid, hipStream_t s, const LoadArgs& a) {
+#define ZF_PREP(S) \
+  do { \
+    if (own_norm) hipLaunchKernelGGL((zf_ns_prep<S, true>), grid, dim3(kThreads), 0, s, a); \
+    else hipLaunchKernelGGL((zf_ns_prep<S, false>), grid, dim3(kThreads), 0, s, a); \
+  } while (0)
+  if (src == 0) ZF_PREP(0);
+  else if (src == ZF_F32) ZF_PREP(ZF_F32);
+  else if (src == ZF_BF16) ZF_PREP(ZF_BF16);
+  else ZF_PREP(ZF_F16);
+#undef ZF_PREP
 }
 
 // ---------------------------------------------------------------------------
@@ -399,11 +434,19 @@ struct Tile {
   // consecutive symmetric tiles of one XCD, as many as it works on at a time
   // (a quarter to three percent less time than runs of 8 along the rows)
   static constexpr int kRun = BM == 256 ? 16 : 32;
-  // a square of 64 x 64 results goes out by one wave, or by the whole block
-  static constexpr int kSquareWaves = TI * TJ >= 4096 ? 1 : 4096 / (TI * TJ);
+  // a square of 64 x 64 results goes out by the waves that hold it
+  static constexpr int kSquareI = TI < 64 ? 64 / TI : 1, kSquareJ = TJ < 64 ? 64 / TJ : 1;
+  static constexpr int kSquareWaves = kSquareI * kSquareJ;
   static_assert(BM % kRows == 0 && BN % kRows == 0 && kRows % 8 == 0 && kRowsX % 16 == 0, "tile");
-  static_assert(kSquareWaves == 1 ? TJ == 64 && TI % 64 == 0
-                                  : BM == 64 && BN == 64 && kWaves == kSquareWaves, "squares");
+  static_assert((TI % 64 == 0 || 64 % TI == 0) && (TJ == 64 || 64 % TJ == 0), "squares");
+  // for a wave at (wi, wj) of the tile: its square's place in shared memory
+  // and its own share of the square
+  static __device__ __forceinline__ int square_of(int wi, int wj) {
+    return wi / (TI < 64 ? 64 : TI) * (BN / 64) + wj / 64;
+  }
+  static __device__ __forceinline__ int share_of(int wi, int wj) {
+    return wi % 64 / (TI < 64 ? TI : 64) * kSquareJ + wj % 64 / TJ;
+  }
 };
 
 // The operands of one tile.  XQ: Q is X, rows along j.
@@ -796,19 +839,19 @@ __global__ __launch_bounds__(T::kThreads, 2) void zf_ns_sym(GemmArgs a) {
   // c ^ (j & 7)) into values by rows of whole 128-byte lines; the values'
   // 16-bit halves then take the sums' place (row j, piece c at c ^ 2 (j & 3))
   // and go out along the other axis, transposed on the way
-  constexpr int kWaves = T::kSquareWaves, E = 8 / kWaves;  // lines of 8 rows a wave takes
-  const int e0 = kWaves == 1 ? 0 : wave * E;
-  ZF_LDS char* square = (ZF_LDS char*)(shared) + (kWaves == 1 ? wave * 16384 : 0);
+  constexpr int E = 8 / T::kSquareWaves;  // lines of 8 rows a wave takes
+  const int e0 = T::share_of(wi - i0, wj - j0) * E;
+  ZF_LDS char* square = (ZF_LDS char*)(shared) + T::square_of(wi - i0, wj - j0) * 16384;
   const int ri = (wi - i0) % 64, rj = (wj - j0) % 64;  // this wave's place in its square
-  static_assert(T::kBuf * T::kBuffers * 2 >= T::kWaves / kWaves * 16384, "squares of 64 fit");
+  static_assert(T::kBuf * T::kBuffers * 2 >= T::kWaves / T::kSquareWaves * 16384, "squares of 64 fit");
   const int row = lane >> 3, c = lane & 7;
 #pragma unroll
   for (int q = 0; q < (T::FI + 3) / 4; ++q) {
     const int si = wi - ri + q * 64, sj = wj - rj;  // the square
-    if (si >= mp || sj >= mp) continue;
+    const bool in = si < mp && sj < mp;
     const int64_t p0 = (int64_t)(sj + e0 * 8 + row) * m.lds + si + c * 8;
     float di[8], dj[E];
-    if constexpr (MODE != kGram) {
+    if (MODE != kGram && in) {
 #pragma unroll
       for (int r = 0; r < 8; ++r) di[r] = d0[si + c * 8 + r];
 #pragma unroll
@@ -825,6 +868,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void zf_ns_sym(GemmArgs a) {
     constexpr int kBatch = E < 4 ? E : 4;  // lines whose loads are on their way together
 #pragma unroll
     for (int eb = 0; eb < E; eb += kBatch) {
+      if (!in) break;
       f16x8 x0[kBatch], x1[kBatch], y0[kBatch], y1[kBatch];
       if constexpr (MODE != kGram) {
 #pragma unroll
@@ -878,10 +922,6 @@ __global__ __launch_bounds__(T::kThreads, 2) void zf_ns_sym(GemmArgs a) {
         *(ZF_LDS f16x8*)(line + (c ^ (2 * (row & 3))) * 16) = hi;
       }
     }
-    if (ti == tj) {  // both places lie in this tile
-      square_ready<T>();
-      continue;
-    }
 #pragma unroll
     for (int half = 0; half < (PRODUCTS == 3 ? 2 : 1); ++half) {
       if (half == 1) {
@@ -892,6 +932,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void zf_ns_sym(GemmArgs a) {
               low[e];
       }
       square_ready<T>();
+      if (ti == tj || !in) continue;  // on the diagonal both places lie in this tile
 #pragma unroll
       for (int k = 0; k < E; ++k) {
         // 16 lines of 32 values: in each group of 16 lanes, source lane (row
@@ -996,23 +1037,24 @@ __global__ __launch_bounds__(T::kThreads, 2) void zf_ns_apply(GemmArgs a) {
   f16* h1 = at<f16>(a.c, m.h[a.turn ^ 1]);
   f16* lo1 = at<f16>(a.c, m.l[a.turn ^ 1]);
   const float* d = at<float>(a.c, m.d[a.in0]);
-  constexpr int kWaves = T::kSquareWaves, E = 8 / kWaves;  // lines of 8 rows a wave takes
-  const int e0 = kWaves == 1 ? 0 : wave * E;
-  ZF_LDS float* square = (ZF_LDS float*)(shared) + (kWaves == 1 ? wave * 4096 : 0);
+  constexpr int E = 8 / T::kSquareWaves;  // lines of 8 rows a wave takes
+  const int e0 = T::share_of(wi - i0, wj - j0) * E;
+  ZF_LDS float* square = (ZF_LDS float*)(shared) + T::square_of(wi - i0, wj - j0) * 4096;
   const int ri = (wi - i0) % 64, rj = (wj - j0) % 64;  // this wave's place in its square
-  static_assert(T::kBuf * T::kBuffers * 2 >= T::kWaves / kWaves * 16384, "squares of 64 fit");
+  static_assert(T::kBuf * T::kBuffers * 2 >= T::kWaves / T::kSquareWaves * 16384, "squares of 64 fit");
 #pragma unroll
   for (int q = 0; q < (T::FI + 3) / 4; ++q) {
     // 64 x 64 of O X to shared memory, and back by rows of whole 128-byte
     // lines: the 16-byte piece c of row i lies at piece c ^ (i & 7)
     const int si = wi - ri + q * 64, sj = wj - rj;
-    if (si >= mp || sj >= np) continue;
+    const bool in = si < mp && sj < np;
     const int row = lane >> 3, c = lane & 7;
     const int64_t p0 = (int64_t)(si + e0 * 8 + row) * m.ldx + sj + c * 8;
     f16x8 x[E], y[E];
     float di[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
+      if (!in) break;
       x[e] = *reinterpret_cast<const f16x8*>(h + p0 + (int64_t)e * 8 * m.ldx);
       y[e] = *reinterpret_cast<const f16x8*>(lo + p0 + (int64_t)e * 8 * m.ldx);
       di[e] = d[si + (e0 + e) * 8 + row];
@@ -1026,6 +1068,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void zf_ns_apply(GemmArgs a) {
     square_ready<T>();
 #pragma unroll
     for (int e = 0; e < E; ++e) {
+      if (!in) break;
       ZF_LDS float* s = square + ((e0 + e) * 8 + row) * 64;
       f16x8 hi, rest;
 #pragma unroll
@@ -1049,7 +1092,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void zf_ns_apply(GemmArgs a) {
     }
     square_ready<T>();
     if constexpr (LAST) {
-      write_square<DST, MUON>(a, m, square, si, sj, e0 * 8, E * 8);
+      if (in) write_square<DST, MUON>(a, m, square, si, sj, e0 * 8, E * 8);
       square_ready<T>();
     }
   }
@@ -1735,10 +1778,7 @@ int zf::ns::enqueue(const Layout& l, const zf_ns_params& p, int products, int sm
     else if (src == ZF_BF16) hipLaunchKernelGGL(zf_ns_load<ZF_BF16>, load, block, 0, s, la);
     else hipLaunchKernelGGL(zf_ns_load<ZF_F16>, load, block, 0, s, la);
     if (!g.own_norm) hipLaunchKernelGGL(zf_ns_norm, dim3(g.count), block, 0, s, c);
-    if (src == 0) hipLaunchKernelGGL(zf_ns_prep<0>, load, block, 0, s, la);
-    else if (src == ZF_F32) hipLaunchKernelGGL(zf_ns_prep<ZF_F32>, load, block, 0, s, la);
-    else if (src == ZF_BF16) hipLaunchKernelGGL(zf_ns_prep<ZF_BF16>, load, block, 0, s, la);
-    else hipLaunchKernelGGL(zf_ns_prep<ZF_F16>, load, block, 0, s, la);
+    launch_prep(src, g.own_norm, load, s, la);
     if (!hip_ok(hipGetLastError())) return ZF_EHIP;
 
     GemmArgs ga;
