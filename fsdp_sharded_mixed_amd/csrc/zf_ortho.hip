@@ -1575,8 +1575,10 @@ int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 // padded elements.
 constexpr int64_t kGroupElements = 1ll << 28;
 constexpr int64_t kMaxSide = 1ll << 20;
-// Partials that every block of the next launch sums by itself: two a thread,
-// a microsecond, against four for a launch of their own.
+// Partials that every block of the next launch sums by itself, where blocks
+// are few: two a thread, a microsecond, against four for a launch of their
+// own.  (With many blocks that microsecond comes again and again: 8 layers of
+// hidden 1024, 120 -> 167 us.)
 constexpr int64_t kOwnNorm = 512;
 
 int32_t stride_of(int32_t side) { return side; }
@@ -1620,7 +1622,7 @@ bool zf::ns::layout(const Shape* shapes, int64_t count, int products, Layout& ou
   auto close = [&]() {
     // tiles a block takes: one while that leaves CUs without a block
     g.load_tiles = load >= 4096 ? kLoadTiles : 1;
-    g.own_norm = 1;
+    g.own_norm = g.load_tiles == 1;
     int64_t blocks = 0;
     for (int32_t k = g.first; k < g.first + g.count; ++k) {
       Mat& m = out.mats[(size_t)k];
