@@ -29,6 +29,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <utility>
 
 #include "zf_device.h"
 #include "zf_hip_status.h"
@@ -72,7 +73,10 @@ struct TableArgs {
   Mat m[kTableChunk];
 };
 
+constexpr size_t kArgBytes = 4096;  // of a launch
+
 __global__ __launch_bounds__(64) void zf_ns_table(TableArgs a) {
+  static_assert(sizeof(TableArgs) <= kArgBytes, "arguments of a launch");
   static_assert(sizeof(Mat) % 8 == 0, "copied in words");
   const uint64_t* s = reinterpret_cast<const uint64_t*>(a.m);
   uint64_t* d = reinterpret_cast<uint64_t*>(a.to);
@@ -138,6 +142,7 @@ struct LoadArgs {
   Common c;
   MuonIo io;
 };
+static_assert(sizeof(LoadArgs) <= kArgBytes, "arguments of a launch");
 
 // Whether 8 elements at a multiple of 8 of any row lie at a multiple of 16
 // bytes.
@@ -696,6 +701,7 @@ struct GemmArgs {
   int32_t in0, in1, out;  // symmetric matrices (kApply: in0)
   int32_t turn;       // which X
 };
+static_assert(sizeof(GemmArgs) <= kArgBytes, "arguments of a launch");
 
 // Blocks go to the 8 XCDs in turn; each XCD takes runs of `run` consecutive
 // tiles, which share rows of their operands in its cache.
@@ -1240,6 +1246,7 @@ struct SmallArgs {
   int32_t steps, src, dst;  // types; src 0: the Muon step
   Mat m[kSmallByValue];
 };
+static_assert(sizeof(SmallArgs) <= kArgBytes, "arguments of a launch");
 
 // Waves along the short side (each takes 2 tiles of it), the rest along the
 // long one.
@@ -1581,8 +1588,6 @@ constexpr int64_t kMaxSide = 1ll << 20;
 // hidden 1024, 120 -> 167 us.)
 constexpr int64_t kOwnNorm = 512;
 
-int32_t stride_of(int32_t side) { return side; }
-
 int small_tiles_of(const zf::ns::Shape& s) {
   return small_tiles(std::min(s.rows, s.cols), std::max(s.rows, s.cols));
 }
@@ -1677,8 +1682,8 @@ bool zf::ns::layout(const Shape* shapes, int64_t count, int products, Layout& ou
       out.small_tiles = std::max(out.small_tiles, tiles_held);
       continue;
     }
-    m.ldx = stride_of(m.np);
-    m.lds = stride_of(m.mp);
+    m.ldx = m.np;
+    m.lds = m.mp;
     const int64_t mn = (int64_t)m.mp * m.ldx, mm = (int64_t)m.mp * m.lds;
     if (g.count > 0 && elements + mn > kGroupElements) close();
     // what the rounding left of X: an operand of the products if there are
@@ -1819,6 +1824,22 @@ int ortho_layout(const zf_matrix* mats, int64_t count, int32_t dst_dtype,
   return zf::ns::layout(shapes.data(), count, products, l) ? ZF_OK : ZF_ESIZE;
 }
 
+// Two results in one place, or a result in another matrix's place, which
+// launches in no given order would mix.  (Partial overlaps are the caller's.)
+bool distinct(const zf_matrix* mats, int64_t count) {
+  std::vector<std::pair<const void*, int64_t>> at((size_t)count);
+  for (int64_t k = 0; k < count; ++k) at[(size_t)k] = {mats[k].dst, k};
+  std::sort(at.begin(), at.end());
+  for (int64_t k = 1; k < count; ++k)
+    if (at[(size_t)k].first == at[(size_t)k - 1].first) return false;
+  for (int64_t k = 0; k < count; ++k) {
+    const std::pair<const void*, int64_t> src(mats[k].src, 0);
+    const auto z = std::lower_bound(at.begin(), at.end(), src);
+    if (z != at.end() && z->first == mats[k].src && z->second != k) return false;
+  }
+  return true;
+}
+
 bool aligned(const void* p, int32_t dtype) {
   return (reinterpret_cast<uintptr_t>(p) & (dtype == ZF_F32 ? 3u : 1u)) == 0;
 }
@@ -1854,6 +1875,7 @@ extern "C" int zf_orthogonalize(const zf_matrix* mats, int64_t count, int32_t sr
       if (z.rows > 1 && (z.src_stride < z.cols || z.dst_stride < z.cols)) return ZF_EINVAL;
       if (!aligned(z.src, src_dtype) || !aligned(z.dst, dst_dtype)) return ZF_EALIGN;
     }
+    if (!distinct(mats, count)) return ZF_EINVAL;
     for (Mat& m : l.mats) {
       const zf_matrix& z = mats[m.slot];
       m.src = z.src;

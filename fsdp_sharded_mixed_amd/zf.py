@@ -549,9 +549,10 @@ def ortho_batch(mats, outs):
         rows, cols = x.shape
         arr[i] = Matrix(_ptr(x), _ptr(y), rows, cols, max(x.stride(0), cols),
                         max(y.stride(0), cols))
-    return OrthoBatch(arr, len(mats), _dtype_of(mats[0]) if mats else BF16,
-                      _dtype_of(outs[0]) if outs else BF16,
-                      mats[0].device if mats else None, mats + outs)
+    src, dst = (_dtype_of(x[0]) if x else BF16 for x in (mats, outs))
+    if mats and not mats[0].is_cuda:
+        raise ValueError("zf_orthogonalize: tensors on a GPU")
+    return OrthoBatch(arr, len(mats), src, dst, mats[0].device if mats else None, mats + outs)
 
 
 def orthogonalize_bytes(batch, ns=None):
@@ -562,8 +563,21 @@ def orthogonalize_bytes(batch, ns=None):
     return n
 
 
+def _on_current_device(name, *devices):
+    """Kernels run on the current device: refuse buffers of another."""
+    for d in devices:
+        if d is None:
+            continue
+        import torch
+        d = torch.device(d)
+        if d.type != "cuda" or d.index != torch.cuda.current_device():
+            raise ValueError(f"{name}: buffers on {d}, not on the current GPU")
+
+
 def orthogonalize(batch, workspace, ns=None, stream=None, workspace_size=None):
-    """zf_orthogonalize of a batch (ortho_batch); ns: None or ns_params()."""
+    """zf_orthogonalize of a batch (ortho_batch); ns: None or ns_params().  The
+    batch's device must be the current one."""
+    _on_current_device("zf_orthogonalize", batch.device, getattr(workspace, "device", None))
     _check(lib.zf_orthogonalize(batch.mats, batch.count, batch.src_dtype, batch.dst_dtype,
                                 _ns(ns), _ptr(workspace), _nbytes(workspace, workspace_size),
                                 _stream(stream)), "zf_orthogonalize")
@@ -607,7 +621,11 @@ def muon_step(muon, hp, mhp, grad_dtype, param_dtype, grads, master, exp_avg, ex
               workspace, state, stream=None, phase_events=None, numel=None,
               workspace_size=None, grad_shards=None, grads_reduced=False):
     """zf_muon_step; the arguments after mhp are shard_step's.  workspace:
-    muon_workspace_bytes(muon, mhp.ns) bytes."""
+    muon_workspace_bytes(muon, mhp.ns) bytes.  The buffers' device must be the
+    current one."""
+    _on_current_device("zf_muon_step", *(getattr(t, "device", None) for t in (
+        list(grads or []) + [master, exp_avg, exp_avg_sq, params, workspace, state,
+                             grad_shards])))
     gp = _ptr_array(grads) if grads is not None else None
     ev = (C.c_void_p * 4)(*phase_events) if phase_events is not None else None
     if numel is None:

@@ -54,8 +54,8 @@
  *   - HIP graphs: zf_shard_step, zf_shard_step_noalloc (after its first
  *     call on the device), zf_reduce_scatter, zf_gather, zf_gather_cast,
  *     zf_bucket_reduce_scatter, zf_accumulate, zf_orthogonalize,
- *     zf_muon_step and zf_state_init enqueue kernels only (no memset, copy, allocation or
- *     synchronisation; every pointer travels by value in the kernel
+ *     zf_muon_step and zf_state_init enqueue kernels only (no memset, copy,
+ *     allocation or synchronisation; every pointer travels by value in the kernel
  *     arguments), so a caller may capture them on a stream and replay the
  *     graph.  The state block carries t, the loss scale and the skip
  *     decision from one replay to the next.  The hyperparameters (and every
@@ -540,10 +540,10 @@ int zf_offload_step(const zf_plan* plan, const zf_hparams* hp, const zf_offload_
  * products: how exactly the matrix products are computed.  1: operands are
  * rounded to 11 bits (fp16 with a common power-of-two factor; sums, the
  * linear term and the diagonals of A and of its polynomial in binary32); the
- * result is within about 1e-3 of the exact one (|error|_F / |X|_F), below
- * bf16's own rounding.  3: operands are sums of two fp16 numbers, about 22
- * bits, for three times the work; the result is within about 1e-5.  0: 1 for
- * a ZF_BF16 result, else 3; in zf_muon_step 1, and 3 for matrices that fit
+ * result of the default steps is within about 1.5e-3 of the exact one
+ * (|error|_F / |X|_F), below bf16's own rounding (1.7e-3).  3: operands are
+ * sums of two fp16 numbers, about 22 bits, for three times the work; the
+ * result is within about 3e-6.  0: 1 for a ZF_BF16 result, else 3; in zf_muon_step 1, and 3 for matrices that fit
  * in a compute unit's shared memory (up to 128 x 128), where they cost
  * little.
  * The operands' range bounds the coefficients: singular values, and the
@@ -579,7 +579,9 @@ int64_t zf_orthogonalize_bytes(const zf_matrix* mats, int64_t count, int32_t dst
  * result for src.  src_dtype and dst_dtype: ZF_F16, ZF_BF16 or ZF_F32, the
  * same for the whole batch; src and dst aligned to their element size.  The
  * shapes may differ; every side is at most 2^20.  dst may be the matrix's
- * own src (same place, stride and type); nothing else may overlap a dst.
+ * own src (same place, stride and type); nothing else may overlap a dst
+ * (two results, or a result and another matrix, that start at the same
+ * address are refused).
  * Elements between the rows of a strided dst are left as they are.
  * A matrix of zeros gives zeros (eps > 0); one that holds an infinity or a
  * NaN gives NaN throughout, and no other matrix of the batch is touched by
@@ -587,8 +589,8 @@ int64_t zf_orthogonalize_bytes(const zf_matrix* mats, int64_t count, int32_t dst
  * workspace: device memory of workspace_size >= zf_orthogonalize_bytes,
  * 16-byte aligned; calls that may overlap in time (two streams, two graphs)
  * need workspaces of their own.
- * Errors: ZF_EINVAL (NULL, count < 0, a side < 1, a stride < cols, params
- * out of range), ZF_EALIGN, ZF_EDTYPE, ZF_ESIZE (workspace too small, a side
+ * Errors: ZF_EINVAL (NULL, count < 0, a side < 1, a stride < cols, a dst
+ * that is another matrix's src or dst, params out of range), ZF_EALIGN, ZF_EDTYPE, ZF_ESIZE (workspace too small, a side
  * above 2^20, more than ZF_ORTHO_MAX_MATRICES matrices), ZF_ENOMEM,
  * ZF_EHIP. */
 int zf_orthogonalize(const zf_matrix* mats, int64_t count, int32_t src_dtype, int32_t dst_dtype,
@@ -642,8 +644,9 @@ typedef struct {
  * and the 16-bit parameters RNE16(W).  args: as zf_shard_step; exp_avg holds
  * M for the matrices' elements, exp_avg_sq is not touched there; grad_shards
  * as zf_shard_step (NULL: the sums go through the workspace); workspace_size
- * must be >= zf_muon_workspace_bytes(muon, &mhp->ns).  phase_events: before pass 1, after pass 1, after the norm
- * reduction and finish, after the updates.  The state block is
+ * must be >= zf_muon_workspace_bytes(muon, &mhp->ns).  phase_events: before
+ * pass 1, after pass 1, after the norm reduction and finish, after the
+ * updates.  The state block is
  * zf_shard_step's: t counts applied steps of both.  Errors: as
  * zf_shard_step, plus ZF_EINVAL (mhp out of range) and ZF_ENOMEM. */
 int zf_muon_step(const zf_muon* muon, const zf_hparams* hp, const zf_muon_hparams* mhp,

@@ -127,13 +127,39 @@ def test_batch_of_many_shapes_with_strides(zf):
         assert (o[:, c:] == 3.0).all() and (w[:, c:] == 7.0).all()
 
 
-def test_same_bits_alone_and_in_a_batch(zf):
+def test_the_same_call_gives_the_same_bits(zf):
     shapes = [(100, 200), (512, 256), (33, 33)]
     xs = [matrix(r, c, torch.float32, i) for i, (r, c) in enumerate(shapes)]
     together = run(zf, xs, [torch.empty_like(x, dtype=torch.bfloat16) for x in xs])
     again = run(zf, xs, [torch.empty_like(x, dtype=torch.bfloat16) for x in xs])
     for a, b in zip(together, again):
         assert torch.equal(G.bits_view(a), G.bits_view(b))
+
+
+def test_more_matrices_than_a_launch_takes_as_arguments(zf):
+    """70 matrices for the products and 20 held in shared memory, mixed: the
+    tables of both, and the search through more first blocks than travel."""
+    shapes = [(130 + i, 200 - i) for i in range(70)]
+    for i in range(20):
+        shapes.insert(4 * i, (5 + i, 90 - 3 * i))
+    xs = [matrix(r, c, torch.float32, i) for i, (r, c) in enumerate(shapes)]
+    ys = run(zf, xs, [torch.empty_like(x, dtype=torch.bfloat16) for x in xs])
+    for x, y in zip(xs, ys):
+        assert off(y, plain(x)) <= limit(1, torch.bfloat16), tuple(x.shape)
+
+
+def test_longest_side_and_more_than_one_group(zf):
+    """Five of 2^26 padded elements: the workspace holds four at a time.  (The
+    sums have 2^20 terms: 2^-25 sqrt(2^20) = 3e-5, within the one product's
+    tolerance.)"""
+    shapes = [(60, 1 << 20), (1 << 20, 60), (33, (1 << 20) - 5), (7, 1 << 20), (64, 1 << 20)]
+    xs = [matrix(r, c, torch.bfloat16, i) for i, (r, c) in enumerate(shapes)]
+    one = zf.orthogonalize_bytes(zf.ortho_batch(xs[:4], [torch.empty_like(x) for x in xs[:4]]))
+    b = zf.ortho_batch(xs, [torch.empty_like(x) for x in xs])
+    assert zf.orthogonalize_bytes(b) < 1.01 * one
+    ys = run(zf, xs, b.tensors[5:])
+    for x, y in zip(xs, ys):
+        assert off(y, plain(x)) <= limit(1, torch.bfloat16), tuple(x.shape)
 
 
 def test_in_place(zf):

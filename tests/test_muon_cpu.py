@@ -55,6 +55,38 @@ def test_bad_batches(zf, kw, want):
     assert status(zf, call, zf, batch(zf, [(8, 8)], **kw)) == want
 
 
+@pytest.mark.parametrize("places,want", [
+    ([(1, 2), (3, 2)], "ZF_EINVAL"),   # two results in one place
+    ([(1, 2), (1, 4)], "ZF_ESIZE"),    # one matrix twice: fine
+    ([(1, 1), (2, 2)], "ZF_ESIZE"),    # each in place: fine
+    ([(1, 2), (2, 3)], "ZF_EINVAL"),   # a result where another matrix lies
+    ([(1, 1), (1, 1)], "ZF_EINVAL"), ([(1, 1), (1, 2)], "ZF_EINVAL")])
+def test_results_in_other_matrices_places(zf, places, want):
+    b = batch(zf, [(8, 8)] * 2)
+    for m, (src, dst) in zip(b.mats, places):
+        m.src, m.dst = src * BASE, dst * BASE
+    # those that pass are refused for their workspace, the last check
+    assert status(zf, call, zf, b, None, 9 * BASE, 0) == want
+
+
+def test_buffers_elsewhere(zf, monkeypatch):
+    import torch
+    b = batch(zf, [(8, 8)])
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    for where in ("cpu", "cuda:1"):
+        b.device = torch.device(where)
+        with pytest.raises(ValueError, match="current GPU"):
+            call(zf, b)
+    b.device = torch.device("cuda:0")
+    assert status(zf, call, zf, b, None, 3 * BASE, 0) == "ZF_ESIZE"
+    with pytest.raises(ValueError, match="current GPU"):
+        call(zf, b, ws=torch.zeros(16))
+    with pytest.raises(ValueError, match="on a GPU"):
+        zf.ortho_batch([torch.zeros(4, 6)], [torch.zeros(4, 6)])
+    with pytest.raises(ValueError, match="current GPU"):
+        step(zf, master=torch.zeros(1 << 18))
+
+
 def test_strides_of_single_rows_are_ignored(zf):
     # refused for its workspace, the last check: the stride has passed
     b = batch(zf, [(1, 8)], src_stride=1, dst_stride=1)
