@@ -58,7 +58,11 @@ typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 constexpr float kScale = 1024.0f, kUnscale = 1.0f / 1024.0f;
 constexpr float kLo = 2048.0f;              // lo halves: 2^11 more
 
-__device__ __forceinline__ f16 rest_of(float x, f16 hi) { return (f16)((x - (float)hi) * kLo); }
+// (x - hi) kLo; the difference is exact either way, and this way takes two
+// instructions
+__device__ __forceinline__ f16 rest_of(float x, f16 hi) {
+  return (f16)__builtin_fmaf((float)hi, -kLo, x * kLo);
+}
 __device__ __forceinline__ float join(f16 hi, f16 lo) {
   return __builtin_fmaf((float)lo, 1.0f / kLo, (float)hi);
 }
@@ -778,6 +782,16 @@ __device__ __forceinline__ float combine(float sum, float o0, float o1, float d0
   }
 }
 
+// x, without its element r if this piece is the one on the diagonal.
+__device__ __forceinline__ f16x8 off_diagonal(f16x8 x, bool on, int r) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  u32x4 w = __builtin_bit_cast(u32x4, x);
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (on && r >> 1 == k) w[k] &= r & 1 ? 0xFFFFu : 0xFFFF0000u;
+  return __builtin_bit_cast(f16x8, w);
+}
+
 // Three products instead of one: hi lo + lo hi, scaled down, + hi hi.
 template <typename T, bool XQ, int PRODUCTS, typename F>
 __device__ __forceinline__ void products(F operands, f16* shared,
@@ -870,6 +884,15 @@ __global__ __launch_bounds__(T::kThreads, 2) void zf_ns_sym(GemmArgs a) {
         *(ZF_LDS f32x4*)(square + (rj + fj * 16 + l) * 256 +
                          ((ri / 4 + f * 4 + g) ^ (l & 7)) * 16) = acc[q * 4 + f][fj];
     square_ready<T>();
+    if (si == sj && in && lane / (E * 8) == e0 / E) {  // the diagonal, before its place is reused
+      const float sum = *(const ZF_LDS float*)(square + lane * 256 +
+                                               ((lane >> 2) ^ (lane & 7)) * 16 + (lane & 3) * 4);
+      float v = sum * kUnscale;
+      if constexpr (MODE != kGram)
+        v = combine<MODE == kPoly>(sum, 0.0f, 0.0f, d0[si + lane], d1[si + lane], true, a.ca, a.cb,
+                                   a.cc);
+      diag[si + lane] = v * kUnscale;
+    }
     f16x8 low[E];
     constexpr int kBatch = E < 4 ? E : 4;  // lines whose loads are on their way together
 #pragma unroll
@@ -892,35 +915,35 @@ __global__ __launch_bounds__(T::kThreads, 2) void zf_ns_sym(GemmArgs a) {
       for (int e = 0; e < kBatch; ++e) {
         const int j = (e0 + eb + e) * 8 + row;  // in the square
         ZF_LDS char* line = square + j * 256;
-        float v[8];
+        float v[8], sum[8];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const f32x4 sum = *(const ZF_LDS f32x4*)(line + ((2 * c + t) ^ row) * 16);
+          const f32x4 x = *(const ZF_LDS f32x4*)(line + ((2 * c + t) ^ row) * 16);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) v[t * 4 + r] = sum[r];
+          for (int r = 0; r < 4; ++r) sum[t * 4 + r] = x[r];
         }
-        f16x8 hi;
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
-          const float sum = v[r];
           if constexpr (MODE == kGram) {
-            v[r] = sum * kUnscale;
+            v[r] = sum[r] * kUnscale;
           } else {
             const float a0 = PRODUCTS == 3 ? join(x0[e][r], y0[e][r]) : (float)x0[e][r];
             float a1 = a0;
             if constexpr (MODE == kMul)
               a1 = PRODUCTS == 3 ? join(x1[e][r], y1[e][r]) : (float)x1[e][r];
-            v[r] = combine<MODE == kPoly>(sum, a0, a1, di[r], dj[eb + e], false, a.ca, a.cb, a.cc);
+            v[r] = combine<MODE == kPoly>(sum[r], a0, a1, di[r], dj[eb + e], false, a.ca, a.cb, a.cc);
           }
-          if (si == sj && c * 8 + r == j) {  // the diagonal
-            if constexpr (MODE != kGram)
-              v[r] = combine<MODE == kPoly>(sum, 0.0f, 0.0f, di[r], dj[eb + e], true, a.ca, a.cb,
-                                            a.cc);
-            diag[sj + j] = v[r] * kUnscale;
-            v[r] = 0.0f;
-          }
+        }
+        f16x8 hi;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
           hi[r] = (f16)v[r];
           if constexpr (PRODUCTS == 3) low[eb + e][r] = rest_of(v[r], hi[r]);
+        }
+        if (si == sj) {
+          hi = off_diagonal(hi, c == e0 + eb + e, row);
+          if constexpr (PRODUCTS == 3)
+            low[eb + e] = off_diagonal(low[eb + e], c == e0 + eb + e, row);
         }
         const int64_t p = p0 + (int64_t)(eb + e) * 8 * m.lds;
         *reinterpret_cast<f16x8*>(out + p) = hi;
