@@ -67,6 +67,35 @@ __device__ __forceinline__ float join(f16 hi, f16 lo) {
   return __builtin_fmaf((float)lo, 1.0f / kLo, (float)hi);
 }
 
+// What the rounding of X left, 8 elements from p on: in 16 bits where the
+// products use it, else (X then has 14 bits, for its linear term) the upper
+// byte of that, a sign, 5 exponent and 2 more bits: an application's traffic
+// is 6 bytes an element instead of 8.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+template <bool BYTES>
+__device__ __forceinline__ f16x8 load_rest(const char* rests, int64_t p) {
+  if constexpr (BYTES) {
+    const u32x2 w = *reinterpret_cast<const u32x2*>(rests + p);
+    return __builtin_bit_cast(f16x8, (u32x4){__builtin_amdgcn_perm(w.x, w.x, 0x010C000Cu),
+                                             __builtin_amdgcn_perm(w.x, w.x, 0x030C020Cu),
+                                             __builtin_amdgcn_perm(w.y, w.y, 0x010C000Cu),
+                                             __builtin_amdgcn_perm(w.y, w.y, 0x030C020Cu)});
+  } else {
+    return *reinterpret_cast<const f16x8*>(rests + p * 2);
+  }
+}
+__device__ __forceinline__ u32x2 upper_bytes(f16x8 x) {
+  typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+  const u32x4 w = __builtin_bit_cast(u32x4, __builtin_bit_cast(u16x8, x) + (uint16_t)0x80);
+  return (u32x2){__builtin_amdgcn_perm(w.y, w.x, 0x07050301u),
+                 __builtin_amdgcn_perm(w.w, w.z, 0x07050301u)};
+}
+template <bool BYTES>
+__device__ __forceinline__ void store_rest(char* rests, int64_t p, f16x8 x) {
+  if constexpr (BYTES) *reinterpret_cast<u32x2*>(rests + p) = upper_bytes(x);
+  else *reinterpret_cast<f16x8*>(rests + p * 2) = x;
+}
+
 // ---------------------------------------------------------------------------
 // The table of matrices travels by value, a chunk a launch, into the
 // workspace, so that a captured call carries it.
@@ -96,6 +125,7 @@ struct Common {
   const Mat* table;       // the group's matrices
   int32_t count;
   int32_t load_tiles, own_norm;
+  int32_t bytes;          // X's remainders are bytes (one product)
   const DevState* st;     // the Muon step's skip flag, or NULL
   double* inv;            // 1 / (|G|_F + eps), by slot
   double* partials;       // squared-norm partials
@@ -224,7 +254,6 @@ __device__ __forceinline__ void load8(const LoadArgs& a, const Mat& m, float gs,
   } else {
     const uint16_t* x = static_cast<const uint16_t*>(m.src) + p;
     if (wide && n >= 8) {
-      typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
       const u32x4 y = *reinterpret_cast<const u32x4*>(x);
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[2 * e] = lo16<SRC>(y[e]), v[2 * e + 1] = hi16<SRC>(y[e]);
@@ -319,7 +348,7 @@ __global__ __launch_bounds__(kThreads) void zf_ns_prep(LoadArgs a) {
   else inv *= a.c.inv[m.slot];
   const bool wide = wide_loads<SRC>(m);
   f16* hp = at<f16>(a.c, m.h[0]);
-  f16* lp = at<f16>(a.c, m.l[0]);
+  char* lp = at<char>(a.c, m.l[0]);
   // 8 values at (i, j) in whole lines that this kernel does not read back
   auto put = [&](int64_t i, int j, const float (&v)[8]) {
     f16x8 hi, lo;
@@ -331,7 +360,10 @@ __global__ __launch_bounds__(kThreads) void zf_ns_prep(LoadArgs a) {
     }
     const int64_t p = i * m.ldx + j;
     __builtin_nontemporal_store(hi, reinterpret_cast<f16x8*>(hp + p));
-    __builtin_nontemporal_store(lo, reinterpret_cast<f16x8*>(lp + p));
+    if (a.c.bytes)
+      __builtin_nontemporal_store(upper_bytes(lo), reinterpret_cast<u32x2*>(lp + p));
+    else
+      __builtin_nontemporal_store(lo, reinterpret_cast<f16x8*>(lp + p * 2));
   };
   if (!m.tall) {
     Walk w((int64_t)block * a.c.load_tiles * 4096, m.np);
@@ -784,7 +816,6 @@ __device__ __forceinline__ float combine(float sum, float o0, float o1, float d0
 
 // x, without its element r if this piece is the one on the diagonal.
 __device__ __forceinline__ f16x8 off_diagonal(f16x8 x, bool on, int r) {
-  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
   u32x4 w = __builtin_bit_cast(u32x4, x);
 #pragma unroll
   for (int k = 0; k < 4; ++k)
@@ -1062,9 +1093,9 @@ __global__ __launch_bounds__(T::kThreads, 2) void zf_ns_apply(GemmArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wi = i0 + wave / T::kWavesJ * T::TI, wj = j0 + wave % T::kWavesJ * T::TJ;
   const f16* h = at<f16>(a.c, m.h[a.turn]);
-  const f16* lo = at<f16>(a.c, m.l[a.turn]);
+  const char* lo = at<char>(a.c, m.l[a.turn]);
   f16* h1 = at<f16>(a.c, m.h[a.turn ^ 1]);
-  f16* lo1 = at<f16>(a.c, m.l[a.turn ^ 1]);
+  char* lo1 = at<char>(a.c, m.l[a.turn ^ 1]);
   const float* d = at<float>(a.c, m.d[a.in0]);
   constexpr int E = 8 / T::kSquareWaves;  // lines of 8 rows a wave takes
   const int e0 = T::share_of(wi - i0, wj - j0) * E;
@@ -1085,7 +1116,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void zf_ns_apply(GemmArgs a) {
     for (int e = 0; e < E; ++e) {
       if (!in) break;
       x[e] = *reinterpret_cast<const f16x8*>(h + p0 + (int64_t)e * 8 * m.ldx);
-      y[e] = *reinterpret_cast<const f16x8*>(lo + p0 + (int64_t)e * 8 * m.ldx);
+      y[e] = load_rest<PRODUCTS == 1>(lo, p0 + (int64_t)e * 8 * m.ldx);
       di[e] = d[si + (e0 + e) * 8 + row];
     }
 #pragma unroll
@@ -1116,7 +1147,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void zf_ns_apply(GemmArgs a) {
       }
       if constexpr (!LAST) {
         *reinterpret_cast<f16x8*>(h1 + p0 + (int64_t)e * 8 * m.ldx) = hi;
-        *reinterpret_cast<f16x8*>(lo1 + p0 + (int64_t)e * 8 * m.ldx) = rest;
+        store_rest<PRODUCTS == 1>(lo1, p0 + (int64_t)e * 8 * m.ldx, rest);
       }
     }
     square_ready<T>();
@@ -1710,10 +1741,10 @@ bool zf::ns::layout(const Shape* shapes, int64_t count, int products, Layout& ou
     const int64_t mn = (int64_t)m.mp * m.ldx, mm = (int64_t)m.mp * m.lds;
     if (g.count > 0 && elements + mn > kGroupElements) close();
     // what the rounding left of X: an operand of the products if there are
-    // three, else used by its own tile alone, in place
+    // three, else bytes used by their own tile alone, in place
     for (int z = 0; z < 2; ++z) {
       m.h[z] = take(mn * 2);
-      m.l[z] = z == 0 || products == 3 ? take(mn * 2) : m.l[0];
+      m.l[z] = z == 0 || products == 3 ? take(mn * (products == 3 ? 2 : 1)) : m.l[0];
     }
     for (int z = 0; z < 3; ++z) {
       m.s[z] = take(mm * 2);
@@ -1793,6 +1824,7 @@ int zf::ns::enqueue(const Layout& l, const zf_ns_params& p, int products, int sm
     c.count = g.count;
     c.load_tiles = g.load_tiles;
     c.own_norm = g.own_norm;
+    c.bytes = products == 1;
     c.st = io ? io->st : nullptr;
     c.inv = reinterpret_cast<double*>(ws + l.inv);
     c.partials = reinterpret_cast<double*>(ws + l.partials);
