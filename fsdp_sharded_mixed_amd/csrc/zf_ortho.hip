@@ -1201,13 +1201,17 @@ void launch_last(const Group& g, int size, hipStream_t s, int32_t dst, bool muon
   }
 }
 
+constexpr int kCus = 256;
+
 // The iteration of one group.  Steps run on X, or in pairs on the m x m side
 // (X_2 = Q_2 Q_1 X with A_2 = Q_1 A Q_1), which touches the long side once
 // for two steps and costs no more products when n = m: 20 m^3 + 9 m^2 (n-m)
 // instead of 20 m^3 + 15 m^2 (n-m) for five.  Pairs and single steps take
 // turns (2, 1, 2): longer stretches lose the small singular values, whose
 // squares vanish in A's rounding (error 1.3e-3 at most for 2, 1, 2; 3e-3 for
-// 3, 2; 0.2 for all five).
+// 3, 2; 0.2 for all five).  Where one round of blocks holds all of X, every
+// launch takes its latency, and single steps need two launches fewer for five
+// (1024 x 1024: 162 -> 150 us).
 template <int PRODUCTS>
 int iterate(const Group& g, const Mat* mats, const zf_ns_params& p, int sym, int app, int32_t dst,
             bool muon, hipStream_t s, GemmArgs a) {
@@ -1217,7 +1221,7 @@ int iterate(const Group& g, const Mat* mats, const zf_ns_params& p, int sym, int
   const auto tri = [](const Mat& m, int size) { return m.tri0[size]; };
   const auto along = [](const Mat& m, int size) { return m.app0[size]; };
   a.turn = 0;
-  bool pair = p.steps > 1;
+  bool pair = g.app_blocks[kLittle] > kCus;
   for (int k = 0; k < p.steps;) {
     const int n = pair && k + 2 <= p.steps ? 2 : 1;
     pair = !pair;
@@ -1261,7 +1265,7 @@ int iterate(const Group& g, const Mat* mats, const zf_ns_params& p, int sym, int
 // 37 and 14 us at 2048 x 2048, 44, 26 and 9.6 at 1024 x 1024; one that is
 // nearly empty about half of that.
 int tile_size(const int32_t (&n)[3]) {
-  const int slots[3] = {256, 512, 512};
+  const int slots[3] = {kCus, 2 * kCus, 2 * kCus};
   const double round[3] = {1.76, 1.0, 0.375};
   double least = 0.0;
   int best = kBig;
