@@ -45,6 +45,7 @@ struct Mat {
 struct Group {
   int32_t first, count;
   int32_t load_tiles;     // 64 x 64 tiles a block of the load takes
+  int32_t pairs;          // steps in pairs on the short side
   int32_t own_norm;       // few enough partials for every block to sum them
   int32_t load_blocks, tri_blocks[3], app_blocks[3];
 };

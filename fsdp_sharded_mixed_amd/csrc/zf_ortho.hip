@@ -20,8 +20,8 @@
 //     there is 1e-3), so a product of two such matrices S = diag(D) + O is
 //     O O + (D_i + D_j) O_ij + D_i^2 on the diagonal.
 // Measured in |.|_F against 64 bits over flat, low-rank-plus-noise and 1/i
-// spectra: 3e-4 to 9e-4 (all three parts in fp16: 3e-4 to 4e-3; bf16
-// throughout: 1e-2 to 3e-2).  A result in more bits than bf16 gets three
+// spectra: 2e-4 to 9e-4, step by step (all three parts in fp16: 3e-4 to 4e-3;
+// bf16 throughout: 1e-2 to 3e-2).  A result in more bits than bf16 gets three
 // products instead of one: every operand is the sum of two fp16 numbers,
 // hi + lo * 2^-11, and hi hi + hi lo + lo hi holds about 22 bits.
 #include "zf_ortho.h"
@@ -434,7 +434,7 @@ void launch_prep(int32_t src, bool own_norm, dim3 grid, hipStream_t s, const Loa
 // 32 bytes a cycle of a CU from the second-level cache at their full rate
 // (128 x 128: 64), and its 8 waves of 128 x 64 read 48 KiB of shared memory
 // per 1024 cycles.  Loads go from global to shared memory directly (no
-// registers), into two buffers of 64 KiB in turn; a step's barrier stands
+// registers), into two buffers in turn (of 64 KiB for 256 x 256); a step's barrier stands
 // between its two halves, so that the fragments of the next half are read
 // while the matrix cores work on this one, and a buffer's loads are on their
 // way for a whole step.  The 16-byte pieces of a row lie permuted by the row
@@ -774,6 +774,7 @@ __device__ __forceinline__ void tri_tile(int b, int rows, int& ti, int& tj) {
   }
 }
 
+constexpr int kCus = 256;
 constexpr int kBig = 0, kMiddle = 1, kLittle = 2;  // places of the tile sizes in the tables
 typedef Tile<256, 256, 2, 4, 2> Big;
 typedef Tile<128, 128, 2, 2, 2> Middle;
@@ -1201,17 +1202,15 @@ void launch_last(const Group& g, int size, hipStream_t s, int32_t dst, bool muon
   }
 }
 
-constexpr int kCus = 256;
-
 // The iteration of one group.  Steps run on X, or in pairs on the m x m side
 // (X_2 = Q_2 Q_1 X with A_2 = Q_1 A Q_1), which touches the long side once
 // for two steps and costs no more products when n = m: 20 m^3 + 9 m^2 (n-m)
 // instead of 20 m^3 + 15 m^2 (n-m) for five.  Pairs and single steps take
 // turns (2, 1, 2): longer stretches lose the small singular values, whose
-// squares vanish in A's rounding (error 1.3e-3 at most for 2, 1, 2; 3e-3 for
-// 3, 2; 0.2 for all five).  Where one round of blocks holds all of X, every
-// launch takes its latency, and single steps need two launches fewer for five
-// (1024 x 1024: 162 -> 150 us).
+// squares vanish in A's rounding.  Errors measured: under 1.1e-3, but 3.1e-3
+// with a few strong directions in a short side of 11; single steps 8e-4 at
+// most, 1, 2, 2 5.5e-3, all five together 0.2.  A group takes single steps
+// where pairs gain little (Group::pairs).
 template <int PRODUCTS>
 int iterate(const Group& g, const Mat* mats, const zf_ns_params& p, int sym, int app, int32_t dst,
             bool muon, hipStream_t s, GemmArgs a) {
@@ -1221,10 +1220,10 @@ int iterate(const Group& g, const Mat* mats, const zf_ns_params& p, int sym, int
   const auto tri = [](const Mat& m, int size) { return m.tri0[size]; };
   const auto along = [](const Mat& m, int size) { return m.app0[size]; };
   a.turn = 0;
-  bool pair = g.app_blocks[kLittle] > kCus;
+  bool pair = g.pairs;
   for (int k = 0; k < p.steps;) {
     const int n = pair && k + 2 <= p.steps ? 2 : 1;
-    pair = !pair;
+    pair = g.pairs && n == 1;
     a.ca = (float)p.a;
     a.cb = (float)p.b;
     a.cc = (float)p.c;
@@ -1682,6 +1681,7 @@ bool zf::ns::layout(const Shape* shapes, int64_t count, int products, Layout& ou
   int64_t partials = 0, region = 0, used = 0, elements = 0;
   Group g{};
   int64_t load = 0, tri[3] = {}, app[3] = {};
+  double cubes = 0.0, longer = 0.0;  // sums of m^3 and of m^2 (n - m)
   auto close = [&]() {
     // tiles a block takes: one while that leaves CUs without a block
     g.load_tiles = load >= 4096 ? kLoadTiles : 1;
@@ -1703,6 +1703,12 @@ bool zf::ns::layout(const Shape* shapes, int64_t count, int products, Layout& ou
       g.app_blocks[z] = (int32_t)app[z];
       tri[z] = app[z] = 0;
     }
+    // Pairs of steps save 6 of 20 m^3 + 15 m^2 (n - m) and are less exact: not
+    // for less than a twentieth of it.  Nor where one round of blocks holds
+    // all of X: there every launch takes its latency, and single steps need
+    // two launches fewer for five (1024 x 1024: 162 -> 138 us).
+    g.pairs = g.app_blocks[kLittle] > kCus && 6.0 * longer > 0.05 * (20.0 * cubes + 15.0 * longer);
+    cubes = longer = 0.0;
     out.groups.push_back(g);
     region = std::max(region, used);
     const int32_t next = g.first + g.count;
@@ -1767,6 +1773,9 @@ bool zf::ns::layout(const Shape* shapes, int64_t count, int products, Layout& ou
       app[z] += tm * tn;
     }
     if (load > 0x7FFFFFFF) return false;
+    const double mm2 = (double)m.mp * m.mp;
+    cubes += mm2 * m.mp;
+    longer += mm2 * (m.np - m.mp);
     elements += mn;
     ++g.count;
   }

@@ -116,6 +116,28 @@ def test_spectra(zf, kind, rows, cols, products):
     assert err <= limit(products, torch.float32)
 
 
+@pytest.mark.parametrize("rows,cols", [(11, 2000), (64, 1400), (100, 1500), (1500, 100),
+                                       (128, 8192), (300, 300), (2048, 2048)])
+@pytest.mark.parametrize("count", [1, 24])
+def test_few_strong_directions_over_noise(zf, rows, cols, count):
+    """One matrix (single steps) and a batch of more than a round of blocks
+    (steps in pairs where the matrices are long): singular values 30 apart,
+    whose squares are what the products hold."""
+    if rows * cols * count > 1 << 26:
+        count = 4
+    xs = []
+    for seed in range(count):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        r = min(8, rows, cols)
+        strong = (torch.randn(rows, r, generator=g, device="cuda")
+                  @ torch.randn(r, cols, generator=g, device="cuda"))
+        xs.append(torch.randn(rows, cols, generator=g, device="cuda") + strong * (2 / math.sqrt(r)))
+    ys = run(zf, xs, [torch.empty_like(x) for x in xs], zf.ns_params(products=1))
+    worst = max(off(y, plain(x)) for x, y in zip(xs, ys))
+    G.say(f"{count} of {rows}x{cols}: {worst:.2e}")
+    assert worst <= limit(1, torch.float32)
+
+
 def test_batch_of_many_shapes_with_strides(zf):
     shapes = [(1, 77), (65, 1), (257, 300), (300, 257), (64, 64), (130, 1030), (999, 101)] * 4
     wide = [matrix(r, c, torch.float16, i, gap=3) for i, (r, c) in enumerate(shapes)]
