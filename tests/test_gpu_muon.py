@@ -366,8 +366,15 @@ MLP_MUON = [0, 2, 4, 6, 8]
 WIDE = [(50 * 96, 0, 0, 50), (96 * 96, 1, 0, 96), (300 * 96, 1, 0, 300), (96 * 300, 1, 0, 96),
         (96, 1, 2, 0), (3, 1, 2, 0), (257 * 511, 2, 0, 257), (50 * 96, 2, 0, 50)]
 WIDE_MUON = [6, 1, 2, 3]
+# weights whose rows keep 16-byte alignment, of both orientations, and the same behind a vector of 3
+EVEN = [(200 * 260, 0, 0, 200), (333 * 148, 0, 0, 333), (130 * 1028, 0, 0, 130),
+        (3, 0, 2, 0), (200 * 260, 0, 0, 200), (333 * 148, 0, 0, 333)]
+EVEN_MUON = [0, 1, 2, 4, 5]
 
 STEPS = [
+    (EVEN, EVEN_MUON, 2, W.GLOBAL_FLAT, "bf16", "bf16", 1.0, True, "rms", False),
+    (EVEN, EVEN_MUON, 4, W.PER_UNIT, "f16", "f16", 64.0, False, "rows", False),
+    (EVEN, EVEN_MUON, 2, W.PER_PARAM_DIM0, "bf16", None, 1.0, True, "rms", False),
     (MLP, MLP_MUON, 4, W.PER_UNIT, "f16", "f16", 1024.0, True, "rms", False),
     (MLP, MLP_MUON, 1, W.GLOBAL_FLAT, "bf16", "bf16", 1.0, False, "rows", False),
     (MLP, MLP_MUON, 7, W.PER_PARAM_DIM0, "bf16", None, 1.0, True, "rows", False),
