@@ -1339,7 +1339,8 @@ int tile_size(const int32_t (&n)[3]) {
 // CJ tiles of 16 x 16 of X (2 x 4 of S, both triangles: cheaper than
 // mirroring one), so that a fragment read from shared memory serves several
 // tiles; tiles past the last one are computed again (no branches) and not
-// stored.  Bound by shared memory's latency and the barriers.
+// stored, and waves without a tile only wait.  Bound by the instructions
+// around the products, two waves of 4 cycles each on a SIMD, and the barriers.
 constexpr int kSmallPad = 32;              // sides padded to this
 constexpr int kSmallThreads = 512, kSmallWaves = 8;
 constexpr int kSmallShared = 147456;       // bytes of X and S
@@ -1500,6 +1501,7 @@ __global__ __launch_bounds__(kSmallThreads) void zf_ns_small(SmallArgs a) {
 
   // S = P P^T for P of `len` columns and row stride ld; finish(i, j, diagonal
   // tile, sums) turns the sums (times 2^20) of (i .. i + 3, j) into values
+  const bool holds_s = i0 < tm && js < tm, holds_x = i0 < tm && jx < tn;
   auto symmetric = [&](const f16* ph, const f16* pl, int ld, int len, auto finish) {
     f32x4 acc[2][4], low[2][4];
     int pi[2], pj[4];
@@ -1511,7 +1513,7 @@ __global__ __launch_bounds__(kSmallThreads) void zf_ns_small(SmallArgs a) {
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = low[i][j] = (f32x4){0, 0, 0, 0};
-    for (int k = 0; k < len; k += 32) {
+    for (int k = holds_s ? 0 : len; k < len; k += 32) {
       f16x8 x[2], y[4], xr[2], yr[4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -1576,13 +1578,17 @@ __global__ __launch_bounds__(kSmallThreads) void zf_ns_small(SmallArgs a) {
       const f16x4 h = *reinterpret_cast<const f16x4*>(sh + j * ls + i);
       f16x4 w = h;
       if constexpr (PRODUCTS == 3) w = *reinterpret_cast<const f16x4*>(sl + j * ls + i);
+      float sum[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const float e = PRODUCTS == 3 ? join(h[r], w[r]) : (float)h[r];
-        const float sum2 = v[r];
-        v[r] = combine<true>(sum2, e, e, di[r], dj, false, a.ca, a.cb, a.cc);
-        if (diagonal && i + r == j)
-          v[r] = combine<true>(sum2, e, e, di[r], dj, true, a.ca, a.cb, a.cc);
+        sum[r] = v[r];
+        v[r] = combine<true>(sum[r], e, e, di[r], dj, false, a.ca, a.cb, a.cc);
+      }
+      if (diagonal) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (i + r == j) v[r] = combine<true>(sum[r], 0.0f, 0.0f, di[r], dj, true, a.ca, a.cb, a.cc);
       }
     });
     const bool last = step + 1 == a.steps;
@@ -1602,7 +1608,7 @@ __global__ __launch_bounds__(kSmallThreads) void zf_ns_small(SmallArgs a) {
       const s16x4 h1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ZF_LDS s16x4*)(x + 4 * lx));
       return __builtin_bit_cast(f16x8, __builtin_shufflevector(h0, h1, 0, 1, 2, 3, 4, 5, 6, 7));
     };
-    for (int k = 0; k < mp; k += 32) {
+    for (int k = holds_x ? 0 : mp; k < mp; k += 32) {
       f16x8 x[CJ], xr[CJ], y[2], yr[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -1627,6 +1633,7 @@ __global__ __launch_bounds__(kSmallThreads) void zf_ns_small(SmallArgs a) {
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+      if (!holds_x) break;
       const int ii = min(i0 + i, tm - 1) * 16 + l;
       const float di = diag[ii];
 #pragma unroll
