@@ -47,7 +47,8 @@ using zf::kThreads;
 // AdamW over ranges [lo, hi) of the flat arrays, from fp32 sums: a block
 // takes 256 quads from a range's first aligned quad on, a thread
 // one quad; a quad that the range covers in part goes element by element.
-// A stream like zf_pass2, for the few parameters Muon leaves.
+// A stream like zf_pass2, for the few parameters Muon leaves: 168M of them
+// take 898 us, 30 bytes each, 5.6 TB/s.
 constexpr int kRangeMax = 64;
 struct RangeArgs {
   const float* sums;
