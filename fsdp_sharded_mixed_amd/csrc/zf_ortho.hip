@@ -124,7 +124,7 @@ struct Common {
   char* ws;
   const Mat* table;       // the group's matrices
   int32_t count;
-  int32_t load_tiles, own_norm;
+  int32_t load_tiles;
   int32_t bytes;          // X's remainders are bytes (one product)
   const DevState* st;     // the Muon step's skip flag, or NULL
   double* inv;            // 1 / (|G|_F + eps), by slot
@@ -1908,7 +1908,6 @@ int zf::ns::enqueue(const Layout& l, const zf_ns_params& p, int products, int sm
     c.table = table + g.first;
     c.count = g.count;
     c.load_tiles = g.load_tiles;
-    c.own_norm = g.own_norm;
     c.bytes = products == 1;
     c.st = io ? io->st : nullptr;
     c.inv = reinterpret_cast<double*>(ws + l.inv);
