@@ -13,8 +13,9 @@
 // normalised m x n matrix are near 1/sqrt(m n), which nears fp16's smallest
 // normal number (2^-14) at 16K x 16K, and none passes 64 = 65536 / 2^10 for
 // coefficients that keep the singular values below that.  Three parts of the
-// iteration stay in 32 bits, because rounding them is what costs accuracy:
-//   - the linear term a X (its rounding would drown small singular values);
+// iteration keep more bits, because rounding them is what costs accuracy:
+//   - the linear term a X (its rounding would drown small singular values): X
+//     is kept with 14 bits (three products: 22), the term and the sum in 32;
 //   - the diagonal of A and of B (B's is near -2.7 once the singular values
 //     near 1, where the rest of a row is near 1/sqrt(m): half a step of fp16
 //     there is 1e-3), so a product of two such matrices S = diag(D) + O is

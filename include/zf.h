@@ -538,13 +538,13 @@ int zf_offload_step(const zf_plan* plan, const zf_hparams* hp, const zf_offload_
  * struct selects steps = 5, products = 0, a = 3.4445, b = -4.7750,
  * c = 2.0315, eps = 1e-7.
  * products: how exactly the matrix products are computed.  1: operands are
- * rounded to 11 bits (fp16 with a common power-of-two factor; sums, the
- * linear term and the diagonals of A and of its polynomial in binary32); the
- * result of the default steps is 2e-4 to 3e-3 from the exact one
- * (|error|_F / |X|_F; below 1.1e-3 but for matrices whose singular values
- * differ by orders of magnitude), where bf16's own rounding is 1.7e-3.  3: operands are
- * sums of two fp16 numbers, about 22 bits, for three times the work; the
- * result is within about 3e-6.  0: 1 for a ZF_BF16 result, else 3; in zf_muon_step 1, and 3 for matrices that fit
+ * rounded to 11 bits (fp16 with a common power-of-two factor; sums and the
+ * diagonals of A and of its polynomial are binary32, and the linear term
+ * takes X with 14 bits); the result of the default steps is 2e-4 to 3e-3
+ * from the exact one (|error|_F / |X|_F; below 1.1e-3 but for matrices whose
+ * singular values differ by orders of magnitude), where bf16's own rounding
+ * is 1.7e-3.  3: operands are sums of two fp16 numbers, about 22 bits, for
+ * three times the work; the result is within about 3e-6.  0: 1 for a ZF_BF16 result, else 3; in zf_muon_step 1, and 3 for matrices that fit
  * in a compute unit's shared memory (up to 128 x 128), where they cost
  * little.
  * The operands' range bounds the coefficients: singular values, and the
