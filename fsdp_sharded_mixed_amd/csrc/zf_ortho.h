@@ -55,6 +55,10 @@ struct Layout {
   std::vector<Group> groups;
   int32_t small_first = 0, small_count = 0;  // matrices held in shared memory,
   int32_t small_tiles = 0;                   // and the most tiles of a wave
+  // the others' X lie in one round of blocks, where every launch is mostly
+  // latency, and their shortest side
+  bool one_round = true;
+  int32_t shortest = INT32_MAX;
   int64_t table = 0, inv = 0, partials = 0;  // byte offsets
   int64_t bytes = 0;
 };

@@ -1751,6 +1751,8 @@ int zf::ns::products_of(const zf_ns_params& p, int32_t dst_dtype) {
 bool zf::ns::layout(const Shape* shapes, int64_t count, int products, Layout& out) {
   out.mats.resize((size_t)count);
   out.groups.clear();
+  out.one_round = true;
+  out.shortest = INT32_MAX;
   int64_t partials = 0, region = 0, used = 0, elements = 0;
   Group g{};
   int64_t load = 0, tri[3] = {}, app[3] = {};
@@ -1780,6 +1782,7 @@ bool zf::ns::layout(const Shape* shapes, int64_t count, int products, Layout& ou
     // for less than a twentieth of it.  Nor where one round of blocks holds
     // all of X: there every launch takes its latency, and single steps need
     // two launches fewer for five (1024 x 1024: 162 -> 138 us).
+    if (g.app_blocks[kLittle] > kCus || !out.groups.empty()) out.one_round = false;
     g.pairs = g.app_blocks[kLittle] > kCus && 6.0 * longer > 0.05 * (20.0 * cubes + 15.0 * longer);
     cubes = longer = 0.0;
     out.groups.push_back(g);
@@ -1819,6 +1822,7 @@ bool zf::ns::layout(const Shape* shapes, int64_t count, int products, Layout& ou
       out.small_tiles = std::max(out.small_tiles, tiles_held);
       continue;
     }
+    out.shortest = std::min(out.shortest, m.m);
     m.ldx = m.np;
     m.lds = m.mp;
     const int64_t mn = (int64_t)m.mp * m.ldx, mm = (int64_t)m.mp * m.lds;

@@ -546,7 +546,8 @@ int zf_offload_step(const zf_plan* plan, const zf_hparams* hp, const zf_offload_
  * is 1.7e-3.  3: operands are sums of two fp16 numbers, about 22 bits, for
  * three times the work; the result is within about 3e-6.  0: 1 for a ZF_BF16 result, else 3; in zf_muon_step 1, and 3 for matrices that fit
  * in a compute unit's shared memory (up to 128 x 128), where they cost
- * little.
+ * little, and for all matrices of a plan if one of the others has a side of
+ * at most 32 and they are at most 256 blocks of 64 x 64 together.
  * The operands' range bounds the coefficients: singular values, and the
  * entries of A and b A + c A A, must stay below 64 (they stay below 8 for
  * the default ones). */

@@ -370,6 +370,7 @@ WIDE_MUON = [6, 1, 2, 3]
 EVEN = [(200 * 260, 0, 0, 200), (333 * 148, 0, 0, 333), (130 * 1028, 0, 0, 130),
         (3, 0, 2, 0), (200 * 260, 0, 0, 200), (333 * 148, 0, 0, 333)]
 EVEN_MUON = [0, 1, 2, 4, 5]
+THIN = [(1293 * 4, 0, 0, 1293), (1293, 0, 2, 0), (9 * 1293, 1, 0, 9), (300 * 700, 1, 0, 300)]
 
 STEPS = [
     (EVEN, EVEN_MUON, 2, W.GLOBAL_FLAT, "bf16", "bf16", 1.0, True, "rms", False),
@@ -435,6 +436,23 @@ def test_muon_step(zf, segs, muon, n, layout, gdt, pdt, scale, nesterov, rule, r
             assert (after["master"][p].double() - want).norm() <= room, (k, r, c)
             if a.params is not None:
                 assert torch.equal(after["params"][p], after["master"][p].to(a.params.dtype))
+
+
+def test_few_thin_blocks_take_three_products(zf):
+    """Less than a round of blocks, thin ones too long for shared memory among
+    them."""
+    m = Model(zf, THIN, [0, 2, 3], 2, W.GLOBAL_FLAT)
+    before = m.buffers()
+    mhp = zf.muon_hparams(0.5, momentum=0.9, weight_decay=0.0, nesterov=False,
+                          scale_rule=zf.MUON_SCALE_ROWS)
+    m.step(zf.hparams(1e-3, max_norm=0.0), mhp)
+    for at, r, c in m.places():
+        p = slice(at, at + r * c)
+        o = plain(m.momentum[p].view(r, c)).reshape(-1)
+        rate = 0.5 * math.sqrt(max(1.0, r / c))
+        want = before["master"][p].double() - rate * o
+        room = TOL[3] * rate * o.norm() + 4 * 2.0 ** -24 * (want.norm() + rate * o.norm())
+        assert (m.master[p].double() - want).norm() <= room, (r, c)
 
 
 def test_padding_stays_zero(zf):

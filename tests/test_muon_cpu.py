@@ -140,8 +140,8 @@ def test_ortho_batch_refuses(zf):
         zf.ortho_batch([x.double()], [x.double()])
 
 
-# the first matrix is too large for shared memory, the second is held there
-SEGS = [(400 * 600, 0, 0, 400), (6, 0, 0, 0), (35, 1, 0, 7), (35, 1, 0, 0)]
+# the first matrix is more than a round of blocks, the second is held in shared memory
+SEGS = [(1100 * 1300, 0, 0, 1100), (6, 0, 0, 0), (35, 1, 0, 7), (35, 1, 0, 0)]
 
 
 def plan(zf, layout=W.PER_UNIT, n=3):
@@ -165,6 +165,17 @@ def test_muon_plan_refuses(zf, segments):
 def test_muon_plan_refuses_rows_that_do_not_divide(zf):
     p = zf.plan_flat([(35, 0, 0, 6)], 2, W.GLOBAL_FLAT, 2)
     assert status(zf, zf.muon_plan, p, [0]) == "ZF_EINVAL"
+
+
+def test_few_thin_blocks_take_three_products(zf):
+    """Up to 256 blocks of 64 x 64 beside the matrices held in shared memory,
+    one of them thin."""
+    exact = zf.ns_params(products=3)
+    for rows, cols, few in ((1024, 1024, False), (32, 16384, True), (32, 16385, False),
+                            (33, 4000, False), (1293, 4, True)):
+        m = zf.muon_plan(zf.plan_flat([(rows * cols, 0, 0, rows), (35, 0, 0, 7)], 2,
+                                      W.GLOBAL_FLAT, 2), [0, 1])
+        assert (zf.muon_workspace_bytes(m) == zf.muon_workspace_bytes(m, exact)) == few
 
 
 def test_muon_plan_outlives_its_plan(zf):
