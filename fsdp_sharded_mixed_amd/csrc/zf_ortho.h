@@ -27,8 +27,8 @@ struct Mat {
   int64_t src_ld, dst_ld; // the Muon step: both = cols
   int64_t flat;           // the Muon step: offset in the padded flat arrays
   int64_t h[2], l[2];     // fp16 [mp][ldx]: X * 2^10 rounded, and what the
-                          // rounding left (one product: the upper byte of
-                          // that); two buffers in turn
+                          // rounding left; two buffers in turn (one product:
+                          // l in place)
   int64_t s[3], sl[3];    // fp16 [mp][lds]: symmetric matrices off the
                           // diagonal, rounded, and what that left
   int64_t d[3];           // fp32 [mp]: their diagonals

@@ -14,14 +14,24 @@
 // normal number (2^-14) at 16K x 16K, and none passes 64 = 65536 / 2^10 for
 // coefficients that keep the singular values below that.  Three parts of the
 // iteration keep more bits, because rounding them is what costs accuracy:
-//   - the linear term a X (its rounding would drown small singular values): X
-//     is kept with 14 bits (three products: 22), the term and the sum in 32;
+//   - the linear term a X: a singular value that starts small grows by a
+//     every step, to 485 times its size in five, and an error of X anywhere
+//     grows with it.  X is kept as two fp16 numbers, hi + lo * 2^-11, about
+//     22 bits; the products take hi, the term both, in 32 bits;
 //   - the diagonal of A and of B (B's is near -2.7 once the singular values
 //     near 1, where the rest of a row is near 1/sqrt(m): half a step of fp16
 //     there is 1e-3), so a product of two such matrices S = diag(D) + O is
 //     O O + (D_i + D_j) O_ij + D_i^2 on the diagonal.
-// Measured in |.|_F against 64 bits over flat, low-rank-plus-noise and 1/i
-// spectra: 2e-4 to 9e-4, step by step (all three parts in fp16: 3e-4 to 4e-3;
+// A product B X with errors E in B and d in X is off by E X + B d; both shrink
+// with the singular value they fall on, X's as it is and B's as its square, so
+// neither outgrows it.  Taken apart, (D + O) X keeps that only if D multiplies
+// what O does, hi: the step is a lo + (a + D) hi + O hi while small singular
+// values still grow.  In the last two steps, where most of a + D + O is D,
+// D takes lo too: (a + D) X + O hi.
+// Measured in |.|_F against 64 bits, over flat, low-rank, low-rank-plus-noise
+// and 1/i spectra and short sides of 4 to 2048, step by step: 5e-5 to 1e-3, up
+// to 1.7e-3 for short sides under 100 (with 14 bits of X in the linear term
+// and lo times a + D throughout, one strong direction comes to 5e-3 to 4e-2;
 // bf16 throughout: 1e-2 to 3e-2).  A result in more bits than bf16 gets three
 // products instead of one: every operand is the sum of two fp16 numbers,
 // hi + lo * 2^-11, and hi hi + hi lo + lo hi holds about 22 bits.
@@ -58,6 +68,7 @@ typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 // is what an epilogue waits for.
 constexpr float kScale = 1024.0f, kUnscale = 1.0f / 1024.0f;
 constexpr float kLo = 2048.0f;              // lo halves: 2^11 more
+constexpr int kLast = 2;                    // steps that the singular values end in
 
 // (x - hi) kLo; the difference is exact either way, and this way takes two
 // instructions
@@ -68,34 +79,7 @@ __device__ __forceinline__ float join(f16 hi, f16 lo) {
   return __builtin_fmaf((float)lo, 1.0f / kLo, (float)hi);
 }
 
-// What the rounding of X left, 8 elements from p on: in 16 bits where the
-// products use it, else (X then has 14 bits, for its linear term) the upper
-// byte of that, a sign, 5 exponent and 2 more bits: an application's traffic
-// is 6 bytes an element instead of 8.
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-template <bool BYTES>
-__device__ __forceinline__ f16x8 load_rest(const char* rests, int64_t p) {
-  if constexpr (BYTES) {
-    const u32x2 w = *reinterpret_cast<const u32x2*>(rests + p);
-    return __builtin_bit_cast(f16x8, (u32x4){__builtin_amdgcn_perm(w.x, w.x, 0x010C000Cu),
-                                             __builtin_amdgcn_perm(w.x, w.x, 0x030C020Cu),
-                                             __builtin_amdgcn_perm(w.y, w.y, 0x010C000Cu),
-                                             __builtin_amdgcn_perm(w.y, w.y, 0x030C020Cu)});
-  } else {
-    return *reinterpret_cast<const f16x8*>(rests + p * 2);
-  }
-}
-__device__ __forceinline__ u32x2 upper_bytes(f16x8 x) {
-  typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
-  const u32x4 w = __builtin_bit_cast(u32x4, __builtin_bit_cast(u16x8, x) + (uint16_t)0x80);
-  return (u32x2){__builtin_amdgcn_perm(w.y, w.x, 0x07050301u),
-                 __builtin_amdgcn_perm(w.w, w.z, 0x07050301u)};
-}
-template <bool BYTES>
-__device__ __forceinline__ void store_rest(char* rests, int64_t p, f16x8 x) {
-  if constexpr (BYTES) *reinterpret_cast<u32x2*>(rests + p) = upper_bytes(x);
-  else *reinterpret_cast<f16x8*>(rests + p * 2) = x;
-}
 
 // ---------------------------------------------------------------------------
 // The table of matrices travels by value, a chunk a launch, into the
@@ -126,7 +110,6 @@ struct Common {
   const Mat* table;       // the group's matrices
   int32_t count;
   int32_t load_tiles;
-  int32_t bytes;          // X's remainders are bytes (one product)
   const DevState* st;     // the Muon step's skip flag, or NULL
   double* inv;            // 1 / (|G|_F + eps), by slot
   double* partials;       // squared-norm partials
@@ -352,7 +335,7 @@ __global__ __launch_bounds__(kThreads) void zf_ns_prep(LoadArgs a) {
   else inv *= a.c.inv[m.slot];
   const bool wide = wide_loads<SRC>(m);
   f16* hp = at<f16>(a.c, m.h[0]);
-  char* lp = at<char>(a.c, m.l[0]);
+  f16* lp = at<f16>(a.c, m.l[0]);
   // 8 values at (i, j) in whole lines that this kernel does not read back
   auto put = [&](int64_t i, int j, const float (&v)[8]) {
     f16x8 hi, lo;
@@ -364,10 +347,7 @@ __global__ __launch_bounds__(kThreads) void zf_ns_prep(LoadArgs a) {
     }
     const int64_t p = i * m.ldx + j;
     __builtin_nontemporal_store(hi, reinterpret_cast<f16x8*>(hp + p));
-    if (a.c.bytes)
-      __builtin_nontemporal_store(upper_bytes(lo), reinterpret_cast<u32x2*>(lp + p));
-    else
-      __builtin_nontemporal_store(lo, reinterpret_cast<f16x8*>(lp + p * 2));
+    __builtin_nontemporal_store(lo, reinterpret_cast<f16x8*>(lp + p));
   };
   if (!m.tall) {
     Walk w((int64_t)block * a.c.load_tiles * 4096, m.np);
@@ -740,6 +720,7 @@ struct GemmArgs {
   float ca, cb, cc;   // kPoly: ca I + cb S + cc S S
   int32_t in0, in1, out;  // symmetric matrices (kApply: in0)
   int32_t turn;       // which X
+  int32_t early;      // kApply, one product: small singular values still grow
 };
 static_assert(sizeof(GemmArgs) <= kArgBytes, "arguments of a launch");
 
@@ -817,6 +798,14 @@ __device__ __forceinline__ float combine(float sum, float o0, float o1, float d0
     if (on) return __builtin_fmaf(d0i * d1j, kScale, sum * kUnscale);
     return __builtin_fmaf(d0i, o1, __builtin_fmaf(o0, d1j, sum * kUnscale));
   }
+}
+
+// D_i X_ij + sum, X_ij from its two halves.  One product: the products take
+// the upper half alone, so the lower one gets `rest` instead of D_i.
+template <int PRODUCTS>
+__device__ __forceinline__ float linear(f16 hi, f16 lo, float d, float rest, float sum) {
+  if constexpr (PRODUCTS == 3) return __builtin_fmaf(d, join(hi, lo), sum);
+  return __builtin_fmaf(rest * (1.0f / kLo), (float)lo, __builtin_fmaf(d, (float)hi, sum));
 }
 
 // x, without its element r if this piece is the one on the diagonal.
@@ -1127,7 +1116,7 @@ __device__ __forceinline__ void update_square(const GemmArgs& a, const Mat& m,
 // X <- S X with S = S_in0: D_i X_ij from both halves of X, and O X; LAST:
 // into the destination, or W <- W dec - rate (S X).
 // The same two layers: 560 us, 865 TFLOP/s; the main loop alone 414 us, the
-// rest is 6 bytes an element in and out after it (13 with Muon's weights).
+// rest is 8 bytes an element in and out after it (14 with Muon's weights).
 // Starting the XCDs or the blocks apart from each other, so that these do not
 // come at once, gains nothing: rows of X leave the second-level caches.
 template <typename T, int SIZE, bool LAST, int PRODUCTS, int DST, bool MUON>
@@ -1154,9 +1143,9 @@ __global__ __launch_bounds__(T::kThreads, 2) void zf_ns_apply(GemmArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wi = i0 + wave / T::kWavesJ * T::TI, wj = j0 + wave % T::kWavesJ * T::TJ;
   const f16* h = at<f16>(a.c, m.h[a.turn]);
-  const char* lo = at<char>(a.c, m.l[a.turn]);
+  const f16* lo = at<f16>(a.c, m.l[a.turn]);
   f16* h1 = at<f16>(a.c, m.h[a.turn ^ 1]);
-  char* lo1 = at<char>(a.c, m.l[a.turn ^ 1]);
+  f16* lo1 = at<f16>(a.c, m.l[a.turn ^ 1]);
   const float* d = at<float>(a.c, m.d[a.in0]);
   constexpr int E = 8 / T::kSquareWaves;  // lines of 8 rows a wave takes
   const int e0 = T::share_of(wi - i0, wj - j0) * E;
@@ -1177,7 +1166,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void zf_ns_apply(GemmArgs a) {
     for (int e = 0; e < E; ++e) {
       if (!in) break;
       x[e] = *reinterpret_cast<const f16x8*>(h + p0 + (int64_t)e * 8 * m.ldx);
-      y[e] = load_rest<PRODUCTS == 1>(lo, p0 + (int64_t)e * 8 * m.ldx);
+      y[e] = *reinterpret_cast<const f16x8*>(lo + p0 + (int64_t)e * 8 * m.ldx);
       di[e] = d[si + (e0 + e) * 8 + row];
     }
 #pragma unroll
@@ -1198,7 +1187,8 @@ __global__ __launch_bounds__(T::kThreads, 2) void zf_ns_apply(GemmArgs a) {
         f32x4 v = *piece * kUnscale;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          v[r] = __builtin_fmaf(di[e], join(x[e][t * 4 + r], y[e][t * 4 + r]), v[r]);
+          v[r] = linear<PRODUCTS>(x[e][t * 4 + r], y[e][t * 4 + r], di[e],
+                                  a.early ? a.ca : di[e], v[r]);
           if constexpr (!LAST) {
             hi[t * 4 + r] = (f16)v[r];
             rest[t * 4 + r] = rest_of(v[r], hi[t * 4 + r]);
@@ -1208,7 +1198,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void zf_ns_apply(GemmArgs a) {
       }
       if constexpr (!LAST) {
         *reinterpret_cast<f16x8*>(h1 + p0 + (int64_t)e * 8 * m.ldx) = hi;
-        store_rest<PRODUCTS == 1>(lo1, p0 + (int64_t)e * 8 * m.ldx, rest);
+        *reinterpret_cast<f16x8*>(lo1 + p0 + (int64_t)e * 8 * m.ldx) = rest;
       }
     }
     square_ready<T>();
@@ -1313,6 +1303,8 @@ int iterate(const Group& g, const Mat* mats, const zf_ns_params& p, int sym, int
       launch_sym<kMul, PRODUCTS>(g, sym, s, a);   // 0 = their product
     }
     a.in0 = n == 2 ? 0 : 1;
+    a.early = k + kLast < p.steps;
+    if (n == 2) a.ca = a.ca * a.ca;
     firsts(along, app);
     k += n;
     if (k == p.steps) launch_last<PRODUCTS>(g, app, s, dst, muon, a);
@@ -1605,7 +1597,7 @@ __global__ __launch_bounds__(kSmallThreads) void zf_ns_small(SmallArgs a) {
           if (i + r == j) v[r] = combine<true>(sum[r], 0.0f, 0.0f, di[r], dj, true, a.ca, a.cb, a.cc);
       }
     });
-    const bool last = step + 1 == a.steps;
+    const bool last = step + 1 == a.steps, early = step + kLast < a.steps;
     f32x4 acc[2][CJ], low[2][CJ];
     int pi[2], pj[CJ];
 #pragma unroll
@@ -1658,7 +1650,8 @@ __global__ __launch_bounds__(kSmallThreads) void zf_ns_small(SmallArgs a) {
         if constexpr (PRODUCTS == 3) acc[i][j] = acc[i][j] + low[i][j] * (1.0f / kLo);
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          acc[i][j][r] = __builtin_fmaf(di, join(h[r], w[r]), acc[i][j][r] * kUnscale);
+          acc[i][j][r] = linear<PRODUCTS>(h[r], w[r], di, early ? a.ca : di,
+                                          acc[i][j][r] * kUnscale);
       }
     }
     __syncthreads();
@@ -1828,10 +1821,10 @@ bool zf::ns::layout(const Shape* shapes, int64_t count, int products, Layout& ou
     const int64_t mn = (int64_t)m.mp * m.ldx, mm = (int64_t)m.mp * m.lds;
     if (g.count > 0 && elements + mn > kGroupElements) close();
     // what the rounding left of X: an operand of the products if there are
-    // three, else bytes used by their own tile alone, in place
+    // three, else used by its own tile alone, in place
     for (int z = 0; z < 2; ++z) {
       m.h[z] = take(mn * 2);
-      m.l[z] = z == 0 || products == 3 ? take(mn * (products == 3 ? 2 : 1)) : m.l[0];
+      m.l[z] = z == 0 || products == 3 ? take(mn * 2) : m.l[0];
     }
     for (int z = 0; z < 3; ++z) {
       m.s[z] = take(mm * 2);
@@ -1913,7 +1906,6 @@ int zf::ns::enqueue(const Layout& l, const zf_ns_params& p, int products, int sm
     c.table = table + g.first;
     c.count = g.count;
     c.load_tiles = g.load_tiles;
-    c.bytes = products == 1;
     c.st = io ? io->st : nullptr;
     c.inv = reinterpret_cast<double*>(ws + l.inv);
     c.partials = reinterpret_cast<double*>(ws + l.partials);

@@ -1,0 +1,95 @@
+"""Orthogonalisation of matrices whose singular values differ by orders of
+magnitude, against the plain form in 64 bits.
+
+Tolerances, in |error|_F / |X|_F, f the map of all steps on singular values.
+
+One product.  u = 2^-11 is half a step of an operand.  To first order an error
+W (in the singular vectors' basis) that arises in X reaches the result as
+W_ij times a divided difference of f: at most (f_i + f_j) / (s_i + s_j) where
+s_i and s_j differ, a^steps for two small ones.  An error of B = b A + c A A,
+E, arises as W_ij = E_ij s_j, one of X's rounding in B X as W_ij = B_i d_ij
+with B_i <= 4.8 s_i^2: both have a factor that cancels the division, so that
+neither grows while the small singular values do.  Every other term must keep
+more bits than that growth (a^5 = 485 for the default steps) costs: X itself
+has 22.  What then arises is the sum over the steps of at most (3.5 + 2 +
+4.8 * 3 * 1.2) u = 23 u if all roundings are aligned; they are spread evenly
+(0.41 u in the mean over a binade), and the last factor is near 0.7 where the
+singular values end: 3.4 u a step, of which two steps' worth survives near 1.
+7 u = 3.4e-3, taken as 2^-8.
+
+Three products.  X is kept to 22 bits (an error of 0.41 * 2^-22 of its norm 1
+in the mean), and every addition of a sum rounds to 24 (0.41 * 2^-24 of the
+partial sum, which grows evenly to the whole one: sqrt(k / 3) for k terms).
+Both arise anywhere, so both grow with the smallest singular values, a^5 over
+a result whose norm is 0.68 at least, and arise anew in every step, 1 + 1/a +
+1/a^2 + ... = 1.41 in all.  An error of the long sums in A does not grow; those
+of B X have min(rows, cols) terms.  (The same iteration in 32-bit arithmetic
+has errors of this size.)
+"""
+import math
+
+import pytest
+import torch
+
+from tests import gpu_common as G
+from tests.test_gpu_muon import plain, off, run
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def zf():
+    from fsdp_sharded_mixed_amd import zf as Z
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    return Z
+
+
+def tolerance(products, rows, cols, steps=5):
+    if products == 1:
+        return 2.0 ** -8
+    noise = 0.41 * (2.0 ** -22 + 2.0 ** -24 * math.sqrt(min(rows, cols) / 3))
+    return max(2e-5, 1.41 / 0.68 * 3.4445 ** steps * noise)
+
+
+def spectrum(kind, rows, cols, seed):
+    """One strong direction over noise, half the directions over noise, or nine
+    in ten of equal strength."""
+    g = torch.Generator().manual_seed(seed)
+    noise = torch.randn(rows, cols, generator=g)
+    if kind == "half":
+        r = max(1, min(rows, cols) // 2)
+        strong = torch.randn(rows, r, generator=g) @ torch.randn(r, cols, generator=g) / math.sqrt(r)
+        return strong + 1e-3 * noise
+    if kind == "equal":
+        r = max(1, min(rows, cols) * 9 // 10)
+        left = torch.linalg.qr(torch.randn(rows, r, generator=g))[0]
+        right = torch.linalg.qr(torch.randn(cols, r, generator=g))[0]
+        return left @ right.t() + 1e-4 * noise / math.sqrt(max(rows, cols))
+    strong = torch.randn(rows, 1, generator=g) @ torch.randn(1, cols, generator=g)
+    return strong + float(kind) * noise
+
+
+KINDS = ["0", "1e-4", "1e-3", "1e-2", "half", "equal"]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows,cols", [(11, 2000), (1400, 64), (256, 1024), (600, 600), (4, 1293),
+                                       (32, 600), (100, 128)])
+@pytest.mark.parametrize("products", [1, 3])
+def test_strong_directions(zf, kind, rows, cols, products):
+    x = spectrum(kind, rows, cols, 0).cuda()
+    y = run(zf, [x], [torch.empty_like(x)], zf.ns_params(products=products))[0]
+    err = off(y, plain(x))
+    G.say(f"{kind} {rows}x{cols} products={products}: {err:.2e}")
+    assert err <= tolerance(products, rows, cols)
+
+
+@pytest.mark.parametrize("rows,cols", [(1024, 1024), (2000, 2048)])
+@pytest.mark.parametrize("kind", ["0", "1e-3", "half"])
+def test_strong_directions_of_a_layer(zf, kind, rows, cols):
+    """Larger matrices in the default mode, from and to bf16."""
+    xs = [spectrum(kind, rows, cols, k).cuda().bfloat16() for k in range(2)]
+    ys = run(zf, xs, [torch.empty_like(x) for x in xs])
+    worst = max(off(y, plain(x)) for x, y in zip(xs, ys))
+    G.say(f"{kind} {rows}x{cols}: {worst:.2e}")
+    assert worst <= tolerance(1, rows, cols) + torch.finfo(torch.bfloat16).eps / 2
