@@ -29,12 +29,13 @@
 // values still grow.  In the last two steps, where most of a + D + O is D,
 // D takes lo too: (a + D) X + O hi.
 // Measured in |.|_F against 64 bits, over flat, low-rank, low-rank-plus-noise
-// and 1/i spectra and short sides of 4 to 2048, step by step: 5e-5 to 1e-3, up
-// to 1.7e-3 for short sides under 100 (with 14 bits of X in the linear term
-// and lo times a + D throughout, one strong direction comes to 5e-3 to 4e-2;
-// bf16 throughout: 1e-2 to 3e-2).  A result in more bits than bf16 gets three
+// and 1/i spectra and short sides of 4 to 2048: 5e-5 to 1.6e-3, 2.2e-3 for a
+// short side of 4 (with 14 bits of X in the linear term and lo times a + D
+// throughout, one strong direction comes to 5e-3 to 4e-2; bf16 throughout:
+// 1e-2 to 3e-2).  A result in more bits than bf16 gets three
 // products instead of one: every operand is the sum of two fp16 numbers,
-// hi + lo * 2^-11, and hi hi + hi lo + lo hi holds about 22 bits.
+// hi + lo * 2^-11, and hi hi + hi lo + lo hi holds about 22 bits, as exact as
+// the iteration in 32-bit arithmetic: 1e-6, to 1e-4 for one strong direction.
 #include "zf_ortho.h"
 
 #include <algorithm>
@@ -1257,15 +1258,21 @@ void launch_last(const Group& g, int size, hipStream_t s, int32_t dst, bool muon
   }
 }
 
-// The iteration of one group.  Steps run on X, or in pairs on the m x m side
-// (X_2 = Q_2 Q_1 X with A_2 = Q_1 A Q_1), which touches the long side once
-// for two steps and costs no more products when n = m: 20 m^3 + 9 m^2 (n-m)
-// instead of 20 m^3 + 15 m^2 (n-m) for five.  Pairs and single steps take
-// turns (2, 1, 2): longer stretches lose the small singular values, whose
-// squares vanish in A's rounding.  Errors measured: under 1.1e-3, but 3.1e-3
-// with a few strong directions in a short side of 11; single steps 8e-4 at
-// most, 1, 2, 2 5.5e-3, all five together 0.2.  A group takes single steps
-// where pairs gain little (Group::pairs).
+// The iteration of one group.  Two steps may run as a pair on the m x m side
+// (X_2 = Q_2 Q_1 X with A_2 = Q_1 A Q_1), which touches the long side once for
+// both and costs no more products when n = m: five single steps take 20 m^3 +
+// 15 m^2 (n - m) operations, every pair 3 m^2 (n - m) less.  A pair sees the
+// small singular values through their squares, which A's rounding drowns, so
+// pairs and single steps take turns.
+//   Three products: 2, 1, 2, as exact as single steps.
+//   One product: 2, 1, 1, 1, for short sides of kPairSide and more: errors up to
+// 1.5e-3 at 64 to 600, as with single steps, but 1.7e-3 at 48, 2.0e-3 at 32 and
+// 5e-3 at 11, where single steps keep 1.6e-3.  A later pair costs accuracy at
+// any size: with 2, 1, 2 half of the directions strong come to 3.2e-3 at 600 x
+// 600 (single steps 1.0e-3).  Single steps throughout are 11 percent slower for
+// two layers of hidden 2048, 2, 1, 2 is 10 percent faster.
+// The number of products and the short side decide, so that a matrix's result
+// does not depend on the others of the call.
 template <int PRODUCTS>
 int iterate(const Group& g, const Mat* mats, const zf_ns_params& p, int sym, int app, int32_t dst,
             bool muon, hipStream_t s, GemmArgs a) {
@@ -1277,8 +1284,8 @@ int iterate(const Group& g, const Mat* mats, const zf_ns_params& p, int sym, int
   a.turn = 0;
   bool pair = g.pairs;
   for (int k = 0; k < p.steps;) {
-    const int n = pair && k + 2 <= p.steps ? 2 : 1;
-    pair = g.pairs && n == 1;
+    const int n = pair && k + 2 <= p.steps - (PRODUCTS == 3 ? 0 : kLast) ? 2 : 1;
+    pair = PRODUCTS == 3 && n == 1;
     a.ca = (float)p.a;
     a.cb = (float)p.b;
     a.cc = (float)p.c;
@@ -1304,7 +1311,7 @@ int iterate(const Group& g, const Mat* mats, const zf_ns_params& p, int sym, int
     }
     a.in0 = n == 2 ? 0 : 1;
     a.early = k + kLast < p.steps;
-    if (n == 2) a.ca = a.ca * a.ca;
+    if (n == 2) a.ca *= a.ca;
     firsts(along, app);
     k += n;
     if (k == p.steps) launch_last<PRODUCTS>(g, app, s, dst, muon, a);
@@ -1711,6 +1718,8 @@ constexpr int64_t kMaxSide = 1ll << 20;
 // hidden 1024, 120 -> 167 us.)
 constexpr int64_t kOwnNorm = 512;
 
+constexpr int kPairSide = 64;  // shortest side of pairs with one product
+
 int small_tiles_of(const zf::ns::Shape& s) {
   return small_tiles(std::min(s.rows, s.cols), std::max(s.rows, s.cols));
 }
@@ -1744,12 +1753,10 @@ int zf::ns::products_of(const zf_ns_params& p, int32_t dst_dtype) {
 bool zf::ns::layout(const Shape* shapes, int64_t count, int products, Layout& out) {
   out.mats.resize((size_t)count);
   out.groups.clear();
-  out.one_round = true;
   out.shortest = INT32_MAX;
   int64_t partials = 0, region = 0, used = 0, elements = 0;
   Group g{};
-  int64_t load = 0, tri[3] = {}, app[3] = {};
-  double cubes = 0.0, longer = 0.0;  // sums of m^3 and of m^2 (n - m)
+  int64_t load = 0, tri[3] = {}, app[3] = {}, all_blocks = 0;
   auto close = [&]() {
     // tiles a block takes: one while that leaves CUs without a block
     g.load_tiles = load >= 4096 ? kLoadTiles : 1;
@@ -1771,13 +1778,7 @@ bool zf::ns::layout(const Shape* shapes, int64_t count, int products, Layout& ou
       g.app_blocks[z] = (int32_t)app[z];
       tri[z] = app[z] = 0;
     }
-    // Pairs of steps save 6 of 20 m^3 + 15 m^2 (n - m) and are less exact: not
-    // for less than a twentieth of it.  Nor where one round of blocks holds
-    // all of X: there every launch takes its latency, and single steps need
-    // two launches fewer for five (1024 x 1024: 162 -> 138 us).
-    if (g.app_blocks[kLittle] > kCus || !out.groups.empty()) out.one_round = false;
-    g.pairs = g.app_blocks[kLittle] > kCus && 6.0 * longer > 0.05 * (20.0 * cubes + 15.0 * longer);
-    cubes = longer = 0.0;
+    all_blocks += g.app_blocks[kLittle];
     out.groups.push_back(g);
     region = std::max(region, used);
     const int32_t next = g.first + g.count;
@@ -1790,19 +1791,26 @@ bool zf::ns::layout(const Shape* shapes, int64_t count, int products, Layout& ou
     used += round_up(bytes, 256);
     return o;
   };
-  int64_t large = 0;
+  // by class: single steps, pairs, held in shared memory
+  enum { kSingle, kPairs, kHeld, kClasses };
+  auto class_of = [&](const Shape& s) {
+    if (small_tiles_of(s) > 0) return kHeld;
+    return products == 3 || std::min(s.rows, s.cols) >= kPairSide ? kPairs : kSingle;
+  };
+  int64_t of_class[kClasses] = {};
   for (int64_t k = 0; k < count; ++k) {
     if (shapes[k].rows > kMaxSide || shapes[k].cols > kMaxSide) return false;
-    large += small_tiles_of(shapes[k]) == 0;
+    ++of_class[class_of(shapes[k])];
   }
+  const int64_t large = count - of_class[kHeld];
   out.small_first = (int32_t)large;
-  out.small_count = (int32_t)(count - large);
+  out.small_count = (int32_t)of_class[kHeld];
   out.small_tiles = 0;
-  int64_t place[2] = {0, large};  // the next large and the next small one
-  for (int64_t k = 0; k < count; ++k) {
+  int64_t placed = 0;
+  for (int c = 0; c < kClasses; ++c) for (int64_t k = 0; of_class[c] > 0 && k < count; ++k) {
+    if (class_of(shapes[k]) != c) continue;
     const int64_t rows = shapes[k].rows, cols = shapes[k].cols;
-    const int tiles_held = small_tiles_of(shapes[k]);
-    Mat& m = out.mats[(size_t)place[tiles_held > 0]++];
+    Mat& m = out.mats[(size_t)placed++];
     m = Mat{};
     m.slot = (int32_t)k;
     m.src_ld = m.dst_ld = cols;
@@ -1811,15 +1819,16 @@ bool zf::ns::layout(const Shape* shapes, int64_t count, int products, Layout& ou
     m.n = (int32_t)std::max(rows, cols);
     m.mp = (int32_t)round_up(m.m, kPad);
     m.np = (int32_t)round_up(m.n, kPad);
-    if (tiles_held > 0) {
-      out.small_tiles = std::max(out.small_tiles, tiles_held);
+    if (c == kHeld) {
+      out.small_tiles = std::max(out.small_tiles, small_tiles_of(shapes[k]));
       continue;
     }
     out.shortest = std::min(out.shortest, m.m);
     m.ldx = m.np;
     m.lds = m.mp;
     const int64_t mn = (int64_t)m.mp * m.ldx, mm = (int64_t)m.mp * m.lds;
-    if (g.count > 0 && elements + mn > kGroupElements) close();
+    if (g.count > 0 && (g.pairs != (c == kPairs) || elements + mn > kGroupElements)) close();
+    g.pairs = c == kPairs;
     // what the rounding left of X: an operand of the products if there are
     // three, else used by its own tile alone, in place
     for (int z = 0; z < 2; ++z) {
@@ -1843,13 +1852,11 @@ bool zf::ns::layout(const Shape* shapes, int64_t count, int products, Layout& ou
       app[z] += tm * tn;
     }
     if (load > 0x7FFFFFFF) return false;
-    const double mm2 = (double)m.mp * m.mp;
-    cubes += mm2 * m.mp;
-    longer += mm2 * (m.np - m.mp);
     elements += mn;
     ++g.count;
   }
   if (g.count > 0) close();
+  out.one_round = all_blocks <= kCus;
   int64_t at = 0;
   out.table = at;
   at += round_up(count * (int64_t)sizeof(Mat), 256);

@@ -540,17 +540,21 @@ int zf_offload_step(const zf_plan* plan, const zf_hparams* hp, const zf_offload_
  * products: how exactly the matrix products are computed.  1: operands are
  * rounded to 11 bits (fp16 with a common power-of-two factor; sums and the
  * diagonals of A and of its polynomial are binary32, and the linear term
- * takes X with 22 bits); the result of the default steps is 2e-4 to 3e-3
- * from the exact one (|error|_F / |X|_F; below 1.1e-3 but for matrices whose
- * singular values differ by orders of magnitude), where bf16's own rounding
- * is 1.7e-3.  3: operands are sums of two fp16 numbers, about 22 bits, for
- * three times the work; the result is within about 3e-6.  0: 1 for a ZF_BF16 result, else 3; in zf_muon_step 1, and 3 for matrices that fit
- * in a compute unit's shared memory (up to 128 x 128), where they cost
- * little, and for all matrices of a plan if one of the others has a side of
- * at most 32 and they are at most 256 blocks of 64 x 64 together.
+ * takes X with 22 bits).  The result of the default steps is 5e-5 to 1.6e-3
+ * from the exact one (|error|_F / |X|_F, measured), up to 2.2e-3 for short
+ * sides under 32, whatever the singular values; bf16's own rounding is
+ * 1.7e-3.  3: operands are sums of two fp16 numbers, about 22 bits, for three
+ * times the work; the result is as exact as the iteration in 32-bit
+ * arithmetic: about 1e-6, and up to 1e-4 where the smallest singular values
+ * vanish beside the largest, because errors grow with them (3.4^5 times).
+ * 0: 1 for a ZF_BF16 result, else 3; in zf_muon_step 1, and 3 for matrices
+ * that fit in a compute unit's shared memory (up to 128 x 128), and for all
+ * matrices of a plan if one of the others has a side of at most 32 and they
+ * are at most 256 blocks of 64 x 64 together.
  * The operands' range bounds the coefficients: singular values, and the
- * entries of A and b A + c A A, must stay below 64 (they stay below 8 for
- * the default ones). */
+ * entries off the diagonal of A, of Q = a I + b A + c A A and of the product of
+ * two steps' Q, must stay below 64 (they stay below 8 for the default
+ * coefficients). */
 #define ZF_NS_MAX_STEPS 32
 typedef struct {
   int32_t steps;     /* 1 .. ZF_NS_MAX_STEPS */

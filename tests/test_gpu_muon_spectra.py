@@ -77,14 +77,19 @@ KINDS = ["0", "1e-4", "1e-3", "1e-2", "half", "equal"]
                                        (32, 600), (100, 128)])
 @pytest.mark.parametrize("products", [1, 3])
 def test_strong_directions(zf, kind, rows, cols, products):
-    x = spectrum(kind, rows, cols, 0).cuda()
-    y = run(zf, [x], [torch.empty_like(x)], zf.ns_params(products=products))[0]
-    err = off(y, plain(x))
-    G.say(f"{kind} {rows}x{cols} products={products}: {err:.2e}")
-    assert err <= tolerance(products, rows, cols)
+    """Alone, and in a batch of more than 256 blocks of 64 x 64 (or 24)."""
+    blocks = -(-rows // 64) * -(-cols // 64)
+    xs = [spectrum(kind, rows, cols, k).cuda() for k in range(min(256 // blocks + 1, 24))]
+    want = [plain(x) for x in xs]
+    for n in (1, len(xs)):
+        ys = run(zf, xs[:n], [torch.empty_like(x) for x in xs[:n]], zf.ns_params(products=products))
+        worst = max(off(y, w) for y, w in zip(ys, want))
+        G.say(f"{kind} {rows}x{cols} products={products} of {n}: {worst:.2e}")
+        assert worst <= tolerance(products, rows, cols)
 
 
-@pytest.mark.parametrize("rows,cols", [(1024, 1024), (2000, 2048)])
+@pytest.mark.parametrize("rows,cols", [(1024, 1024), (2000, 2048), (2048, 1024),
+                                       (1024, 4096)])
 @pytest.mark.parametrize("kind", ["0", "1e-3", "half"])
 def test_strong_directions_of_a_layer(zf, kind, rows, cols):
     """Larger matrices in the default mode, from and to bf16."""
@@ -93,3 +98,15 @@ def test_strong_directions_of_a_layer(zf, kind, rows, cols):
     worst = max(off(y, plain(x)) for x, y in zip(xs, ys))
     G.say(f"{kind} {rows}x{cols}: {worst:.2e}")
     assert worst <= tolerance(1, rows, cols) + torch.finfo(torch.bfloat16).eps / 2
+
+
+@pytest.mark.parametrize("dst", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("shape", [(300, 2500), (1293, 4), (1024, 1024), (90, 70)])
+def test_alone_and_among_others(zf, shape, dst):
+    """The same bits whatever else is in the call."""
+    x = spectrum("half", *shape, 3).cuda()
+    others = [spectrum("1e-2", *s, k).cuda() for k, s in enumerate([(256, 2048)] * 9 + [(20, 30)] * 15)]
+    alone = run(zf, [x], [torch.empty_like(x, dtype=dst)])[0]
+    xs = others + [x]
+    among = run(zf, xs, [torch.empty_like(z, dtype=dst) for z in xs])[-1]
+    assert torch.equal(G.bits_view(alone), G.bits_view(among))
