@@ -153,8 +153,8 @@ __device__ __forceinline__ T* at(const Common& c, int64_t offset) {
 }
 
 // ---------------------------------------------------------------------------
-// The squared norm, one partial (64 bits) a block; the Muon step's momentum
-// update on the way.  A stream: 122M weights with momentum 261 us, 12 bytes
+// The squared norm, one partial (64 bits) for 4096 padded elements, however
+// many a block takes; the Muon step's momentum update on the way.  A stream: 122M weights with momentum 261 us, 12 bytes
 // each, 5.6 TB/s.
 constexpr int kTile = 64, kLoadTiles = 4;  // tiles of a block, if there are many
 
@@ -280,7 +280,7 @@ __global__ __launch_bounds__(kThreads) void zf_ns_load(LoadArgs a) {
   const int rows = m.tall ? m.n : m.m, cols = m.tall ? m.m : m.n;
   const int steps = a.c.load_tiles * 2;
   Walk w((int64_t)block * a.c.load_tiles * 4096, m.tall ? m.mp : m.np);
-  double ss = 0.0;
+  double ss[kLoadTiles] = {};
 #pragma unroll
   for (int t = 0; t < kLoadTiles * 2; ++t, w.next()) {
     if (t >= steps) break;
@@ -288,18 +288,31 @@ __global__ __launch_bounds__(kThreads) void zf_ns_load(LoadArgs a) {
     float v[8];
     load8<SRC, true>(a, m, gs, wide, w.r, w.c, cols, v);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss += (double)v[e] * (double)v[e];
+    for (int e = 0; e < 8; ++e) ss[t / 2] += (double)v[e] * (double)v[e];
   }
-  uint32_t unused = 0;
-  block_reduce(ss, unused);
-  if (threadIdx.x == 0) a.c.partials[m.part + block] = ss;
+  constexpr int kWaves = kThreads / 64;
+  __shared__ double sum[kLoadTiles][kWaves];
+#pragma unroll
+  for (int k = 0; k < kLoadTiles; ++k) {
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) ss[k] = ss[k] + __shfl_xor(ss[k], off, 64);
+    if ((threadIdx.x & 63) == 0) sum[k][threadIdx.x >> 6] = ss[k];
+    if (k + 1 == a.c.load_tiles) break;
+  }
+  __syncthreads();
+  const int k = threadIdx.x, tile = block * a.c.load_tiles + k;
+  if (k < a.c.load_tiles && tile < (m.mp / kTile) * (m.np / kTile)) {
+    double t = sum[k][0];
+#pragma unroll
+    for (int x = 1; x < kWaves; ++x) t = t + sum[k][x];
+    a.c.partials[m.part + tile] = t;
+  }
 }
 
 // The inverse norm of a matrix from its partials, in an order that depends on
 // its shape alone; valid in every thread.
 __device__ __forceinline__ double inverse_norm(const Common& c, const Mat& m) {
-  const int64_t tiles = (int64_t)(m.mp / kTile) * (m.np / kTile);
-  const int64_t parts = (tiles + c.load_tiles - 1) / c.load_tiles;
+  const int64_t parts = (int64_t)(m.mp / kTile) * (m.np / kTile);
   double ss = 0.0;
   for (int64_t i = threadIdx.x; i < parts; i += kThreads) ss += c.partials[m.part + i];
   uint32_t unused = 0;
@@ -1765,12 +1778,11 @@ bool zf::ns::layout(const Shape* shapes, int64_t count, int products, Layout& ou
     for (int32_t k = g.first; k < g.first + g.count; ++k) {
       Mat& m = out.mats[(size_t)k];
       const int64_t tiles = (int64_t)(m.mp / kTile) * (m.np / kTile);
-      const int64_t parts = (tiles + g.load_tiles - 1) / g.load_tiles;
-      if (parts > kOwnNorm) g.own_norm = 0;
+      if (tiles > kOwnNorm) g.own_norm = 0;
       m.part = partials;
-      partials += parts;
+      partials += tiles;
       m.load0 = (int32_t)blocks;
-      blocks += parts;
+      blocks += (tiles + g.load_tiles - 1) / g.load_tiles;
     }
     g.load_blocks = (int32_t)blocks;
     for (int z = 0; z < 3; ++z) {

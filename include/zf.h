@@ -591,7 +591,8 @@ int64_t zf_orthogonalize_bytes(const zf_matrix* mats, int64_t count, int32_t dst
  * Elements between the rows of a strided dst are left as they are.
  * A matrix of zeros gives zeros (eps > 0); one that holds an infinity or a
  * NaN gives NaN throughout, and no other matrix of the batch is touched by
- * it.  Sums are taken in a fixed order: the same call gives the same bits.
+ * it.  Sums are taken in a fixed order: the same matrix gives the same bits,
+ * alone or among any others, with the same result type and params.
  * workspace: device memory of workspace_size >= zf_orthogonalize_bytes,
  * 16-byte aligned; calls that may overlap in time (two streams, two graphs)
  * need workspaces of their own.

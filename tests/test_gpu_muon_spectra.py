@@ -102,10 +102,13 @@ def test_strong_directions_of_a_layer(zf, kind, rows, cols):
 
 @pytest.mark.parametrize("dst", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("shape", [(300, 2500), (1293, 4), (1024, 1024), (90, 70)])
-def test_alone_and_among_others(zf, shape, dst):
-    """The same bits whatever else is in the call."""
+@pytest.mark.parametrize("large", [9, 36])
+def test_alone_and_among_others(zf, shape, large, dst):
+    """The same bits whatever else is in the call (36: blocks of the first
+    launches take 4 tiles each)."""
     x = spectrum("half", *shape, 3).cuda()
-    others = [spectrum("1e-2", *s, k).cuda() for k, s in enumerate([(256, 2048)] * 9 + [(20, 30)] * 15)]
+    others = [spectrum("1e-2", *s, k % 5).cuda()
+              for k, s in enumerate([(256, 2048)] * large + [(20, 30)] * 15)]
     alone = run(zf, [x], [torch.empty_like(x, dtype=dst)])[0]
     xs = others + [x]
     among = run(zf, xs, [torch.empty_like(z, dtype=dst) for z in xs])[-1]
