@@ -135,7 +135,7 @@ int enqueue_rest(const zf_muon* mu, const zf_hparams* hp, const zf_step_args* ar
   return ZF_OK;
 }
 
-constexpr int32_t kThin = 32;
+constexpr int32_t kThin = 32;  // longest short side of a thin matrix
 
 bool valid(const zf_muon* m) { return m && m->magic == kMuonMagic; }
 
@@ -161,22 +161,24 @@ Places places(const zf_muon* m, const zf::ns::Layout& l) {
   return p;
 }
 
-int muon_layout(const zf_muon* m, const zf_ns_params* params, zf::ns::Layout& l, zf_ns_params& p,
-                int& products) {
+int muon_layout(const zf_muon* m, const zf_ns_params* params, zf::ns::Layout& l, zf_ns_params& p) {
   p = params ? *params : zf::ns::defaults();
   const int rc = zf::ns::check_params(p);
   if (rc != ZF_OK) return rc;
   const int64_t n = (int64_t)m->shapes.size();
-  products = p.products ? p.products : 1;
-  if (!zf::ns::layout(m->shapes.data(), n, products, l)) return ZF_ESIZE;
-  // A thin matrix takes large steps (the factor sqrt(R / C)), so the
-  // products' error counts against its weights: over 1e-6 of them for 1293 x 4 at
-  // a rate of 1e-4, 1e-8 with three products.  In one round of blocks those
-  // cost 170 us a step instead of 114.
-  if (p.products == 0 && l.one_round && l.shortest <= kThin) {
-    products = 3;
-    if (!zf::ns::layout(m->shapes.data(), n, products, l)) return ZF_ESIZE;
-  }
+  // A thin matrix takes three products where the caller leaves the choice:
+  // one is least exact there, and a tall one's updates are large under
+  // ZF_MUON_SCALE_ROWS, 1 / sqrt(m) of the rate beside the 0.2 of
+  // ZF_MUON_SCALE_RMS.  (The shape decides, not the rule: the workspace is
+  // asked for before the rule is known.)
+  if (!zf::ns::layout(m->shapes.data(), n, p.products ? p.products : 1, p.products ? 0 : kThin, l))
+    return ZF_ESIZE;
+  // Beside a thin one the others of a plan that fits in a round of blocks take
+  // three products too, which is quicker than launches of their own: 300 x 700
+  // and 1293 x 4 take 193 us together, apart 110 with one product and 145 with
+  // three.
+  if (p.products == 0 && l.one_round && l.shortest <= kThin)
+    if (!zf::ns::layout(m->shapes.data(), n, 3, 0, l)) return ZF_ESIZE;
   return ZF_OK;
 }
 
@@ -214,7 +216,7 @@ extern "C" int zf_muon_plan(const zf_plan* plan, const int64_t* segments, int64_
     }
     if (at < plan->summary.psi_pad) m->rest.push_back({at, plan->summary.psi_pad});
     zf::ns::Layout l;
-    if (!zf::ns::layout(m->shapes.data(), (int64_t)m->shapes.size(), 3, l)) {
+    if (!zf::ns::layout(m->shapes.data(), (int64_t)m->shapes.size(), 3, 0, l)) {
       delete m;
       return ZF_ESIZE;
     }
@@ -237,8 +239,7 @@ extern "C" int64_t zf_muon_workspace_bytes(const zf_muon* muon, const zf_ns_para
   try {
     zf::ns::Layout l;
     zf_ns_params p;
-    int products = 1;
-    const int rc = muon_layout(muon, params, l, p, products);
+    const int rc = muon_layout(muon, params, l, p);
     return rc == ZF_OK ? places(muon, l).bytes : rc;
   } catch (const std::bad_alloc&) {
     return ZF_ENOMEM;
@@ -263,8 +264,7 @@ extern "C" int zf_muon_step(const zf_muon* muon, const zf_hparams* hp,
   try {
     zf::ns::Layout l;
     zf_ns_params p;
-    int products = 1;
-    int rc = muon_layout(muon, &mhp->ns, l, p, products);
+    int rc = muon_layout(muon, &mhp->ns, l, p);
     if (rc != ZF_OK) return rc;
     const Places at = places(muon, l);
     if (!args->workspace) return ZF_EINVAL;
@@ -300,8 +300,8 @@ extern "C" int zf_muon_step(const zf_muon* muon, const zf_hparams* hp,
     io.param_dtype = args->param_dtype;
     // matrices held in shared memory take three products unless the caller
     // chose: nearly all of a launch's time is latency
-    rc = zf::ns::enqueue(l, p, products, p.products ? p.products : 3, ZF_F32, args->param_dtype,
-                         &io, ws + at.engine, s);
+    rc = zf::ns::enqueue(l, p, p.products ? p.products : 3, ZF_F32, args->param_dtype, &io,
+                         ws + at.engine, s);
     if (rc != ZF_OK) return rc;
     rc = enqueue_rest(muon, hp, args, front.grad_shards, s);
     if (rc != ZF_OK) return rc;

@@ -45,6 +45,8 @@ struct Mat {
 struct Group {
   int32_t first, count;
   int32_t load_tiles;     // 64 x 64 tiles a block of the load takes
+  int32_t kind;           // its matrices' class
+  int32_t products;       // 1 or 3
   int32_t pairs;          // steps in pairs on the short side
   int32_t own_norm;       // few enough partials for every block to sum them
   int32_t load_blocks, tri_blocks[3], app_blocks[3];
@@ -68,8 +70,10 @@ struct Shape {
 };
 
 // Plans the buffers of `count` matrices; products: 1, or 3 with the second
-// 16-bit halves.  false: a size out of range.
-bool layout(const Shape* shapes, int64_t count, int products, Layout& out);
+// 16-bit halves; thin: with one product, a matrix with a side of at most this
+// takes three all the same, unless it is too long.  false: a size out of
+// range.
+bool layout(const Shape* shapes, int64_t count, int products, int32_t thin, Layout& out);
 
 // Products a call computes: the caller's choice, or by the result's type.
 int products_of(const zf_ns_params& p, int32_t dst_dtype);
@@ -91,8 +95,8 @@ struct MuonIo {
 // Enqueues the orthogonalisation of every matrix of `l` on `s`.  io == NULL:
 // from Mat.src (src_dtype) to Mat.dst (dst_dtype); else the Muon update.
 // small_products: of the matrices held in shared memory.
-int enqueue(const Layout& l, const zf_ns_params& p, int products, int small_products,
-            int32_t src_dtype, int32_t dst_dtype, const MuonIo* io, char* ws, hipStream_t s);
+int enqueue(const Layout& l, const zf_ns_params& p, int small_products, int32_t src_dtype,
+            int32_t dst_dtype, const MuonIo* io, char* ws, hipStream_t s);
 
 }  // namespace ns
 }  // namespace zf

@@ -1763,7 +1763,7 @@ int zf::ns::products_of(const zf_ns_params& p, int32_t dst_dtype) {
   return dst_dtype == ZF_BF16 ? 1 : 3;
 }
 
-bool zf::ns::layout(const Shape* shapes, int64_t count, int products, Layout& out) {
+bool zf::ns::layout(const Shape* shapes, int64_t count, int products, int32_t thin, Layout& out) {
   out.mats.resize((size_t)count);
   out.groups.clear();
   out.shortest = INT32_MAX;
@@ -1803,11 +1803,16 @@ bool zf::ns::layout(const Shape* shapes, int64_t count, int products, Layout& ou
     used += round_up(bytes, 256);
     return o;
   };
-  // by class: single steps, pairs, held in shared memory
-  enum { kSingle, kPairs, kHeld, kClasses };
+  // by class: one product by single steps or a pair first, three products,
+  // held in shared memory
+  enum { kSingle, kPairs, kThree, kHeld, kClasses };
   auto class_of = [&](const Shape& s) {
     if (small_tiles_of(s) > 0) return kHeld;
-    return products == 3 || std::min(s.rows, s.cols) >= kPairSide ? kPairs : kSingle;
+    const int64_t m = std::min(s.rows, s.cols), n = std::max(s.rows, s.cols);
+    // one block walks a thin matrix's whole sum: 16 x 16384 takes 490 us with
+    // three products instead of 295, 16 x 262144 6.5 ms instead of 3.7
+    if (products == 3 || (m <= thin && n <= kCus * kPad)) return kThree;
+    return m >= kPairSide ? kPairs : kSingle;
   };
   int64_t of_class[kClasses] = {};
   for (int64_t k = 0; k < count; ++k) {
@@ -1839,17 +1844,19 @@ bool zf::ns::layout(const Shape* shapes, int64_t count, int products, Layout& ou
     m.ldx = m.np;
     m.lds = m.mp;
     const int64_t mn = (int64_t)m.mp * m.ldx, mm = (int64_t)m.mp * m.lds;
-    if (g.count > 0 && (g.pairs != (c == kPairs) || elements + mn > kGroupElements)) close();
-    g.pairs = c == kPairs;
+    if (g.count > 0 && (g.kind != c || elements + mn > kGroupElements)) close();
+    g.kind = c;
+    g.products = c == kThree ? 3 : 1;
+    g.pairs = c != kSingle;
     // what the rounding left of X: an operand of the products if there are
     // three, else used by its own tile alone, in place
     for (int z = 0; z < 2; ++z) {
       m.h[z] = take(mn * 2);
-      m.l[z] = z == 0 || products == 3 ? take(mn * 2) : m.l[0];
+      m.l[z] = z == 0 || g.products == 3 ? take(mn * 2) : m.l[0];
     }
     for (int z = 0; z < 3; ++z) {
       m.s[z] = take(mm * 2);
-      m.sl[z] = products == 3 ? take(mm * 2) : m.s[z];
+      m.sl[z] = g.products == 3 ? take(mm * 2) : m.s[z];
       m.d[z] = take((int64_t)m.mp * 4);
     }
     const int64_t tiles = (int64_t)(m.mp / kTile) * (m.np / kTile);
@@ -1884,9 +1891,8 @@ bool zf::ns::layout(const Shape* shapes, int64_t count, int products, Layout& ou
   return true;
 }
 
-int zf::ns::enqueue(const Layout& l, const zf_ns_params& p, int products, int small_products,
-                    int32_t src_dtype, int32_t dst_dtype, const MuonIo* io, char* ws,
-                    hipStream_t s) {
+int zf::ns::enqueue(const Layout& l, const zf_ns_params& p, int small_products, int32_t src_dtype,
+                    int32_t dst_dtype, const MuonIo* io, char* ws, hipStream_t s) {
   Mat* table = reinterpret_cast<Mat*>(ws + l.table);
   // a few small matrices, and a few large ones, go as arguments and need no
   // table
@@ -1947,7 +1953,7 @@ int zf::ns::enqueue(const Layout& l, const zf_ns_params& p, int products, int sm
     ga.c = c;
     ga.io = la.io;
     const int sym = tile_size(g.tri_blocks), app = tile_size(g.app_blocks);
-    const int rc = products == 3
+    const int rc = g.products == 3
                        ? iterate<3>(g, l.mats.data() + g.first, p, sym, app, dst_dtype, io != nullptr, s, ga)
                        : iterate<1>(g, l.mats.data() + g.first, p, sym, app, dst_dtype, io != nullptr, s, ga);
     if (rc != ZF_OK) return rc;
@@ -1976,7 +1982,7 @@ int ortho_layout(const zf_matrix* mats, int64_t count, int32_t dst_dtype,
     if (mats[k].rows < 1 || mats[k].cols < 1) return ZF_EINVAL;
     shapes[(size_t)k] = {mats[k].rows, mats[k].cols};
   }
-  return zf::ns::layout(shapes.data(), count, products, l) ? ZF_OK : ZF_ESIZE;
+  return zf::ns::layout(shapes.data(), count, products, 0, l) ? ZF_OK : ZF_ESIZE;
 }
 
 // Two results in one place, or a result in another matrix's place, which
@@ -2043,7 +2049,7 @@ extern "C" int zf_orthogonalize(const zf_matrix* mats, int64_t count, int32_t sr
     if ((reinterpret_cast<uintptr_t>(workspace) & 15u) != 0) return ZF_EALIGN;
     if (workspace_size < l.bytes) return ZF_ESIZE;
     (void)hipGetLastError();
-    return zf::ns::enqueue(l, p, products, products, src_dtype, dst_dtype, nullptr,
+    return zf::ns::enqueue(l, p, products, src_dtype, dst_dtype, nullptr,
                            static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
   } catch (const std::bad_alloc&) {
     return ZF_ENOMEM;

@@ -547,10 +547,11 @@ int zf_offload_step(const zf_plan* plan, const zf_hparams* hp, const zf_offload_
  * times the work; the result is as exact as the iteration in 32-bit
  * arithmetic: about 1e-6, and up to 1e-4 where the smallest singular values
  * vanish beside the largest, because errors grow with them (3.4^5 times).
- * 0: 1 for a ZF_BF16 result, else 3; in zf_muon_step 1, and 3 for matrices
- * that fit in a compute unit's shared memory (up to 128 x 128), and for all
- * matrices of a plan if one of the others has a side of at most 32 and they
- * are at most 256 blocks of 64 x 64 together.
+ * 0: 1 for a ZF_BF16 result, else 3; in zf_muon_step 1, but 3 for matrices
+ * that fit in a compute unit's shared memory (up to 128 x 128) and for thin
+ * ones (one side at most 32, the other at most 16384), and for all matrices
+ * of a plan with a thin one whose matrices, those in shared memory apart, are
+ * at most 256 blocks of 64 x 64 together.
  * The operands' range bounds the coefficients: singular values, and the
  * entries off the diagonal of A, of Q = a I + b A + c A A and of the product of
  * two steps' Q, must stay below 64 (they stay below 8 for the default
