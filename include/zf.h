@@ -590,17 +590,19 @@ int64_t zf_orthogonalize_bytes(const zf_matrix* mats, int64_t count, int32_t dst
  * (two results, or a result and another matrix, that start at the same
  * address are refused).
  * Elements between the rows of a strided dst are left as they are.
- * A matrix of zeros gives zeros (eps > 0); one that holds an infinity or a
- * NaN gives NaN throughout, and no other matrix of the batch is touched by
- * it.  Sums are taken in a fixed order: the same matrix gives the same bits,
+ * A matrix of zeros gives zeros (eps > 0); one of a norm far below eps gives
+ * about a^steps / eps times itself, with an absolute error of 1e-11 an element
+ * at most (what the operands hold); one that holds an infinity or a NaN
+ * gives NaN throughout, and no other matrix of the batch is touched by it.
+ * Sums are taken in a fixed order: the same matrix gives the same bits,
  * alone or among any others, with the same result type and params.
  * workspace: device memory of workspace_size >= zf_orthogonalize_bytes,
  * 16-byte aligned; calls that may overlap in time (two streams, two graphs)
  * need workspaces of their own.
  * Errors: ZF_EINVAL (NULL, count < 0, a side < 1, a stride < cols, a dst
- * that is another matrix's src or dst, params out of range), ZF_EALIGN, ZF_EDTYPE, ZF_ESIZE (workspace too small, a side
- * above 2^20, more than ZF_ORTHO_MAX_MATRICES matrices), ZF_ENOMEM,
- * ZF_EHIP. */
+ * that is another matrix's src or dst, params out of range), ZF_EALIGN,
+ * ZF_EDTYPE, ZF_ESIZE (workspace too small, a side above 2^20, more than
+ * ZF_ORTHO_MAX_MATRICES matrices), ZF_ENOMEM, ZF_EHIP. */
 int zf_orthogonalize(const zf_matrix* mats, int64_t count, int32_t src_dtype, int32_t dst_dtype,
                      const zf_ns_params* params, void* workspace, int64_t workspace_size,
                      void* stream);

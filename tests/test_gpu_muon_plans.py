@@ -177,3 +177,91 @@ def test_one_element_without_a_value(zf, shape, products, value):
     assert torch.isnan(ys[1]).all()
     for k in (0, 2):
         assert torch.equal(G.bits_view(ys[k]), G.bits_view(clean[k]))
+
+
+@pytest.mark.parametrize("segs", [TABLE, matrices(*[(40 + i, 90 - i) for i in range(20)])
+                                  + [(7, 0, 2, 0)] + matrices((130, 1000), (20, 3000))])
+def test_tables_captured_and_replayed(zf, segs):
+    """Plans whose matrices travel through a table in the workspace: replays
+    beside an eager twin, with new gradients between."""
+    chosen = [i for i, s in enumerate(segs) if s[3] > 0]
+    a, b = (Model(zf, segs, chosen, 2, W.GLOBAL_FLAT) for _ in range(2))
+    hp, mhp = zf.hparams(1e-3), zf.muon_hparams(1e-2)
+    for m in (a, b):
+        m.step(hp, mhp)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a.step(hp, mhp)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    for k in range(3):
+        for q, r in zip(a.grads, b.grads):
+            q.copy_((torch.randn(q.shape, generator=g, device="cuda") * a.real).to(q.dtype))
+            r.copy_(q)
+        a.workspace.fill_(0xFF)
+        graph.replay()
+        b.step(hp, mhp)
+        torch.cuda.synchronize()
+        x, y = a.buffers(), b.buffers()
+        for name in x:
+            assert torch.equal(x[name].view(torch.uint8), y[name].view(torch.uint8)), (k, name)
+
+
+def test_phase_events(zf):
+    """Recorded in order around the passes."""
+    m = Model(zf, ROUND, [0, 1, 2], 2, W.GLOBAL_FLAT)
+    events = [torch.cuda.Event(enable_timing=True) for _ in range(4)]
+    for e in events:
+        e.record()  # makes the handle
+    args = (m.muon, zf.hparams(1e-3), zf.muon_hparams(1e-2), *m.codes(), m.grads, m.master,
+            m.momentum, m.square, m.params, m.workspace, m.state)
+    for _ in range(2):
+        zf.muon_step(*args, phase_events=[e.cuda_event for e in events])
+        torch.cuda.synchronize()
+        spans = [x.elapsed_time(y) for x, y in zip(events, events[1:])]
+        assert all(s >= 0 for s in spans) and spans[2] > 0
+
+
+def test_a_matrix_without_momentum_only_decays(zf):
+    """Zero gradients on zero momentum: the update is zero."""
+    segs = matrices((30, 40), (300, 500), (9, 2000), (1100, 1300))
+    m = Model(zf, segs, [0, 1, 2, 3], 2, W.GLOBAL_FLAT)
+    for t in m.grads + [m.momentum]:
+        t.zero_()
+    before = m.master.clone()
+    m.step(zf.hparams(1e-3), zf.muon_hparams(0.25, weight_decay=0.5))
+    assert torch.equal(m.master[m.real], (before * 0.875)[m.real])
+
+
+@pytest.mark.parametrize("products", [1, 3])
+@pytest.mark.parametrize("shape", [(40, 60), (500, 700), (1100, 1300)])
+@pytest.mark.parametrize("norm", [1e-9, 1e-12, 1e-15, 1e-20])
+def test_norms_far_below_eps(zf, shape, products, norm):
+    """The result is a^5 X0 or so, which may be below what the operands hold:
+    elements of X are rounded to 2^-46 (2^-25 of lo's scale of 2^21) at worst,
+    in each of five steps, and grow."""
+    from tests.test_gpu_muon import matrix, run
+    x = matrix(*shape, torch.float32, 4)
+    x *= norm / x.norm()
+    y = run(zf, [x], [torch.empty_like(x)], zf.ns_params(products=products))[0]
+    want = plain(x)
+    least = 1.41 * 3.4445 ** 5 * 2.0 ** -46 * math.sqrt(x.numel())
+    limit = 2.0 ** -8 if products == 1 else 2e-5
+    assert (y.double() - want).norm().item() <= limit * want.norm().item() + least
+
+
+@pytest.mark.parametrize("steps,coefficients", [
+    (1, (3.4445, -4.7750, 2.0315)), (2, (3.4445, -4.7750, 2.0315)), (3, (3.4445, -4.7750, 2.0315)),
+    (4, (3.4445, -4.7750, 2.0315)), (8, (3.4445, -4.7750, 2.0315)), (12, (1.5, -0.5, 0.0)),
+    (6, (1.875, -1.25, 0.375))])
+@pytest.mark.parametrize("shape", [(100, 140), (192, 320), (20, 2000), (1024, 1500)])
+def test_other_iterations_with_one_product(zf, steps, coefficients, shape):
+    from tests.test_gpu_muon import matrix, run
+    a, b, c = coefficients
+    x = matrix(*shape, torch.float32, 8)
+    y = run(zf, [x], [torch.empty_like(x)],
+            zf.ns_params(steps=steps, products=1, a=a, b=b, c=c))[0]
+    want = plain(x, steps, coefficients=coefficients)
+    err = (y.double() - want).norm().item() / want.norm().item()
+    G.say(f"{shape} {steps} {coefficients}: {err:.2e}")
+    assert err <= TOL[1]
