@@ -27,7 +27,10 @@
 // neither outgrows it.  Taken apart, (D + O) X keeps that only if D multiplies
 // what O does, hi: the step is a lo + (a + D) hi + O hi while small singular
 // values still grow.  In the last two steps, where most of a + D + O is D,
-// D takes lo too: (a + D) X + O hi.
+// D takes lo too: (a + D) X + O hi.  Where sums are short, in shared memory
+// and for short sides of one tile, lo goes through the product as well,
+// (a + D + O) X: with few singular values a lo alone costs up to 2e-3 (1 x 77:
+// 1.4e-3 against 1e-4).
 // Measured in |.|_F against 64 bits, over flat, low-rank, low-rank-plus-noise
 // and 1/i spectra and short sides of 4 to 2048: 5e-5 to 1.6e-3, 2.2e-3 for a
 // short side of 4 (with 14 bits of X in the linear term and lo times a + D
@@ -818,7 +821,7 @@ __device__ __forceinline__ float combine(float sum, float o0, float o1, float d0
 // the upper half alone, so the lower one gets `rest` instead of D_i.
 template <int PRODUCTS>
 __device__ __forceinline__ float linear(f16 hi, f16 lo, float d, float rest, float sum) {
-  if constexpr (PRODUCTS == 3) return __builtin_fmaf(d, join(hi, lo), sum);
+  if constexpr (PRODUCTS > 1) return __builtin_fmaf(d, join(hi, lo), sum);
   return __builtin_fmaf(rest * (1.0f / kLo), (float)lo, __builtin_fmaf(d, (float)hi, sum));
 }
 
@@ -831,7 +834,8 @@ __device__ __forceinline__ f16x8 off_diagonal(f16x8 x, bool on, int r) {
   return __builtin_bit_cast(f16x8, w);
 }
 
-// Three products instead of one: hi lo + lo hi, scaled down, + hi hi.
+// Three products instead of one: hi lo + lo hi, scaled down, + hi hi.  Two: P
+// hi alone, Q's both halves.
 template <typename T, bool XQ, int PRODUCTS, typename F>
 __device__ __forceinline__ void products(F operands, f16* shared,
                                          f32x4 (&acc)[T::FI][T::FJ]) {
@@ -841,13 +845,13 @@ __device__ __forceinline__ void products(F operands, f16* shared,
     for (int j = 0; j < T::FJ; ++j) acc[i][j] = (f32x4){0, 0, 0, 0};
 #pragma unroll 1
   for (int pass = 0; pass < PRODUCTS; ++pass) {
-    if (PRODUCTS == 3 && pass == 2) {
+    if (PRODUCTS > 1 && pass == PRODUCTS - 1) {
 #pragma unroll
       for (int i = 0; i < T::FI; ++i)
 #pragma unroll
         for (int j = 0; j < T::FJ; ++j) acc[i][j] = acc[i][j] * (1.0f / kLo);
     }
-    product(operands(PRODUCTS == 3 && pass == 1, PRODUCTS == 3 && pass == 0), shared, acc);
+    product(operands(PRODUCTS == 3 && pass == 1, PRODUCTS > 1 && pass == 0), shared, acc);
   }
 }
 
@@ -1244,7 +1248,10 @@ void launch_sym(const Group& g, int size, hipStream_t s, const GemmArgs& a) {
 template <bool LAST, int PRODUCTS, int DST, bool MUON>
 void launch_apply(const Group& g, int size, hipStream_t s, const GemmArgs& a) {
   const dim3 grid(g.app_blocks[size]);
-  if (size == kBig)
+  if constexpr (PRODUCTS == 2) {  // short sides of one tile
+    hipLaunchKernelGGL((zf_ns_apply<Little, kLittle, LAST, PRODUCTS, DST, MUON>),
+                       dim3(g.app_blocks[kLittle]), dim3(Little::kThreads), 0, s, a);
+  } else if (size == kBig)
     hipLaunchKernelGGL((zf_ns_apply<Big, kBig, LAST, PRODUCTS, DST, MUON>), grid,
                        dim3(Big::kThreads), 0, s, a);
   else if (size == kMiddle)
@@ -1277,7 +1284,8 @@ void launch_last(const Group& g, int size, hipStream_t s, int32_t dst, bool muon
 // 15 m^2 (n - m) operations, every pair 3 m^2 (n - m) less.  A pair sees the
 // small singular values through their squares, which A's rounding drowns, so
 // pairs and single steps take turns.
-//   Three products: 2, 1, 2, as exact as single steps.
+//   Three products: 2, 1, 2, as exact as single steps but for short sides
+// under 32 (7 x 1198: 3e-6 against 1.5e-6).
 //   One product: 2, 1, 1, 1, for short sides of kPairSide and more: errors up to
 // 1.5e-3 at 64 to 600, as with single steps, but 1.7e-3 at 48, 2.0e-3 at 32 and
 // 5e-3 at 11, where single steps keep 1.6e-3.  A later pair costs accuracy at
@@ -1286,7 +1294,7 @@ void launch_last(const Group& g, int size, hipStream_t s, int32_t dst, bool muon
 // two layers of hidden 2048, 2, 1, 2 is 10 percent faster.
 // The number of products and the short side decide, so that a matrix's result
 // does not depend on the others of the call.
-template <int PRODUCTS>
+template <int PRODUCTS, int APPLY>
 int iterate(const Group& g, const Mat* mats, const zf_ns_params& p, int sym, int app, int32_t dst,
             bool muon, hipStream_t s, GemmArgs a) {
   auto firsts = [&](int32_t (*of)(const Mat&, int), int size) {
@@ -1327,8 +1335,8 @@ int iterate(const Group& g, const Mat* mats, const zf_ns_params& p, int sym, int
     if (n == 2) a.ca *= a.ca;
     firsts(along, app);
     k += n;
-    if (k == p.steps) launch_last<PRODUCTS>(g, app, s, dst, muon, a);
-    else launch_apply<false, PRODUCTS, ZF_F32, false>(g, app, s, a);
+    if (k == p.steps) launch_last<APPLY>(g, app, s, dst, muon, a);
+    else launch_apply<false, APPLY, ZF_F32, false>(g, app, s, a);
     a.turn ^= 1;
     if (!hip_ok(hipGetLastError())) return ZF_EHIP;
   }
@@ -1360,7 +1368,7 @@ int tile_size(const int32_t (&n)[3]) {
 // Small matrices: the whole iteration in one block, X and one symmetric
 // matrix in shared memory, one launch for all of them.  Such a matrix would
 // spend its time in launches (128 x 128: 20 of them, 190 us); here a step is
-// three products between barriers (53 us, with three products for each 98).
+// three products between barriers (58 us, with three products for each 98).
 // Each of the 8 waves takes a block of 2 x
 // CJ tiles of 16 x 16 of X (2 x 4 of S, both triangles: cheaper than
 // mirroring one), so that a fragment read from shared memory serves several
@@ -1617,7 +1625,7 @@ __global__ __launch_bounds__(kSmallThreads) void zf_ns_small(SmallArgs a) {
           if (i + r == j) v[r] = combine<true>(sum[r], 0.0f, 0.0f, di[r], dj, true, a.ca, a.cb, a.cc);
       }
     });
-    const bool last = step + 1 == a.steps, early = step + kLast < a.steps;
+    const bool last = step + 1 == a.steps;
     f32x4 acc[2][CJ], low[2][CJ];
     int pi[2], pj[CJ];
 #pragma unroll
@@ -1644,17 +1652,16 @@ __global__ __launch_bounds__(kSmallThreads) void zf_ns_small(SmallArgs a) {
 #pragma unroll
       for (int j = 0; j < CJ; ++j) {
         x[j] = turned(xh + pj[j] + k * lx);
-        if constexpr (PRODUCTS == 3) xr[j] = turned(xl + pj[j] + k * lx);
+        xr[j] = turned(xl + pj[j] + k * lx);
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < CJ; ++j) {
           acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[j], y[i], acc[i][j], 0, 0, 0);
-          if constexpr (PRODUCTS == 3) {
+          if constexpr (PRODUCTS == 3)
             low[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[j], yr[i], low[i][j], 0, 0, 0);
-            low[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xr[j], y[i], low[i][j], 0, 0, 0);
-          }
+          low[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xr[j], y[i], low[i][j], 0, 0, 0);
         }
     }
 #pragma unroll
@@ -1667,11 +1674,10 @@ __global__ __launch_bounds__(kSmallThreads) void zf_ns_small(SmallArgs a) {
         const int p = ii * lx + min(jx + j, tn - 1) * 16 + 4 * g;
         const f16x4 h = *reinterpret_cast<const f16x4*>(xh + p);
         const f16x4 w = *reinterpret_cast<const f16x4*>(xl + p);
-        if constexpr (PRODUCTS == 3) acc[i][j] = acc[i][j] + low[i][j] * (1.0f / kLo);
+        acc[i][j] = acc[i][j] + low[i][j] * (1.0f / kLo);
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          acc[i][j][r] = linear<PRODUCTS>(h[r], w[r], di, early ? a.ca : di,
-                                          acc[i][j][r] * kUnscale);
+          acc[i][j][r] = __builtin_fmaf(di, join(h[r], w[r]), acc[i][j][r] * kUnscale);
       }
     }
     __syncthreads();
@@ -1732,6 +1738,11 @@ constexpr int64_t kMaxSide = 1ll << 20;
 constexpr int64_t kOwnNorm = 512;
 
 constexpr int kPairSide = 64;  // shortest side of pairs with one product
+
+// Classes of matrices: one product by single steps (short sides of one tile)
+// or a pair first, three products, held in shared memory.
+enum { kSingle, kPairs, kThree, kHeld, kClasses };
+static_assert(kPairSide <= Little::BM, "short sides of one tile");
 
 int small_tiles_of(const zf::ns::Shape& s) {
   return small_tiles(std::min(s.rows, s.cols), std::max(s.rows, s.cols));
@@ -1803,9 +1814,6 @@ bool zf::ns::layout(const Shape* shapes, int64_t count, int products, int32_t th
     used += round_up(bytes, 256);
     return o;
   };
-  // by class: one product by single steps or a pair first, three products,
-  // held in shared memory
-  enum { kSingle, kPairs, kThree, kHeld, kClasses };
   auto class_of = [&](const Shape& s) {
     if (small_tiles_of(s) > 0) return kHeld;
     const int64_t m = std::min(s.rows, s.cols), n = std::max(s.rows, s.cols);
@@ -1952,10 +1960,10 @@ int zf::ns::enqueue(const Layout& l, const zf_ns_params& p, int small_products, 
     GemmArgs ga;
     ga.c = c;
     ga.io = la.io;
-    const int sym = tile_size(g.tri_blocks), app = tile_size(g.app_blocks);
-    const int rc = g.products == 3
-                       ? iterate<3>(g, l.mats.data() + g.first, p, sym, app, dst_dtype, io != nullptr, s, ga)
-                       : iterate<1>(g, l.mats.data() + g.first, p, sym, app, dst_dtype, io != nullptr, s, ga);
+    const int sym = tile_size(g.tri_blocks);
+    const int app = g.kind == kSingle ? kLittle : tile_size(g.app_blocks);
+    const auto run = g.kind == kThree ? iterate<3, 3> : g.kind == kPairs ? iterate<1, 1> : iterate<1, 2>;
+    const int rc = run(g, l.mats.data() + g.first, p, sym, app, dst_dtype, io != nullptr, s, ga);
     if (rc != ZF_OK) return rc;
   }
   return ZF_OK;

@@ -541,12 +541,12 @@ int zf_offload_step(const zf_plan* plan, const zf_hparams* hp, const zf_offload_
  * rounded to 11 bits (fp16 with a common power-of-two factor; sums and the
  * diagonals of A and of its polynomial are binary32, and the linear term
  * takes X with 22 bits).  The result of the default steps is 5e-5 to 1.6e-3
- * from the exact one (|error|_F / |X|_F, measured), up to 2.2e-3 for short
+ * from the exact one (|error|_F / |X|_F, measured), up to 3e-3 for short
  * sides under 32, whatever the singular values; bf16's own rounding is
  * 1.7e-3.  3: operands are sums of two fp16 numbers, about 22 bits, for three
- * times the work; the result is as exact as the iteration in 32-bit
- * arithmetic: about 1e-6, and up to 1e-4 where the smallest singular values
- * vanish beside the largest, because errors grow with them (3.4^5 times).
+ * times the work; the result is 1e-6 to 5e-6 from the exact one, and up to
+ * 1e-4 where the smallest singular values vanish beside the largest, because
+ * errors grow with them (3.4^5 times), as they do in 32-bit arithmetic.
  * 0: 1 for a ZF_BF16 result, else 3; in zf_muon_step 1, but 3 for matrices
  * that fit in a compute unit's shared memory (up to 128 x 128) and for thin
  * ones (one side at most 32, the other at most 16384), and for all matrices

@@ -113,3 +113,16 @@ def test_alone_and_among_others(zf, shape, large, dst):
     xs = others + [x]
     among = run(zf, xs, [torch.empty_like(z, dtype=dst) for z in xs])[-1]
     assert torch.equal(G.bits_view(alone), G.bits_view(among))
+
+
+@pytest.mark.parametrize("shape", [(1, 77), (65, 1), (1, 1000), (3000, 1), (1, 8191)])
+def test_rows_and_columns_with_one_product(zf, shape):
+    """One singular value s, A = |hi|^2 the only inexact number: off by 2 * 0.41
+    * 2^-11 / sqrt(n / 3) in the mean for n normal elements, so under 1e-4 a
+    step, of which five steps at a slope of up to 1.7 make 7e-4: 2^-10."""
+    for seed in range(5):
+        x = torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).cuda()
+        y = run(zf, [x], [torch.empty_like(x)], zf.ns_params(products=1))[0]
+        err = off(y, plain(x))
+        G.say(f"{shape}: {err:.2e}")
+        assert err <= 2.0 ** -10
