@@ -37,8 +37,9 @@
 // throughout, one strong direction comes to 5e-3 to 4e-2; bf16 throughout:
 // 1e-2 to 3e-2).  A result in more bits than bf16 gets three
 // products instead of one: every operand is the sum of two fp16 numbers,
-// hi + lo * 2^-11, and hi hi + hi lo + lo hi holds about 22 bits, as exact as
-// the iteration in 32-bit arithmetic: 1e-6, to 1e-4 for one strong direction.
+// hi + lo * 2^-11, and hi hi + hi lo + lo hi holds about 22 bits: 1e-6, 5e-6
+// for short sides under 32, and 1e-4 for one strong direction, as the
+// iteration in 32-bit arithmetic has there.
 #include "zf_ortho.h"
 
 #include <algorithm>
@@ -338,8 +339,8 @@ __global__ __launch_bounds__(kThreads) void zf_ns_norm(Common c) {
 // X in 16-bit halves from the matrix and its inverse norm, transposed if the
 // matrix is tall (by tiles of 64 x 64), with zero padding.  Non-temporal
 // stores: 143 -> 85 us for a layer of hidden 2048.  Two such layers from bf16
-// take 215 us, 5 bytes an element at 2.8 TB/s; from momenta and sums 345 us,
-// 11 at 3.9.
+// take 225 us, 6 bytes an element at 3.2 TB/s; from momenta and sums 364 us,
+// 12 at 4.0.
 template <int SRC, bool OWN_NORM>
 __global__ __launch_bounds__(kThreads) void zf_ns_prep(LoadArgs a) {
   if (a.c.st && a.c.st->skipped) return;
@@ -861,7 +862,7 @@ __device__ __forceinline__ void products(F operands, f16* shared,
 //   kMul   S_out = S_in0 S_in1 (which commute: polynomials of one matrix)
 // A symmetric matrix is diag(D) + O, with O in 16 bits.
 // Two layers of hidden 2048 / intermediate 8192 (14 matrices), a symmetric
-// result counted once: kGram 304 us, 800 TFLOP/s; kPoly and kMul 125 us, 690.
+// result counted once: kGram 310 us, 785 TFLOP/s; kPoly and kMul 128 us, 675.
 // The main loops alone take 250 and 78 us; the rest is the epilogue's traffic
 // and the last round of blocks, which is partly empty.  1024 x 1024: 8.6 us
 // each, a launch and the latency of 16 steps.
@@ -1086,8 +1087,8 @@ __device__ __forceinline__ void write_square(const GemmArgs& a, const Mat& m,
 
 // The same for the Muon step where rows of the weights keep 16-byte alignment:
 // 4 rows of 64 weights an instruction, 32 rows on their way together (a row
-// an instruction, 8 together: 602 us instead of 343 for the last product of
-// 71M weights, where the others, without 7 bytes an element, take 222).
+// an instruction, 8 together: 602 us instead of 344 for the last product of
+// 71M weights, where the others, without 6 bytes an element, take 241).
 template <int DST, int LINES>
 __device__ __forceinline__ void update_square(const GemmArgs& a, const Mat& m,
                                               const ZF_LDS float* square, int i0, int j0,
@@ -1133,7 +1134,7 @@ __device__ __forceinline__ void update_square(const GemmArgs& a, const Mat& m,
 
 // X <- S X with S = S_in0: D_i X_ij from both halves of X, and O X; LAST:
 // into the destination, or W <- W dec - rate (S X).
-// The same two layers: 560 us, 865 TFLOP/s; the main loop alone 414 us, the
+// The same two layers: 590 us, 820 TFLOP/s; the main loop alone 414 us, the
 // rest is 8 bytes an element in and out after it (14 with Muon's weights).
 // Starting the XCDs or the blocks apart from each other, so that these do not
 // come at once, gains nothing: rows of X leave the second-level caches.
