@@ -31,13 +31,13 @@
 // and for short sides of one tile, lo goes through the product as well,
 // (a + D + O) X: with few singular values a lo alone costs up to 2e-3 (1 x 77:
 // 1.4e-3 against 1e-4).
-// Measured in |.|_F against 64 bits, over flat, low-rank, low-rank-plus-noise
-// and 1/i spectra and short sides of 4 to 2048: 5e-5 to 1.6e-3, 2.2e-3 for a
-// short side of 4 (with 14 bits of X in the linear term and lo times a + D
-// throughout, one strong direction comes to 5e-3 to 4e-2; bf16 throughout:
-// 1e-2 to 3e-2).  A result in more bits than bf16 gets three
-// products instead of one: every operand is the sum of two fp16 numbers,
-// hi + lo * 2^-11, and hi hi + hi lo + lo hi holds about 22 bits: 1e-6, 5e-6
+// Measured in |.|_F against 64 bits, over flat, low-rank, low-rank-plus-noise,
+// 1/i and log-uniform spectra, sparse matrices and rows of different scales:
+// 5e-5 to 2e-3, up to 3e-3 for short sides under 32 (with 14 bits of X in the
+// linear term and lo times a + D throughout, one strong direction comes to
+// 5e-3 to 4e-2; bf16 throughout: 1e-2 to 3e-2).  A result in more bits than
+// bf16 gets three products instead of one: every operand is the sum of two fp16
+// numbers, hi + lo * 2^-11, and hi hi + hi lo + lo hi holds about 22 bits: 1e-6, 5e-6
 // for short sides under 32, and 1e-4 for one strong direction, as the
 // iteration in 32-bit arithmetic has there.
 #include "zf_ortho.h"

@@ -540,7 +540,7 @@ int zf_offload_step(const zf_plan* plan, const zf_hparams* hp, const zf_offload_
  * products: how exactly the matrix products are computed.  1: operands are
  * rounded to 11 bits (fp16 with a common power-of-two factor; sums and the
  * diagonals of A and of its polynomial are binary32, and the linear term
- * takes X with 22 bits).  The result of the default steps is 5e-5 to 1.6e-3
+ * takes X with 22 bits).  The result of the default steps is 5e-5 to 2e-3
  * from the exact one (|error|_F / |X|_F, measured), up to 3e-3 for short
  * sides under 32, whatever the singular values; bf16's own rounding is
  * 1.7e-3.  3: operands are sums of two fp16 numbers, about 22 bits, for three

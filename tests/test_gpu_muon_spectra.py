@@ -126,3 +126,34 @@ def test_rows_and_columns_with_one_product(zf, shape):
         err = off(y, plain(x))
         G.say(f"{shape}: {err:.2e}")
         assert err <= 2.0 ** -10
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_random_shapes_and_kinds(zf, seed):
+    """Sparse matrices, rows of different scales, one large element and random
+    ranks over noise, in batches of random shapes."""
+    g = torch.Generator().manual_seed(1000 + seed)
+
+    def number(lo, hi):
+        return int(round(math.exp(math.log(lo) + math.log(hi / lo) * torch.rand(1, generator=g).item())))
+    xs = []
+    for k in range(12):
+        r, c = number(1, 1500), number(1, 2500)
+        x = torch.randn(r, c, generator=g)
+        if k % 4 == 0:
+            x = x * (torch.rand(r, c, generator=g) < 0.02)
+            x[number(1, r) - 1, 0] = 1.0
+        elif k % 4 == 1:
+            x = x * 10 ** (-3 * torch.rand(r, 1, generator=g))
+        elif k % 4 == 2:
+            x[0, 0] *= 1000.0
+        else:
+            n = number(1, min(r, c))
+            x = torch.randn(r, n, generator=g) @ torch.randn(n, c, generator=g) + 1e-3 * x
+        xs.append(x.cuda())
+    for products in (1, 3):
+        ys = run(zf, xs, [torch.empty_like(x) for x in xs], zf.ns_params(products=products))
+        for x, y in zip(xs, ys):
+            err = off(y, plain(x))
+            G.say(f"{tuple(x.shape)} products={products}: {err:.2e}")
+            assert err <= tolerance(products, *x.shape), tuple(x.shape)
