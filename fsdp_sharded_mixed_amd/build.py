@@ -1,7 +1,9 @@
 """Compile the HIP libraries in-tree for gfx950.
 
 libzf.so         the step (planner + kernels + C ABI, include/zf.h), Muon
-                 (orthogonalisation, the Muon step) and the host side of
+                 (orthogonalisation, the Muon step), the forward and backward
+                 calls beside the step (embedding, norms, 8-bit checkpoints,
+                 weight gradients) and the host side of
                  ZeRO-Offload (CPU-Adam, the offload step)
 libzf_inputs.so  the seeded input generator (include/zf_inputs.h)
 libzf_window_test.so
@@ -62,7 +64,8 @@ def _libraries():
         return os.path.join(CSRC, f)
     step = [(c(f), "hip", (), "") for f in
             ("zf_step.hip", "zf_backward.hip", "zf_gather.hip", "zf_offload.hip", "zf_ortho.hip",
-             "zf_muon.hip")]
+             "zf_muon.hip", "zf_act8.hip", "zf_embedding.hip", "zf_norm.hip",
+             "zf_weight_grad.hip")]
     host = [(c(f), "c++", (), "") for f in ("zf_plan.cpp", "zf_cpu_adam.cpp")]
     window = ("-DZF_TEST_CACHED_SUMS_MB=1",)
     return [

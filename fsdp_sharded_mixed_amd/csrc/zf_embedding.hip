@@ -1,0 +1,507 @@
+// zf_embedding.hip -- the embedding lookup with scaling and its gradient.
+//
+// The gradient of row v is scale times the sum of dout[t] over the tokens t
+// with ids[t] = v.  Tokens are sorted by id (stable, so a row's tokens stay in
+// order), the sorted positions are cut into spans of equal length, and a group
+// of lanes adds its span's rows of dout in registers, writing a row of the
+// gradient where its run of equal ids ends.  A run that a span cuts leaves
+// partial sums, which a last launch adds in order.  So no float is added
+// atomically, and a token that fills a tenth of the batch takes as many groups
+// as it needs.
+//
+// Bound by HBM: dout is read once, each touched row written (or read and
+// written) once.  The sort moves 16 bytes a token and pass.  Where the
+// gradient is stored, the rows without tokens are cleared by blocks of the
+// first launch, beside the sort's first pass.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "zf_hip_status.h"
+#include "zf_rows.h"
+
+namespace {
+
+using namespace zf::dev;
+using zf::hip_ok;
+using zf::kThreads;
+
+// ids as keys: one outside the vocabulary becomes vocab, the last one.
+__device__ __forceinline__ uint32_t key_of(const void* ids, bool wide, int64_t t, uint32_t vocab) {
+  const uint64_t v = wide ? static_cast<const uint64_t*>(ids)[t]
+                          : (uint64_t) static_cast<const uint32_t*>(ids)[t];
+  return v < vocab ? (uint32_t)v : vocab;
+}
+
+// ---------------------------------------------------------------------------
+// Lookup.
+
+struct LookupArgs {
+  const void* ids;
+  const void* table;
+  void* out;
+  int64_t out_ld, tokens, cols;
+  float scale;
+  uint32_t vocab;
+  int32_t wide, log_lanes;
+};
+
+template <int TDT, int DT>
+__global__ __launch_bounds__(kThreads) void zf_embedding_kernel(LookupArgs a) {
+  const int lanes = 1 << a.log_lanes, per = kThreads >> a.log_lanes;
+  const int64_t j = ((int64_t)blockIdx.y * lanes + (threadIdx.x & (lanes - 1))) * kChunk;
+  const int n = (int)min((int64_t)kChunk, a.cols - j);
+  if (n <= 0) return;
+  int64_t t = (int64_t)blockIdx.x * per + (threadIdx.x >> a.log_lanes);
+  for (; t < a.tokens; t += (int64_t)gridDim.x * per) {
+    const uint32_t v = key_of(a.ids, a.wide, t, a.vocab);
+    float x[kChunk];
+#pragma unroll
+    for (int k = 0; k < kChunk; ++k) x[k] = 0;
+    if (v < a.vocab) load8<TDT>(a.table, (int64_t)v * a.cols + j, n, x);
+#pragma unroll
+    for (int k = 0; k < kChunk; ++k) x[k] = v < a.vocab ? x[k] * a.scale : 0.0f;
+    store8<DT, true>(a.out, t * a.out_ld + j, n, x);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Sort of the tokens by id: by 9 bits or fewer a pass, from the lowest.  A
+// block takes `items` consecutive tokens, its waves consecutive parts of them.
+// A pass needs how many of each digit every block holds: the first launch
+// counts them for the first pass, and each pass counts for the next one while
+// it writes.
+
+constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
+constexpr int kBins = 512;
+
+struct SortArgs {
+  const void* ids;
+  uint32_t* keys[2];
+  uint32_t* places[2];
+  uint32_t* counts;  // [passes][blocks][bins]
+  void* grad;        // to clear, or NULL
+  int64_t tokens, cols;
+  int64_t clear_rows;  // rows of the table that a clearing block looks after
+  uint32_t vocab;
+  int32_t wide, blocks, items, bits, passes, gdt;
+};
+
+__device__ __forceinline__ uint32_t digit(uint32_t key, int pass, int bits) {
+  return key >> (pass * bits) & ((1u << bits) - 1);
+}
+
+// Rows of the gradient that no token of the batch has become zero.
+__device__ __forceinline__ void clear_rows(const SortArgs& a, int block) {
+  extern __shared__ uint32_t seen[];
+  const int64_t r0 = block * a.clear_rows;
+  const int64_t rows = min(a.clear_rows, (int64_t)a.vocab - r0);
+  if (rows <= 0) return;
+  const int words = (int)((rows + 31) / 32);
+  for (int k = threadIdx.x; k < words; k += kSortThreads) seen[k] = 0;
+  __syncthreads();
+  for (int64_t t = threadIdx.x; t < a.tokens; t += kSortThreads) {
+    const int64_t r = (int64_t)key_of(a.ids, a.wide, t, a.vocab) - r0;
+    if (r >= 0 && r < rows) atomicOr(&seen[r >> 5], 1u << (r & 31));
+  }
+  __syncthreads();
+  const int eb = a.gdt == ZF_F32 ? 4 : 2;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  for (int64_t r = wave; r < rows; r += kSortWaves) {
+    if (seen[r >> 5] >> (r & 31) & 1) continue;
+    char* p = static_cast<char*>(a.grad) + (r0 + r) * a.cols * eb;
+    const int64_t bytes = a.cols * eb;
+    for (int64_t k = lane * 16; k < bytes; k += 64 * 16) {
+      if (k + 16 <= bytes) {
+        store_any<true, u32x4_any>(p + k, (u32x4){0, 0, 0, 0});
+      } else {
+        for (int64_t e = k; e < bytes; e += 2) *reinterpret_cast<uint16_t*>(p + e) = 0;
+      }
+    }
+  }
+}
+
+__global__ __launch_bounds__(kSortThreads) void zf_sort_count(SortArgs a) {
+  if ((int)blockIdx.x >= a.blocks) return clear_rows(a, blockIdx.x - a.blocks);
+  __shared__ uint32_t count[kBins];
+  const int bins = 1 << a.bits;
+  for (int k = threadIdx.x; k < bins; k += kSortThreads) {
+    count[k] = 0;
+    for (int p = 1; p < a.passes; ++p)
+      a.counts[((int64_t)p * a.blocks + blockIdx.x) * bins + k] = 0;
+  }
+  __syncthreads();
+  const int64_t t0 = (int64_t)blockIdx.x * a.items, t1 = min(t0 + a.items, a.tokens);
+  for (int64_t t = t0 + threadIdx.x; t < t1; t += kSortThreads)
+    atomicAdd(&count[digit(key_of(a.ids, a.wide, t, a.vocab), 0, a.bits)], 1u);
+  __syncthreads();
+  for (int k = threadIdx.x; k < bins; k += kSortThreads)
+    a.counts[(int64_t)blockIdx.x * bins + k] = count[k];
+}
+
+__global__ __launch_bounds__(kSortThreads) void zf_sort_pass(SortArgs a, int pass) {
+  __shared__ uint32_t at[kSortWaves][kBins];
+  __shared__ uint32_t waves[kBins / 64];
+  const int bins = 1 << a.bits, tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const uint32_t* keys = a.keys[(pass + 1) & 1];
+  const uint32_t* places = a.places[(pass + 1) & 1];
+  const int64_t t0 = (int64_t)blockIdx.x * a.items + (int64_t)wave * (a.items / kSortWaves);
+  const int64_t t1 = min(t0 + a.items / kSortWaves, a.tokens);
+  auto key_at = [&](int64_t t) {
+    return pass == 0 ? key_of(a.ids, a.wide, t, a.vocab) : keys[t];
+  };
+  for (int k = tid; k < kSortWaves * kBins; k += kSortThreads) (&at[0][0])[k] = 0;
+  __syncthreads();
+  for (int64_t t = t0 + lane; t < t1; t += 64) atomicAdd(&at[wave][digit(key_at(t), pass, a.bits)], 1u);
+  // a bin's first place: all smaller digits, then this digit in the blocks
+  // before, then in the waves before
+  uint32_t total = 0, before = 0;
+  if (tid < bins) {
+    const uint32_t* c = a.counts + (int64_t)pass * a.blocks * bins + tid;
+    for (int b = 0; b < a.blocks; ++b) {
+      const uint32_t x = c[(int64_t)b * bins];
+      total += x;
+      before += b < (int)blockIdx.x ? x : 0;
+    }
+  }
+  uint32_t upto = total;
+  for (int off = 1; off < 64; off <<= 1) {
+    const uint32_t x = __shfl_up(upto, off, 64);
+    if (lane >= off) upto += x;
+  }
+  if (tid < kBins && lane == 63) waves[wave] = upto;
+  __syncthreads();
+  if (tid < bins) {
+    uint32_t first = upto - total + before;
+    for (int w = 0; w < wave; ++w) first += waves[w];
+    for (int w = 0; w < kSortWaves; ++w) {
+      const uint32_t x = at[w][tid];
+      at[w][tid] = first;
+      first += x;
+    }
+  }
+  __syncthreads();
+  volatile uint32_t* mine = at[wave];
+  const bool last = pass + 1 == a.passes;
+  for (int64_t r = t0; r < t1; r += 64) {  // the wave's lanes together
+    const int64_t t = r + lane;
+    const bool in = t < t1;
+    const uint32_t key = in ? key_at(t) : 0, d = digit(key, pass, a.bits);
+    uint64_t same = __ballot(in);
+    for (int b = 0; b < a.bits; ++b) {
+      const uint64_t one = __ballot(d >> b & 1);
+      same &= (d >> b & 1) ? one : ~one;
+    }
+    const int rank = __popcll(same & ((1ull << lane) - 1));
+    const uint32_t to = in ? mine[d] + rank : 0;
+    __builtin_amdgcn_wave_barrier();
+    if (in && rank == 0) mine[d] = to + (uint32_t)__popcll(same);
+    __builtin_amdgcn_wave_barrier();
+    if (in) {
+      a.keys[pass & 1][to] = key;
+      a.places[pass & 1][to] = pass == 0 ? (uint32_t)t : places[t];
+      if (!last)
+        atomicAdd(&a.counts[((int64_t)(pass + 1) * a.blocks + to / (uint32_t)a.items) * bins +
+                            digit(key, pass + 1, a.bits)], 1u);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Sums of the runs.
+
+struct RunArgs {
+  const uint32_t* keys;
+  const uint32_t* places;
+  const void* dout;
+  void* grad;
+  float* partial;  // [spans][2][cols]: of a run that began before its span, and of one that goes on after it
+  int64_t dout_ld, tokens, cols, spans;
+  float scale;
+  uint32_t vocab;
+  int32_t log_lanes, length, gdt, accumulate;
+};
+
+__device__ __forceinline__ void write_row(const RunArgs& a, uint32_t v, int64_t j, int n,
+                                          const float (&sum)[kChunk]) {
+  const int64_t at = (int64_t)v * a.cols + j;
+  float x[kChunk], old[kChunk];
+#pragma unroll
+  for (int k = 0; k < kChunk; ++k) x[k] = sum[k] * a.scale;
+  if (a.accumulate) {
+    load8_of(a.gdt, a.grad, at, n, old);
+#pragma unroll
+    for (int k = 0; k < kChunk; ++k) x[k] += old[k];
+  }
+  if (a.gdt == ZF_F32) store8<ZF_F32>(a.grad, at, n, x);
+  else if (a.gdt == ZF_BF16) store8<ZF_BF16>(a.grad, at, n, x);
+  else store8<ZF_F16>(a.grad, at, n, x);
+}
+
+template <int DT>
+__global__ __launch_bounds__(kThreads) void zf_run_sums(RunArgs a) {
+  const int lanes = 1 << a.log_lanes, per = kThreads >> a.log_lanes;
+  const int64_t j = ((int64_t)blockIdx.y * lanes + (threadIdx.x & (lanes - 1))) * kChunk;
+  const int n = (int)min((int64_t)kChunk, a.cols - j);
+  if (n <= 0) return;
+  int64_t span = (int64_t)blockIdx.x * per + (threadIdx.x >> a.log_lanes);
+  for (; span < a.spans; span += (int64_t)gridDim.x * per) {
+    const int64_t p0 = span * a.length, p1 = min(p0 + a.length, a.tokens);
+    uint32_t cur = a.keys[p0];
+    bool head = p0 > 0 && a.keys[p0 - 1] == cur;
+    float sum[kChunk];
+#pragma unroll
+    for (int k = 0; k < kChunk; ++k) sum[k] = 0;
+    auto flush = [&](bool tail) {
+      if (cur >= a.vocab) return;
+      if (head || tail) store8<ZF_F32>(a.partial + (span * 2 + (head ? 0 : 1)) * a.cols, j, n, sum);
+      else write_row(a, cur, j, n, sum);
+    };
+    constexpr int U = 8;  // rows on their way together
+    for (int64_t p = p0; p < p1; p += U) {
+      Raw<DT> r[U];
+      uint32_t key[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        key[u] = p + u < p1 ? a.keys[p + u] : a.vocab;
+        if (key[u] < a.vocab)
+          r[u] = load_raw<DT, true>(a.dout, (int64_t)a.places[p + u] * a.dout_ld + j, n);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (p + u >= p1) break;
+        if (key[u] != cur) {
+          flush(false);
+#pragma unroll
+          for (int k = 0; k < kChunk; ++k) sum[k] = 0;
+          cur = key[u];
+          head = false;
+        }
+        if (key[u] < a.vocab) {
+          float x[kChunk];
+          widen8<DT>(r[u], x);
+#pragma unroll
+          for (int k = 0; k < kChunk; ++k) sum[k] += x[k];
+        }
+      }
+    }
+    flush(p1 < a.tokens && a.keys[p1] == cur);
+  }
+}
+
+// Runs that spans cut: the block of the span where one begins adds its partial
+// sums, 8 of them at a time, 32 lanes of 8 columns each, then the 8 in order.
+__global__ __launch_bounds__(kThreads) void zf_run_join(RunArgs a) {
+  constexpr int kLanes = 32, kRows = kThreads / kLanes;
+  __shared__ float s[kRows][kChunk][kLanes];
+  for (int64_t span = blockIdx.x; span + 1 < a.spans; span += gridDim.x) {
+    const int64_t p0 = span * a.length, p1 = p0 + a.length;
+    const uint32_t key = a.keys[p1 - 1];
+    if (key >= a.vocab || a.keys[p1] != key || (p0 > 0 && a.keys[p0 - 1] == key)) continue;
+    int64_t lo = p1, hi = a.tokens;  // the run's end
+    while (lo < hi) {
+      const int64_t mid = (lo + hi) / 2;
+      if (a.keys[mid] <= key) lo = mid + 1;
+      else hi = mid;
+    }
+    const int64_t last = (lo - 1) / a.length;
+    const int lane = threadIdx.x % kLanes, row = threadIdx.x / kLanes;
+    const int64_t j = ((int64_t)blockIdx.y * kLanes + lane) * kChunk;
+    const int n = (int)min((int64_t)kChunk, a.cols - j);
+    float sum[kChunk], x[kChunk];
+#pragma unroll
+    for (int k = 0; k < kChunk; ++k) sum[k] = 0;
+    if (n > 0) {
+#pragma unroll 4
+      for (int64_t c = span + row; c <= last; c += kRows) {
+        load8<ZF_F32>(a.partial + (c * 2 + (c == span ? 1 : 0)) * a.cols, j, n, x);
+#pragma unroll
+        for (int k = 0; k < kChunk; ++k) sum[k] += x[k];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kChunk; ++k) s[row][k][lane] = sum[k];
+    __syncthreads();
+    if (row > 0 || n <= 0) continue;
+#pragma unroll
+    for (int r = 1; r < kRows; ++r)
+#pragma unroll
+      for (int k = 0; k < kChunk; ++k) sum[k] += s[r][k][lane];
+    write_row(a, key, j, n, sum);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side.
+
+// 2^log lanes of 8 columns, up to a block.
+int log_lanes_of(int64_t cols) {
+  int log = 0;
+  while (log < 8 && ((int64_t)kChunk << log) < cols) ++log;
+  return log;
+}
+
+struct GradPlan {
+  int32_t blocks, items, bits, passes, length;
+  int64_t spans, clear_blocks, clear_rows;
+  int64_t keys, places, counts, partial, bytes;  // offsets
+};
+
+GradPlan grad_plan(int64_t tokens, int64_t vocab, int64_t cols) {
+  GradPlan g;
+  int width = 1;
+  while (vocab >> width) ++width;
+  g.passes = (width + 8) / 9;
+  g.bits = (width + g.passes - 1) / g.passes;
+  // 4096 tokens a block, more where that would be more than 1024 blocks
+  g.items = (int32_t)(std::max<int64_t>(4, (tokens + (1 << 20) - 1) >> 20) * kSortThreads);
+  g.blocks = (int32_t)((tokens + g.items - 1) / g.items);
+  // spans of 32 tokens, shorter ones where those would be under 2048 waves
+  const int log = log_lanes_of(cols);
+  const int64_t waves = std::max<int64_t>(1, ((int64_t)1 << log) / 64);
+  g.length = 32;
+  while (g.length > 8 && tokens / g.length * waves < 2048) g.length /= 2;
+  g.spans = (tokens + g.length - 1) / g.length;
+  // clearing blocks of half a megabyte and more, and a bit of shared memory a
+  // row (32 KiB at most)
+  g.clear_blocks = std::max<int64_t>(1, std::min<int64_t>(512, vocab * cols >> 18));
+  g.clear_blocks = std::max<int64_t>(g.clear_blocks, (vocab + (1 << 18) - 1) >> 18);
+  g.clear_rows = (vocab + g.clear_blocks - 1) / g.clear_blocks;
+  auto place = [&](int64_t n) {
+    const int64_t at = g.bytes;
+    g.bytes += (n + 255) / 256 * 256;
+    return at;
+  };
+  g.bytes = 0;
+  g.keys = place(tokens * 8);
+  g.places = place(tokens * 8);
+  g.counts = place((int64_t)g.passes * g.blocks * 4 << g.bits);
+  g.partial = place(g.spans > 1 ? g.spans * 2 * cols * 4 : 0);
+  return g;
+}
+
+int sizes_ok(int64_t tokens, int64_t vocab, int64_t cols) {
+  const int rc = shape_ok(tokens, cols);
+  if (rc != ZF_OK) return rc;
+  if (vocab < 1) return ZF_EINVAL;
+  return vocab > ZF_MAX_ROWS ? ZF_ESIZE : ZF_OK;
+}
+
+int ids_ok(const void* ids, int32_t id_bytes, int64_t tokens) {
+  if (id_bytes != 4 && id_bytes != 8) return ZF_EINVAL;
+  if (tokens > 0 && !ids) return ZF_EINVAL;
+  return (reinterpret_cast<uintptr_t>(ids) & (uintptr_t)(id_bytes - 1)) == 0 ? ZF_OK : ZF_EALIGN;
+}
+
+}  // namespace
+
+extern "C" int zf_embedding(const zf_embedding_args* args, void* stream) {
+  if (!args) return ZF_EINVAL;
+  const zf_embedding_args& p = *args;
+  if (!row_dtype(p.table_dtype) || !row_dtype(p.dtype)) return ZF_EDTYPE;
+  int rc = sizes_ok(p.tokens, p.vocab, p.cols);
+  if (rc == ZF_OK) rc = ids_ok(p.ids, p.id_bytes, p.tokens);
+  if (rc == ZF_OK) rc = rows_ok(p.out, p.dtype, p.tokens, p.cols, p.out_stride);
+  if (rc != ZF_OK) return rc;
+  if (p.tokens > 0 && !p.table) return ZF_EINVAL;
+  if (!aligned_to(p.table, p.table_dtype)) return ZF_EALIGN;
+  if (p.tokens == 0) return ZF_OK;
+  const LookupArgs a{p.ids, p.table, p.out, p.out_stride, p.tokens, p.cols, p.scale,
+                     (uint32_t)p.vocab, p.id_bytes == 8, log_lanes_of(p.cols)};
+  const int64_t per = kThreads >> a.log_lanes, span = (int64_t)kChunk << a.log_lanes;
+  const dim3 grid((uint32_t)std::min<int64_t>((p.tokens + per - 1) / per, kMaxBlocks),
+                  (uint32_t)((p.cols + span - 1) / span));
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  (void)hipGetLastError();
+#define ZF_LOOKUP(T, D) hipLaunchKernelGGL((zf_embedding_kernel<T, D>), grid, dim3(kThreads), 0, s, a)
+#define ZF_LOOKUP_TO(T) \
+  do { \
+    if (p.dtype == ZF_F32) ZF_LOOKUP(T, ZF_F32); \
+    else if (p.dtype == ZF_BF16) ZF_LOOKUP(T, ZF_BF16); \
+    else ZF_LOOKUP(T, ZF_F16); \
+  } while (0)
+  if (p.table_dtype == ZF_F32) ZF_LOOKUP_TO(ZF_F32);
+  else if (p.table_dtype == ZF_BF16) ZF_LOOKUP_TO(ZF_BF16);
+  else ZF_LOOKUP_TO(ZF_F16);
+#undef ZF_LOOKUP_TO
+#undef ZF_LOOKUP
+  return hip_ok(hipGetLastError()) ? ZF_OK : ZF_EHIP;
+}
+
+extern "C" int64_t zf_embedding_grad_bytes(int64_t tokens, int64_t vocab, int64_t cols) {
+  const int rc = sizes_ok(tokens, vocab, cols);
+  return rc != ZF_OK ? rc : grad_plan(tokens, vocab, cols).bytes;
+}
+
+extern "C" int zf_embedding_grad(const zf_embedding_grad_args* args, void* stream) {
+  if (!args || args->reserved != 0 || !flag(args->accumulate)) return ZF_EINVAL;
+  const zf_embedding_grad_args& p = *args;
+  if (!row_dtype(p.dtype) || !row_dtype(p.grad_dtype)) return ZF_EDTYPE;
+  int rc = sizes_ok(p.tokens, p.vocab, p.cols);
+  if (rc == ZF_OK) rc = ids_ok(p.ids, p.id_bytes, p.tokens);
+  if (rc == ZF_OK) rc = rows_ok(p.dout, p.dtype, p.tokens, p.cols, p.dout_stride);
+  if (rc != ZF_OK) return rc;
+  if (!p.grad) return ZF_EINVAL;
+  if (!aligned_to(p.grad, p.grad_dtype) || !aligned16(p.workspace)) return ZF_EALIGN;
+  const GradPlan g = grad_plan(p.tokens, p.vocab, p.cols);
+  if (p.tokens > 0 && !p.workspace) return ZF_EINVAL;
+  if (p.workspace_size < g.bytes) return ZF_ESIZE;
+  if (p.tokens == 0 && p.accumulate) return ZF_OK;
+  char* ws = static_cast<char*>(p.workspace);
+  SortArgs so;
+  so.ids = p.ids;
+  for (int k = 0; k < 2; ++k) {
+    so.keys[k] = reinterpret_cast<uint32_t*>(ws + g.keys) + k * p.tokens;
+    so.places[k] = reinterpret_cast<uint32_t*>(ws + g.places) + k * p.tokens;
+  }
+  so.counts = reinterpret_cast<uint32_t*>(ws + g.counts);
+  so.grad = p.grad;
+  so.tokens = p.tokens;
+  so.cols = p.cols;
+  so.clear_rows = g.clear_rows;
+  so.vocab = (uint32_t)p.vocab;
+  so.wide = p.id_bytes == 8;
+  so.blocks = g.blocks;
+  so.items = g.items;
+  so.bits = g.bits;
+  so.passes = g.passes;
+  so.gdt = p.grad_dtype;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  (void)hipGetLastError();
+  const int64_t clear = p.accumulate ? 0 : g.clear_blocks;
+  hipLaunchKernelGGL(zf_sort_count, dim3((uint32_t)(g.blocks + clear)), dim3(kSortThreads),
+                     clear ? (uint32_t)((g.clear_rows + 31) / 32 * 4) : 0, s, so);
+  if (p.tokens > 0) {
+    for (int pass = 0; pass < g.passes; ++pass)
+      hipLaunchKernelGGL(zf_sort_pass, dim3(g.blocks), dim3(kSortThreads), 0, s, so, pass);
+    RunArgs r;
+    r.keys = so.keys[(g.passes - 1) & 1];
+    r.places = so.places[(g.passes - 1) & 1];
+    r.dout = p.dout;
+    r.grad = p.grad;
+    r.partial = reinterpret_cast<float*>(ws + g.partial);
+    r.dout_ld = p.dout_stride;
+    r.tokens = p.tokens;
+    r.cols = p.cols;
+    r.spans = g.spans;
+    r.scale = p.scale;
+    r.vocab = (uint32_t)p.vocab;
+    r.log_lanes = log_lanes_of(p.cols);
+    r.length = g.length;
+    r.gdt = p.grad_dtype;
+    r.accumulate = p.accumulate;
+    const int64_t per = kThreads >> r.log_lanes, span = (int64_t)kChunk << r.log_lanes;
+    const dim3 grid((uint32_t)std::min<int64_t>((g.spans + per - 1) / per, kMaxBlocks),
+                    (uint32_t)((p.cols + span - 1) / span));
+    if (p.dtype == ZF_F32) hipLaunchKernelGGL(zf_run_sums<ZF_F32>, grid, dim3(kThreads), 0, s, r);
+    else if (p.dtype == ZF_BF16) hipLaunchKernelGGL(zf_run_sums<ZF_BF16>, grid, dim3(kThreads), 0, s, r);
+    else hipLaunchKernelGGL(zf_run_sums<ZF_F16>, grid, dim3(kThreads), 0, s, r);
+    if (g.spans > 1)
+      hipLaunchKernelGGL(zf_run_join, dim3((uint32_t)std::min<int64_t>(g.spans - 1, kMaxBlocks),
+                                           (uint32_t)((p.cols + 255) / 256)),
+                         dim3(kThreads), 0, s, r);
+  }
+  return hip_ok(hipGetLastError()) ? ZF_OK : ZF_EHIP;
+}

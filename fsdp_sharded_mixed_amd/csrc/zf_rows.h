@@ -1,0 +1,327 @@
+// zf_rows.h -- pieces shared by the kernels that work on rows of activations
+// (norms, checkpoints, embedding, weight gradients): 8 elements a lane at any
+// alignment, the 8-bit checkpoint's codes and scales, reductions over lanes.
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "zf_device.h"
+#include "zf_internal.h"
+
+namespace zf {
+namespace dev {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+// Wide accesses at any element's address: rows of activations and parameters
+// inside a flat buffer keep their element's alignment only.  gfx950 takes
+// global loads and stores of 8 and 16 bytes there (unaligned access mode,
+// which the HSA runtime sets), so there is one path, not one an alignment.
+typedef u32x4 u32x4_any __attribute__((aligned(1)));
+typedef u32x2 u32x2_any __attribute__((aligned(1)));
+
+constexpr int kChunk = 8;  // consecutive elements of a lane
+// Blocks of a launch along x: a launch holds fewer than 2^32 threads there,
+// so kernels walk further rows in steps of the grid.
+constexpr int64_t kMaxBlocks = 1 << 22;
+
+template <int DT>
+constexpr int kElem = DT == ZF_F32 ? 4 : 2;
+
+inline int elem_bytes(int32_t dt) { return dt == ZF_F32 ? 4 : 2; }
+
+template <bool NT, typename V>
+__device__ __forceinline__ V load_any(const void* p) {
+  if constexpr (NT) return __builtin_nontemporal_load(static_cast<const V*>(p));
+  else return *static_cast<const V*>(p);
+}
+template <bool NT, typename V>
+__device__ __forceinline__ void store_any(void* p, V x) {
+  if constexpr (NT) __builtin_nontemporal_store(x, static_cast<V*>(p));
+  else *static_cast<V*>(p) = x;
+}
+
+template <int DT>
+__device__ __forceinline__ float load1(const void* base, int64_t i) {
+  if constexpr (DT == ZF_F32) return static_cast<const float*>(base)[i];
+  else return widen1<DT>(static_cast<const uint16_t*>(base)[i]);
+}
+// A binary32 value about to be rounded to fp16.  The compiler otherwise joins
+// a product and its rounding into one v_fma_mixlo_f16, which skips binary32's
+// rounding: results would depend on which code it joins.
+__device__ __forceinline__ float settled(float x) {
+  asm("" : "+v"(x));
+  return x;
+}
+template <int DT>
+__device__ __forceinline__ uint16_t narrow(float x) {
+  return narrow1<DT>(DT == ZF_F16 ? settled(x) : x);
+}
+template <int DT>
+__device__ __forceinline__ void store1(void* base, int64_t i, float x) {
+  if constexpr (DT == ZF_F32) static_cast<float*>(base)[i] = x;
+  else static_cast<uint16_t*>(base)[i] = narrow<DT>(x);
+}
+
+// 8 elements of type DT from element i on as the registers hold them; n of
+// them (1..8) exist, the others read as zero.
+template <int DT>
+struct Raw {
+  u32x4 w[DT == ZF_F32 ? 2 : 1];
+};
+template <int DT, bool NT = false>
+__device__ __forceinline__ Raw<DT> load_raw(const void* base, int64_t i, int n) {
+  const char* p = static_cast<const char*>(base) + i * kElem<DT>;
+  Raw<DT> r;
+  if (n >= kChunk) {
+    r.w[0] = load_any<NT, u32x4_any>(p);
+    if constexpr (DT == ZF_F32) r.w[1] = load_any<NT, u32x4_any>(p + 16);
+    return r;
+  }
+  r.w[0] = (u32x4){0, 0, 0, 0};
+  if constexpr (DT == ZF_F32) r.w[1] = (u32x4){0, 0, 0, 0};
+#pragma unroll
+  for (int k = 0; k < kChunk - 1; ++k) {
+    if (k >= n) break;
+    if constexpr (DT == ZF_F32) r.w[k >> 2][k & 3] = reinterpret_cast<const uint32_t*>(p)[k];
+    else r.w[0][k >> 1] |= (uint32_t) reinterpret_cast<const uint16_t*>(p)[k] << (k & 1) * 16;
+  }
+  return r;
+}
+template <int DT>
+__device__ __forceinline__ void widen8(const Raw<DT>& r, float (&v)[kChunk]) {
+#pragma unroll
+  for (int k = 0; k < kChunk; ++k) {
+    if constexpr (DT == ZF_F32) v[k] = __uint_as_float(r.w[k >> 2][k & 3]);
+    else v[k] = (k & 1) ? hi16<DT>(r.w[0][k >> 1]) : lo16<DT>(r.w[0][k >> 1]);
+  }
+}
+template <int DT>
+__device__ __forceinline__ Raw<DT> narrow8(const float (&v)[kChunk]) {
+  Raw<DT> r;
+#pragma unroll
+  for (int k = 0; k < kChunk; k += 2) {
+    if constexpr (DT == ZF_F32) {
+      r.w[k >> 2][k & 3] = __float_as_uint(v[k]);
+      r.w[k >> 2][(k & 3) + 1] = __float_as_uint(v[k + 1]);
+    } else {
+      r.w[0][k >> 1] = (uint32_t)narrow<DT>(v[k]) | (uint32_t)narrow<DT>(v[k + 1]) << 16;
+    }
+  }
+  return r;
+}
+template <int DT, bool NT = false>
+__device__ __forceinline__ void store_raw(void* base, int64_t i, int n, const Raw<DT>& r) {
+  char* p = static_cast<char*>(base) + i * kElem<DT>;
+  if (n >= kChunk) {
+    store_any<NT, u32x4_any>(p, r.w[0]);
+    if constexpr (DT == ZF_F32) store_any<NT, u32x4_any>(p + 16, r.w[1]);
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < kChunk - 1; ++k) {
+    if (k >= n) break;
+    if constexpr (DT == ZF_F32) reinterpret_cast<uint32_t*>(p)[k] = r.w[k >> 2][k & 3];
+    else reinterpret_cast<uint16_t*>(p)[k] = (uint16_t)(r.w[0][k >> 1] >> (k & 1) * 16);
+  }
+}
+template <int DT, bool NT = false>
+__device__ __forceinline__ void load8(const void* base, int64_t i, int n, float (&v)[kChunk]) {
+  widen8<DT>(load_raw<DT, NT>(base, i, n), v);
+}
+template <int DT, bool NT = false>
+__device__ __forceinline__ void store8(void* base, int64_t i, int n, const float (&v)[kChunk]) {
+  store_raw<DT, NT>(base, i, n, narrow8<DT>(v));
+}
+
+// The same with the type known at run time (parameters: once a row or less).
+__device__ __forceinline__ void load8_of(int32_t dt, const void* base, int64_t i, int n,
+                                         float (&v)[kChunk]) {
+  if (dt == ZF_F32) load8<ZF_F32>(base, i, n, v);
+  else if (dt == ZF_BF16) load8<ZF_BF16>(base, i, n, v);
+  else load8<ZF_F16>(base, i, n, v);
+}
+__device__ __forceinline__ float load1_of(int32_t dt, const void* base, int64_t i) {
+  return dt == ZF_F32 ? load1<ZF_F32>(base, i)
+                      : dt == ZF_BF16 ? load1<ZF_BF16>(base, i) : load1<ZF_F16>(base, i);
+}
+__device__ __forceinline__ void store1_of(int32_t dt, void* base, int64_t i, float x) {
+  if (dt == ZF_F32) store1<ZF_F32>(base, i, x);
+  else if (dt == ZF_BF16) store1<ZF_BF16>(base, i, x);
+  else store1<ZF_F16>(base, i, x);
+}
+
+// ---------------------------------------------------------------------------
+// The checkpoint's numbers.  A group of 32 elements lies in 4 neighbouring
+// lanes of 8.  Scales are powers of two, so x / 2^k and code * 2^k are exact
+// (but for what underflows far below e4m3's least step) and the only rounding
+// is the conversion's, to nearest even.
+
+constexpr int kScaleLeast = 27;  // k = -100: every number stays normal in bf16
+
+// Magnitude bits of 8 elements' largest; FINITE: without infinities and NaN.
+template <bool FINITE>
+__device__ __forceinline__ uint32_t amax8(const float (&v)[kChunk]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int k = 0; k < kChunk; ++k) {
+    const uint32_t a = __float_as_uint(v[k]) & 0x7FFFFFFFu;
+    m = max(m, FINITE && a >= 0x7F800000u ? 0u : a);
+  }
+  return m;
+}
+// The largest over each 4 neighbouring lanes (quad_perm 1 0 3 2 and 2 3 0 1).
+__device__ __forceinline__ uint32_t max_quad(uint32_t m) {
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, true));
+  return max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xF, 0xF, true));
+}
+// The scale's byte: k + 127 with k the least integer from -100 on for which
+// the magnitude is at most 448 2^k = 1.75 * 2^(k + 8).
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
+  const int b = (int)(amax >> 23) - 8 + ((amax & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return (uint32_t)max(b, kScaleLeast);
+}
+// 8 codes of finite elements with their group's scale.  At the largest scale
+// of the type DT (f16 k = 8, else 120) the magnitudes end below 256 2^k, which
+// the type does not hold: codes end at 240 there.
+template <int DT>
+__device__ __forceinline__ u32x2 encode8(const float (&v)[kChunk], uint32_t scale) {
+  const float inv = __uint_as_float((254u - scale) << 23);
+  float s[kChunk];
+#pragma unroll
+  for (int k = 0; k < kChunk; ++k) s[k] = v[k] * inv;
+  if (scale == (DT == ZF_F16 ? 135u : 247u)) {
+#pragma unroll
+    for (int k = 0; k < kChunk; ++k) s[k] = fminf(fmaxf(s[k], -240.0f), 240.0f);
+  }
+  u32x2 c;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(s[h * 4], s[h * 4 + 1], 0, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(s[h * 4 + 2], s[h * 4 + 3], w, true);
+    c[h] = (uint32_t)w;
+  }
+  return c;
+}
+__device__ __forceinline__ void decode8(u32x2 c, uint32_t scale, float (&v)[kChunk]) {
+  const float s = __uint_as_float(scale << 23);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c[h], s, false);
+    const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c[h], s, true);
+    v[h * 4] = a.x;
+    v[h * 4 + 1] = a.y;
+    v[h * 4 + 2] = b.x;
+    v[h * 4 + 3] = b.y;
+  }
+}
+
+struct Act8 {
+  uint8_t* codes;
+  uint8_t* scales;
+  int64_t code_ld, scale_ld;
+};
+
+template <bool NT = false>
+__device__ __forceinline__ u32x2 load_codes(const uint8_t* p, int n) {
+  if (n >= kChunk) return load_any<NT, u32x2_any>(p);
+  u32x2 c = {0, 0};
+#pragma unroll
+  for (int k = 0; k < kChunk - 1; ++k)
+    if (k < n) c[k >> 2] |= (uint32_t)p[k] << (k & 3) * 8;
+  return c;
+}
+template <bool NT = false>
+__device__ __forceinline__ void store_codes(uint8_t* p, int n, u32x2 c) {
+  if (n >= kChunk) {
+    store_any<NT, u32x2_any>(p, c);
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < kChunk - 1; ++k)
+    if (k < n) p[k] = (uint8_t)(c[k >> 2] >> (k & 3) * 8);
+}
+
+// Keeps this lane's 8 elements (n of them exist; none: n <= 0) of row i from
+// column j on.  All 4 lanes of a group call it together.
+template <int DT, bool NT = false>
+__device__ __forceinline__ void keep8(const Act8& a, int64_t i, int64_t j, int n,
+                                      const float (&v)[kChunk]) {
+  uint32_t top = n > 0 ? amax8<false>(v) : 0u;
+  const bool odd = top >= 0x7F800000u;  // rare: infinities or NaN among them
+  if (odd) top = amax8<true>(v);
+  const uint32_t scale = scale_byte(max_quad(top));
+  if (n <= 0) return;
+  u32x2 c = encode8<DT>(v, scale);
+  if (odd) {
+#pragma unroll
+    for (int k = 0; k < kChunk; ++k)
+      if (nonfinite(v[k])) c[k >> 2] = (c[k >> 2] & ~(0xFFu << (k & 3) * 8)) | 0x7Fu << (k & 3) * 8;
+  }
+  store_codes<NT>(a.codes + i * a.code_ld + j, n, c);
+  if ((j & (ZF_ACT8_GROUP - 1)) == 0)
+    a.scales[i * a.scale_ld + j / ZF_ACT8_GROUP] = (uint8_t)scale;
+}
+
+// ---------------------------------------------------------------------------
+// Sums over G neighbouring lanes (G a power of two up to 64; every lane ends
+// with the same bits) and over the waves of a block.
+
+template <int G>
+__device__ __forceinline__ float sum_lanes(float x) {
+#pragma unroll
+  for (int off = G / 2; off > 0; off >>= 1) x += __shfl_xor(x, off, 64);
+  return x;
+}
+// Over all threads of a block of 64 W; `slot` is W floats of shared memory
+// that the block's next sum does not use.
+template <int W>
+__device__ __forceinline__ float sum_block(float x, float* slot) {
+  x = sum_lanes<64>(x);
+  if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = x;
+  __syncthreads();
+  float t = slot[0];
+#pragma unroll
+  for (int w = 1; w < W; ++w) t += slot[w];
+  return t;
+}
+
+// ---------------------------------------------------------------------------
+// Argument checks.
+
+inline bool row_dtype(int32_t d) { return d == ZF_F16 || d == ZF_BF16 || d == ZF_F32; }
+inline bool aligned_to(const void* p, int32_t dt) {
+  return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(elem_bytes(dt) - 1)) == 0;
+}
+inline bool flag(int32_t f) { return f == 0 || f == 1; }
+
+// A row-major matrix: rows in [0, ZF_MAX_ROWS], cols in [1, ZF_MAX_COLS].
+inline int shape_ok(int64_t rows, int64_t cols) {
+  if (rows < 0 || cols < 1) return ZF_EINVAL;
+  return rows > ZF_MAX_ROWS || cols > ZF_MAX_COLS ? ZF_ESIZE : ZF_OK;
+}
+// Its rows; a stride's product with the rows must fit an offset in bytes.
+inline int rows_ok(const void* p, int32_t dt, int64_t rows, int64_t cols, int64_t stride) {
+  if (rows > 1 && stride < cols) return ZF_EINVAL;
+  if (rows > 0 && !p) return ZF_EINVAL;
+  if (!aligned_to(p, dt)) return ZF_EALIGN;
+  if (rows > 1 && stride > (int64_t)1 << 31) return ZF_ESIZE;
+  return ZF_OK;
+}
+inline int act8_ok(const zf_act8* a, int64_t rows, int64_t cols) {
+  if (!a || a->rows != rows || a->cols != cols) return ZF_EINVAL;
+  const int64_t groups = (cols + ZF_ACT8_GROUP - 1) / ZF_ACT8_GROUP;
+  if (rows > 0 && (!a->codes || !a->scales)) return ZF_EINVAL;
+  if (rows > 1 && (a->code_stride < cols || a->scale_stride < groups)) return ZF_EINVAL;
+  if (rows > 1 && (a->code_stride > (int64_t)1 << 31 || a->scale_stride > (int64_t)1 << 31))
+    return ZF_ESIZE;
+  return ZF_OK;
+}
+inline Act8 act8_of(const zf_act8* a) {
+  if (!a) return Act8{nullptr, nullptr, 0, 0};
+  return Act8{static_cast<uint8_t*>(a->codes), static_cast<uint8_t*>(a->scales), a->code_stride,
+              a->scale_stride};
+}
+
+}  // namespace dev
+}  // namespace zf

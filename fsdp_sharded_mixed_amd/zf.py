@@ -109,6 +109,54 @@ class MuonHparams(C.Structure):
                 ("nesterov", C.c_int32), ("scale_rule", C.c_int32), ("ns", NsParams)]
 
 
+class EmbeddingArgs(C.Structure):
+    _fields_ = [("table_dtype", C.c_int32), ("dtype", C.c_int32), ("id_bytes", C.c_int32),
+                ("scale", C.c_float), ("tokens", C.c_int64), ("vocab", C.c_int64),
+                ("cols", C.c_int64), ("ids", C.c_void_p), ("table", C.c_void_p),
+                ("out", C.c_void_p), ("out_stride", C.c_int64)]
+
+
+class EmbeddingGradArgs(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("grad_dtype", C.c_int32), ("id_bytes", C.c_int32),
+                ("accumulate", C.c_int32), ("scale", C.c_float), ("reserved", C.c_int32),
+                ("tokens", C.c_int64), ("vocab", C.c_int64), ("cols", C.c_int64),
+                ("ids", C.c_void_p), ("dout", C.c_void_p), ("dout_stride", C.c_int64),
+                ("grad", C.c_void_p), ("workspace", C.c_void_p), ("workspace_size", C.c_int64)]
+
+
+class Act8Struct(C.Structure):
+    _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p), ("rows", C.c_int64),
+                ("cols", C.c_int64), ("code_stride", C.c_int64), ("scale_stride", C.c_int64)]
+
+
+class LayerNormArgs(C.Structure):
+    _fields_ = [("kind", C.c_int32), ("dtype", C.c_int32), ("weight_dtype", C.c_int32),
+                ("reserved", C.c_int32), ("eps", C.c_double), ("rows", C.c_int64),
+                ("cols", C.c_int64), ("x", C.c_void_p), ("x_stride", C.c_int64),
+                ("weight", C.c_void_p), ("bias", C.c_void_p), ("y", C.c_void_p),
+                ("y_stride", C.c_int64), ("mean", C.c_void_p), ("rstd", C.c_void_p),
+                ("x8", C.POINTER(Act8Struct)), ("y8", C.POINTER(Act8Struct))]
+
+
+class LayerNormGradArgs(C.Structure):
+    _fields_ = [("kind", C.c_int32), ("dtype", C.c_int32), ("weight_dtype", C.c_int32),
+                ("grad_dtype", C.c_int32), ("accumulate", C.c_int32), ("reserved", C.c_int32),
+                ("rows", C.c_int64), ("cols", C.c_int64), ("dy", C.c_void_p),
+                ("dy_stride", C.c_int64), ("x", C.c_void_p), ("x_stride", C.c_int64),
+                ("x8", C.POINTER(Act8Struct)), ("weight", C.c_void_p), ("mean", C.c_void_p),
+                ("rstd", C.c_void_p), ("dx", C.c_void_p), ("dx_stride", C.c_int64),
+                ("weight_grad", C.c_void_p), ("bias_grad", C.c_void_p),
+                ("workspace", C.c_void_p), ("workspace_size", C.c_int64)]
+
+
+class WeightGradArgs(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("grad_dtype", C.c_int32), ("accumulate", C.c_int32),
+                ("reserved", C.c_int32), ("rows", C.c_int64), ("out_features", C.c_int64),
+                ("in_features", C.c_int64), ("dy", C.c_void_p), ("dy_stride", C.c_int64),
+                ("x8", C.POINTER(Act8Struct)), ("grad", C.c_void_p), ("workspace", C.c_void_p),
+                ("workspace_size", C.c_int64)]
+
+
 # Every function declared in include/zf.h, with its ctypes signature.
 _SIGNATURES = {
     "zf_plan_flat": (C.c_int, [C.POINTER(Segment), C.c_int64, C.c_int32, C.c_int32, C.c_int32,
@@ -153,6 +201,18 @@ _SIGNATURES = {
     "zf_muon_workspace_bytes": (C.c_int64, [C.c_void_p, C.POINTER(NsParams)]),
     "zf_muon_step": (C.c_int, [C.c_void_p, C.POINTER(Hparams), C.POINTER(MuonHparams),
                                C.POINTER(StepArgs), C.c_void_p]),
+    "zf_embedding": (C.c_int, [C.POINTER(EmbeddingArgs), C.c_void_p]),
+    "zf_embedding_grad_bytes": (C.c_int64, [C.c_int64, C.c_int64, C.c_int64]),
+    "zf_embedding_grad": (C.c_int, [C.POINTER(EmbeddingGradArgs), C.c_void_p]),
+    "zf_act8_store": (C.c_int, [C.POINTER(Act8Struct), C.c_int32, C.c_void_p, C.c_int64,
+                                C.c_void_p]),
+    "zf_act8_load": (C.c_int, [C.POINTER(Act8Struct), C.c_int32, C.c_void_p, C.c_int64,
+                               C.c_void_p]),
+    "zf_layer_norm": (C.c_int, [C.POINTER(LayerNormArgs), C.c_void_p]),
+    "zf_layer_norm_grad_bytes": (C.c_int64, [C.c_int64, C.c_int64]),
+    "zf_layer_norm_grad": (C.c_int, [C.POINTER(LayerNormGradArgs), C.c_void_p]),
+    "zf_weight_grad_bytes": (C.c_int64, [C.c_int64, C.c_int64, C.c_int64]),
+    "zf_weight_grad": (C.c_int, [C.POINTER(WeightGradArgs), C.c_void_p]),
     "zf_strerror": (C.c_char_p, [C.c_int]),
     "zf_hip_error_name": (C.c_char_p, []),
 }
@@ -518,11 +578,11 @@ class OrthoBatch:
     tensors: tuple
 
 
-def _dtype_of(t):
+def _dtype_of(t, where="zf_orthogonalize"):
     import torch
     code = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}.get(t.dtype)
     if code is None:
-        raise ValueError(f"zf_orthogonalize: unsupported dtype {t.dtype}")
+        raise ValueError(f"{where}: unsupported dtype {t.dtype}")
     return code
 
 
@@ -637,3 +697,250 @@ def muon_step(muon, hp, mhp, grad_dtype, param_dtype, grads, master, exp_avg, ex
                     _ptr(state), ev)
     _check(lib.zf_muon_step(muon.handle, C.byref(hp), C.byref(mhp), C.byref(args),
                             _stream(stream)), "zf_muon_step")
+
+
+# ---- beside the step: a rank's forward and backward pass -----------------------
+
+NORM_LAYER, NORM_RMS = 0, 1
+ACT8_GROUP = 32
+
+
+def _matrix(where, t, rows, cols):
+    """(dtype code, row stride) of a 2-D tensor [rows, cols] with contiguous
+    rows that do not overlap."""
+    if t.dim() != 2 or tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{where}: a tensor of {rows} x {cols} was expected, got {tuple(t.shape)}")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{where}: rows must be contiguous")
+    if rows > 1 and t.stride(0) < cols:
+        raise ValueError(f"{where}: rows must not overlap")
+    return _dtype_of(t, where), max(t.stride(0), cols) if rows > 1 else cols
+
+
+def _vector(where, t, n, dtype=None):
+    """Dtype code of a contiguous tensor of n elements (a slice of a flat
+    buffer, of any shape)."""
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{where}: a contiguous tensor of {n} elements was expected")
+    code = _dtype_of(t, where)
+    if dtype is not None and code != dtype:
+        raise ValueError(f"{where}: dtype {t.dtype} does not fit")
+    return code
+
+
+def _on_gpu(where, *tensors):
+    _on_current_device(where, *(t.device for t in tensors if t is not None and
+                                not isinstance(t, int)))
+
+
+def _ids(where, ids):
+    import torch
+    size = {torch.int32: 4, torch.int64: 8}.get(ids.dtype)
+    if size is None:
+        raise ValueError(f"{where}: ids are int32 or int64, not {ids.dtype}")
+    if not ids.is_contiguous():
+        raise ValueError(f"{where}: ids must be contiguous")
+    return size
+
+
+def _accumulate(flag):
+    return int(bool(flag))
+
+
+def _bytes(n, where):
+    if n < 0:
+        raise ZfError(n, where)
+    return n
+
+
+def embedding(table, ids, out, scale=1.0, stream=None):
+    """zf_embedding: out[t] = scale * table[ids[t]].  table: [vocab, cols],
+    rows end to end; ids: contiguous int32 or int64 of any shape; out:
+    [tokens, cols] with contiguous rows.  An id outside the vocabulary (-1:
+    padding) gives a row of zeros."""
+    where = "zf_embedding"
+    _on_gpu(where, table, ids, out)
+    if table.dim() != 2:
+        raise ValueError(f"{where}: a table of vocab x cols was expected")
+    vocab, cols = table.shape
+    n = ids.numel()
+    dtype, ld = _matrix(where, out, n, cols)
+    args = EmbeddingArgs(_vector(where, table, vocab * cols), dtype, _ids(where, ids),
+                         float(scale), n, vocab, cols, _ptr(ids), _ptr(table), _ptr(out), ld)
+    _check(lib.zf_embedding(C.byref(args), _stream(stream)), where)
+
+
+def embedding_grad_bytes(tokens, vocab, cols):
+    """zf_embedding_grad_bytes: the workspace of embedding_grad."""
+    return _bytes(lib.zf_embedding_grad_bytes(int(tokens), int(vocab), int(cols)),
+                  "zf_embedding_grad_bytes")
+
+
+def embedding_grad(dout, ids, grad, workspace, scale=1.0, accumulate=False, stream=None,
+                   workspace_size=None):
+    """zf_embedding_grad: grad[v] (+)= scale * the sum of dout[t] over the
+    tokens with ids[t] == v.  dout: [tokens, cols] with contiguous rows; grad:
+    [vocab, cols], rows end to end."""
+    where = "zf_embedding_grad"
+    _on_gpu(where, dout, ids, grad, workspace)
+    if grad.dim() != 2:
+        raise ValueError(f"{where}: a gradient of vocab x cols was expected")
+    vocab, cols = grad.shape
+    n = ids.numel()
+    dtype, ld = _matrix(where, dout, n, cols)
+    args = EmbeddingGradArgs(dtype, _vector(where, grad, vocab * cols), _ids(where, ids),
+                             _accumulate(accumulate), float(scale), 0, n, vocab, cols, _ptr(ids),
+                             _ptr(dout), ld, _ptr(grad), _ptr(workspace),
+                             _nbytes(workspace, workspace_size))
+    _check(lib.zf_embedding_grad(C.byref(args), _stream(stream)), where)
+
+
+@dataclass
+class Act8:
+    """An activation checkpoint in 8 bits: its buffers and their C record.
+    Holds the tensors, so the addresses stay good."""
+    struct: Act8Struct
+    codes: object
+    scales: object
+
+    @property
+    def shape(self):
+        return self.struct.rows, self.struct.cols
+
+
+def act8(codes, scales):
+    """The checkpoint in `codes` ([rows, cols] of one-byte elements) and
+    `scales` ([rows, ceil(cols / 32)] of one-byte elements), both with
+    contiguous rows."""
+    where = "zf_act8"
+    for t in (codes, scales):
+        if t.dim() != 2 or t.element_size() != 1:
+            raise ValueError(f"{where}: codes and scales are 2-D tensors of one-byte elements")
+        if t.shape[1] > 1 and t.stride(1) != 1:
+            raise ValueError(f"{where}: rows must be contiguous")
+        if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+            raise ValueError(f"{where}: rows must not overlap")
+    rows, cols = codes.shape
+    groups = -(-cols // ACT8_GROUP)
+    if tuple(scales.shape) != (rows, groups) or scales.device != codes.device:
+        raise ValueError(f"{where}: {rows} x {groups} scales were expected beside the codes")
+    return Act8(Act8Struct(_ptr(codes), _ptr(scales), rows, cols, max(codes.stride(0), cols),
+                           max(scales.stride(0), groups)), codes, scales)
+
+
+def act8_store(a, x, stream=None):
+    """zf_act8_store: keep x ([rows, cols], contiguous rows) as checkpoint a."""
+    where = "zf_act8_store"
+    _on_gpu(where, a.codes, x)
+    dtype, ld = _matrix(where, x, *a.shape)
+    _check(lib.zf_act8_store(C.byref(a.struct), dtype, _ptr(x), ld, _stream(stream)), where)
+
+
+def act8_load(a, x, stream=None):
+    """zf_act8_load: x = the numbers that checkpoint a stands for."""
+    where = "zf_act8_load"
+    _on_gpu(where, a.codes, x)
+    dtype, ld = _matrix(where, x, *a.shape)
+    _check(lib.zf_act8_load(C.byref(a.struct), dtype, _ptr(x), ld, _stream(stream)), where)
+
+
+def _kept(where, a, rows, cols):
+    if a is None:
+        return None
+    if a.shape != (rows, cols):
+        raise ValueError(f"{where}: a checkpoint of {rows} x {cols} was expected, got {a.shape}")
+    return C.pointer(a.struct)
+
+
+def _statistics(where, kind, rows, mean, rstd):
+    if kind == NORM_LAYER and mean is None:
+        raise ValueError(f"{where}: layer norm has means")
+    for t in (mean if kind == NORM_LAYER else None, rstd):
+        if t is not None:
+            _vector(where, t, rows, F32)
+
+
+def layer_norm(kind, x, weight, bias, eps, y, mean, rstd, x8=None, y8=None, stream=None):
+    """zf_layer_norm of every row of x ([rows, cols], contiguous rows) into y
+    (x itself, or a tensor of its own) and the statistics mean (None for
+    NORM_RMS) and rstd (fp32, [rows]).  weight, bias (or None): cols elements
+    of one dtype.  x8, y8: None, or checkpoints (act8) that receive x and y."""
+    where = "zf_layer_norm"
+    _on_gpu(where, x, weight, bias, y, mean, rstd, x8 and x8.codes, y8 and y8.codes)
+    if x.dim() != 2:
+        raise ValueError(f"{where}: x is rows x cols")
+    rows, cols = x.shape
+    dtype, x_ld = _matrix(where, x, rows, cols)
+    y_dtype, y_ld = _matrix(where, y, rows, cols)
+    if y_dtype != dtype:
+        raise ValueError(f"{where}: y has x's dtype")
+    wdt = _vector(where, weight, cols)
+    if bias is not None:
+        _vector(where, bias, cols, wdt)
+    _statistics(where, kind, rows, mean, rstd)
+    args = LayerNormArgs(int(kind), dtype, wdt, 0, float(eps), rows, cols, _ptr(x), x_ld,
+                         _ptr(weight), _ptr(bias), _ptr(y), y_ld, _ptr(mean), _ptr(rstd),
+                         _kept(where, x8, rows, cols), _kept(where, y8, rows, cols))
+    _check(lib.zf_layer_norm(C.byref(args), _stream(stream)), where)
+
+
+def layer_norm_grad_bytes(rows, cols):
+    """zf_layer_norm_grad_bytes: the workspace of layer_norm_grad."""
+    return _bytes(lib.zf_layer_norm_grad_bytes(int(rows), int(cols)), "zf_layer_norm_grad_bytes")
+
+
+def layer_norm_grad(kind, dy, x, weight, mean, rstd, dx, weight_grad, bias_grad, workspace,
+                    accumulate=False, stream=None, workspace_size=None):
+    """zf_layer_norm_grad: dx (dy itself, or a tensor of its own) and, where
+    they are not None, weight_grad and bias_grad (cols elements of one dtype,
+    stored or added to).  x: the forward pass's input, or its checkpoint
+    (act8)."""
+    where = "zf_layer_norm_grad"
+    x8 = x if isinstance(x, Act8) else None
+    _on_gpu(where, dy, x8.codes if x8 else x, weight, mean, rstd, dx, weight_grad, bias_grad,
+            workspace)
+    if dy.dim() != 2:
+        raise ValueError(f"{where}: dy is rows x cols")
+    rows, cols = dy.shape
+    dtype, dy_ld = _matrix(where, dy, rows, cols)
+    dx_dtype, dx_ld = _matrix(where, dx, rows, cols)
+    x_dtype, x_ld = (dtype, cols) if x8 else _matrix(where, x, rows, cols)
+    if x_dtype != dtype or dx_dtype != dtype:
+        raise ValueError(f"{where}: x, dy and dx have one dtype")
+    grads = [t for t in (weight_grad, bias_grad) if t is not None]
+    gdt = _dtype_of(grads[0], where) if grads else F32
+    for t in grads:
+        _vector(where, t, cols, gdt)
+    wdt = _vector(where, weight, cols)
+    _statistics(where, kind, rows, mean, rstd)
+    args = LayerNormGradArgs(int(kind), dtype, wdt, gdt, _accumulate(accumulate), 0, rows, cols,
+                             _ptr(dy), dy_ld, None if x8 else _ptr(x), x_ld,
+                             _kept(where, x8, rows, cols), _ptr(weight), _ptr(mean), _ptr(rstd),
+                             _ptr(dx), dx_ld, _ptr(weight_grad), _ptr(bias_grad), _ptr(workspace),
+                             _nbytes(workspace, workspace_size))
+    _check(lib.zf_layer_norm_grad(C.byref(args), _stream(stream)), where)
+
+
+def weight_grad_bytes(rows, out_features, in_features):
+    """zf_weight_grad_bytes: the workspace of weight_grad."""
+    return _bytes(lib.zf_weight_grad_bytes(int(rows), int(out_features), int(in_features)),
+                  "zf_weight_grad_bytes")
+
+
+def weight_grad(dy, x8, grad, workspace, accumulate=False, stream=None, workspace_size=None):
+    """zf_weight_grad: grad (+)= dy^T x8 for dy [rows, out_features] (fp16 or
+    bf16, contiguous rows) and the checkpoint x8 of the Linear's input; grad:
+    [out_features, in_features], rows end to end."""
+    where = "zf_weight_grad"
+    _on_gpu(where, dy, x8.codes, grad, workspace)
+    if dy.dim() != 2:
+        raise ValueError(f"{where}: dy is rows x out_features")
+    rows, outs = dy.shape
+    ins = x8.shape[1]
+    dtype, ld = _matrix(where, dy, rows, outs)
+    if tuple(grad.shape) != (outs, ins):
+        raise ValueError(f"{where}: a gradient of {outs} x {ins} was expected")
+    args = WeightGradArgs(dtype, _vector(where, grad, outs * ins), _accumulate(accumulate), 0,
+                          rows, outs, ins, _ptr(dy), ld, _kept(where, x8, rows, ins), _ptr(grad),
+                          _ptr(workspace), _nbytes(workspace, workspace_size))
+    _check(lib.zf_weight_grad(C.byref(args), _stream(stream)), where)

@@ -54,7 +54,8 @@
  *   - HIP graphs: zf_shard_step, zf_shard_step_noalloc (after its first
  *     call on the device), zf_reduce_scatter, zf_gather, zf_gather_cast,
  *     zf_bucket_reduce_scatter, zf_accumulate, zf_orthogonalize,
- *     zf_muon_step and zf_state_init enqueue kernels only (no memset, copy,
+ *     zf_muon_step, zf_state_init and the calls of a rank's forward and
+ *     backward pass (from zf_embedding on) enqueue kernels only (no memset, copy,
  *     allocation or synchronisation; every pointer travels by value in the kernel
  *     arguments), so a caller may capture them on a stream and replay the
  *     graph.  The state block carries t, the loss scale and the skip
@@ -661,6 +662,189 @@ typedef struct {
  * zf_shard_step, plus ZF_EINVAL (mhp out of range) and ZF_ENOMEM. */
 int zf_muon_step(const zf_muon* muon, const zf_hparams* hp, const zf_muon_hparams* mhp,
                  const zf_step_args* args, void* stream);
+
+/* ---- Beside the step: a rank's forward and backward pass ----------------
+ * What reads the flat parameters and writes the flat gradients: the embedding
+ * lookup, layer norm and RMS norm, their gradients, activation checkpoints in
+ * 8 bits, and a Linear's weight gradient from one.  A parameter is given by
+ * its first element, anywhere in a flat buffer (params, a gathered unit, the
+ * fp32 master of ZF_PER_PARAM_DIM0; a replica's 16-bit gradient or an fp32
+ * main gradient), aligned to its element size only.
+ *   - Matrices of activations are row-major with a row stride in elements
+ *     (ignored for a single row); elements between the rows are left as they
+ *     are.  Every dtype is ZF_F16, ZF_BF16 or ZF_F32 unless a call says
+ *     otherwise; arithmetic is binary32, rounded once to a result's type.
+ *   - Gradients of parameters: with accumulate = 0 the gradient is stored
+ *     (every element, whatever the buffer held), with 1 it is added to what
+ *     the buffer holds: binary32 sum, then one rounding to grad_dtype.
+ *     A non-finite gradient reaches zf_shard_step's overflow check.
+ *   - Sums are taken in a fixed order (no atomics on floats): the same call
+ *     gives the same bits.
+ *   - Rows (or tokens) may be 0: nothing is read, and gradients are those of
+ *     an empty batch (stored zeros, or nothing added).
+ *   - Kernels only, no allocation: every call may be captured in a HIP graph
+ *     (pointers, sizes and scalars are those of the capture).  A workspace is
+ *     caller-owned device memory, 16-byte aligned, that each call writes
+ *     before it reads; calls that may overlap in time (two streams, two
+ *     graphs) need workspaces of their own.
+ *   - Buffers of a call do not overlap unless it says so.
+ * Errors: ZF_EINVAL (NULL, a count or size out of range, a stride < cols, a
+ * flag that is not 0 or 1), ZF_EDTYPE, ZF_EALIGN (a pointer that is not
+ * aligned to its element size, or a workspace to 16 bytes), ZF_ESIZE (rows or
+ * tokens above ZF_MAX_ROWS, cols above ZF_MAX_COLS, a vocabulary above
+ * ZF_MAX_ROWS, a workspace too small), ZF_EHIP. */
+#define ZF_MAX_ROWS ((1ll << 30))
+#define ZF_MAX_COLS ((1ll << 20))
+
+typedef struct {
+  int32_t table_dtype;   /* of the table */
+  int32_t dtype;         /* of out */
+  int32_t id_bytes;      /* 4 or 8: ids are int32 or int64 */
+  float scale;
+  int64_t tokens, vocab, cols;
+  const void* ids;       /* tokens ids */
+  const void* table;     /* vocab x cols, rows end to end */
+  void* out;             /* tokens x cols */
+  int64_t out_stride;
+} zf_embedding_args;
+
+/* Embedding lookup: out[t] = scale * table[ids[t]].  A token whose id is not
+ * in [0, vocab) (-1 marks padding) takes a row of zeros. */
+int zf_embedding(const zf_embedding_args* args, void* stream);
+
+typedef struct {
+  int32_t dtype;         /* of dout */
+  int32_t grad_dtype;    /* of grad */
+  int32_t id_bytes;      /* 4 or 8 */
+  int32_t accumulate;    /* 0 or 1 */
+  float scale;
+  int32_t reserved;      /* must be 0 */
+  int64_t tokens, vocab, cols;
+  const void* ids;       /* tokens ids */
+  const void* dout;      /* tokens x cols */
+  int64_t dout_stride;
+  void* grad;            /* vocab x cols, rows end to end */
+  void* workspace;
+  int64_t workspace_size;  /* >= zf_embedding_grad_bytes */
+} zf_embedding_grad_args;
+
+/* Device workspace of zf_embedding_grad.  < 0 on error. */
+int64_t zf_embedding_grad_bytes(int64_t tokens, int64_t vocab, int64_t cols);
+
+/* Gradient of zf_embedding's table: grad[v] = scale * (sum of dout[t] over the
+ * tokens with ids[t] == v), each row's sum in an order that depends on the
+ * ids, tokens and cols alone.  Tokens outside the vocabulary give nothing. */
+int zf_embedding_grad(const zf_embedding_grad_args* args, void* stream);
+
+/* An activation checkpoint in 8 bits.  Each group of ZF_ACT8_GROUP elements
+ * of a row (the last one may be shorter) has a scale 2^k, k the least integer
+ * from -100 on for which the group's largest finite magnitude is at most
+ * 448 * 2^k, kept as the byte k + 127; an element is kept as the e4m3 number
+ * nearest to x / 2^k, ties to even, so it is off by at most a sixteenth of
+ * itself, or by 2^(k-10) if that is more.  An infinity or a NaN is kept as
+ * NaN (0x7F).  A magnitude that would be rounded past the largest number of x's type
+ * (or, from fp32, of bf16) takes the next code below.  Buffers are the
+ * caller's: rows x cols codes, and rows x ceil(cols / 32) scales. */
+#define ZF_ACT8_GROUP 32
+typedef struct {
+  void* codes;           /* element (i, j) at i * code_stride + j */
+  void* scales;          /* of its group at i * scale_stride + j / 32 */
+  int64_t rows, cols;
+  int64_t code_stride, scale_stride;  /* bytes (ignored for a single row) */
+} zf_act8;
+
+/* Keep x (rows x cols of dtype) as *a. */
+int zf_act8_store(const zf_act8* a, int32_t dtype, const void* x, int64_t x_stride, void* stream);
+
+/* x = the numbers that *a stands for, rounded to dtype (exact in the type
+ * that they were stored from, in bf16 and in fp32). */
+int zf_act8_load(const zf_act8* a, int32_t dtype, void* x, int64_t x_stride, void* stream);
+
+enum zf_norm_kind { ZF_NORM_LAYER = 0, ZF_NORM_RMS = 1 };
+
+typedef struct {
+  int32_t kind;          /* zf_norm_kind */
+  int32_t dtype;         /* of x and y */
+  int32_t weight_dtype;  /* of weight and bias */
+  int32_t reserved;      /* must be 0 */
+  double eps;            /* >= 0, finite */
+  int64_t rows, cols;
+  const void* x;         /* rows x cols */
+  int64_t x_stride;
+  const void* weight;    /* cols */
+  const void* bias;      /* cols, or NULL: none */
+  void* y;               /* rows x cols; may be x, with its stride */
+  int64_t y_stride;
+  float* mean;           /* rows; ZF_NORM_RMS: ignored, may be NULL */
+  float* rstd;           /* rows */
+  const zf_act8* x8;     /* NULL, or receives the checkpoint of x */
+  const zf_act8* y8;     /* NULL, or receives the checkpoint of y as y's type
+                            holds it (rows and cols as x) */
+} zf_layer_norm_args;
+
+/* Layer norm or RMS norm of every row, and checkpoints of its input and its
+ * output from the same pass:
+ *   mean = avg(x) (ZF_NORM_RMS: 0),  rstd = 1 / sqrt(avg((x - mean)^2) + eps),
+ *   y = (x - mean) * rstd * weight + bias. */
+int zf_layer_norm(const zf_layer_norm_args* args, void* stream);
+
+typedef struct {
+  int32_t kind;          /* zf_norm_kind */
+  int32_t dtype;         /* of dy, x and dx */
+  int32_t weight_dtype;
+  int32_t grad_dtype;    /* of weight_grad and bias_grad */
+  int32_t accumulate;    /* 0 or 1 */
+  int32_t reserved;      /* must be 0 */
+  int64_t rows, cols;
+  const void* dy;        /* rows x cols */
+  int64_t dy_stride;
+  const void* x;         /* rows x cols, or NULL: x8 is given */
+  int64_t x_stride;
+  const zf_act8* x8;     /* NULL, or the checkpoint of x */
+  const void* weight;    /* cols */
+  const float* mean;     /* rows (ZF_NORM_RMS: ignored, may be NULL) */
+  const float* rstd;     /* rows */
+  void* dx;              /* rows x cols; may be dy, with its stride */
+  int64_t dx_stride;
+  void* weight_grad;     /* cols, or NULL: not wanted */
+  void* bias_grad;       /* cols, or NULL: not wanted */
+  void* workspace;       /* needed for weight_grad or bias_grad alone */
+  int64_t workspace_size;  /* >= zf_layer_norm_grad_bytes */
+} zf_layer_norm_grad_args;
+
+/* Device workspace of zf_layer_norm_grad.  < 0 on error. */
+int64_t zf_layer_norm_grad_bytes(int64_t rows, int64_t cols);
+
+/* Gradients of zf_layer_norm from mean and rstd as it left them, with
+ * xh = (x - mean) * rstd and h = dy * weight:
+ *   dx = rstd * (h - avg(h) - xh * avg(h * xh))   (ZF_NORM_RMS: no avg(h)),
+ *   weight_grad = sum over rows of dy * xh,  bias_grad = sum of dy.
+ * From a checkpoint, x is the numbers that it stands for. */
+int zf_layer_norm_grad(const zf_layer_norm_grad_args* args, void* stream);
+
+typedef struct {
+  int32_t dtype;         /* of dy: ZF_F16 or ZF_BF16 */
+  int32_t grad_dtype;
+  int32_t accumulate;    /* 0 or 1 */
+  int32_t reserved;      /* must be 0 */
+  int64_t rows, out_features, in_features;
+  const void* dy;        /* rows x out_features */
+  int64_t dy_stride;
+  const zf_act8* x8;     /* rows x in_features */
+  void* grad;            /* out_features x in_features, rows end to end */
+  void* workspace;       /* may be NULL if zf_weight_grad_bytes is 0 */
+  int64_t workspace_size;  /* >= zf_weight_grad_bytes */
+} zf_weight_grad_args;
+
+/* Device workspace of zf_weight_grad.  < 0 on error. */
+int64_t zf_weight_grad_bytes(int64_t rows, int64_t out_features, int64_t in_features);
+
+/* Weight gradient of a Linear whose input was kept as a checkpoint:
+ *   grad[o][i] = sum over rows t of dy[t][o] * x8[t][i],
+ * on the matrix cores, with x8's numbers in dy's type (exact for a checkpoint
+ * stored from that type, and always for ZF_BF16), products exact and sums in
+ * binary32.  out_features and in_features are at most ZF_MAX_COLS. */
+int zf_weight_grad(const zf_weight_grad_args* args, void* stream);
 
 /* Text for a status code (static storage). */
 const char* zf_strerror(int status);
