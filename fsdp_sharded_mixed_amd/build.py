@@ -65,7 +65,7 @@ def _libraries():
     step = [(c(f), "hip", (), "") for f in
             ("zf_step.hip", "zf_backward.hip", "zf_gather.hip", "zf_offload.hip", "zf_ortho.hip",
              "zf_muon.hip", "zf_act8.hip", "zf_embedding.hip", "zf_norm.hip",
-             "zf_weight_grad.hip")]
+             "zf_norm_grad.hip", "zf_weight_grad.hip")]
     host = [(c(f), "c++", (), "") for f in ("zf_plan.cpp", "zf_cpu_adam.cpp")]
     window = ("-DZF_TEST_CACHED_SUMS_MB=1",)
     return [

@@ -37,7 +37,7 @@ __global__ __launch_bounds__(kThreads) void zf_act8_kernel(Act8Args a) {
   for (; i < a.rows; i += (int64_t)gridDim.x * per) {  // the lanes of a row together
     float v[kChunk];
     if constexpr (STORE) {
-      if (left > 0) load8<DT, true>(a.x, i * a.x_ld + j, left, v);
+      load8<DT, true>(a.x, i * a.x_ld + j, left, v);
       keep8<DT>(a.a, i, j, left, v);
     } else {
       if (left <= 0) return;

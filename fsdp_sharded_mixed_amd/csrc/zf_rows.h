@@ -19,6 +19,8 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 // which the HSA runtime sets), so there is one path, not one an alignment.
 typedef u32x4 u32x4_any __attribute__((aligned(1)));
 typedef u32x2 u32x2_any __attribute__((aligned(1)));
+typedef uint32_t u32_any __attribute__((aligned(1)));
+typedef uint16_t u16_any __attribute__((aligned(1)));
 
 constexpr int kChunk = 8;  // consecutive elements of a lane
 // Blocks of a launch along x: a launch holds fewer than 2^32 threads there,
@@ -57,6 +59,14 @@ template <int DT>
 __device__ __forceinline__ uint16_t narrow(float x) {
   return narrow1<DT>(DT == ZF_F16 ? settled(x) : x);
 }
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+template <int DT>
+__device__ __forceinline__ uint32_t narrow2(float a, float b) {
+  if constexpr (DT == ZF_BF16)
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
+  else
+    return (uint32_t)narrow<DT>(a) | (uint32_t)narrow<DT>(b) << 16;
+}
 template <int DT>
 __device__ __forceinline__ void store1(void* base, int64_t i, float x) {
   if constexpr (DT == ZF_F32) static_cast<float*>(base)[i] = x;
@@ -64,12 +74,13 @@ __device__ __forceinline__ void store1(void* base, int64_t i, float x) {
 }
 
 // 8 elements of type DT from element i on as the registers hold them; n of
-// them (1..8) exist, the others read as zero.
+// them exist (all, if 8 or more; none, if 0 or less), the others read as zero.
+// WHOLE: all or none exist, as in rows of a multiple of 8 elements.
 template <int DT>
 struct Raw {
   u32x4 w[DT == ZF_F32 ? 2 : 1];
 };
-template <int DT, bool NT = false>
+template <int DT, bool NT = false, bool WHOLE = false>
 __device__ __forceinline__ Raw<DT> load_raw(const void* base, int64_t i, int n) {
   const char* p = static_cast<const char*>(base) + i * kElem<DT>;
   Raw<DT> r;
@@ -80,11 +91,25 @@ __device__ __forceinline__ Raw<DT> load_raw(const void* base, int64_t i, int n) 
   }
   r.w[0] = (u32x4){0, 0, 0, 0};
   if constexpr (DT == ZF_F32) r.w[1] = (u32x4){0, 0, 0, 0};
-#pragma unroll
-  for (int k = 0; k < kChunk - 1; ++k) {
-    if (k >= n) break;
-    if constexpr (DT == ZF_F32) r.w[k >> 2][k & 3] = reinterpret_cast<const uint32_t*>(p)[k];
-    else r.w[0][k >> 1] |= (uint32_t) reinterpret_cast<const uint16_t*>(p)[k] << (k & 1) * 16;
+  if (WHOLE || n <= 0) return r;
+  // 4, 2 and 1 of them, as the bits of n say
+  if constexpr (DT == ZF_F32) {
+    u32x2 two = {0, 0};
+    uint32_t one = 0;
+    if (n & 4) r.w[0] = load_any<NT, u32x4_any>(p);
+    if (n & 2) two = load_any<NT, u32x2_any>(p + (n & 4) * 4);
+    if (n & 1) one = load_any<NT, uint32_t>(p + (n & 6) * 4);
+    const u32x4 rest = n & 2 ? (u32x4){two.x, two.y, one, 0} : (u32x4){one, 0, 0, 0};
+    if (n & 4) r.w[1] = rest;
+    else r.w[0] = rest;
+  } else {
+    u32x2 four = {0, 0};
+    uint32_t two = 0, one = 0;
+    if (n & 4) four = load_any<NT, u32x2_any>(p);
+    if (n & 2) two = load_any<NT, u32_any>(p + (n & 4) * 2);
+    if (n & 1) one = load_any<NT, uint16_t>(p + (n & 6) * 2);
+    const u32x2 rest = n & 2 ? (u32x2){two, one} : (u32x2){one, 0};
+    r.w[0] = n & 4 ? (u32x4){four.x, four.y, rest.x, rest.y} : (u32x4){rest.x, rest.y, 0, 0};
   }
   return r;
 }
@@ -105,12 +130,12 @@ __device__ __forceinline__ Raw<DT> narrow8(const float (&v)[kChunk]) {
       r.w[k >> 2][k & 3] = __float_as_uint(v[k]);
       r.w[k >> 2][(k & 3) + 1] = __float_as_uint(v[k + 1]);
     } else {
-      r.w[0][k >> 1] = (uint32_t)narrow<DT>(v[k]) | (uint32_t)narrow<DT>(v[k + 1]) << 16;
+      r.w[0][k >> 1] = narrow2<DT>(v[k], v[k + 1]);
     }
   }
   return r;
 }
-template <int DT, bool NT = false>
+template <int DT, bool NT = false, bool WHOLE = false>
 __device__ __forceinline__ void store_raw(void* base, int64_t i, int n, const Raw<DT>& r) {
   char* p = static_cast<char*>(base) + i * kElem<DT>;
   if (n >= kChunk) {
@@ -118,28 +143,35 @@ __device__ __forceinline__ void store_raw(void* base, int64_t i, int n, const Ra
     if constexpr (DT == ZF_F32) store_any<NT, u32x4_any>(p + 16, r.w[1]);
     return;
   }
-#pragma unroll
-  for (int k = 0; k < kChunk - 1; ++k) {
-    if (k >= n) break;
-    if constexpr (DT == ZF_F32) reinterpret_cast<uint32_t*>(p)[k] = r.w[k >> 2][k & 3];
-    else reinterpret_cast<uint16_t*>(p)[k] = (uint16_t)(r.w[0][k >> 1] >> (k & 1) * 16);
+  if (WHOLE || n <= 0) return;
+  if constexpr (DT == ZF_F32) {
+    const u32x4 rest = n & 4 ? r.w[1] : r.w[0];
+    if (n & 4) store_any<NT, u32x4_any>(p, r.w[0]);
+    if (n & 2) store_any<NT, u32x2_any>(p + (n & 4) * 4, (u32x2){rest.x, rest.y});
+    if (n & 1) store_any<NT, uint32_t>(p + (n & 6) * 4, n & 2 ? rest.z : rest.x);
+  } else {
+    const u32x2 rest = n & 4 ? (u32x2){r.w[0].z, r.w[0].w} : (u32x2){r.w[0].x, r.w[0].y};
+    if (n & 4) store_any<NT, u32x2_any>(p, (u32x2){r.w[0].x, r.w[0].y});
+    if (n & 2) store_any<NT, u32_any>(p + (n & 4) * 2, rest.x);
+    if (n & 1) store_any<NT, uint16_t>(p + (n & 6) * 2, (uint16_t)(n & 2 ? rest.y : rest.x));
   }
 }
-template <int DT, bool NT = false>
+template <int DT, bool NT = false, bool WHOLE = false>
 __device__ __forceinline__ void load8(const void* base, int64_t i, int n, float (&v)[kChunk]) {
-  widen8<DT>(load_raw<DT, NT>(base, i, n), v);
+  widen8<DT>(load_raw<DT, NT, WHOLE>(base, i, n), v);
 }
-template <int DT, bool NT = false>
+template <int DT, bool NT = false, bool WHOLE = false>
 __device__ __forceinline__ void store8(void* base, int64_t i, int n, const float (&v)[kChunk]) {
-  store_raw<DT, NT>(base, i, n, narrow8<DT>(v));
+  store_raw<DT, NT, WHOLE>(base, i, n, narrow8<DT>(v));
 }
 
 // The same with the type known at run time (parameters: once a row or less).
+template <bool WHOLE = false>
 __device__ __forceinline__ void load8_of(int32_t dt, const void* base, int64_t i, int n,
                                          float (&v)[kChunk]) {
-  if (dt == ZF_F32) load8<ZF_F32>(base, i, n, v);
-  else if (dt == ZF_BF16) load8<ZF_BF16>(base, i, n, v);
-  else load8<ZF_F16>(base, i, n, v);
+  if (dt == ZF_F32) load8<ZF_F32, false, WHOLE>(base, i, n, v);
+  else if (dt == ZF_BF16) load8<ZF_BF16, false, WHOLE>(base, i, n, v);
+  else load8<ZF_F16, false, WHOLE>(base, i, n, v);
 }
 __device__ __forceinline__ float load1_of(int32_t dt, const void* base, int64_t i) {
   return dt == ZF_F32 ? load1<ZF_F32>(base, i)
@@ -158,6 +190,10 @@ __device__ __forceinline__ void store1_of(int32_t dt, void* base, int64_t i, flo
 // is the conversion's, to nearest even.
 
 constexpr int kScaleLeast = 27;  // k = -100: every number stays normal in bf16
+
+// A condition that hardly any wave meets: a branch around its code, instead of
+// both sides and selects.
+__device__ __forceinline__ bool rare(bool x) { return __builtin_expect(__any(x), 0) && x; }
 
 // Magnitude bits of 8 elements' largest; FINITE: without infinities and NaN.
 template <bool FINITE>
@@ -190,7 +226,7 @@ __device__ __forceinline__ u32x2 encode8(const float (&v)[kChunk], uint32_t scal
   float s[kChunk];
 #pragma unroll
   for (int k = 0; k < kChunk; ++k) s[k] = v[k] * inv;
-  if (scale == (DT == ZF_F16 ? 135u : 247u)) {
+  if (rare(scale == (DT == ZF_F16 ? 135u : 247u))) {
 #pragma unroll
     for (int k = 0; k < kChunk; ++k) s[k] = fminf(fmaxf(s[k], -240.0f), 240.0f);
   }
@@ -222,43 +258,48 @@ struct Act8 {
   int64_t code_ld, scale_ld;
 };
 
-template <bool NT = false>
+// 8 codes, of which n exist, as load_raw and store_raw take elements.
+template <bool NT = false, bool WHOLE = false>
 __device__ __forceinline__ u32x2 load_codes(const uint8_t* p, int n) {
   if (n >= kChunk) return load_any<NT, u32x2_any>(p);
-  u32x2 c = {0, 0};
-#pragma unroll
-  for (int k = 0; k < kChunk - 1; ++k)
-    if (k < n) c[k >> 2] |= (uint32_t)p[k] << (k & 3) * 8;
-  return c;
+  uint32_t four = 0, two = 0, one = 0;
+  if (WHOLE || n <= 0) return (u32x2){0, 0};
+  if (n & 4) four = load_any<NT, u32_any>(p);
+  if (n & 2) two = load_any<NT, u16_any>(p + (n & 4));
+  if (n & 1) one = load_any<NT, uint8_t>(p + (n & 6));
+  const uint32_t rest = n & 2 ? two | one << 16 : one;
+  return n & 4 ? (u32x2){four, rest} : (u32x2){rest, 0};
 }
-template <bool NT = false>
+template <bool NT = false, bool WHOLE = false>
 __device__ __forceinline__ void store_codes(uint8_t* p, int n, u32x2 c) {
   if (n >= kChunk) {
     store_any<NT, u32x2_any>(p, c);
     return;
   }
-#pragma unroll
-  for (int k = 0; k < kChunk - 1; ++k)
-    if (k < n) p[k] = (uint8_t)(c[k >> 2] >> (k & 3) * 8);
+  if (WHOLE || n <= 0) return;
+  const uint32_t rest = n & 4 ? c.y : c.x;
+  if (n & 4) store_any<NT, u32_any>(p, c.x);
+  if (n & 2) store_any<NT, u16_any>(p + (n & 4), (uint16_t)rest);
+  if (n & 1) store_any<NT, uint8_t>(p + (n & 6), (uint8_t)(n & 2 ? rest >> 16 : rest));
 }
 
-// Keeps this lane's 8 elements (n of them exist; none: n <= 0) of row i from
-// column j on.  All 4 lanes of a group call it together.
-template <int DT, bool NT = false>
+// Keeps this lane's 8 elements of row i from column j on, of which n exist;
+// the others are zero.  All 4 lanes of a group call it together.
+template <int DT, bool NT = false, bool WHOLE = false>
 __device__ __forceinline__ void keep8(const Act8& a, int64_t i, int64_t j, int n,
                                       const float (&v)[kChunk]) {
-  uint32_t top = n > 0 ? amax8<false>(v) : 0u;
-  const bool odd = top >= 0x7F800000u;  // rare: infinities or NaN among them
-  if (odd) top = amax8<true>(v);
+  uint32_t top = amax8<false>(v);
+  const bool odd = top >= 0x7F800000u;  // infinities or NaN among them
+  if (rare(odd)) top = amax8<true>(v);
   const uint32_t scale = scale_byte(max_quad(top));
   if (n <= 0) return;
   u32x2 c = encode8<DT>(v, scale);
-  if (odd) {
+  if (rare(odd)) {
 #pragma unroll
     for (int k = 0; k < kChunk; ++k)
       if (nonfinite(v[k])) c[k >> 2] = (c[k >> 2] & ~(0xFFu << (k & 3) * 8)) | 0x7Fu << (k & 3) * 8;
   }
-  store_codes<NT>(a.codes + i * a.code_ld + j, n, c);
+  store_codes<NT, WHOLE>(a.codes + i * a.code_ld + j, n, c);
   if ((j & (ZF_ACT8_GROUP - 1)) == 0)
     a.scales[i * a.scale_ld + j / ZF_ACT8_GROUP] = (uint8_t)scale;
 }
