@@ -8,42 +8,62 @@
 namespace zf {
 namespace dev {
 
-constexpr int kWaves = kThreads / 64;
-
-// Sum over the G lanes of a row; every lane gets it.  G == kThreads: `slots`
-// alternates between two sets, so one barrier a sum is enough.
-template <int G>
-__device__ __forceinline__ float row_sum(float x, float (*slots)[kWaves], int& turn) {
-  if constexpr (G <= 64) {
-    return sum_lanes<G>(x);
-  } else {
+// N sums over the G lanes of a row in a block of T threads; every lane gets
+// them.  G == T: `slots` alternates between two sets, so one barrier is enough.
+template <int G, int T, int N>
+__device__ __forceinline__ void row_sums(float (&x)[N], float (*slots)[N][T / 64], int& turn) {
+  static_assert(G <= 64 || G == T, "lanes of a row");
+#pragma unroll
+  for (int k = 0; k < N; ++k) x[k] = sum_lanes<(G < 64 ? G : 64)>(x[k]);
+  if constexpr (G > 64) {
     turn ^= 1;
-    return sum_block<kWaves>(x, slots[turn]);
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) slots[turn][k][threadIdx.x >> 6] = x[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      x[k] = slots[turn][k][0];
+#pragma unroll
+      for (int w = 1; w < T / 64; ++w) x[k] += slots[turn][k][w];
+    }
   }
 }
+template <int G, int T>
+__device__ __forceinline__ float row_sum(float x, float (*slots)[1][T / 64], int& turn) {
+  float one[1] = {x};
+  row_sums<G, T, 1>(one, slots, turn);
+  return one[0];
+}
 
-// A row lies in the registers of G lanes, 8 elements a lane and V times: 16
-// lanes for up to 128 columns, a wave for up to 2048, a block for up to 16384.
-// Rows of a multiple of 8 elements (WHOLE) have kernels without the code for a
-// last lane's part of 8, which is most of the others' code.
-constexpr int kMostCols = kThreads * kChunk * 8;  // of a row in registers
+constexpr int64_t kMostCols = 16384;  // of a row in registers
 
+// The form of a row's kernel: T threads a block, G lanes a row, V times 8
+// elements a lane.  Rows of a multiple of 8 elements (WHOLE) have kernels
+// without the code for a part of 8, which is most of the others' code (rows of
+// 2048, a wave each: 115 us with it, 77 without); other rows have fewer forms.
+template <int T_, int G_, int V_, bool WHOLE_>
+struct Shape {
+  static constexpr int T = T_, G = G_, V = V_;
+  static constexpr bool WHOLE = WHOLE_;
+};
 template <typename F>
 inline void by_shape(int64_t cols, F f) {
-#define ZF_SHAPE(G, V, WHOLE) \
-  f(std::integral_constant<int, G>(), std::integral_constant<int, V>(), std::bool_constant<WHOLE>())
   if (cols % kChunk != 0) {
-    if (cols <= 128) ZF_SHAPE(16, 1, false);
-    else if (cols <= 2048) ZF_SHAPE(64, 4, false);
-    else ZF_SHAPE(256, 8, false);
-  } else if (cols <= 128) ZF_SHAPE(16, 1, true);
-  else if (cols <= 512) ZF_SHAPE(64, 1, true);
-  else if (cols <= 1024) ZF_SHAPE(64, 2, true);
-  else if (cols <= 2048) ZF_SHAPE(64, 4, true);
-  else if (cols <= 4096) ZF_SHAPE(256, 2, true);
-  else if (cols <= 8192) ZF_SHAPE(256, 4, true);
-  else ZF_SHAPE(256, 8, true);
-#undef ZF_SHAPE
+    if (cols <= 128) f(Shape<256, 16, 1, false>());
+    else if (cols <= 512) f(Shape<256, 64, 1, false>());
+    else if (cols <= 2048) f(Shape<256, 256, 1, false>());
+    else if (cols <= 4096) f(Shape<512, 512, 1, false>());
+    else if (cols <= 8192) f(Shape<1024, 1024, 1, false>());
+    else f(Shape<1024, 1024, 2, false>());
+  } else if (cols <= 128) f(Shape<256, 16, 1, true>());
+  else if (cols <= 512) f(Shape<256, 64, 1, true>());
+  else if (cols <= 1024) f(Shape<128, 128, 1, true>());
+  else if (cols <= 2048) f(Shape<256, 256, 1, true>());
+  else if (cols <= 4096) f(Shape<512, 512, 1, true>());
+  else if (cols <= 8192) f(Shape<512, 512, 2, true>());
+  else f(Shape<1024, 1024, 2, true>());
 }
 
 template <typename F>

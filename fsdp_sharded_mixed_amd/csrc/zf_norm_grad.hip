@@ -31,7 +31,8 @@ struct NormGradArgs {
   const float* mean;
   const float* rstd;
   void* dx;
-  float* partial;  // [2][blocks][cols]: dw, db; NULL: neither is wanted
+  float* dw;  // the blocks' sums, [blocks][cols]; NULL: not wanted
+  float* db;
   int64_t dy_ld, x_ld, dx_ld, rows;
   float inv_cols;
   int32_t cols, wdt;
@@ -64,15 +65,21 @@ __device__ __forceinline__ void widen_x(const RawX<DT, KEPT>& r, float (&x)[kChu
   else widen8<DT>(r.r, x);
 }
 
-// As the forward pass: parameters and the columns' sums stay in registers, the
-// next row is on its way while this one is worked on.  Elements past the
-// row's end have dy = 0 and add nothing (where rstd is not finite, the row's
-// own elements are not either).
-template <int DT, bool KEPT, bool LAYER, int G, int V, bool WHOLE>
-__global__ __launch_bounds__(kThreads, 2) void zf_norm_grad_kernel(NormGradArgs a) {
-  __shared__ float slots[2][kWaves];
+// A group of G lanes takes a row at a time, 8 V elements a lane; its parameters
+// and the columns' sums stay in registers, and the next row is on its way while
+// this one is worked on.  Rows of more than 512 elements take a block and its
+// barrier instead of a wave: parameters, two columns' sums and a row's
+// operands are 40 V registers beside the loads, and with V = 4 (2048 columns a
+// wave) they spill.  32768 rows of 2048 from a checkpoint: 70 us with V = 1,
+// 4.8 TB/s (two rows at a time 80, a wave a row 90).
+// Elements past the row's end have dy = 0 and add nothing (where rstd is not
+// finite, the row's own elements are not either).
+template <int DT, bool KEPT, bool LAYER, int T, int G, int V, bool WHOLE>
+__global__ __launch_bounds__(T) void zf_norm_grad_kernel(NormGradArgs a) {
+  constexpr int N = LAYER ? 2 : 1;  // sums of a row: h xh, and h
+  __shared__ float slots[2][N][T / 64];
   int turn = 0;
-  constexpr int kGroups = kThreads / G;
+  constexpr int kGroups = T / G;
   const int lane = threadIdx.x % G, group = threadIdx.x / G;
   const int64_t step = (int64_t)gridDim.x * kGroups;
   int64_t i = (int64_t)blockIdx.x * kGroups + group;
@@ -100,43 +107,44 @@ __global__ __launch_bounds__(kThreads, 2) void zf_norm_grad_kernel(NormGradArgs 
     for (int k = 0; k < kChunk; ++k) dw[v][k] = db[v][k] = 0;
   }
   for (; i < a.rows; i += step) {
-    float xh[V][kChunk], dy[V][kChunk], s1 = 0, s2 = 0, c1 = 0;
+    float xh[V][kChunk], h[V][kChunk], sums[N];
     const float rstd = next_rstd, mean = next_mean;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      widen8<DT>(next_dy[v], dy[v]);
+      widen8<DT>(next_dy[v], h[v]);
       widen_x<DT, KEPT>(next_x[v], xh[v]);
     }
     fetch(i + step);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
+    for (int k = 0; k < N; ++k) sums[k] = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
 #pragma unroll
       for (int k = 0; k < kChunk; ++k) {
         xh[v][k] = (LAYER ? xh[v][k] - mean : xh[v][k]) * rstd;
-        dw[v][k] = __builtin_fmaf(dy[v][k], xh[v][k], dw[v][k]);
-        db[v][k] += dy[v][k];
-        dy[v][k] *= w[v][k];  // h from here on
-        s1 += dy[v][k];
-        s2 = __builtin_fmaf(dy[v][k], xh[v][k], s2);
+        dw[v][k] = __builtin_fmaf(h[v][k], xh[v][k], dw[v][k]);
+        db[v][k] += h[v][k];
+        h[v][k] *= w[v][k];
+        sums[0] = __builtin_fmaf(h[v][k], xh[v][k], sums[0]);
+        if constexpr (LAYER) sums[N - 1] += h[v][k];
       }
-    }
-    if constexpr (LAYER) c1 = row_sum<G>(s1, slots, turn) * a.inv_cols;
-    const float c2 = row_sum<G>(s2, slots, turn) * a.inv_cols;
+    row_sums<G, T, N>(sums, slots, turn);
+    const float c2 = sums[0] * a.inv_cols, c1 = LAYER ? sums[N - 1] * a.inv_cols : 0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int j = (v * G + lane) * kChunk;
 #pragma unroll
       for (int k = 0; k < kChunk; ++k)
-        dy[v][k] = rstd * __builtin_fmaf(-xh[v][k], c2, LAYER ? dy[v][k] - c1 : dy[v][k]);
-      store8<DT, true, WHOLE>(a.dx, i * a.dx_ld + j, a.cols - j, dy[v]);
+        h[v][k] = rstd * __builtin_fmaf(-xh[v][k], c2, LAYER ? h[v][k] - c1 : h[v][k]);
+      store8<DT, true, WHOLE>(a.dx, i * a.dx_ld + j, a.cols - j, h[v]);
     }
   }
-  if (!a.partial) return;
   // the groups' sums, in order, one of the two at a time
   __shared__ float join[kGroups > 1 ? (kGroups - 1) * G * V * kChunk : 1];
-  float* out = a.partial + (int64_t)blockIdx.x * a.cols;
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
+    float* out = half ? a.db : a.dw;
+    if (!out) continue;
     float(&sum)[V][kChunk] = half ? db : dw;
     if constexpr (kGroups > 1) {
       __syncthreads();
@@ -158,8 +166,8 @@ __global__ __launch_bounds__(kThreads, 2) void zf_norm_grad_kernel(NormGradArgs 
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int j = (v * G + lane) * kChunk, n = a.cols - j;
-      store8<ZF_F32, false, WHOLE>(out + (int64_t)half * gridDim.x * a.cols, j, n, sum[v]);
+      const int j = (v * G + lane) * kChunk;
+      store8<ZF_F32, false, WHOLE>(out + (int64_t)blockIdx.x * a.cols, j, a.cols - j, sum[v]);
     }
   }
 }
@@ -168,13 +176,13 @@ __global__ __launch_bounds__(kThreads, 2) void zf_norm_grad_kernel(NormGradArgs 
 // for dx, and the columns' sums by a launch of their own.
 template <int DT, bool KEPT, bool LAYER>
 __global__ __launch_bounds__(kThreads) void zf_norm_grad_long(NormGradArgs a) {
-  __shared__ float slots[2][kWaves];
+  __shared__ float slots[2][2][kThreads / 64];
   int turn = 0;
   constexpr int kSpan = kThreads * kChunk;
   for (int64_t i = blockIdx.x; i < a.rows; i += gridDim.x) {
     const float rstd = a.rstd[i];
     const float mean = LAYER ? a.mean[i] : 0;
-    float s1 = 0, s2 = 0, c1 = 0;
+    float s1 = 0, s2 = 0;
     float xh[kChunk], h[kChunk], w[kChunk];
     auto take = [&](int j, int n) {
       load8<DT>(a.dy, i * a.dy_ld + j, n, h);
@@ -194,8 +202,9 @@ __global__ __launch_bounds__(kThreads) void zf_norm_grad_long(NormGradArgs a) {
         s2 += h[k] * xh[k];
       }
     }
-    if constexpr (LAYER) c1 = row_sum<kThreads>(s1, slots, turn) * a.inv_cols;
-    const float c2 = row_sum<kThreads>(s2, slots, turn) * a.inv_cols;
+    float sums[2] = {s2, s1};
+    row_sums<kThreads, kThreads, 2>(sums, slots, turn);
+    const float c1 = LAYER ? sums[1] * a.inv_cols : 0, c2 = sums[0] * a.inv_cols;
     for (int j = threadIdx.x * kChunk; j < a.cols; j += kSpan) {
       take(j, a.cols - j);
 #pragma unroll
@@ -225,9 +234,8 @@ __global__ __launch_bounds__(kThreads) void zf_norm_grad_columns(NormGradArgs a)
       db[k] += dy[k];
     }
   }
-  float* out = a.partial + (int64_t)blockIdx.y * a.cols;
-  store8<ZF_F32>(out, j, n, dw);
-  store8<ZF_F32>(out + (int64_t)gridDim.y * a.cols, j, n, db);
+  if (a.dw) store8<ZF_F32>(a.dw + (int64_t)blockIdx.y * a.cols, j, n, dw);
+  if (a.db) store8<ZF_F32>(a.db + (int64_t)blockIdx.y * a.cols, j, n, db);
 }
 
 // Adds the blocks' partial sums: 64 columns a block, its 16 waves every 16th
@@ -262,13 +270,36 @@ __global__ __launch_bounds__(kJoinThreads) void zf_norm_grad_join(JoinArgs a) {
 // ---------------------------------------------------------------------------
 // Host side.
 
-// Blocks of the backward pass, each with a partial sum: 4 for each compute
-// unit at most, and rows enough for each that the partial sums are little
-// beside them.
+template <typename F>
+void by_grad_shape(int64_t cols, F f) {
+  if (cols % kChunk != 0) {
+    if (cols <= 128) f(Shape<256, 16, 1, false>());
+    else if (cols <= 512) f(Shape<256, 64, 1, false>());
+    else if (cols <= 2048) f(Shape<256, 256, 1, false>());
+    else if (cols <= 4096) f(Shape<512, 512, 1, false>());
+    else if (cols <= 8192) f(Shape<1024, 1024, 1, false>());
+    else f(Shape<1024, 1024, 2, false>());
+  } else if (cols <= 128) f(Shape<256, 16, 1, true>());
+  else if (cols <= 512) f(Shape<256, 64, 1, true>());
+  else if (cols <= 1024) f(Shape<128, 128, 1, true>());
+  else if (cols <= 2048) f(Shape<256, 256, 1, true>());
+  else if (cols <= 4096) f(Shape<512, 512, 1, true>());
+  else if (cols <= 8192) f(Shape<1024, 1024, 1, true>());
+  else f(Shape<1024, 1024, 2, true>());
+}
+
+// Blocks of the backward pass, each with a partial sum: 1024 threads for each
+// compute unit (32768 rows of 2048 from a checkpoint: 70 us; half or twice as
+// many threads 90 and 76), and 4 rows at least for each group of lanes.
 int grad_blocks(int64_t rows, int64_t cols) {
-  const int64_t groups = cols <= 128 ? 16 : cols <= 2048 ? 4 : 1;
-  const int64_t want = (rows + groups * 4 - 1) / (groups * 4);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(want, 1024));
+  int64_t per = 4, most = 1024;
+  if (cols <= kMostCols)
+    by_grad_shape(cols, [&](auto shape) {
+      typedef decltype(shape) S;
+      per = S::T / S::G;
+      most = 256 * 1024 / S::T;
+    });
+  return (int)std::max<int64_t>(1, std::min<int64_t>((rows + per * 4 - 1) / (per * 4), most));
 }
 
 }  // namespace
@@ -313,7 +344,9 @@ extern "C" int zf_layer_norm_grad(const zf_layer_norm_grad_args* args, void* str
   a.mean = p.mean;
   a.rstd = p.rstd;
   a.dx = p.dx;
-  a.partial = sums ? static_cast<float*>(p.workspace) : nullptr;
+  float* partial = static_cast<float*>(p.workspace);
+  a.dw = p.weight_grad ? partial : nullptr;
+  a.db = p.bias_grad ? partial + blocks * p.cols : nullptr;
   a.dy_ld = p.dy_stride;
   a.x_ld = p.x_stride;
   a.dx_ld = p.dx_stride;
@@ -337,16 +370,16 @@ extern "C" int zf_layer_norm_grad(const zf_layer_norm_grad_args* args, void* str
           hipLaunchKernelGGL((zf_norm_grad_long<DT, KEPT, LAYER>), grid, dim3(kThreads), 0, s, a);
           return;
         }
-        by_shape(p.cols, [&](auto g, auto v, auto whole) {
-          hipLaunchKernelGGL((zf_norm_grad_kernel<DT, KEPT, LAYER, decltype(g)::value, decltype(v)::value,
-                                                  decltype(whole)::value>),
-                             dim3(blocks), dim3(kThreads), 0, s, a);
+        by_grad_shape(p.cols, [&](auto shape) {
+          typedef decltype(shape) S;
+          hipLaunchKernelGGL((zf_norm_grad_kernel<DT, KEPT, LAYER, S::T, S::G, S::V, S::WHOLE>),
+                             dim3(blocks), dim3(S::T), 0, s, a);
         });
       });
     });
   }
   if (sums) {
-    const JoinArgs j{static_cast<const float*>(p.workspace), {p.weight_grad, p.bias_grad}, blocks,
+    const JoinArgs j{partial, {p.weight_grad, p.bias_grad}, blocks,
                      (int32_t)p.cols, p.grad_dtype, p.accumulate};
     hipLaunchKernelGGL(zf_norm_grad_join, dim3((uint32_t)((p.cols + 63) / 64), 2),
                        dim3(kJoinThreads), 0, s, j);

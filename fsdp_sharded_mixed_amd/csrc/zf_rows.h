@@ -305,26 +305,32 @@ __device__ __forceinline__ void keep8(const Act8& a, int64_t i, int64_t j, int n
 }
 
 // ---------------------------------------------------------------------------
-// Sums over G neighbouring lanes (G a power of two up to 64; every lane ends
-// with the same bits) and over the waves of a block.
+// Sums over G neighbouring lanes (16 or 64; every lane ends with the same
+// bits).
 
+template <int CTRL>
+__device__ __forceinline__ float add_dpp(float x) {
+  return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xF, 0xF, true));
+}
+// By lane permutations of the vector unit alone: quads, the mirrored half of 8
+// and of 16 lanes, then rows of 16 and halves of the wave swapped between two
+// copies.  (Through shared memory, as __shfl_xor goes, a sum waits six times.)
 template <int G>
 __device__ __forceinline__ float sum_lanes(float x) {
-#pragma unroll
-  for (int off = G / 2; off > 0; off >>= 1) x += __shfl_xor(x, off, 64);
+  static_assert(G == 16 || G == 64, "a row of lanes or a wave");
+  x = add_dpp<0xB1>(x);   // quad_perm 1 0 3 2
+  x = add_dpp<0x4E>(x);   // quad_perm 2 3 0 1
+  x = add_dpp<0x141>(x);  // row_half_mirror
+  x = add_dpp<0x140>(x);  // row_mirror
+  if constexpr (G == 64) {
+    const uint32_t u = __float_as_uint(x);
+    const auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    x = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+    const uint32_t w = __float_as_uint(x);
+    const auto q = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+    x = __uint_as_float(q[0]) + __uint_as_float(q[1]);
+  }
   return x;
-}
-// Over all threads of a block of 64 W; `slot` is W floats of shared memory
-// that the block's next sum does not use.
-template <int W>
-__device__ __forceinline__ float sum_block(float x, float* slot) {
-  x = sum_lanes<64>(x);
-  if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = x;
-  __syncthreads();
-  float t = slot[0];
-#pragma unroll
-  for (int w = 1; w < W; ++w) t += slot[w];
-  return t;
 }
 
 // ---------------------------------------------------------------------------
