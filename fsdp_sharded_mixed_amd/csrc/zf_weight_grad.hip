@@ -15,6 +15,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <cstdlib>
 
 #include "zf_hip_status.h"
 #include "zf_rows.h"
@@ -39,10 +40,15 @@ struct Tile {
   static constexpr int BM = BM_, BN = BN_, kThreads = WI * WJ * 64, kWavesJ = WJ;
   static constexpr int TI = BM / WI, TJ = BN / WJ, FI = TI / 16, FJ = TJ / 16;
   static constexpr int kPBytes = kBK * BM * 2, kQBytes = kBK * BN * 2;
+  static constexpr int kShared = 2 * (kPBytes + kQBytes);  // two steps' operands, or squares of results
+  static_assert(kShared >= WI * WJ * 16384, "squares fit");
   static constexpr int kPPieces = kBK * BM / 8 / kThreads;   // of 8 gradients a thread
   static constexpr int kQPieces = kBK * BN / 16 / kThreads;  // of 16 codes a thread
 };
 typedef Tile<128, 128, 2, 2> Middle;
+typedef Tile<256, 256, 2, 4> Big;
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+typedef __amdgpu_buffer_rsrc_t Rsrc;
 
 struct GradArgs {
   const void* dy;
@@ -94,9 +100,61 @@ __device__ __forceinline__ s16x8 fragment(const char* tile, int k0, int c0) {
   return __builtin_shufflevector(half[0], half[1], 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
+// Results leave by whole lines: a wave's squares of 64 x 64 go to shared memory
+// (16 KiB a wave; 16-byte pieces permuted by the row, for the banks) and out
+// again 8 columns a lane, with one piece of code for every type.
+// acc[i][j][r] is row l, column 4 g + r of a 16 x 16 square.
+template <typename T>
+__device__ __forceinline__ void write_tile(const GradArgs& a, const f32x4 (&acc)[T::FI][T::FJ], char* shared,
+                                           int i0, int j0, int split) {
+  static_assert(T::TJ == 64 && T::TI % 64 == 0, "squares");
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
+  ZF_LDS float* square = (ZF_LDS float*)shared + wave * 4096;
+  float* partial = a.partial ? a.partial + (int64_t)split * a.out * a.in : nullptr;
+  const int32_t gdt = partial ? (int32_t)ZF_F32 : a.gdt;
+  void* to = partial ? partial : a.grad;
+  const bool add = a.accumulate && !partial;
+  const int c = lane & 7, j = j0 + wave % T::kWavesJ * T::TJ + c * 8, n = a.in - j;
+#pragma unroll
+  for (int q = 0; q < T::TI / 64; ++q) {
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
+#pragma unroll
+      for (int fj = 0; fj < T::FJ; ++fj)
+        *(ZF_LDS f32x4*)(square + (f * 16 + l) * 64 + ((fj * 4 + g) ^ (l & 7)) * 4) = acc[q * 4 + f][fj];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    const int o0 = i0 + wave / T::kWavesJ * T::TI + q * 64;
+#pragma unroll 1
+    for (int r = lane >> 3; r < 64; r += 8) {
+      if (o0 + r >= a.out || n <= 0) break;
+      const int64_t at = (int64_t)(o0 + r) * a.in + j;
+      float v[kChunk], old[kChunk];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const f32x4 x = *(ZF_LDS f32x4*)(square + r * 64 + ((2 * c + h) ^ (r & 7)) * 4);
+        v[h * 4] = x.x;
+        v[h * 4 + 1] = x.y;
+        v[h * 4 + 2] = x.z;
+        v[h * 4 + 3] = x.w;
+      }
+      if (add) {
+        load8_of(gdt, to, at, n, old);
+#pragma unroll
+        for (int k = 0; k < kChunk; ++k) v[k] += old[k];
+      }
+      if (gdt == ZF_F32) store8<ZF_F32>(to, at, n, v);
+      else if (gdt == ZF_BF16) store8<ZF_BF16>(to, at, n, v);
+      else store8<ZF_F16>(to, at, n, v);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
 template <typename T, int DT>
 __global__ __launch_bounds__(T::kThreads) void zf_weight_grad_kernel(GradArgs a) {
-  __shared__ __align__(16) char shared[T::kPBytes + T::kQBytes];
+  __shared__ __align__(16) char shared[T::kShared];
   const int tid = threadIdx.x;
   const int tile = blockIdx.x % a.tiles, split = blockIdx.x / a.tiles;
   const int i0 = tile / a.tiles_in * T::BM, j0 = tile % a.tiles_in * T::BN;
@@ -174,28 +232,249 @@ __global__ __launch_bounds__(T::kThreads) void zf_weight_grad_kernel(GradArgs a)
         for (int j = 0; j < T::FJ; ++j) acc[i][j] = mma<DT>(fq[j], fp[i], acc[i][j]);
     }
   }
+  __syncthreads();
+  write_tile<T>(a, acc, shared, i0, j0, split);
+}
 
-  // acc[i][j][r]: row l, columns 4 g + r of a 16 x 16 square
-  const int lane = tid & 63, l = lane & 15, g = lane >> 4;
+// ---------------------------------------------------------------------------
+// The same for whole 16-byte pieces at 16-byte alignment: gradients go from
+// global to shared memory directly, into two buffers in turn, and codes come a
+// step earlier into registers, from where they are converted into the buffer.
+
+// Where a matrix's next step lies: the address of its first row in this tile's
+// columns, and the rows that are left.  Loads past the matrix's end give zeros
+// (in shared memory too), so tokens behind the last one add nothing; loads past
+// a row's end give elements of columns that are not written.
+struct Walk {
+  const char* at;
+  int32_t left, ld, tail;  // rows; bytes of a stride, and of a row from here on
+
+  __device__ __forceinline__ Walk(const void* base, int64_t row, int64_t rows, int64_t row_bytes, int64_t skip,
+                                  int64_t width) {
+    at = static_cast<const char*>(base) + row * row_bytes + skip;
+    left = (int32_t)rows;
+    ld = (int32_t)row_bytes;
+    tail = (int32_t)(width - skip);
+  }
+  // A step's buffer.  128 rows are as good as more: a tile's columns reach 64
+  // rows on and, past the rows' ends, 32 more at most.  All of it is 32-bit
+  // scalar arithmetic without branches, which would part the step's
+  // instructions.
+  __device__ __forceinline__ uint32_t extent() const {
+    const int32_t rows = min(left, 128);
+    return rows > 0 ? (uint32_t)(rows - 1) * (uint32_t)ld + (uint32_t)tail : 0u;
+  }
+  __device__ __forceinline__ Rsrc buffer(uint32_t n) const {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(at), 0, n, 0x00020000);
+  }
+  __device__ __forceinline__ void next() {
+    at += (int64_t)kBK * ld;
+    left -= kBK;
+  }
+};
+// An offset that all lanes share, clamped: the hardware compares a lane's own
+// offset with n less the shared one, which must not wrap.
+__device__ __forceinline__ int within(uint32_t at, uint32_t n) { return (int)min(at, n); }
+
+// (The compiler's pass over the host code does not know the 16-byte form.)
+__device__ __forceinline__ void to_shared(Rsrc from, ZF_LDS char* to, int lane_at, int at) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (ZF_LDS void*)to, 16, lane_at, at, 0, 0);
+#endif
+}
+
+template <typename T>
+struct Frags {
+  s16x8 p[T::FI], q[T::FJ];
+};
+
+template <typename T, int DT>
+struct Pipe {
+  static constexpr int kBuf = T::kPBytes + T::kQBytes;
+  static constexpr int kPRows = T::kThreads / (T::BM / 8);   // rows that a load of all threads covers
+  static constexpr int kQRows = T::kThreads / (T::BN / 16);
+  static constexpr int kPLoads = kBK / kPRows, kQLoads = kBK / kQRows;
+  static_assert(kPRows % 16 == 0 && kQRows % 16 == 0, "rows of one load are permuted alike");
+
+  Walk p, q, s;  // gradients, codes, scales
+  int vp, vq, vs, wq, rp, rq;
+  u32x4 codes[kQLoads];
+  uint32_t scale[kQLoads];
+
+  __device__ __forceinline__ Pipe(const GradArgs& a, int i0, int j0, int64_t first, int64_t rows)
+      : p(a.dy, first, rows, a.dy_ld * 2, (int64_t)i0 * 2, (int64_t)a.out * 2),
+        q(a.x.codes, first, rows, a.x.code_ld, j0, a.in),
+        s(a.x.scales, first, rows, a.x.scale_ld, j0 / ZF_ACT8_GROUP, (a.in + ZF_ACT8_GROUP - 1) / ZF_ACT8_GROUP) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l = lane & 15, g = lane >> 4;
+    // shared memory is filled in order, so a lane loads the piece that belongs
+    // at its place
+    const int row = tid / (T::BM / 8), at = place<T::BM / 8>(row, tid % (T::BM / 8));
+    vp = row * p.ld + at % (T::BM * 2);
+    const int qrow = tid / (T::BN / 16), piece = tid % (T::BN / 16);
+    vq = qrow * q.ld + piece * 16;
+    vs = qrow * s.ld + piece * 16 / ZF_ACT8_GROUP;
+    wq = T::kPBytes + place<T::BN / 8>(qrow, piece * 2);
+    const int frow = 8 * g + (l >> 2), half = (l & 3) >> 1, wi = wave / T::kWavesJ * T::TI,
+              wj = wave % T::kWavesJ * T::TJ;
+    rp = place<T::BM / 8>(frow, wi / 8 + half) + (l & 1) * 8;
+    rq = T::kPBytes + place<T::BN / 8>(frow, wj / 8 + half) + (l & 1) * 8;
+  }
+
+  // gradients of the next step into `buf`
+  __device__ __forceinline__ void fetch_p(char* buf) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t n = p.extent();
+    const Rsrc from = p.buffer(n);
+    ZF_LDS char* to = (ZF_LDS char*)buf + wave * 1024;
+#pragma unroll
+    for (int h = 0; h < kPLoads; ++h)
+      to_shared(from, to + h * T::kThreads * 16, vp, within(h * kPRows * (uint32_t)p.ld, n));
+    p.next();
+  }
+  // codes of the next step into registers
+  __device__ __forceinline__ void fetch_q() {
+    const uint32_t nq = q.extent(), ns = s.extent();
+    const Rsrc from = q.buffer(nq), scales = s.buffer(ns);
+#pragma unroll
+    for (int h = 0; h < kQLoads; ++h) {
+      codes[h] = __builtin_bit_cast(
+          u32x4, __builtin_amdgcn_raw_buffer_load_b128(from, vq, within(h * kQRows * (uint32_t)q.ld, nq), 0));
+      scale[h] = __builtin_amdgcn_raw_buffer_load_b8(scales, vs, within(h * kQRows * (uint32_t)s.ld, ns), 0);
+    }
+    q.next();
+    s.next();
+  }
+  // the codes in registers as 16-bit numbers into `buf`
+  __device__ __forceinline__ void put_q(char* buf) const {
+#pragma unroll
+    for (int h = 0; h < kQLoads; ++h) {
+      const float s = __uint_as_float(scale[h] << 23);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const u32x4 x = {decode2<DT, false>(codes[h][e * 2], s), decode2<DT, true>(codes[h][e * 2], s),
+                         decode2<DT, false>(codes[h][e * 2 + 1], s), decode2<DT, true>(codes[h][e * 2 + 1], s)};
+        *(ZF_LDS u32x4*)((ZF_LDS char*)buf + (wq ^ (e * 16)) + h * kQRows * T::BN * 2) = x;
+      }
+    }
+  }
+  __device__ __forceinline__ s16x8 one(const char* at, int row_bytes) const {
+    s16x4 half[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      half[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ZF_LDS s16x4*)((const ZF_LDS char*)at + e * 4 * row_bytes));
+    return __builtin_shufflevector(half[0], half[1], 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+  // Fragment f's pieces lie at the first one's place ^ 32 f: its bits of the
+  // piece's number are zero in the first (a wave's columns begin at a multiple
+  // of 64 or 128).  The places are computed anew each time, since 12 registers
+  // that hold them would be spilled.
+  __device__ __forceinline__ void read(const char* buf, int kk, Frags<T>& f) const {
+    int p = rp, q = rq;
+    asm volatile("" : "+v"(p), "+v"(q));
+#pragma unroll
+    for (int j = 0; j < T::FJ; ++j) f.q[j] = one(buf + (q ^ (j * 32)) + kk * 32 * T::BN * 2, T::BN * 2);
+#pragma unroll
+    for (int i = 0; i < T::FI; ++i) f.p[i] = one(buf + (p ^ (i * 32)) + kk * 32 * T::BM * 2, T::BM * 2);
+  }
+  static_assert((T::BM / 8) % (2 * T::FI) == 0 && (T::BN / 8) % (2 * T::FJ) == 0, "fragments' pieces");
+};
+
+template <typename T, int DT>
+__device__ __forceinline__ void multiply(const Frags<T>& f, f32x4 (&acc)[T::FI][T::FJ]) {
 #pragma unroll
   for (int i = 0; i < T::FI; ++i)
 #pragma unroll
-    for (int j = 0; j < T::FJ; ++j) {
-      const int o = i0 + wi + i * 16 + l, c = j0 + wj + j * 16 + g * 4;
-      if (o >= a.out) continue;
-      const int64_t at = (int64_t)o * a.in + c;
+    for (int j = 0; j < T::FJ; ++j) acc[i][j] = mma<DT>(f.q[j], f.p[i], acc[i][j]);
+}
+
+// The order within a half: one read of shared memory, one load, then a share of
+// the matrix instructions, again and again.
+template <typename T, int LOADS>
+__device__ __forceinline__ void interleave() {
+  constexpr int reads = 2 * (T::FI + T::FJ), mma = T::FI * T::FJ;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        if (c + r >= a.in) break;
-        float v = acc[i][j][r];
-        if (a.partial) {
-          a.partial[(int64_t)split * a.out * a.in + at + r] = v;
-        } else {
-          if (a.accumulate) v += load1_of(a.gdt, a.grad, at + r);
-          store1_of(a.gdt, a.grad, at + r, v);
-        }
-      }
-    }
+  for (int k = 0; k < reads; ++k) {
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    if (k < LOADS) __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x8, mma / reads, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x8, mma % reads, 0);
+}
+
+// Loads before this stay before those after it, so that a wait that leaves the
+// last N loads on their way knows which those are.
+__device__ __forceinline__ void loads_in_order() { __builtin_amdgcn_sched_barrier(0x38F); }
+
+// All but the wave's last N loads have arrived and its accesses of shared
+// memory are done, for all waves.
+template <int N>
+__device__ __forceinline__ void arrive() {
+  static_assert(N < 64, "the counter's range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0070);
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+template <typename T, int DT>
+__global__ __launch_bounds__(T::kThreads) void zf_weight_grad_pipe(GradArgs a) {
+  typedef Pipe<T, DT> P;
+  __shared__ __align__(16) char shared[T::kShared];
+  char *s0 = shared, *s1 = shared + P::kBuf;
+  const int tile = blockIdx.x % a.tiles, split = blockIdx.x / a.tiles;
+  const int i0 = tile / a.tiles_in * T::BM, j0 = tile % a.tiles_in * T::BN;
+  const int64_t first = split * a.split_rows, end = min(first + a.split_rows, a.rows);
+  f32x4 acc[T::FI][T::FJ];
+#pragma unroll
+  for (int i = 0; i < T::FI; ++i)
+#pragma unroll
+    for (int j = 0; j < T::FJ; ++j) acc[i][j] = (f32x4){0, 0, 0, 0};
+  const int steps = (int)((end - first + kBK - 1) / kBK);
+  P o(a, i0, j0, first, end - first);
+  Frags<T> fa, fb;
+  // A step's barrier stands between its two halves: the next half's fragments
+  // are read while this one's products run, and a buffer is filled again as
+  // soon as its second half is in registers, a whole step before its use.
+  auto half0 = [&](const char* cur) {
+    o.read(cur, 1, fb);
+    multiply<T, DT>(fa, acc);
+    interleave<T, 0>();
+  };
+  auto half1 = [&](char* cur, const char* nxt) {
+    o.fetch_p(cur);
+    loads_in_order();
+    o.read(nxt, 0, fa);
+    o.put_q(cur);
+    o.fetch_q();
+    multiply<T, DT>(fb, acc);
+    interleave<T, P::kPLoads>();
+  };
+  constexpr int ahead = 2 * P::kQLoads;  // loads of codes after a step's loads of gradients
+  o.fetch_p(s0);
+  o.fetch_q();
+  o.put_q(s0);
+  o.fetch_q();
+  o.fetch_p(s1);
+  o.put_q(s1);
+  o.fetch_q();
+  arrive<0>();
+  o.read(s0, 0, fa);
+  int k = 0;
+#pragma unroll 1
+  for (; k + 2 <= steps; k += 2) {
+    half0(s0);
+    arrive<ahead>();
+    half1(s0, s1);
+    half0(s1);
+    arrive<ahead>();
+    half1(s1, s0);
+  }
+  if (k < steps) {
+    half0(s0);
+    multiply<T, DT>(fb, acc);
+  }
+  arrive<0>();
+  write_tile<T>(a, acc, shared, i0, j0, split);
 }
 
 // Adds the splits' partial results in order.
@@ -230,28 +509,57 @@ __global__ __launch_bounds__(kThreads) void zf_weight_grad_join(JoinArgs a) {
 }
 
 struct Plan {
-  int32_t tiles_out, tiles_in, splits;
+  bool big;
+  int32_t splits;
   int64_t split_rows, bytes;
 };
+
+int64_t tiles_of(int64_t out, int64_t in, int side) {
+  return ((out + side - 1) / side) * ((in + side - 1) / side);
+}
 
 int plan(int64_t rows, int64_t out, int64_t in, Plan& g) {
   int rc = shape_ok(rows, in);
   if (rc == ZF_OK) rc = shape_ok(0, out);
   if (rc != ZF_OK) return rc;
-  typedef Middle T;
-  const int64_t tiles_out = (out + T::BM - 1) / T::BM, tiles_in = (in + T::BN - 1) / T::BN;
-  const int64_t tiles = tiles_out * tiles_in, steps = (rows + kBK - 1) / kBK;
-  if (tiles > kMaxBlocks) return ZF_ESIZE;
-  // blocks for two rounds of the compute units, of 4 steps at least
-  int64_t splits = std::min((512 + tiles - 1) / tiles, (steps + 3) / 4);
+  const int64_t steps = (rows + kBK - 1) / kBK;
+  if (tiles_of(out, in, Middle::BM) > kMaxBlocks) return ZF_ESIZE;
+  static const int force = getenv("ZF_TILE") ? atoi(getenv("ZF_TILE")) : 0;
+  static const int slots = getenv("ZF_SLOTS") ? atoi(getenv("ZF_SLOTS")) : 0;
+  g.big = tiles_of(out, in, Big::BM) >= 128;
+  if (force) g.big = force == 256;
+  const int64_t tiles = tiles_of(out, in, g.big ? Big::BM : Middle::BM);
+  // blocks for all places of the compute units, of 4 steps at least
+  const int64_t places = slots ? slots : g.big ? 256 : 512;
+  int64_t splits = std::min(places / tiles, (steps + 3) / 4);
   splits = std::max<int64_t>(splits, 1);
   const int64_t per = std::max<int64_t>((steps + splits - 1) / splits, 1);
-  g.tiles_out = (int32_t)tiles_out;
-  g.tiles_in = (int32_t)tiles_in;
   g.split_rows = per * kBK;
   g.splits = (int32_t)std::max<int64_t>((steps + per - 1) / per, 1);
   g.bytes = g.splits > 1 ? (g.splits * out * in * 4 + 15) / 16 * 16 : 0;
   return ZF_OK;
+}
+
+// Whole 16-byte pieces at 16-byte alignment, and 64 rows within an offset of
+// 31 bits.
+bool whole_pieces(const GradArgs& a) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(a.dy) | reinterpret_cast<uintptr_t>(a.x.codes);
+  return (at & 15) == 0 && ((a.dy_ld | a.out) & 7) == 0 && ((a.x.code_ld | a.in) & 15) == 0 &&
+         a.dy_ld < 1 << 23 && a.x.code_ld < 1 << 24 && a.x.scale_ld < 1 << 24;
+}
+
+template <typename T, bool PIPE>
+void launch(GradArgs a, int32_t dtype, hipStream_t s) {
+  a.tiles_in = (a.in + T::BN - 1) / T::BN;
+  a.tiles = a.tiles_in * ((a.out + T::BM - 1) / T::BM);
+  const dim3 grid((uint32_t)a.tiles * (uint32_t)a.splits), block(T::kThreads);
+  if constexpr (PIPE) {
+    if (dtype == ZF_BF16) hipLaunchKernelGGL((zf_weight_grad_pipe<T, ZF_BF16>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((zf_weight_grad_pipe<T, ZF_F16>), grid, block, 0, s, a);
+  } else {
+    if (dtype == ZF_BF16) hipLaunchKernelGGL((zf_weight_grad_kernel<T, ZF_BF16>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((zf_weight_grad_kernel<T, ZF_F16>), grid, block, 0, s, a);
+  }
 }
 
 }  // namespace
@@ -281,22 +589,23 @@ extern "C" int zf_weight_grad(const zf_weight_grad_args* args, void* stream) {
   a.grad = p.grad;
   a.partial = g.splits > 1 ? static_cast<float*>(p.workspace) : nullptr;
   a.dy_ld = p.dy_stride;
+  if (p.rows <= 1) {  // strides of a single row are not looked at
+    a.dy_ld = (p.out_features + 7) / 8 * 8;
+    a.x.code_ld = (p.in_features + 15) / 16 * 16;
+    a.x.scale_ld = 0;
+  }
   a.rows = p.rows;
   a.split_rows = g.split_rows;
   a.out = (int32_t)p.out_features;
   a.in = (int32_t)p.in_features;
-  a.tiles_in = g.tiles_in;
-  a.tiles = g.tiles_out * g.tiles_in;
   a.splits = g.splits;
   a.gdt = p.grad_dtype;
   a.accumulate = p.accumulate;
   hipStream_t s = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();
-  const dim3 grid((uint32_t)a.tiles * (uint32_t)g.splits);
-  if (p.dtype == ZF_BF16)
-    hipLaunchKernelGGL((zf_weight_grad_kernel<Middle, ZF_BF16>), grid, dim3(Middle::kThreads), 0, s, a);
-  else
-    hipLaunchKernelGGL((zf_weight_grad_kernel<Middle, ZF_F16>), grid, dim3(Middle::kThreads), 0, s, a);
+  if (!whole_pieces(a)) launch<Middle, false>(a, p.dtype, s);
+  else if (g.big) launch<Big, true>(a, p.dtype, s);
+  else launch<Middle, true>(a, p.dtype, s);
   if (g.splits > 1) {
     const JoinArgs j{a.partial, p.grad, p.out_features * p.in_features, g.splits, p.grad_dtype,
                      p.accumulate};
