@@ -107,24 +107,27 @@ __device__ __forceinline__ s16x8 fragment(const char* tile, int k0, int c0) {
 template <typename T>
 __device__ __forceinline__ void write_tile(const GradArgs& a, const f32x4 (&acc)[T::FI][T::FJ], char* shared,
                                            int i0, int j0, int split) {
-  static_assert(T::TJ == 64 && T::TI % 64 == 0, "squares");
+  static_assert(T::TJ % 64 == 0 && T::TI % 64 == 0, "squares");
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
   ZF_LDS float* square = (ZF_LDS float*)shared + wave * 4096;
   float* partial = a.partial ? a.partial + (int64_t)split * a.out * a.in : nullptr;
   const int32_t gdt = partial ? (int32_t)ZF_F32 : a.gdt;
   void* to = partial ? partial : a.grad;
   const bool add = a.accumulate && !partial;
-  const int c = lane & 7, j = j0 + wave % T::kWavesJ * T::TJ + c * 8, n = a.in - j;
+  const int c = lane & 7;
 #pragma unroll
-  for (int q = 0; q < T::TI / 64; ++q) {
+  for (int q = 0; q < T::TI / 64 * (T::TJ / 64); ++q) {
+    const int qi = q / (T::TJ / 64), qj = q % (T::TJ / 64);
+    const int j = j0 + wave % T::kWavesJ * T::TJ + qj * 64 + c * 8, n = a.in - j;
 #pragma unroll
     for (int f = 0; f < 4; ++f)
 #pragma unroll
-      for (int fj = 0; fj < T::FJ; ++fj)
-        *(ZF_LDS f32x4*)(square + (f * 16 + l) * 64 + ((fj * 4 + g) ^ (l & 7)) * 4) = acc[q * 4 + f][fj];
+      for (int fj = 0; fj < 4; ++fj)
+        *(ZF_LDS f32x4*)(square + (f * 16 + l) * 64 + ((fj * 4 + g) ^ (l & 7)) * 4) =
+            acc[qi * 4 + f][qj * 4 + fj];
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    const int o0 = i0 + wave / T::kWavesJ * T::TI + q * 64;
+    const int o0 = i0 + wave / T::kWavesJ * T::TI + qi * 64;
 #pragma unroll 1
     for (int r = lane >> 3; r < 64; r += 8) {
       if (o0 + r >= a.out || n <= 0) break;
@@ -152,12 +155,33 @@ __device__ __forceinline__ void write_tile(const GradArgs& a, const f32x4 (&acc)
   }
 }
 
+// Blocks go to the 8 XCDs in turn.  Each XCD takes runs of consecutive places,
+// as many as it works on at a time, and consecutive places form squares of 8 x
+// 8 tiles, which share rows of their operands in its cache; the splits follow
+// one another.
+struct Place {
+  int i, j, split;
+  __device__ __forceinline__ explicit Place(const GradArgs& a) {
+    const int all = gridDim.x, run = min(max(all / 8, 1), 64), whole = all / (8 * run) * (8 * run);
+    int b = blockIdx.x;
+    if (b < whole) b = (b / 8 / run * 8 + b % 8) * run + b / 8 % run;
+    split = b / a.tiles;
+    b -= split * a.tiles;
+    const int i8 = b / (8 * a.tiles_in) * 8, h = min(8, a.tiles / a.tiles_in - i8);
+    b -= i8 * a.tiles_in;
+    const int j8 = b / (8 * h) * 8, w = min(8, a.tiles_in - j8);
+    b -= j8 * h;
+    i = i8 + b / w;
+    j = j8 + b % w;
+  }
+};
+
 template <typename T, int DT>
 __global__ __launch_bounds__(T::kThreads) void zf_weight_grad_kernel(GradArgs a) {
   __shared__ __align__(16) char shared[T::kShared];
   const int tid = threadIdx.x;
-  const int tile = blockIdx.x % a.tiles, split = blockIdx.x / a.tiles;
-  const int i0 = tile / a.tiles_in * T::BM, j0 = tile % a.tiles_in * T::BN;
+  const Place at(a);
+  const int i0 = at.i * T::BM, j0 = at.j * T::BN, split = at.split;
   const int64_t first = split * a.split_rows, end = min(first + a.split_rows, a.rows);
   const int wave = tid >> 6, wi = wave / T::kWavesJ * T::TI, wj = wave % T::kWavesJ * T::TJ;
 
@@ -241,7 +265,10 @@ __global__ __launch_bounds__(T::kThreads) void zf_weight_grad_kernel(GradArgs a)
 // global to shared memory directly, into two buffers in turn, and codes come a
 // step earlier into registers, from where they are converted into the buffer.
 
-// Where a matrix's next step lies: the address of its first row in this tile's
+// A stage is 32 tokens; kStages of them lie in shared memory in turn.
+constexpr int kStages = 4, kDepth = 32;
+
+// Where a matrix's next stage lies: the address of its first row in this tile's
 // columns, and the rows that are left.  Loads past the matrix's end give zeros
 // (in shared memory too), so tokens behind the last one add nothing; loads past
 // a row's end give elements of columns that are not written.
@@ -256,10 +283,10 @@ struct Walk {
     ld = (int32_t)row_bytes;
     tail = (int32_t)(width - skip);
   }
-  // A step's buffer.  128 rows are as good as more: a tile's columns reach 64
-  // rows on and, past the rows' ends, 32 more at most.  All of it is 32-bit
-  // scalar arithmetic without branches, which would part the step's
-  // instructions.
+  // A stage's buffer.  128 rows are as good as more: it has 32, and its tile's
+  // columns reach 32 further rows at most past the rows' ends.  All of it is 32-bit
+  // scalar arithmetic without branches, which would part the
+  // stage's instructions.
   __device__ __forceinline__ uint32_t extent() const {
     const int32_t rows = min(left, 128);
     return rows > 0 ? (uint32_t)(rows - 1) * (uint32_t)ld + (uint32_t)tail : 0u;
@@ -268,8 +295,8 @@ struct Walk {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(at), 0, n, 0x00020000);
   }
   __device__ __forceinline__ void next() {
-    at += (int64_t)kBK * ld;
-    left -= kBK;
+    at += (int64_t)kDepth * ld;
+    left -= kDepth;
   }
 };
 // An offset that all lanes share, clamped: the hardware compares a lane's own
@@ -283,23 +310,24 @@ __device__ __forceinline__ void to_shared(Rsrc from, ZF_LDS char* to, int lane_a
 #endif
 }
 
-template <typename T>
-struct Frags {
-  s16x8 p[T::FI], q[T::FJ];
-};
-
 template <typename T, int DT>
 struct Pipe {
-  static constexpr int kBuf = T::kPBytes + T::kQBytes;
+  static constexpr int kPBytes = kDepth * T::BM * 2, kQBytes = kDepth * T::BN * 2;
+  static constexpr int kBuf = kPBytes + kQBytes;
+  static_assert(kStages * kBuf <= T::kShared, "stages fit");
   static constexpr int kPRows = T::kThreads / (T::BM / 8);   // rows that a load of all threads covers
-  static constexpr int kQRows = T::kThreads / (T::BN / 16);
-  static constexpr int kPLoads = kBK / kPRows, kQLoads = kBK / kQRows;
-  static_assert(kPRows % 16 == 0 && kQRows % 16 == 0, "rows of one load are permuted alike");
+  static constexpr int kPLoads = kDepth / kPRows;
+  static_assert(kPRows % 16 == 0, "the rows of a lane's loads are permuted alike");
+  static_assert(T::kThreads / (T::BN / 16) == kDepth, "16 codes a thread");
+  static constexpr int kLoads = kPLoads + 2;  // of a thread and stage
 
   Walk p, q, s;  // gradients, codes, scales
   int vp, vq, vs, wq, rp, rq;
-  u32x4 codes[kQLoads];
-  uint32_t scale[kQLoads];
+
+  struct Codes {
+    u32x4 c;
+    uint32_t scale;
+  };
 
   __device__ __forceinline__ Pipe(const GradArgs& a, int i0, int j0, int64_t first, int64_t rows)
       : p(a.dy, first, rows, a.dy_ld * 2, (int64_t)i0 * 2, (int64_t)a.out * 2),
@@ -313,15 +341,15 @@ struct Pipe {
     const int qrow = tid / (T::BN / 16), piece = tid % (T::BN / 16);
     vq = qrow * q.ld + piece * 16;
     vs = qrow * s.ld + piece * 16 / ZF_ACT8_GROUP;
-    wq = T::kPBytes + place<T::BN / 8>(qrow, piece * 2);
+    wq = kPBytes + place<T::BN / 8>(qrow, piece * 2);
     const int frow = 8 * g + (l >> 2), half = (l & 3) >> 1, wi = wave / T::kWavesJ * T::TI,
               wj = wave % T::kWavesJ * T::TJ;
     rp = place<T::BM / 8>(frow, wi / 8 + half) + (l & 1) * 8;
-    rq = T::kPBytes + place<T::BN / 8>(frow, wj / 8 + half) + (l & 1) * 8;
+    rq = kPBytes + place<T::BN / 8>(frow, wj / 8 + half) + (l & 1) * 8;
   }
 
-  // gradients of the next step into `buf`
-  __device__ __forceinline__ void fetch_p(char* buf) {
+  // gradients of the next stage into `buf`
+  __device__ __forceinline__ void fetch_p(char* __restrict buf) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t n = p.extent();
     const Rsrc from = p.buffer(n);
@@ -331,75 +359,37 @@ struct Pipe {
       to_shared(from, to + h * T::kThreads * 16, vp, within(h * kPRows * (uint32_t)p.ld, n));
     p.next();
   }
-  // codes of the next step into registers
-  __device__ __forceinline__ void fetch_q() {
-    const uint32_t nq = q.extent(), ns = s.extent();
-    const Rsrc from = q.buffer(nq), scales = s.buffer(ns);
-#pragma unroll
-    for (int h = 0; h < kQLoads; ++h) {
-      codes[h] = __builtin_bit_cast(
-          u32x4, __builtin_amdgcn_raw_buffer_load_b128(from, vq, within(h * kQRows * (uint32_t)q.ld, nq), 0));
-      scale[h] = __builtin_amdgcn_raw_buffer_load_b8(scales, vs, within(h * kQRows * (uint32_t)s.ld, ns), 0);
-    }
+  // codes of the next stage into registers
+  __device__ __forceinline__ void fetch_q(Codes& c) {
+    c.c = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(q.buffer(q.extent()), vq, 0, 0));
+    c.scale = __builtin_amdgcn_raw_buffer_load_b8(s.buffer(s.extent()), vs, 0, 0);
     q.next();
     s.next();
   }
-  // the codes in registers as 16-bit numbers into `buf`
-  __device__ __forceinline__ void put_q(char* buf) const {
+  // codes as 16-bit numbers into `buf`
+  __device__ __forceinline__ void put_q(char* __restrict buf, const Codes& c) const {
+    const float scale = __uint_as_float(c.scale << 23);
 #pragma unroll
-    for (int h = 0; h < kQLoads; ++h) {
-      const float s = __uint_as_float(scale[h] << 23);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const u32x4 x = {decode2<DT, false>(codes[h][e * 2], s), decode2<DT, true>(codes[h][e * 2], s),
-                         decode2<DT, false>(codes[h][e * 2 + 1], s), decode2<DT, true>(codes[h][e * 2 + 1], s)};
-        *(ZF_LDS u32x4*)((ZF_LDS char*)buf + (wq ^ (e * 16)) + h * kQRows * T::BN * 2) = x;
-      }
+    for (int e = 0; e < 2; ++e) {
+      const u32x4 x = {decode2<DT, false>(c.c[e * 2], scale), decode2<DT, true>(c.c[e * 2], scale),
+                       decode2<DT, false>(c.c[e * 2 + 1], scale), decode2<DT, true>(c.c[e * 2 + 1], scale)};
+      *(ZF_LDS u32x4*)((ZF_LDS char*)buf + (wq ^ (e * 16))) = x;
     }
   }
-  __device__ __forceinline__ s16x8 one(const char* at, int row_bytes) const {
+  // Fragment f of 8 tokens a lane.  Its pieces lie at the first one's place ^ 32
+  // f: those bits of the piece's number are zero in the first (a wave's columns
+  // begin at a multiple of 64 or 128).
+  template <int COLS>
+  __device__ __forceinline__ s16x8 read(const char* __restrict buf, int first, int f) const {
+    const ZF_LDS char* at = (const ZF_LDS char*)buf + (first ^ (f * 32));
     s16x4 half[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e)
-      half[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ZF_LDS s16x4*)((const ZF_LDS char*)at + e * 4 * row_bytes));
+      half[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ZF_LDS s16x4*)(at + e * 4 * COLS * 2));
     return __builtin_shufflevector(half[0], half[1], 0, 1, 2, 3, 4, 5, 6, 7);
-  }
-  // Fragment f's pieces lie at the first one's place ^ 32 f: its bits of the
-  // piece's number are zero in the first (a wave's columns begin at a multiple
-  // of 64 or 128).  The places are computed anew each time, since 12 registers
-  // that hold them would be spilled.
-  __device__ __forceinline__ void read(const char* buf, int kk, Frags<T>& f) const {
-    int p = rp, q = rq;
-    asm volatile("" : "+v"(p), "+v"(q));
-#pragma unroll
-    for (int j = 0; j < T::FJ; ++j) f.q[j] = one(buf + (q ^ (j * 32)) + kk * 32 * T::BN * 2, T::BN * 2);
-#pragma unroll
-    for (int i = 0; i < T::FI; ++i) f.p[i] = one(buf + (p ^ (i * 32)) + kk * 32 * T::BM * 2, T::BM * 2);
   }
   static_assert((T::BM / 8) % (2 * T::FI) == 0 && (T::BN / 8) % (2 * T::FJ) == 0, "fragments' pieces");
 };
-
-template <typename T, int DT>
-__device__ __forceinline__ void multiply(const Frags<T>& f, f32x4 (&acc)[T::FI][T::FJ]) {
-#pragma unroll
-  for (int i = 0; i < T::FI; ++i)
-#pragma unroll
-    for (int j = 0; j < T::FJ; ++j) acc[i][j] = mma<DT>(f.q[j], f.p[i], acc[i][j]);
-}
-
-// The order within a half: one read of shared memory, one load, then a share of
-// the matrix instructions, again and again.
-template <typename T, int LOADS>
-__device__ __forceinline__ void interleave() {
-  constexpr int reads = 2 * (T::FI + T::FJ), mma = T::FI * T::FJ;
-#pragma unroll
-  for (int k = 0; k < reads; ++k) {
-    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-    if (k < LOADS) __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(0x8, mma / reads, 0);
-  }
-  __builtin_amdgcn_sched_group_barrier(0x8, mma % reads, 0);
-}
 
 // Loads before this stay before those after it, so that a wait that leaves the
 // last N loads on their way knows which those are.
@@ -414,64 +404,92 @@ __device__ __forceinline__ void arrive() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);  // products stay in their stage
+}
+
+// Stage k, whose fragments p and q are in registers: its products, while the
+// next stage's fragments are read from `next`, the codes of stage k + 2 are
+// written to `fill_q` and the gradients of stage k + 4 are on their way to the
+// buffer that stage k has left.  Loads are on their way for two stages (codes)
+// and three (gradients).
+template <typename T, int DT>
+__device__ __forceinline__ void stage(Pipe<T, DT>& o, const char* __restrict next, char* __restrict fill_q,
+                                      char* __restrict fill_p, s16x8 (&p)[T::FI], const s16x8 (&q)[T::FJ],
+                                      s16x8 (&q_next)[T::FJ], typename Pipe<T, DT>::Codes& codes,
+                                      f32x4 (&acc)[T::FI][T::FJ]) {
+  typedef Pipe<T, DT> P;
+  // stage k + 1 is complete: its gradients were followed by the codes of the
+  // same stage and by all loads of two more
+  arrive<2 + 2 * P::kLoads>();
+  // fragments' places are computed anew in each stage: registers that hold them
+  // would be spilled
+  int rp = o.rp, rq = o.rq;
+  asm volatile("" : "+v"(rp), "+v"(rq));
+  o.fetch_p(fill_p);
+#pragma unroll
+  for (int i = 0; i < T::FI; ++i) {
+#pragma unroll
+    for (int j = 0; j < T::FJ; ++j) acc[i][j] = mma<DT>(q[j], p[i], acc[i][j]);
+    p[i] = o.template read<T::BM>(next, rp, i);
+    if (i < T::FJ) q_next[i] = o.template read<T::BN>(next, rq, i);
+  }
+  o.put_q(fill_q, codes);
+  o.fetch_q(codes);
+  // the order: gradients' loads; a row of products and the reads that may follow
+  // it, again and again; the codes' conversion with the last rows
+  __builtin_amdgcn_sched_group_barrier(0x20, P::kPLoads, 0);
+#pragma unroll
+  for (int i = 0; i < T::FI; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x8, T::FJ, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+    if (i < T::FJ) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+    if (i >= T::FI - 2) __builtin_amdgcn_sched_group_barrier(0x2, 6, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x200, 2, 0);
+  __builtin_amdgcn_sched_group_barrier(0x20, 2, 0);
 }
 
 template <typename T, int DT>
-__global__ __launch_bounds__(T::kThreads) void zf_weight_grad_pipe(GradArgs a) {
+__global__ __launch_bounds__(T::kThreads, 2) void zf_weight_grad_pipe(GradArgs a) {
   typedef Pipe<T, DT> P;
   __shared__ __align__(16) char shared[T::kShared];
-  char *s0 = shared, *s1 = shared + P::kBuf;
-  const int tile = blockIdx.x % a.tiles, split = blockIdx.x / a.tiles;
-  const int i0 = tile / a.tiles_in * T::BM, j0 = tile % a.tiles_in * T::BN;
+  char *s0 = shared, *s1 = s0 + P::kBuf, *s2 = s1 + P::kBuf, *s3 = s2 + P::kBuf;
+  const Place at(a);
+  const int i0 = at.i * T::BM, j0 = at.j * T::BN, split = at.split;
   const int64_t first = split * a.split_rows, end = min(first + a.split_rows, a.rows);
+  const int stages = (int)((end - first + kDepth - 1) / kDepth);
   f32x4 acc[T::FI][T::FJ];
 #pragma unroll
   for (int i = 0; i < T::FI; ++i)
 #pragma unroll
     for (int j = 0; j < T::FJ; ++j) acc[i][j] = (f32x4){0, 0, 0, 0};
-  const int steps = (int)((end - first + kBK - 1) / kBK);
   P o(a, i0, j0, first, end - first);
-  Frags<T> fa, fb;
-  // A step's barrier stands between its two halves: the next half's fragments
-  // are read while this one's products run, and a buffer is filled again as
-  // soon as its second half is in registers, a whole step before its use.
-  auto half0 = [&](const char* cur) {
-    o.read(cur, 1, fb);
-    multiply<T, DT>(fa, acc);
-    interleave<T, 0>();
-  };
-  auto half1 = [&](char* cur, const char* nxt) {
-    o.fetch_p(cur);
-    loads_in_order();
-    o.read(nxt, 0, fa);
-    o.put_q(cur);
-    o.fetch_q();
-    multiply<T, DT>(fb, acc);
-    interleave<T, P::kPLoads>();
-  };
-  constexpr int ahead = 2 * P::kQLoads;  // loads of codes after a step's loads of gradients
+  typename P::Codes c0, c1;
+  s16x8 p[T::FI], qa[T::FJ], qb[T::FJ];
   o.fetch_p(s0);
-  o.fetch_q();
-  o.put_q(s0);
-  o.fetch_q();
   o.fetch_p(s1);
-  o.put_q(s1);
-  o.fetch_q();
+  o.fetch_q(c0);
+  o.fetch_q(c1);
+  o.put_q(s0, c0);
+  o.put_q(s1, c1);
   arrive<0>();
-  o.read(s0, 0, fa);
-  int k = 0;
+  o.fetch_p(s2);
+  o.fetch_q(c0);
+  loads_in_order();
+  o.fetch_p(s3);
+  o.fetch_q(c1);
+  loads_in_order();
+#pragma unroll
+  for (int i = 0; i < T::FI; ++i) p[i] = o.template read<T::BM>(s0, o.rp, i);
+#pragma unroll
+  for (int j = 0; j < T::FJ; ++j) qa[j] = o.template read<T::BN>(s0, o.rq, j);
+  // stages past the last one are zeros
 #pragma unroll 1
-  for (; k + 2 <= steps; k += 2) {
-    half0(s0);
-    arrive<ahead>();
-    half1(s0, s1);
-    half0(s1);
-    arrive<ahead>();
-    half1(s1, s0);
-  }
-  if (k < steps) {
-    half0(s0);
-    multiply<T, DT>(fb, acc);
+  for (int k = 0; k < stages; k += kStages) {
+    stage<T, DT>(o, s1, s2, s0, p, qa, qb, c0, acc);
+    stage<T, DT>(o, s2, s3, s1, p, qb, qa, c1, acc);
+    stage<T, DT>(o, s3, s0, s2, p, qa, qb, c0, acc);
+    stage<T, DT>(o, s0, s1, s3, p, qb, qa, c1, acc);
   }
   arrive<0>();
   write_tile<T>(a, acc, shared, i0, j0, split);
