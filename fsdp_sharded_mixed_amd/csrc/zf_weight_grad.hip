@@ -15,7 +15,6 @@
 
 #include <algorithm>
 #include <cstdint>
-#include <cstdlib>
 
 #include "zf_hip_status.h"
 #include "zf_rows.h"
@@ -33,17 +32,15 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 #define ZF_LDS __attribute__((address_space(3)))
 
-constexpr int kBK = 64;  // tokens a step
+// A stage is 32 tokens; kStages of them lie in shared memory in turn.
+constexpr int kStages = 4, kDepth = 32;
 
 template <int BM_, int BN_, int WI, int WJ>
 struct Tile {
   static constexpr int BM = BM_, BN = BN_, kThreads = WI * WJ * 64, kWavesJ = WJ;
   static constexpr int TI = BM / WI, TJ = BN / WJ, FI = TI / 16, FJ = TJ / 16;
-  static constexpr int kPBytes = kBK * BM * 2, kQBytes = kBK * BN * 2;
-  static constexpr int kShared = 2 * (kPBytes + kQBytes);  // two steps' operands, or squares of results
+  static constexpr int kShared = kStages * kDepth * (BM + BN) * 2;  // operands, or squares of results
   static_assert(kShared >= WI * WJ * 16384, "squares fit");
-  static constexpr int kPPieces = kBK * BM / 8 / kThreads;   // of 8 gradients a thread
-  static constexpr int kQPieces = kBK * BN / 16 / kThreads;  // of 16 codes a thread
 };
 typedef Tile<128, 128, 2, 2> Middle;
 typedef Tile<256, 256, 2, 4> Big;
@@ -85,19 +82,6 @@ __device__ __forceinline__ f32x4 mma(s16x8 a, s16x8 b, f32x4 c) {
   else
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
                                                   __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
-}
-
-// 8 tokens from k0 + 8 (lane / 16) on of column c0 + lane % 16.
-template <int PIECES>
-__device__ __forceinline__ s16x8 fragment(const char* tile, int k0, int c0) {
-  const int lane = threadIdx.x & 63, l = lane & 15, row = k0 + 8 * (lane >> 4) + (l >> 2);
-  s16x4 half[2];
-#pragma unroll
-  for (int e = 0; e < 2; ++e)
-    half[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (ZF_LDS s16x4*)((const ZF_LDS char*)tile + place<PIECES>(row + 4 * e, c0 / 8 + ((l & 3) >> 1)) +
-                        (l & 1) * 8));
-  return __builtin_shufflevector(half[0], half[1], 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
 // Results leave by whole lines: a wave's squares of 64 x 64 go to shared memory
@@ -176,98 +160,6 @@ struct Place {
   }
 };
 
-template <typename T, int DT>
-__global__ __launch_bounds__(T::kThreads) void zf_weight_grad_kernel(GradArgs a) {
-  __shared__ __align__(16) char shared[T::kShared];
-  const int tid = threadIdx.x;
-  const Place at(a);
-  const int i0 = at.i * T::BM, j0 = at.j * T::BN, split = at.split;
-  const int64_t first = split * a.split_rows, end = min(first + a.split_rows, a.rows);
-  const int wave = tid >> 6, wi = wave / T::kWavesJ * T::TI, wj = wave % T::kWavesJ * T::TJ;
-
-  u32x4 p[T::kPPieces], q[T::kQPieces];
-  float scale[T::kQPieces];
-  auto fetch = [&](int64_t t0) {
-#pragma unroll
-    for (int h = 0; h < T::kPPieces; ++h) {
-      const int k = h * T::kThreads + tid, c = i0 + k % (T::BM / 8) * 8;
-      const int64_t t = t0 + k / (T::BM / 8);
-      p[h] = (u32x4){0, 0, 0, 0};
-      if (t < end && c < a.out) p[h] = load_raw<ZF_BF16>(a.dy, t * a.dy_ld + c, a.out - c).w[0];
-    }
-#pragma unroll
-    for (int h = 0; h < T::kQPieces; ++h) {
-      const int k = h * T::kThreads + tid, c = j0 + k % (T::BN / 16) * 16;
-      const int64_t t = t0 + k / (T::BN / 16);
-      q[h] = (u32x4){0, 0, 0, 0};
-      scale[h] = 1;
-      if (t >= end || c >= a.in) continue;
-      const uint8_t* from = a.x.codes + t * a.x.code_ld + c;
-      if (c + 16 <= a.in) {
-        q[h] = load_any<false, u32x4_any>(from);
-      } else {
-        const u32x2 lo = load_codes(from, min(8, a.in - c));
-        const u32x2 hi = c + 8 < a.in ? load_codes(from + 8, a.in - c - 8) : (u32x2){0, 0};
-        q[h] = (u32x4){lo.x, lo.y, hi.x, hi.y};
-      }
-      scale[h] = __uint_as_float((uint32_t)a.x.scales[t * a.x.scale_ld + c / ZF_ACT8_GROUP] << 23);
-    }
-  };
-  auto put = [&]() {
-#pragma unroll
-    for (int h = 0; h < T::kPPieces; ++h) {
-      const int k = h * T::kThreads + tid;
-      *reinterpret_cast<u32x4*>(shared + place<T::BM / 8>(k / (T::BM / 8), k % (T::BM / 8))) = p[h];
-    }
-#pragma unroll
-    for (int h = 0; h < T::kQPieces; ++h) {
-      const int k = h * T::kThreads + tid, row = k / (T::BN / 16), piece = k % (T::BN / 16) * 2;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const u32x4 x = {decode2<DT, false>(q[h][e * 2], scale[h]), decode2<DT, true>(q[h][e * 2], scale[h]),
-                         decode2<DT, false>(q[h][e * 2 + 1], scale[h]),
-                         decode2<DT, true>(q[h][e * 2 + 1], scale[h])};
-        *reinterpret_cast<u32x4*>(shared + T::kPBytes + place<T::BN / 8>(row, piece + e)) = x;
-      }
-    }
-  };
-
-  f32x4 acc[T::FI][T::FJ];
-#pragma unroll
-  for (int i = 0; i < T::FI; ++i)
-#pragma unroll
-    for (int j = 0; j < T::FJ; ++j) acc[i][j] = (f32x4){0, 0, 0, 0};
-  if (first < end) fetch(first);
-  for (int64_t t = first; t < end; t += kBK) {
-    __syncthreads();
-    put();
-    __syncthreads();
-    if (t + kBK < end) fetch(t + kBK);
-#pragma unroll
-    for (int k = 0; k < kBK; k += 32) {
-      s16x8 fp[T::FI], fq[T::FJ];
-#pragma unroll
-      for (int i = 0; i < T::FI; ++i) fp[i] = fragment<T::BM / 8>(shared, k, wi + i * 16);
-#pragma unroll
-      for (int j = 0; j < T::FJ; ++j) fq[j] = fragment<T::BN / 8>(shared + T::kPBytes, k, wj + j * 16);
-#pragma unroll
-      for (int i = 0; i < T::FI; ++i)
-#pragma unroll
-        for (int j = 0; j < T::FJ; ++j) acc[i][j] = mma<DT>(fq[j], fp[i], acc[i][j]);
-    }
-  }
-  __syncthreads();
-  write_tile<T>(a, acc, shared, i0, j0, split);
-}
-
-// ---------------------------------------------------------------------------
-// The same for whole 16-byte pieces at 16-byte alignment: gradients go from
-// global to shared memory directly, into two buffers in turn, and codes come a
-// step earlier into registers, from where they are converted into the buffer.
-
-// A stage is 32 tokens; kStages of them lie in shared memory in turn.
-constexpr int kStages = 4, kDepth = 32;
-
 // Where a matrix's next stage lies: the address of its first row in this tile's
 // columns, and the rows that are left.  Loads past the matrix's end give zeros
 // (in shared memory too), so tokens behind the last one add nothing; loads past
@@ -310,23 +202,29 @@ __device__ __forceinline__ void to_shared(Rsrc from, ZF_LDS char* to, int lane_a
 #endif
 }
 
-template <typename T, int DT>
+// DIRECT: operands in whole 16-byte pieces.  Gradients then go from global to
+// shared memory directly; otherwise through registers, as the codes do.
+template <typename T, int DT, bool DIRECT>
 struct Pipe {
   static constexpr int kPBytes = kDepth * T::BM * 2, kQBytes = kDepth * T::BN * 2;
   static constexpr int kBuf = kPBytes + kQBytes;
-  static_assert(kStages * kBuf <= T::kShared, "stages fit");
   static constexpr int kPRows = T::kThreads / (T::BM / 8);   // rows that a load of all threads covers
   static constexpr int kPLoads = kDepth / kPRows;
   static_assert(kPRows % 16 == 0, "the rows of a lane's loads are permuted alike");
   static_assert(T::kThreads / (T::BN / 16) == kDepth, "16 codes a thread");
   static constexpr int kLoads = kPLoads + 2;  // of a thread and stage
+  static constexpr int kInFlight = DIRECT ? 2 + 2 * kLoads : 63;  // see stage()
 
   Walk p, q, s;  // gradients, codes, scales
-  int vp, vq, vs, wq, rp, rq;
+  int vp, vq, vs, wp, wq, rp, rq;
+  int prow, qrow;
+  const char *gp, *gq, *gs, *p_end, *q_end;  // !DIRECT: this lane's pieces, the matrices' ends
 
-  struct Codes {
+  // What a thread has of a stage in registers.
+  struct Held {
     u32x4 c;
     uint32_t scale;
+    u32x4 g[DIRECT ? 1 : kPLoads];
   };
 
   __device__ __forceinline__ Pipe(const GradArgs& a, int i0, int j0, int64_t first, int64_t rows)
@@ -336,12 +234,23 @@ struct Pipe {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l = lane & 15, g = lane >> 4;
     // shared memory is filled in order, so a lane loads the piece that belongs
     // at its place
-    const int row = tid / (T::BM / 8), at = place<T::BM / 8>(row, tid % (T::BM / 8));
-    vp = row * p.ld + at % (T::BM * 2);
-    const int qrow = tid / (T::BN / 16), piece = tid % (T::BN / 16);
-    vq = qrow * q.ld + piece * 16;
-    vs = qrow * s.ld + piece * 16 / ZF_ACT8_GROUP;
+    prow = tid / (T::BM / 8);
+    qrow = tid / (T::BN / 16);
+    const int at = place<T::BM / 8>(prow, tid % (T::BM / 8)) % (T::BM * 2), piece = tid % (T::BN / 16);
     wq = kPBytes + place<T::BN / 8>(qrow, piece * 2);
+    if constexpr (DIRECT) {
+      vp = prow * p.ld + at;
+      vq = qrow * q.ld + piece * 16;
+      vs = qrow * s.ld + piece * 16 / ZF_ACT8_GROUP;
+    } else {
+      const int64_t row = first + prow, column = min(j0 + piece * 16, a.in - 1);
+      wp = tid * 16;
+      gp = static_cast<const char*>(a.dy) + (row * a.dy_ld + i0) * 2 + at;
+      gq = reinterpret_cast<const char*>(a.x.codes) + (first + qrow) * a.x.code_ld + j0 + piece * 16;
+      gs = reinterpret_cast<const char*>(a.x.scales) + (first + qrow) * a.x.scale_ld + column / ZF_ACT8_GROUP;
+      p_end = static_cast<const char*>(a.dy) + ((a.rows - 1) * a.dy_ld + a.out) * 2;
+      q_end = reinterpret_cast<const char*>(a.x.codes) + (a.rows - 1) * a.x.code_ld + a.in;
+    }
     const int frow = 8 * g + (l >> 2), half = (l & 3) >> 1, wi = wave / T::kWavesJ * T::TI,
               wj = wave % T::kWavesJ * T::TJ;
     rp = place<T::BM / 8>(frow, wi / 8 + half) + (l & 1) * 8;
@@ -359,21 +268,57 @@ struct Pipe {
       to_shared(from, to + h * T::kThreads * 16, vp, within(h * kPRows * (uint32_t)p.ld, n));
     p.next();
   }
-  // codes of the next stage into registers
-  __device__ __forceinline__ void fetch_q(Codes& c) {
-    c.c = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(q.buffer(q.extent()), vq, 0, 0));
-    c.scale = __builtin_amdgcn_raw_buffer_load_b8(s.buffer(s.extent()), vs, 0, 0);
-    q.next();
-    s.next();
+  // codes (!DIRECT: and gradients) of the next stage into registers
+  __device__ __forceinline__ void fetch(Held& r) {
+    if constexpr (DIRECT) {
+      r.c = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(q.buffer(q.extent()), vq, 0, 0));
+      r.scale = __builtin_amdgcn_raw_buffer_load_b8(s.buffer(s.extent()), vs, 0, 0);
+      q.next();
+      s.next();
+    } else {
+      // A piece that ends past its row holds the next row's first elements, for
+      // columns that are not written; only one that ends past the matrix is
+      // loaded in parts.  Tokens behind the last one are zeros.
+#pragma unroll
+      for (int h = 0; h < kPLoads; ++h) {
+        r.g[h] = (u32x4){0, 0, 0, 0};
+        const char* at = gp + (int64_t)(h * kPRows) * p.ld;
+        const bool in = prow + h * kPRows < p.left;
+        if (in && at + 16 <= p_end) r.g[h] = load_any<false, u32x4_any>(at);
+        if (rare(in && at + 16 > p_end))
+          r.g[h] = load_raw<ZF_BF16>(at, 0, (int)max((p_end - at) / 2, (int64_t)0)).w[0];
+      }
+      r.c = (u32x4){0, 0, 0, 0};
+      r.scale = 127;
+      const bool in = qrow < q.left;
+      if (in) r.scale = *reinterpret_cast<const uint8_t*>(gs);
+      if (in && gq + 16 <= q_end) r.c = load_any<false, u32x4_any>(gq);
+      if (rare(in && gq + 16 > q_end)) {
+        const int n = (int)max(q_end - gq, (int64_t)0);
+        const uint8_t* at = reinterpret_cast<const uint8_t*>(gq);
+        const u32x2 lo = load_codes(at, min(8, n)), hi = load_codes(at + 8, n - 8);
+        r.c = (u32x4){lo.x, lo.y, hi.x, hi.y};
+      }
+      gp += (int64_t)kDepth * p.ld;
+      gq += (int64_t)kDepth * q.ld;
+      gs += (int64_t)kDepth * s.ld;
+      p.left -= kDepth;
+      q.left -= kDepth;
+    }
   }
-  // codes as 16-bit numbers into `buf`
-  __device__ __forceinline__ void put_q(char* __restrict buf, const Codes& c) const {
-    const float scale = __uint_as_float(c.scale << 23);
+  // codes as 16-bit numbers (!DIRECT: and gradients) into `buf`
+  __device__ __forceinline__ void put(char* __restrict buf, const Held& r) const {
+    const float scale = __uint_as_float(r.scale << 23);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const u32x4 x = {decode2<DT, false>(c.c[e * 2], scale), decode2<DT, true>(c.c[e * 2], scale),
-                       decode2<DT, false>(c.c[e * 2 + 1], scale), decode2<DT, true>(c.c[e * 2 + 1], scale)};
+      const u32x4 x = {decode2<DT, false>(r.c[e * 2], scale), decode2<DT, true>(r.c[e * 2], scale),
+                       decode2<DT, false>(r.c[e * 2 + 1], scale), decode2<DT, true>(r.c[e * 2 + 1], scale)};
       *(ZF_LDS u32x4*)((ZF_LDS char*)buf + (wq ^ (e * 16))) = x;
+    }
+    if constexpr (!DIRECT) {
+#pragma unroll
+      for (int h = 0; h < kPLoads; ++h)
+        *(ZF_LDS u32x4*)((ZF_LDS char*)buf + wp + h * T::kThreads * 16) = r.g[h];
     }
   }
   // Fragment f of 8 tokens a lane.  Its pieces lie at the first one's place ^ 32
@@ -404,28 +349,31 @@ __device__ __forceinline__ void arrive() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);  // products stay in their stage
 }
 
 // Stage k, whose fragments p and q are in registers: its products, while the
 // next stage's fragments are read from `next`, the codes of stage k + 2 are
-// written to `fill_q` and the gradients of stage k + 4 are on their way to the
-// buffer that stage k has left.  Loads are on their way for two stages (codes)
-// and three (gradients).
-template <typename T, int DT>
-__device__ __forceinline__ void stage(Pipe<T, DT>& o, const char* __restrict next, char* __restrict fill_q,
-                                      char* __restrict fill_p, s16x8 (&p)[T::FI], const s16x8 (&q)[T::FJ],
-                                      s16x8 (&q_next)[T::FJ], typename Pipe<T, DT>::Codes& codes,
+// written to `fill` and the gradients of stage k + 4 are on their way to the
+// buffer `left` that stage k has left (!DIRECT: gradients go as the codes do).
+// Loads are on their way for two stages (to registers) or three.
+template <typename T, int DT, bool DIRECT>
+__device__ __forceinline__ void stage(Pipe<T, DT, DIRECT>& o, const char* __restrict next, char* __restrict fill,
+                                      char* __restrict left, s16x8 (&p)[T::FI], const s16x8 (&q)[T::FJ],
+                                      s16x8 (&q_next)[T::FJ], typename Pipe<T, DT, DIRECT>::Held& held,
                                       f32x4 (&acc)[T::FI][T::FJ]) {
-  typedef Pipe<T, DT> P;
+  typedef Pipe<T, DT, DIRECT> P;
   // stage k + 1 is complete: its gradients were followed by the codes of the
   // same stage and by all loads of two more
-  arrive<2 + 2 * P::kLoads>();
+  arrive<P::kInFlight>();
+  if constexpr (T::BM == 256) __builtin_amdgcn_sched_barrier(0);  // products stay in their stage
   // fragments' places are computed anew in each stage: registers that hold them
   // would be spilled
   int rp = o.rp, rq = o.rq;
   asm volatile("" : "+v"(rp), "+v"(rq));
-  o.fetch_p(fill_p);
+  if constexpr (DIRECT) {
+    o.fetch_p(left);
+    loads_in_order();
+  }
 #pragma unroll
   for (int i = 0; i < T::FI; ++i) {
 #pragma unroll
@@ -433,25 +381,27 @@ __device__ __forceinline__ void stage(Pipe<T, DT>& o, const char* __restrict nex
     p[i] = o.template read<T::BM>(next, rp, i);
     if (i < T::FJ) q_next[i] = o.template read<T::BN>(next, rq, i);
   }
-  o.put_q(fill_q, codes);
-  o.fetch_q(codes);
-  // the order: gradients' loads; a row of products and the reads that may follow
-  // it, again and again; the codes' conversion with the last rows
-  __builtin_amdgcn_sched_group_barrier(0x20, P::kPLoads, 0);
+  o.put(fill, held);
+  o.fetch(held);
+  if constexpr (DIRECT) {
+    // the order: gradients' loads; a row of products and the reads that may
+    // follow it, again and again; the codes' conversion with the last rows
+    __builtin_amdgcn_sched_group_barrier(0x20, P::kPLoads, 0);
 #pragma unroll
-  for (int i = 0; i < T::FI; ++i) {
-    __builtin_amdgcn_sched_group_barrier(0x8, T::FJ, 0);
-    __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-    if (i < T::FJ) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-    if (i >= T::FI - 2) __builtin_amdgcn_sched_group_barrier(0x2, 6, 0);
+    for (int i = 0; i < T::FI; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x8, T::FJ, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+      if (i < T::FJ) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+      if (i >= T::FI - 2) __builtin_amdgcn_sched_group_barrier(0x2, 6, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x200, 2, 0);
+    __builtin_amdgcn_sched_group_barrier(0x20, 2, 0);
   }
-  __builtin_amdgcn_sched_group_barrier(0x200, 2, 0);
-  __builtin_amdgcn_sched_group_barrier(0x20, 2, 0);
 }
 
-template <typename T, int DT>
-__global__ __launch_bounds__(T::kThreads, 2) void zf_weight_grad_pipe(GradArgs a) {
-  typedef Pipe<T, DT> P;
+template <typename T, int DT, bool DIRECT>
+__global__ __launch_bounds__(T::kThreads, 2) void zf_weight_grad_kernel(GradArgs a) {
+  typedef Pipe<T, DT, DIRECT> P;
   __shared__ __align__(16) char shared[T::kShared];
   char *s0 = shared, *s1 = s0 + P::kBuf, *s2 = s1 + P::kBuf, *s3 = s2 + P::kBuf;
   const Place at(a);
@@ -464,20 +414,22 @@ __global__ __launch_bounds__(T::kThreads, 2) void zf_weight_grad_pipe(GradArgs a
 #pragma unroll
     for (int j = 0; j < T::FJ; ++j) acc[i][j] = (f32x4){0, 0, 0, 0};
   P o(a, i0, j0, first, end - first);
-  typename P::Codes c0, c1;
+  typename P::Held h0, h1;
   s16x8 p[T::FI], qa[T::FJ], qb[T::FJ];
-  o.fetch_p(s0);
-  o.fetch_p(s1);
-  o.fetch_q(c0);
-  o.fetch_q(c1);
-  o.put_q(s0, c0);
-  o.put_q(s1, c1);
+  if constexpr (DIRECT) {
+    o.fetch_p(s0);
+    o.fetch_p(s1);
+  }
+  o.fetch(h0);
+  o.fetch(h1);
+  o.put(s0, h0);
+  o.put(s1, h1);
   arrive<0>();
-  o.fetch_p(s2);
-  o.fetch_q(c0);
+  if constexpr (DIRECT) o.fetch_p(s2);
+  o.fetch(h0);
   loads_in_order();
-  o.fetch_p(s3);
-  o.fetch_q(c1);
+  if constexpr (DIRECT) o.fetch_p(s3);
+  o.fetch(h1);
   loads_in_order();
 #pragma unroll
   for (int i = 0; i < T::FI; ++i) p[i] = o.template read<T::BM>(s0, o.rp, i);
@@ -486,10 +438,10 @@ __global__ __launch_bounds__(T::kThreads, 2) void zf_weight_grad_pipe(GradArgs a
   // stages past the last one are zeros
 #pragma unroll 1
   for (int k = 0; k < stages; k += kStages) {
-    stage<T, DT>(o, s1, s2, s0, p, qa, qb, c0, acc);
-    stage<T, DT>(o, s2, s3, s1, p, qb, qa, c1, acc);
-    stage<T, DT>(o, s3, s0, s2, p, qa, qb, c0, acc);
-    stage<T, DT>(o, s0, s1, s3, p, qb, qa, c1, acc);
+    stage<T, DT>(o, s1, s2, s0, p, qa, qb, h0, acc);
+    stage<T, DT>(o, s2, s3, s1, p, qb, qa, h1, acc);
+    stage<T, DT>(o, s3, s0, s2, p, qa, qb, h0, acc);
+    stage<T, DT>(o, s0, s1, s3, p, qb, qa, h1, acc);
   }
   arrive<0>();
   write_tile<T>(a, acc, shared, i0, j0, split);
@@ -529,33 +481,46 @@ __global__ __launch_bounds__(kThreads) void zf_weight_grad_join(JoinArgs a) {
 struct Plan {
   bool big;
   int32_t splits;
-  int64_t split_rows, bytes;
+  int64_t split_rows;
 };
 
-int64_t tiles_of(int64_t out, int64_t in, int side) {
-  return ((out + side - 1) / side) * ((in + side - 1) / side);
+// The tokens are split where a form's tiles leave places of the GPU free, into
+// parts of `least` at least.
+int64_t splits_of(int64_t rows, int64_t tiles, int64_t places, int64_t least) {
+  return std::max<int64_t>(1, std::min(places / tiles, rows / least));
+}
+// Microseconds of a form: rounds of blocks, each of `stage` for 32 tokens and
+// `more` before and after them; with splits a second launch that reads the
+// partial results at 5 TB/s.
+double cost(int64_t rows, int64_t size, int64_t tiles, int64_t splits, int64_t places, double stage, double more) {
+  const double rounds = (double)((tiles * splits + places - 1) / places);
+  const double join = splits > 1 ? 4.0 + (double)(splits * size) * 4 / 5e6 : 0;
+  return rounds * ((double)((rows + splits * kDepth - 1) / (splits * kDepth)) * stage + more) + join;
 }
 
-int plan(int64_t rows, int64_t out, int64_t in, Plan& g) {
+// WHOLE: operands in whole 16-byte pieces.
+int plan(int64_t rows, int64_t out, int64_t in, bool whole, Plan& g) {
   int rc = shape_ok(rows, in);
   if (rc == ZF_OK) rc = shape_ok(0, out);
   if (rc != ZF_OK) return rc;
-  const int64_t steps = (rows + kBK - 1) / kBK;
-  if (tiles_of(out, in, Middle::BM) > kMaxBlocks) return ZF_ESIZE;
-  static const int force = getenv("ZF_TILE") ? atoi(getenv("ZF_TILE")) : 0;
-  static const int slots = getenv("ZF_SLOTS") ? atoi(getenv("ZF_SLOTS")) : 0;
-  g.big = tiles_of(out, in, Big::BM) >= 128;
-  if (force) g.big = force == 256;
-  const int64_t tiles = tiles_of(out, in, g.big ? Big::BM : Middle::BM);
-  // blocks for all places of the compute units, of 4 steps at least
-  const int64_t places = slots ? slots : g.big ? 256 : 512;
-  int64_t splits = std::min(places / tiles, (steps + 3) / 4);
-  splits = std::max<int64_t>(splits, 1);
-  const int64_t per = std::max<int64_t>((steps + splits - 1) / splits, 1);
-  g.split_rows = per * kBK;
-  g.splits = (int32_t)std::max<int64_t>((steps + per - 1) / per, 1);
-  g.bytes = g.splits > 1 ? (g.splits * out * in * 4 + 15) / 16 * 16 : 0;
+  auto tiles_of = [&](int64_t side) { return ((out + side - 1) / side) * ((in + side - 1) / side); };
+  const int64_t middle = tiles_of(Middle::BM), big = tiles_of(Big::BM);
+  if (middle > kMaxBlocks) return ZF_ESIZE;
+  // A compute unit holds one block of 256 x 256 or two of 128 x 128.  8192
+  // tokens of 2048 x 2048: 84 us in large tiles, 89 in small ones; 16384 of 1024 x
+  // 1024: 56 and 52.  Parts of 1024 tokens at least (4096 of 1024 x 1024: parts of
+  // 512 30.8 us, of 1024 29.9, of 4096 50); without whole pieces a stage takes
+  // longer, and 256 are enough (1000 tokens of 128 x 40: 13 us, in one part 27).
+  const int64_t sb = splits_of(rows, big, 256, 1024), sm = splits_of(rows, middle, 512, whole ? 1024 : 256);
+  g.big = whole && cost(rows, out * in, big, sb, 256, 0.92, 10) < cost(rows, out * in, middle, sm, 512, 0.57, 5);
+  const int64_t stages = (rows + kDepth - 1) / kDepth, splits = g.big ? sb : sm;
+  const int64_t per = std::max<int64_t>((stages + splits - 1) / splits, 1);
+  g.split_rows = per * kDepth;
+  g.splits = (int32_t)std::max<int64_t>((stages + per - 1) / per, 1);
   return ZF_OK;
+}
+int64_t partial_bytes(const Plan& g, int64_t out, int64_t in) {
+  return g.splits > 1 ? (g.splits * out * in * 4 + 15) / 16 * 16 : 0;
 }
 
 // Whole 16-byte pieces at 16-byte alignment, and 64 rows within an offset of
@@ -566,46 +531,45 @@ bool whole_pieces(const GradArgs& a) {
          a.dy_ld < 1 << 23 && a.x.code_ld < 1 << 24 && a.x.scale_ld < 1 << 24;
 }
 
-template <typename T, bool PIPE>
+template <typename T, bool DIRECT>
 void launch(GradArgs a, int32_t dtype, hipStream_t s) {
   a.tiles_in = (a.in + T::BN - 1) / T::BN;
   a.tiles = a.tiles_in * ((a.out + T::BM - 1) / T::BM);
   const dim3 grid((uint32_t)a.tiles * (uint32_t)a.splits), block(T::kThreads);
-  if constexpr (PIPE) {
-    if (dtype == ZF_BF16) hipLaunchKernelGGL((zf_weight_grad_pipe<T, ZF_BF16>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((zf_weight_grad_pipe<T, ZF_F16>), grid, block, 0, s, a);
-  } else {
-    if (dtype == ZF_BF16) hipLaunchKernelGGL((zf_weight_grad_kernel<T, ZF_BF16>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((zf_weight_grad_kernel<T, ZF_F16>), grid, block, 0, s, a);
-  }
+  if (dtype == ZF_BF16) hipLaunchKernelGGL((zf_weight_grad_kernel<T, ZF_BF16, DIRECT>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((zf_weight_grad_kernel<T, ZF_F16, DIRECT>), grid, block, 0, s, a);
 }
 
 }  // namespace
 
 extern "C" int64_t zf_weight_grad_bytes(int64_t rows, int64_t out_features, int64_t in_features) {
-  Plan g;
-  const int rc = plan(rows, out_features, in_features, g);
-  return rc != ZF_OK ? rc : g.bytes;
+  int64_t most = 0;
+  for (bool whole : {false, true}) {
+    Plan g;
+    const int rc = plan(rows, out_features, in_features, whole, g);
+    if (rc != ZF_OK) return rc;
+    most = std::max(most, partial_bytes(g, out_features, in_features));
+  }
+  return most;
 }
 
 extern "C" int zf_weight_grad(const zf_weight_grad_args* args, void* stream) {
   if (!args || args->reserved != 0 || !flag(args->accumulate)) return ZF_EINVAL;
   const zf_weight_grad_args& p = *args;
   if (!valid_dtype(p.dtype) || !row_dtype(p.grad_dtype)) return ZF_EDTYPE;
-  Plan g;
-  int rc = plan(p.rows, p.out_features, p.in_features, g);
+  const int64_t need = zf_weight_grad_bytes(p.rows, p.out_features, p.in_features);
+  int rc = need < 0 ? (int)need : ZF_OK;
   if (rc == ZF_OK) rc = rows_ok(p.dy, p.dtype, p.rows, p.out_features, p.dy_stride);
   if (rc == ZF_OK) rc = act8_ok(p.x8, p.rows, p.in_features);
   if (rc != ZF_OK) return rc;
-  if (!p.grad || (g.bytes > 0 && !p.workspace)) return ZF_EINVAL;
+  if (!p.grad || (need > 0 && !p.workspace)) return ZF_EINVAL;
   if (!aligned_to(p.grad, p.grad_dtype) || !aligned16(p.workspace)) return ZF_EALIGN;
-  if (p.workspace_size < g.bytes) return ZF_ESIZE;
+  if (p.workspace_size < need) return ZF_ESIZE;
   if (p.rows == 0 && p.accumulate) return ZF_OK;
   GradArgs a;
   a.dy = p.dy;
   a.x = act8_of(p.x8);
   a.grad = p.grad;
-  a.partial = g.splits > 1 ? static_cast<float*>(p.workspace) : nullptr;
   a.dy_ld = p.dy_stride;
   if (p.rows <= 1) {  // strides of a single row are not looked at
     a.dy_ld = (p.out_features + 7) / 8 * 8;
@@ -613,15 +577,20 @@ extern "C" int zf_weight_grad(const zf_weight_grad_args* args, void* stream) {
     a.x.scale_ld = 0;
   }
   a.rows = p.rows;
-  a.split_rows = g.split_rows;
   a.out = (int32_t)p.out_features;
   a.in = (int32_t)p.in_features;
-  a.splits = g.splits;
   a.gdt = p.grad_dtype;
   a.accumulate = p.accumulate;
+  const bool whole = whole_pieces(a);
+  Plan g;
+  rc = plan(p.rows, p.out_features, p.in_features, whole, g);
+  if (rc != ZF_OK) return rc;
+  a.splits = g.splits;
+  a.split_rows = g.split_rows;
+  a.partial = g.splits > 1 ? static_cast<float*>(p.workspace) : nullptr;
   hipStream_t s = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();
-  if (!whole_pieces(a)) launch<Middle, false>(a, p.dtype, s);
+  if (!whole) launch<Middle, false>(a, p.dtype, s);
   else if (g.big) launch<Big, true>(a, p.dtype, s);
   else launch<Middle, true>(a, p.dtype, s);
   if (g.splits > 1) {
