@@ -47,40 +47,56 @@ struct LookupArgs {
   int32_t wide, log_lanes;
 };
 
-template <int TDT, int DT>
+// A group of lanes takes kRows tokens at a time, all their rows on their way
+// together.
+constexpr int kRows = 4;
+template <int TDT, int DT, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void zf_embedding_kernel(LookupArgs a) {
   const int lanes = 1 << a.log_lanes, per = kThreads >> a.log_lanes;
   const int64_t j = ((int64_t)blockIdx.y * lanes + (threadIdx.x & (lanes - 1))) * kChunk;
   const int n = (int)min((int64_t)kChunk, a.cols - j);
   if (n <= 0) return;
+  const int64_t step = (int64_t)gridDim.x * per;
   int64_t t = (int64_t)blockIdx.x * per + (threadIdx.x >> a.log_lanes);
-  for (; t < a.tokens; t += (int64_t)gridDim.x * per) {
-    const uint32_t v = key_of(a.ids, a.wide, t, a.vocab);
-    float x[kChunk];
+  for (; t < a.tokens; t += step * kRows) {
+    Raw<TDT> r[kRows];
+    uint32_t v[kRows];
 #pragma unroll
-    for (int k = 0; k < kChunk; ++k) x[k] = 0;
-    if (v < a.vocab) load8<TDT>(a.table, (int64_t)v * a.cols + j, n, x);
+    for (int u = 0; u < kRows; ++u)
+      v[u] = t + u * step < a.tokens ? key_of(a.ids, a.wide, t + u * step, a.vocab) : a.vocab;
 #pragma unroll
-    for (int k = 0; k < kChunk; ++k) x[k] = v < a.vocab ? x[k] * a.scale : 0.0f;
-    store8<DT, true>(a.out, t * a.out_ld + j, n, x);
+    for (int u = 0; u < kRows; ++u)
+      r[u] = load_raw<TDT, false, WHOLE>(a.table, (int64_t)v[u] * a.cols + j, v[u] < a.vocab ? n : 0);
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      if (t + u * step >= a.tokens) break;
+      float x[kChunk];
+      widen8<TDT>(r[u], x);
+#pragma unroll
+      for (int k = 0; k < kChunk; ++k) x[k] = v[u] < a.vocab ? x[k] * a.scale : 0.0f;
+      store8<DT, true, WHOLE>(a.out, (t + u * step) * a.out_ld + j, n, x);
+    }
   }
 }
 
 // ---------------------------------------------------------------------------
-// Sort of the tokens by id: by 9 bits or fewer a pass, from the lowest.  A
-// block takes `items` consecutive tokens, its waves consecutive parts of them.
-// A pass needs how many of each digit every block holds: the first launch
-// counts them for the first pass, and each pass counts for the next one while
-// it writes.
+// Sort of the tokens by id: by 9 bits or fewer a pass, from the lowest.  Up to
+// 4096 tokens are sorted by one block in shared memory, all passes in one launch.
+// For more, a block takes 1024 consecutive tokens (more where that would be
+// over 1024 blocks), a wave consecutive parts of them; a pass needs how many of
+// each digit every block holds: the first launch counts them for the first
+// pass, and each pass counts for the next one while it writes.
 
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 constexpr int kBins = 512;
+constexpr int kSmall = 4096;
 
 struct SortArgs {
   const void* ids;
   uint32_t* keys[2];
   uint32_t* places[2];
   uint32_t* counts;  // [passes][blocks][bins]
+  uint32_t* cut;     // cleared for the runs: how many of them spans cut
   void* grad;        // to clear, or NULL
   int64_t tokens, cols;
   int64_t clear_rows;  // rows of the table that a clearing block looks after
@@ -101,6 +117,7 @@ __device__ __forceinline__ void clear_rows(const SortArgs& a, int block) {
   const int words = (int)((rows + 31) / 32);
   for (int k = threadIdx.x; k < words; k += kSortThreads) seen[k] = 0;
   __syncthreads();
+#pragma unroll 4
   for (int64_t t = threadIdx.x; t < a.tokens; t += kSortThreads) {
     const int64_t r = (int64_t)key_of(a.ids, a.wide, t, a.vocab) - r0;
     if (r >= 0 && r < rows) atomicOr(&seen[r >> 5], 1u << (r & 31));
@@ -122,10 +139,97 @@ __device__ __forceinline__ void clear_rows(const SortArgs& a, int block) {
   }
 }
 
+// One pass over this block's n tokens: place(i, to) is called for token i of
+// the block with its place `to` among all tokens, in order for equal digits.
+// Thread d < bins brings the tokens of smaller blocks and of all blocks with
+// digit d; all_blocks false: they are this block's own.
+struct SortShared {
+  uint32_t at[kSortWaves][kBins];
+  uint32_t waves[kBins / 64];
+};
+template <typename D, typename P>
+__device__ __forceinline__ void sort_pass(SortShared& s, int bits, int n, int per_wave, bool all_blocks,
+                                          uint32_t total, uint32_t before, D digit_of, P place) {
+  const int bins = 1 << bits, tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int i0 = wave * per_wave, i1 = min(i0 + per_wave, n);
+  for (int k = tid; k < kSortWaves * kBins; k += kSortThreads) (&s.at[0][0])[k] = 0;
+  __syncthreads();
+  for (int i = i0 + lane; i < i1; i += 64) atomicAdd(&s.at[wave][digit_of(i)], 1u);
+  __syncthreads();
+  if (!all_blocks && tid < bins) {
+    for (int w = 0; w < kSortWaves; ++w) total += s.at[w][tid];
+  }
+  // a digit's first place: all smaller digits, then this one in the blocks
+  // before, then in the waves before
+  uint32_t upto = total;
+  for (int off = 1; off < 64; off <<= 1) {
+    const uint32_t x = __shfl_up(upto, off, 64);
+    if (lane >= off) upto += x;
+  }
+  if (tid < kBins && lane == 63) s.waves[wave] = upto;
+  __syncthreads();
+  if (tid < bins) {
+    uint32_t first = upto - total + before;
+    for (int w = 0; w < wave; ++w) first += s.waves[w];
+    for (int w = 0; w < kSortWaves; ++w) {
+      const uint32_t x = s.at[w][tid];
+      s.at[w][tid] = first;
+      first += x;
+    }
+  }
+  __syncthreads();
+  volatile uint32_t* mine = s.at[wave];
+  for (int r = i0; r < i1; r += 64) {  // the wave's lanes together
+    const int i = r + lane;
+    const bool in = i < i1;
+    const uint32_t d = in ? digit_of(i) : 0;
+    uint64_t same = __ballot(in);
+    for (int b = 0; b < bits; ++b) {
+      const uint64_t one = __ballot(d >> b & 1);
+      same &= (d >> b & 1) ? one : ~one;
+    }
+    const int rank = __popcll(same & ((1ull << lane) - 1));
+    const uint32_t to = in ? mine[d] + rank : 0;
+    __builtin_amdgcn_wave_barrier();
+    if (in && rank == 0) mine[d] = to + (uint32_t)__popcll(same);
+    __builtin_amdgcn_wave_barrier();
+    if (in) place(i, to);
+  }
+}
+
+// Up to kSmall tokens: block 0 sorts them, the others clear.
+__global__ __launch_bounds__(kSortThreads) void zf_sort_small(SortArgs a) {
+  if (blockIdx.x > 0) return clear_rows(a, blockIdx.x - 1);
+  __shared__ SortShared s;
+  __shared__ uint32_t keys[2][kSmall], places[2][kSmall];
+  const int n = (int)a.tokens, per_wave = (n + kSortThreads - 1) / kSortThreads * 64;
+  if (n == 0) return;  // nothing to sort, and no workspace
+  if (threadIdx.x == 0) *a.cut = 0;
+  for (int t = threadIdx.x; t < n; t += kSortThreads) {
+    keys[0][t] = key_of(a.ids, a.wide, t, a.vocab);
+    places[0][t] = t;
+  }
+  __syncthreads();
+  for (int p = 0; p < a.passes; ++p) {
+    const int from = p & 1;
+    sort_pass(s, a.bits, n, per_wave, false, 0, 0, [&](int i) { return digit(keys[from][i], p, a.bits); },
+              [&](int i, uint32_t to) {
+                keys[from ^ 1][to] = keys[from][i];
+                places[from ^ 1][to] = places[from][i];
+              });
+    __syncthreads();
+  }
+  for (int t = threadIdx.x; t < n; t += kSortThreads) {
+    a.keys[(a.passes - 1) & 1][t] = keys[a.passes & 1][t];
+    a.places[(a.passes - 1) & 1][t] = places[a.passes & 1][t];
+  }
+}
+
 __global__ __launch_bounds__(kSortThreads) void zf_sort_count(SortArgs a) {
   if ((int)blockIdx.x >= a.blocks) return clear_rows(a, blockIdx.x - a.blocks);
   __shared__ uint32_t count[kBins];
   const int bins = 1 << a.bits;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.cut = 0;
   for (int k = threadIdx.x; k < bins; k += kSortThreads) {
     count[k] = 0;
     for (int p = 1; p < a.passes; ++p)
@@ -141,71 +245,34 @@ __global__ __launch_bounds__(kSortThreads) void zf_sort_count(SortArgs a) {
 }
 
 __global__ __launch_bounds__(kSortThreads) void zf_sort_pass(SortArgs a, int pass) {
-  __shared__ uint32_t at[kSortWaves][kBins];
-  __shared__ uint32_t waves[kBins / 64];
-  const int bins = 1 << a.bits, tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  __shared__ SortShared s;
+  const int bins = 1 << a.bits;
   const uint32_t* keys = a.keys[(pass + 1) & 1];
   const uint32_t* places = a.places[(pass + 1) & 1];
-  const int64_t t0 = (int64_t)blockIdx.x * a.items + (int64_t)wave * (a.items / kSortWaves);
-  const int64_t t1 = min(t0 + a.items / kSortWaves, a.tokens);
-  auto key_at = [&](int64_t t) {
-    return pass == 0 ? key_of(a.ids, a.wide, t, a.vocab) : keys[t];
-  };
-  for (int k = tid; k < kSortWaves * kBins; k += kSortThreads) (&at[0][0])[k] = 0;
-  __syncthreads();
-  for (int64_t t = t0 + lane; t < t1; t += 64) atomicAdd(&at[wave][digit(key_at(t), pass, a.bits)], 1u);
-  // a bin's first place: all smaller digits, then this digit in the blocks
-  // before, then in the waves before
+  const int64_t t0 = (int64_t)blockIdx.x * a.items;
+  const int n = (int)min((int64_t)a.items, a.tokens - t0);
+  auto key_at = [&](int i) { return pass == 0 ? key_of(a.ids, a.wide, t0 + i, a.vocab) : keys[t0 + i]; };
   uint32_t total = 0, before = 0;
-  if (tid < bins) {
-    const uint32_t* c = a.counts + (int64_t)pass * a.blocks * bins + tid;
+  if ((int)threadIdx.x < bins) {
+    const uint32_t* c = a.counts + (int64_t)pass * a.blocks * bins + threadIdx.x;
+#pragma unroll 8
     for (int b = 0; b < a.blocks; ++b) {
       const uint32_t x = c[(int64_t)b * bins];
       total += x;
       before += b < (int)blockIdx.x ? x : 0;
     }
   }
-  uint32_t upto = total;
-  for (int off = 1; off < 64; off <<= 1) {
-    const uint32_t x = __shfl_up(upto, off, 64);
-    if (lane >= off) upto += x;
-  }
-  if (tid < kBins && lane == 63) waves[wave] = upto;
-  __syncthreads();
-  if (tid < bins) {
-    uint32_t first = upto - total + before;
-    for (int w = 0; w < wave; ++w) first += waves[w];
-    for (int w = 0; w < kSortWaves; ++w) {
-      const uint32_t x = at[w][tid];
-      at[w][tid] = first;
-      first += x;
-    }
-  }
-  __syncthreads();
-  volatile uint32_t* mine = at[wave];
   const bool last = pass + 1 == a.passes;
-  for (int64_t r = t0; r < t1; r += 64) {  // the wave's lanes together
-    const int64_t t = r + lane;
-    const bool in = t < t1;
-    const uint32_t key = in ? key_at(t) : 0, d = digit(key, pass, a.bits);
-    uint64_t same = __ballot(in);
-    for (int b = 0; b < a.bits; ++b) {
-      const uint64_t one = __ballot(d >> b & 1);
-      same &= (d >> b & 1) ? one : ~one;
-    }
-    const int rank = __popcll(same & ((1ull << lane) - 1));
-    const uint32_t to = in ? mine[d] + rank : 0;
-    __builtin_amdgcn_wave_barrier();
-    if (in && rank == 0) mine[d] = to + (uint32_t)__popcll(same);
-    __builtin_amdgcn_wave_barrier();
-    if (in) {
-      a.keys[pass & 1][to] = key;
-      a.places[pass & 1][to] = pass == 0 ? (uint32_t)t : places[t];
-      if (!last)
-        atomicAdd(&a.counts[((int64_t)(pass + 1) * a.blocks + to / (uint32_t)a.items) * bins +
-                            digit(key, pass + 1, a.bits)], 1u);
-    }
-  }
+  sort_pass(s, a.bits, n, a.items / kSortWaves, true, total, before,
+            [&](int i) { return digit(key_at(i), pass, a.bits); },
+            [&](int i, uint32_t to) {
+              const uint32_t key = key_at(i);
+              a.keys[pass & 1][to] = key;
+              a.places[pass & 1][to] = pass == 0 ? (uint32_t)(t0 + i) : places[t0 + i];
+              if (!last)
+                atomicAdd(&a.counts[((int64_t)(pass + 1) * a.blocks + to / (uint32_t)a.items) * bins +
+                                    digit(key, pass + 1, a.bits)], 1u);
+            });
 }
 
 // ---------------------------------------------------------------------------
@@ -216,120 +283,154 @@ struct RunArgs {
   const uint32_t* places;
   const void* dout;
   void* grad;
-  float* partial;  // [spans][2][cols]: of a run that began before its span, and of one that goes on after it
+  float* partial;   // [spans][2][cols]: of a run that began before its span, and of one that goes on after it
+  uint32_t* cut;    // [1 + spans]: how many runs begin in a span and go on after it, and in which
   int64_t dout_ld, tokens, cols, spans;
   float scale;
   uint32_t vocab;
   int32_t log_lanes, length, gdt, accumulate;
 };
 
-__device__ __forceinline__ void write_row(const RunArgs& a, uint32_t v, int64_t j, int n,
+// The sum's row of the gradient; `old` is what it held.
+template <int GDT, bool WHOLE = false>
+__device__ __forceinline__ void write_row(const RunArgs& a, uint32_t v, int64_t j, int n, const Raw<GDT>& old,
                                           const float (&sum)[kChunk]) {
-  const int64_t at = (int64_t)v * a.cols + j;
-  float x[kChunk], old[kChunk];
+  float x[kChunk], o[kChunk];
 #pragma unroll
   for (int k = 0; k < kChunk; ++k) x[k] = sum[k] * a.scale;
   if (a.accumulate) {
-    load8_of(a.gdt, a.grad, at, n, old);
+    widen8<GDT>(old, o);
 #pragma unroll
-    for (int k = 0; k < kChunk; ++k) x[k] += old[k];
+    for (int k = 0; k < kChunk; ++k) x[k] += o[k];
   }
-  if (a.gdt == ZF_F32) store8<ZF_F32>(a.grad, at, n, x);
-  else if (a.gdt == ZF_BF16) store8<ZF_BF16>(a.grad, at, n, x);
-  else store8<ZF_F16>(a.grad, at, n, x);
+  store8<GDT, false, WHOLE>(a.grad, (int64_t)v * a.cols + j, n, x);
+}
+template <int GDT, bool WHOLE = false>
+__device__ __forceinline__ Raw<GDT> old_row(const RunArgs& a, uint32_t v, int64_t j, int n) {
+  return load_raw<GDT, true, WHOLE>(a.grad, (int64_t)v * a.cols + j, a.accumulate ? n : 0);
 }
 
-template <int DT>
+// A group of lanes adds the rows of a span, kU of them and, where runs end,
+// the rows that they are added to on their way together.  WAVE: groups are
+// whole waves, which hold the span's keys and places a lane each and read them
+// as scalars, so that a row's address and every branch are the wave's.
+constexpr int kU = 4, kLongest = 32;
+template <int DT, int GDT, bool WHOLE, bool WAVE>
 __global__ __launch_bounds__(kThreads) void zf_run_sums(RunArgs a) {
-  const int lanes = 1 << a.log_lanes, per = kThreads >> a.log_lanes;
+  const int lanes = 1 << a.log_lanes, per = kThreads >> a.log_lanes, lane = threadIdx.x & 63;
   const int64_t j = ((int64_t)blockIdx.y * lanes + (threadIdx.x & (lanes - 1))) * kChunk;
   const int n = (int)min((int64_t)kChunk, a.cols - j);
-  if (n <= 0) return;
-  int64_t span = (int64_t)blockIdx.x * per + (threadIdx.x >> a.log_lanes);
+  if (!WAVE && n <= 0) return;
+  int group = threadIdx.x >> a.log_lanes;
+  if constexpr (WAVE) group = __builtin_amdgcn_readfirstlane(group);
+  int64_t span = (int64_t)blockIdx.x * per + group;
   for (; span < a.spans; span += (int64_t)gridDim.x * per) {
-    const int64_t p0 = span * a.length, p1 = min(p0 + a.length, a.tokens);
-    uint32_t cur = a.keys[p0];
-    bool head = p0 > 0 && a.keys[p0 - 1] == cur;
+    const int64_t p0 = span * a.length;
+    const int count = (int)min((int64_t)a.length, a.tokens - p0);
+    uint32_t held_key = 0, held_place = 0;
+    if constexpr (WAVE) {
+      held_key = p0 + lane < a.tokens && lane <= kLongest ? a.keys[p0 + lane] : a.vocab + 1;
+      held_place = lane < count ? a.places[p0 + lane] : 0;
+    }
+    auto key_at = [&](int i) -> uint32_t {
+      if constexpr (WAVE) return __builtin_amdgcn_readlane(held_key, i);
+      else return p0 + i < a.tokens ? a.keys[p0 + i] : a.vocab + 1;
+    };
+    auto place_at = [&](int i) -> uint32_t {
+      if constexpr (WAVE) return __builtin_amdgcn_readlane(held_place, i);
+      else return a.places[p0 + i];
+    };
+    bool head = p0 > 0 && a.keys[p0 - 1] == key_at(0);
     float sum[kChunk];
 #pragma unroll
     for (int k = 0; k < kChunk; ++k) sum[k] = 0;
-    auto flush = [&](bool tail) {
-      if (cur >= a.vocab) return;
-      if (head || tail) store8<ZF_F32>(a.partial + (span * 2 + (head ? 0 : 1)) * a.cols, j, n, sum);
-      else write_row(a, cur, j, n, sum);
-    };
-    constexpr int U = 8;  // rows on their way together
-    for (int64_t p = p0; p < p1; p += U) {
-      Raw<DT> r[U];
-      uint32_t key[U];
+    for (int i = 0; i < count; i += kU) {
+      Raw<DT> r[kU];
+      Raw<GDT> old[kU];
+      uint32_t key[kU + 1];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        key[u] = p + u < p1 ? a.keys[p + u] : a.vocab;
-        if (key[u] < a.vocab)
-          r[u] = load_raw<DT, true>(a.dout, (int64_t)a.places[p + u] * a.dout_ld + j, n);
+      for (int u = 0; u <= kU; ++u) key[u] = key_at(i + u);
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        if (key[u] >= a.vocab) break;
+        r[u] = load_raw<DT, true, WHOLE>(a.dout, (int64_t)place_at(i + u) * a.dout_ld + j, n);
+        if (key[u] != key[u + 1]) old[u] = old_row<GDT, WHOLE>(a, key[u], j, n);
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (p + u >= p1) break;
-        if (key[u] != cur) {
-          flush(false);
+      for (int u = 0; u < kU; ++u) {
+        if (key[u] >= a.vocab) break;
+        float x[kChunk];
+        widen8<DT>(r[u], x);
 #pragma unroll
-          for (int k = 0; k < kChunk; ++k) sum[k] = 0;
-          cur = key[u];
-          head = false;
+        for (int k = 0; k < kChunk; ++k) sum[k] += x[k];
+        const bool ends = key[u] != key[u + 1], tail = !ends && i + u + 1 == count;
+        if (!ends && !tail) continue;
+        if (head || tail) {
+          store8<ZF_F32, false, WHOLE>(a.partial + (span * 2 + (head ? 0 : 1)) * a.cols, j, n, sum);
+          if (!head && j == 0) a.cut[1 + atomicAdd(a.cut, 1u)] = (uint32_t)span;
+        } else {
+          write_row<GDT, WHOLE>(a, key[u], j, n, old[u], sum);
         }
-        if (key[u] < a.vocab) {
-          float x[kChunk];
-          widen8<DT>(r[u], x);
+        head = false;
 #pragma unroll
-          for (int k = 0; k < kChunk; ++k) sum[k] += x[k];
-        }
+        for (int k = 0; k < kChunk; ++k) sum[k] = 0;
       }
     }
-    flush(p1 < a.tokens && a.keys[p1] == cur);
   }
 }
 
-// Runs that spans cut: the block of the span where one begins adds its partial
-// sums, 8 of them at a time, 32 lanes of 8 columns each, then the 8 in order.
+// Runs that spans cut (in any order: each has its row): a block adds a run's
+// partial sums, every 8th to each of 8 rows of 32 lanes of 8 columns, then the 8
+// in order.
+template <int GDT>
 __global__ __launch_bounds__(kThreads) void zf_run_join(RunArgs a) {
   constexpr int kLanes = 32, kRows = kThreads / kLanes;
   __shared__ float s[kRows][kChunk][kLanes];
-  for (int64_t span = blockIdx.x; span + 1 < a.spans; span += gridDim.x) {
-    const int64_t p0 = span * a.length, p1 = p0 + a.length;
-    const uint32_t key = a.keys[p1 - 1];
-    if (key >= a.vocab || a.keys[p1] != key || (p0 > 0 && a.keys[p0 - 1] == key)) continue;
-    int64_t lo = p1, hi = a.tokens;  // the run's end
-    while (lo < hi) {
-      const int64_t mid = (lo + hi) / 2;
-      if (a.keys[mid] <= key) lo = mid + 1;
-      else hi = mid;
-    }
-    const int64_t last = (lo - 1) / a.length;
-    const int lane = threadIdx.x % kLanes, row = threadIdx.x / kLanes;
-    const int64_t j = ((int64_t)blockIdx.y * kLanes + lane) * kChunk;
-    const int n = (int)min((int64_t)kChunk, a.cols - j);
-    float sum[kChunk], x[kChunk];
+  const int lane = threadIdx.x % kLanes, row = threadIdx.x / kLanes;
+  const int64_t j = ((int64_t)blockIdx.y * kLanes + lane) * kChunk;
+  const int n = (int)min((int64_t)kChunk, a.cols - j);
+  const uint32_t count = *a.cut;
+  for (uint32_t c = blockIdx.x; c < count; c += gridDim.x) {
+    const int64_t span = a.cut[1 + c], p1 = (span + 1) * a.length;
+    const uint32_t key = a.keys[p1];
+    const Raw<GDT> old = old_row<GDT>(a, key, j, row == 0 ? n : 0);
+    float sum[kChunk];
 #pragma unroll
     for (int k = 0; k < kChunk; ++k) sum[k] = 0;
-    if (n > 0) {
-#pragma unroll 4
-      for (int64_t c = span + row; c <= last; c += kRows) {
-        load8<ZF_F32>(a.partial + (c * 2 + (c == span ? 1 : 0)) * a.cols, j, n, x);
+    constexpr int kAhead = 4;
+    for (int64_t q = span + row;; q += kAhead * kRows) {
+      bool in[kAhead];
+      Raw<ZF_F32> part[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {  // a span belongs to the run if it begins with its key
+        const int64_t c = q + u * kRows;
+        in[u] = c == span || (c < a.spans && a.keys[c * a.length] == key);
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int64_t c = q + u * kRows;
+        part[u] = load_raw<ZF_F32>(a.partial, (c * 2 + (c == span ? 1 : 0)) * a.cols + j, in[u] ? n : 0);
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        float x[kChunk];
+        widen8<ZF_F32>(part[u], x);
 #pragma unroll
         for (int k = 0; k < kChunk; ++k) sum[k] += x[k];
       }
+      if (!in[kAhead - 1]) break;
     }
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < kChunk; ++k) s[row][k][lane] = sum[k];
     __syncthreads();
-    if (row > 0 || n <= 0) continue;
+    if (row == 0) {
 #pragma unroll
-    for (int r = 1; r < kRows; ++r)
+      for (int r = 1; r < kRows; ++r)
 #pragma unroll
-      for (int k = 0; k < kChunk; ++k) sum[k] += s[r][k][lane];
-    write_row(a, key, j, n, sum);
+        for (int k = 0; k < kChunk; ++k) sum[k] += s[r][k][lane];
+      write_row<GDT>(a, key, j, n, old, sum);
+    }
   }
 }
 
@@ -346,7 +447,7 @@ int log_lanes_of(int64_t cols) {
 struct GradPlan {
   int32_t blocks, items, bits, passes, length;
   int64_t spans, clear_blocks, clear_rows;
-  int64_t keys, places, counts, partial, bytes;  // offsets
+  int64_t keys, places, counts, cut, partial, bytes;  // offsets
 };
 
 GradPlan grad_plan(int64_t tokens, int64_t vocab, int64_t cols) {
@@ -355,13 +456,12 @@ GradPlan grad_plan(int64_t tokens, int64_t vocab, int64_t cols) {
   while (vocab >> width) ++width;
   g.passes = (width + 8) / 9;
   g.bits = (width + g.passes - 1) / g.passes;
-  // 4096 tokens a block, more where that would be more than 1024 blocks
-  g.items = (int32_t)(std::max<int64_t>(4, (tokens + (1 << 20) - 1) >> 20) * kSortThreads);
+  g.items = (int32_t)(std::max<int64_t>(1, (tokens + (1 << 20) - 1) >> 20) * kSortThreads);
   g.blocks = (int32_t)((tokens + g.items - 1) / g.items);
   // spans of 32 tokens, shorter ones where those would be under 2048 waves
   const int log = log_lanes_of(cols);
   const int64_t waves = std::max<int64_t>(1, ((int64_t)1 << log) / 64);
-  g.length = 32;
+  g.length = kLongest;
   while (g.length > 8 && tokens / g.length * waves < 2048) g.length /= 2;
   g.spans = (tokens + g.length - 1) / g.length;
   // clearing blocks of half a megabyte and more, and a bit of shared memory a
@@ -377,7 +477,8 @@ GradPlan grad_plan(int64_t tokens, int64_t vocab, int64_t cols) {
   g.bytes = 0;
   g.keys = place(tokens * 8);
   g.places = place(tokens * 8);
-  g.counts = place((int64_t)g.passes * g.blocks * 4 << g.bits);
+  g.counts = place(tokens > kSmall ? (int64_t)g.passes * g.blocks * 4 << g.bits : 0);
+  g.cut = place(tokens > 0 ? (1 + g.spans) * 4 : 0);
   g.partial = place(g.spans > 1 ? g.spans * 2 * cols * 4 : 0);
   return g;
 }
@@ -411,11 +512,18 @@ extern "C" int zf_embedding(const zf_embedding_args* args, void* stream) {
   const LookupArgs a{p.ids, p.table, p.out, p.out_stride, p.tokens, p.cols, p.scale,
                      (uint32_t)p.vocab, p.id_bytes == 8, log_lanes_of(p.cols)};
   const int64_t per = kThreads >> a.log_lanes, span = (int64_t)kChunk << a.log_lanes;
-  const dim3 grid((uint32_t)std::min<int64_t>((p.tokens + per - 1) / per, kMaxBlocks),
-                  (uint32_t)((p.cols + span - 1) / span));
+  const bool whole = p.cols % kChunk == 0;
+  // a block for each set of rows up to 2048 blocks, then several sets a block
+  int64_t blocks = (p.tokens + per - 1) / per;
+  if (blocks > 2048) blocks = std::max<int64_t>(2048, (blocks + kRows - 1) / kRows);
+  const dim3 grid((uint32_t)std::min<int64_t>(blocks, kMaxBlocks), (uint32_t)((p.cols + span - 1) / span));
   hipStream_t s = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();
-#define ZF_LOOKUP(T, D) hipLaunchKernelGGL((zf_embedding_kernel<T, D>), grid, dim3(kThreads), 0, s, a)
+#define ZF_LOOKUP(T, D) \
+  do { \
+    if (whole) hipLaunchKernelGGL((zf_embedding_kernel<T, D, true>), grid, dim3(kThreads), 0, s, a); \
+    else hipLaunchKernelGGL((zf_embedding_kernel<T, D, false>), grid, dim3(kThreads), 0, s, a); \
+  } while (0)
 #define ZF_LOOKUP_TO(T) \
   do { \
     if (p.dtype == ZF_F32) ZF_LOOKUP(T, ZF_F32); \
@@ -457,6 +565,7 @@ extern "C" int zf_embedding_grad(const zf_embedding_grad_args* args, void* strea
     so.places[k] = reinterpret_cast<uint32_t*>(ws + g.places) + k * p.tokens;
   }
   so.counts = reinterpret_cast<uint32_t*>(ws + g.counts);
+  so.cut = reinterpret_cast<uint32_t*>(ws + g.cut);
   so.grad = p.grad;
   so.tokens = p.tokens;
   so.cols = p.cols;
@@ -471,17 +580,22 @@ extern "C" int zf_embedding_grad(const zf_embedding_grad_args* args, void* strea
   hipStream_t s = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();
   const int64_t clear = p.accumulate ? 0 : g.clear_blocks;
-  hipLaunchKernelGGL(zf_sort_count, dim3((uint32_t)(g.blocks + clear)), dim3(kSortThreads),
-                     clear ? (uint32_t)((g.clear_rows + 31) / 32 * 4) : 0, s, so);
-  if (p.tokens > 0) {
+  const uint32_t bits = clear ? (uint32_t)((g.clear_rows + 31) / 32 * 4) : 0;
+  if (p.tokens <= kSmall) {
+    hipLaunchKernelGGL(zf_sort_small, dim3((uint32_t)(1 + clear)), dim3(kSortThreads), bits, s, so);
+  } else {
+    hipLaunchKernelGGL(zf_sort_count, dim3((uint32_t)(g.blocks + clear)), dim3(kSortThreads), bits, s, so);
     for (int pass = 0; pass < g.passes; ++pass)
       hipLaunchKernelGGL(zf_sort_pass, dim3(g.blocks), dim3(kSortThreads), 0, s, so, pass);
+  }
+  if (p.tokens > 0) {
     RunArgs r;
     r.keys = so.keys[(g.passes - 1) & 1];
     r.places = so.places[(g.passes - 1) & 1];
     r.dout = p.dout;
     r.grad = p.grad;
     r.partial = reinterpret_cast<float*>(ws + g.partial);
+    r.cut = so.cut;
     r.dout_ld = p.dout_stride;
     r.tokens = p.tokens;
     r.cols = p.cols;
@@ -495,13 +609,26 @@ extern "C" int zf_embedding_grad(const zf_embedding_grad_args* args, void* strea
     const int64_t per = kThreads >> r.log_lanes, span = (int64_t)kChunk << r.log_lanes;
     const dim3 grid((uint32_t)std::min<int64_t>((g.spans + per - 1) / per, kMaxBlocks),
                     (uint32_t)((p.cols + span - 1) / span));
-    if (p.dtype == ZF_F32) hipLaunchKernelGGL(zf_run_sums<ZF_F32>, grid, dim3(kThreads), 0, s, r);
-    else if (p.dtype == ZF_BF16) hipLaunchKernelGGL(zf_run_sums<ZF_BF16>, grid, dim3(kThreads), 0, s, r);
-    else hipLaunchKernelGGL(zf_run_sums<ZF_F16>, grid, dim3(kThreads), 0, s, r);
-    if (g.spans > 1)
-      hipLaunchKernelGGL(zf_run_join, dim3((uint32_t)std::min<int64_t>(g.spans - 1, kMaxBlocks),
-                                           (uint32_t)((p.cols + 255) / 256)),
-                         dim3(kThreads), 0, s, r);
+    const bool whole = p.cols % kChunk == 0;
+    const dim3 join((uint32_t)std::min<int64_t>(g.spans - 1, 1024), (uint32_t)((p.cols + 255) / 256));
+#define ZF_RUNS(D, G) \
+  do { \
+    if (!whole) hipLaunchKernelGGL((zf_run_sums<D, G, false, false>), grid, dim3(kThreads), 0, s, r); \
+    else if (r.log_lanes < 6) hipLaunchKernelGGL((zf_run_sums<D, G, true, false>), grid, dim3(kThreads), 0, s, r); \
+    else hipLaunchKernelGGL((zf_run_sums<D, G, true, true>), grid, dim3(kThreads), 0, s, r); \
+    if (g.spans > 1) hipLaunchKernelGGL(zf_run_join<G>, join, dim3(kThreads), 0, s, r); \
+  } while (0)
+#define ZF_RUNS_TO(D) \
+  do { \
+    if (p.grad_dtype == ZF_F32) ZF_RUNS(D, ZF_F32); \
+    else if (p.grad_dtype == ZF_BF16) ZF_RUNS(D, ZF_BF16); \
+    else ZF_RUNS(D, ZF_F16); \
+  } while (0)
+    if (p.dtype == ZF_F32) ZF_RUNS_TO(ZF_F32);
+    else if (p.dtype == ZF_BF16) ZF_RUNS_TO(ZF_BF16);
+    else ZF_RUNS_TO(ZF_F16);
+#undef ZF_RUNS_TO
+#undef ZF_RUNS
   }
   return hip_ok(hipGetLastError()) ? ZF_OK : ZF_EHIP;
 }
