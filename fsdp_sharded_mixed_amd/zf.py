@@ -578,11 +578,11 @@ class OrthoBatch:
     tensors: tuple
 
 
-def _dtype_of(t, where="zf_orthogonalize"):
+def _dtype_of(t):
     import torch
     code = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}.get(t.dtype)
     if code is None:
-        raise ValueError(f"{where}: unsupported dtype {t.dtype}")
+        raise ValueError(f"zf_orthogonalize: unsupported dtype {t.dtype}")
     return code
 
 
@@ -705,16 +705,42 @@ NORM_LAYER, NORM_RMS = 0, 1
 ACT8_GROUP = 32
 
 
+_ROW_DTYPES, _ID_BYTES = {}, {}
+
+
+def _torch():
+    """torch, with the tables of its dtypes filled on first use (a small call's
+    time is mostly this module's)."""
+    import torch
+    if not _ROW_DTYPES:
+        _ROW_DTYPES.update({torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32})
+        _ID_BYTES.update({torch.int32: 4, torch.int64: 8})
+    return torch
+
+
+def _row_dtype(where, t):
+    code = _ROW_DTYPES.get(t.dtype)
+    if code is None:
+        _torch()
+        code = _ROW_DTYPES.get(t.dtype)
+        if code is None:
+            raise ValueError(f"{where}: unsupported dtype {t.dtype}")
+    return code
+
+
 def _matrix(where, t, rows, cols):
     """(dtype code, row stride) of a 2-D tensor [rows, cols] with contiguous
     rows that do not overlap."""
-    if t.dim() != 2 or tuple(t.shape) != (rows, cols):
+    if t.shape != (rows, cols):
         raise ValueError(f"{where}: a tensor of {rows} x {cols} was expected, got {tuple(t.shape)}")
-    if cols > 1 and t.stride(1) != 1:
+    ld, one = t.stride()
+    if cols > 1 and one != 1:
         raise ValueError(f"{where}: rows must be contiguous")
-    if rows > 1 and t.stride(0) < cols:
+    if rows <= 1:
+        ld = cols
+    elif ld < cols:
         raise ValueError(f"{where}: rows must not overlap")
-    return _dtype_of(t, where), max(t.stride(0), cols) if rows > 1 else cols
+    return _row_dtype(where, t), ld
 
 
 def _vector(where, t, n, dtype=None):
@@ -722,22 +748,36 @@ def _vector(where, t, n, dtype=None):
     buffer, of any shape)."""
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{where}: a contiguous tensor of {n} elements was expected")
-    code = _dtype_of(t, where)
+    code = _row_dtype(where, t)
     if dtype is not None and code != dtype:
         raise ValueError(f"{where}: dtype {t.dtype} does not fit")
     return code
 
 
-def _on_gpu(where, *tensors):
-    _on_current_device(where, *(t.device for t in tensors if t is not None and
-                                not isinstance(t, int)))
+def _on_gpu(where, stream, *tensors):
+    """Kernels run on the current device: the stream to launch on, with every
+    tensor (None entries and addresses skipped) on that device."""
+    cuda = _torch().cuda
+    current = None
+    for t in tensors:
+        if t is None or isinstance(t, int):
+            continue
+        if current is None:
+            current = cuda.current_device() if t.is_cuda else -1
+        if not t.is_cuda or t.get_device() != current:
+            raise ValueError(f"{where}: buffers on {t.device}, not on the current GPU")
+    if stream is None:
+        return cuda.current_stream(current).cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _ids(where, ids):
-    import torch
-    size = {torch.int32: 4, torch.int64: 8}.get(ids.dtype)
+    size = _ID_BYTES.get(ids.dtype)
     if size is None:
-        raise ValueError(f"{where}: ids are int32 or int64, not {ids.dtype}")
+        _torch()
+        size = _ID_BYTES.get(ids.dtype)
+        if size is None:
+            raise ValueError(f"{where}: ids are int32 or int64, not {ids.dtype}")
     if not ids.is_contiguous():
         raise ValueError(f"{where}: ids must be contiguous")
     return size
@@ -759,7 +799,7 @@ def embedding(table, ids, out, scale=1.0, stream=None):
     [tokens, cols] with contiguous rows.  An id outside the vocabulary (-1:
     padding) gives a row of zeros."""
     where = "zf_embedding"
-    _on_gpu(where, table, ids, out)
+    s = _on_gpu(where, stream, table, ids, out)
     if table.dim() != 2:
         raise ValueError(f"{where}: a table of vocab x cols was expected")
     vocab, cols = table.shape
@@ -767,7 +807,7 @@ def embedding(table, ids, out, scale=1.0, stream=None):
     dtype, ld = _matrix(where, out, n, cols)
     args = EmbeddingArgs(_vector(where, table, vocab * cols), dtype, _ids(where, ids),
                          float(scale), n, vocab, cols, _ptr(ids), _ptr(table), _ptr(out), ld)
-    _check(lib.zf_embedding(C.byref(args), _stream(stream)), where)
+    _check(lib.zf_embedding(C.byref(args), s), where)
 
 
 def embedding_grad_bytes(tokens, vocab, cols):
@@ -782,7 +822,7 @@ def embedding_grad(dout, ids, grad, workspace, scale=1.0, accumulate=False, stre
     tokens with ids[t] == v.  dout: [tokens, cols] with contiguous rows; grad:
     [vocab, cols], rows end to end."""
     where = "zf_embedding_grad"
-    _on_gpu(where, dout, ids, grad, workspace)
+    s = _on_gpu(where, stream, dout, ids, grad, workspace)
     if grad.dim() != 2:
         raise ValueError(f"{where}: a gradient of vocab x cols was expected")
     vocab, cols = grad.shape
@@ -792,7 +832,7 @@ def embedding_grad(dout, ids, grad, workspace, scale=1.0, accumulate=False, stre
                              _accumulate(accumulate), float(scale), 0, n, vocab, cols, _ptr(ids),
                              _ptr(dout), ld, _ptr(grad), _ptr(workspace),
                              _nbytes(workspace, workspace_size))
-    _check(lib.zf_embedding_grad(C.byref(args), _stream(stream)), where)
+    _check(lib.zf_embedding_grad(C.byref(args), s), where)
 
 
 @dataclass
@@ -831,17 +871,17 @@ def act8(codes, scales):
 def act8_store(a, x, stream=None):
     """zf_act8_store: keep x ([rows, cols], contiguous rows) as checkpoint a."""
     where = "zf_act8_store"
-    _on_gpu(where, a.codes, x)
+    s = _on_gpu(where, stream, a.codes, x)
     dtype, ld = _matrix(where, x, *a.shape)
-    _check(lib.zf_act8_store(C.byref(a.struct), dtype, _ptr(x), ld, _stream(stream)), where)
+    _check(lib.zf_act8_store(C.byref(a.struct), dtype, _ptr(x), ld, s), where)
 
 
 def act8_load(a, x, stream=None):
     """zf_act8_load: x = the numbers that checkpoint a stands for."""
     where = "zf_act8_load"
-    _on_gpu(where, a.codes, x)
+    s = _on_gpu(where, stream, a.codes, x)
     dtype, ld = _matrix(where, x, *a.shape)
-    _check(lib.zf_act8_load(C.byref(a.struct), dtype, _ptr(x), ld, _stream(stream)), where)
+    _check(lib.zf_act8_load(C.byref(a.struct), dtype, _ptr(x), ld, s), where)
 
 
 def _kept(where, a, rows, cols):
@@ -866,7 +906,7 @@ def layer_norm(kind, x, weight, bias, eps, y, mean, rstd, x8=None, y8=None, stre
     NORM_RMS) and rstd (fp32, [rows]).  weight, bias (or None): cols elements
     of one dtype.  x8, y8: None, or checkpoints (act8) that receive x and y."""
     where = "zf_layer_norm"
-    _on_gpu(where, x, weight, bias, y, mean, rstd, x8 and x8.codes, y8 and y8.codes)
+    s = _on_gpu(where, stream, x, weight, bias, y, mean, rstd, x8 and x8.codes, y8 and y8.codes)
     if x.dim() != 2:
         raise ValueError(f"{where}: x is rows x cols")
     rows, cols = x.shape
@@ -881,7 +921,7 @@ def layer_norm(kind, x, weight, bias, eps, y, mean, rstd, x8=None, y8=None, stre
     args = LayerNormArgs(int(kind), dtype, wdt, 0, float(eps), rows, cols, _ptr(x), x_ld,
                          _ptr(weight), _ptr(bias), _ptr(y), y_ld, _ptr(mean), _ptr(rstd),
                          _kept(where, x8, rows, cols), _kept(where, y8, rows, cols))
-    _check(lib.zf_layer_norm(C.byref(args), _stream(stream)), where)
+    _check(lib.zf_layer_norm(C.byref(args), s), where)
 
 
 def layer_norm_grad_bytes(rows, cols):
@@ -897,7 +937,7 @@ def layer_norm_grad(kind, dy, x, weight, mean, rstd, dx, weight_grad, bias_grad,
     (act8)."""
     where = "zf_layer_norm_grad"
     x8 = x if isinstance(x, Act8) else None
-    _on_gpu(where, dy, x8.codes if x8 else x, weight, mean, rstd, dx, weight_grad, bias_grad,
+    s = _on_gpu(where, stream, dy, x8.codes if x8 else x, weight, mean, rstd, dx, weight_grad, bias_grad,
             workspace)
     if dy.dim() != 2:
         raise ValueError(f"{where}: dy is rows x cols")
@@ -908,7 +948,7 @@ def layer_norm_grad(kind, dy, x, weight, mean, rstd, dx, weight_grad, bias_grad,
     if x_dtype != dtype or dx_dtype != dtype:
         raise ValueError(f"{where}: x, dy and dx have one dtype")
     grads = [t for t in (weight_grad, bias_grad) if t is not None]
-    gdt = _dtype_of(grads[0], where) if grads else F32
+    gdt = _row_dtype(where, grads[0]) if grads else F32
     for t in grads:
         _vector(where, t, cols, gdt)
     wdt = _vector(where, weight, cols)
@@ -918,7 +958,7 @@ def layer_norm_grad(kind, dy, x, weight, mean, rstd, dx, weight_grad, bias_grad,
                              _kept(where, x8, rows, cols), _ptr(weight), _ptr(mean), _ptr(rstd),
                              _ptr(dx), dx_ld, _ptr(weight_grad), _ptr(bias_grad), _ptr(workspace),
                              _nbytes(workspace, workspace_size))
-    _check(lib.zf_layer_norm_grad(C.byref(args), _stream(stream)), where)
+    _check(lib.zf_layer_norm_grad(C.byref(args), s), where)
 
 
 def weight_grad_bytes(rows, out_features, in_features):
@@ -932,7 +972,7 @@ def weight_grad(dy, x8, grad, workspace, accumulate=False, stream=None, workspac
     bf16, contiguous rows) and the checkpoint x8 of the Linear's input; grad:
     [out_features, in_features], rows end to end."""
     where = "zf_weight_grad"
-    _on_gpu(where, dy, x8.codes, grad, workspace)
+    s = _on_gpu(where, stream, dy, x8.codes, grad, workspace)
     if dy.dim() != 2:
         raise ValueError(f"{where}: dy is rows x out_features")
     rows, outs = dy.shape
@@ -943,4 +983,4 @@ def weight_grad(dy, x8, grad, workspace, accumulate=False, stream=None, workspac
     args = WeightGradArgs(dtype, _vector(where, grad, outs * ins), _accumulate(accumulate), 0,
                           rows, outs, ins, _ptr(dy), ld, _kept(where, x8, rows, ins), _ptr(grad),
                           _ptr(workspace), _nbytes(workspace, workspace_size))
-    _check(lib.zf_weight_grad(C.byref(args), _stream(stream)), where)
+    _check(lib.zf_weight_grad(C.byref(args), s), where)
