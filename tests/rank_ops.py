@@ -142,10 +142,11 @@ def assert_within(got, want, bound, what=""):
     f, exponent = torch.finfo(got.dtype), math.frexp(torch.finfo(got.dtype).max)[1]
     limit = f.max + f.eps * 2.0 ** (exponent - 2)
     got = got.double()
+    bound = torch.as_tensor(bound, dtype=torch.float64, device=want.device).expand_as(want)
     over = torch.isinf(got) & (got.sign() == want.sign()) & (want.abs() + bound >= limit)
     got = torch.where(over, want, got)
     fine = torch.isfinite(want)
-    assert bool((want.abs()[fine & ~over] - torch.as_tensor(bound).expand_as(want)[fine & ~over] < limit).all()), \
+    assert bool((want.abs()[fine & ~over] - bound[fine & ~over] < limit).all()), \
         f"{what}: numbers where the type has none"
     assert torch.equal(fine, torch.isfinite(got)), f"{what}: other elements are infinite or NaN"
     bad = fine & ((got - want).abs() > bound)
@@ -153,7 +154,7 @@ def assert_within(got, want, bound, what=""):
         at = int(bad.flatten().nonzero()[0])
         raise AssertionError(f"{what}: {int(bad.sum())} of {bad.numel()} elements are off, the first at {at}: "
                              f"{float(got.flatten()[at])} for {float(want.flatten()[at])}, "
-                             f"bound {float(torch.as_tensor(bound).expand_as(want).flatten()[at])}")
+                             f"bound {float(bound.flatten()[at])}")
 
 
 def rounded(want, error, dtype):
