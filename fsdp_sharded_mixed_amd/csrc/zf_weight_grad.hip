@@ -166,13 +166,14 @@ struct Place {
 // a row's end give elements of columns that are not written.
 struct Walk {
   const char* at;
-  int32_t left, ld, tail;  // rows; bytes of a stride, and of a row from here on
+  int64_t ld;          // bytes of a stride
+  int32_t left, tail;  // rows; bytes of a row from here on
 
   __device__ __forceinline__ Walk(const void* base, int64_t row, int64_t rows, int64_t row_bytes, int64_t skip,
                                   int64_t width) {
     at = static_cast<const char*>(base) + row * row_bytes + skip;
     left = (int32_t)rows;
-    ld = (int32_t)row_bytes;
+    ld = row_bytes;
     tail = (int32_t)(width - skip);
   }
   // A stage's buffer.  128 rows are as good as more: it has 32, and its tile's
@@ -187,7 +188,7 @@ struct Walk {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(at), 0, n, 0x00020000);
   }
   __device__ __forceinline__ void next() {
-    at += (int64_t)kDepth * ld;
+    at += kDepth * ld;
     left -= kDepth;
   }
 };
@@ -239,9 +240,9 @@ struct Pipe {
     const int at = place<T::BM / 8>(prow, tid % (T::BM / 8)) % (T::BM * 2), piece = tid % (T::BN / 16);
     wq = kPBytes + place<T::BN / 8>(qrow, piece * 2);
     if constexpr (DIRECT) {
-      vp = prow * p.ld + at;
-      vq = qrow * q.ld + piece * 16;
-      vs = qrow * s.ld + piece * 16 / ZF_ACT8_GROUP;
+      vp = prow * (int)p.ld + at;
+      vq = qrow * (int)q.ld + piece * 16;
+      vs = qrow * (int)s.ld + piece * 16 / ZF_ACT8_GROUP;
     } else {
       const int64_t row = first + prow, column = min(j0 + piece * 16, a.in - 1);
       wp = tid * 16;
@@ -282,7 +283,7 @@ struct Pipe {
 #pragma unroll
       for (int h = 0; h < kPLoads; ++h) {
         r.g[h] = (u32x4){0, 0, 0, 0};
-        const char* at = gp + (int64_t)(h * kPRows) * p.ld;
+        const char* at = gp + h * kPRows * p.ld;
         const bool in = prow + h * kPRows < p.left;
         if (in && at + 16 <= p_end) r.g[h] = load_any<false, u32x4_any>(at);
         if (rare(in && at + 16 > p_end))
@@ -299,9 +300,9 @@ struct Pipe {
         const u32x2 lo = load_codes(at, min(8, n)), hi = load_codes(at + 8, n - 8);
         r.c = (u32x4){lo.x, lo.y, hi.x, hi.y};
       }
-      gp += (int64_t)kDepth * p.ld;
-      gq += (int64_t)kDepth * q.ld;
-      gs += (int64_t)kDepth * s.ld;
+      gp += kDepth * p.ld;
+      gq += kDepth * q.ld;
+      gs += kDepth * s.ld;
       p.left -= kDepth;
       q.left -= kDepth;
     }
@@ -426,9 +427,11 @@ __global__ __launch_bounds__(T::kThreads, 2) void zf_weight_grad_kernel(GradArgs
   o.put(s1, h1);
   arrive<0>();
   if constexpr (DIRECT) o.fetch_p(s2);
+  loads_in_order();
   o.fetch(h0);
   loads_in_order();
   if constexpr (DIRECT) o.fetch_p(s3);
+  loads_in_order();
   o.fetch(h1);
   loads_in_order();
 #pragma unroll

@@ -705,26 +705,28 @@ NORM_LAYER, NORM_RMS = 0, 1
 ACT8_GROUP = 32
 
 
-_ROW_DTYPES, _ID_BYTES = {}, {}
+# torch's functions and dtypes, filled on first use: a small call's time is
+# mostly this module's.
+_ROW_DTYPES, _ID_BYTES, _NOW = {}, {}, []
 
 
-def _torch():
-    """torch, with the tables of its dtypes filled on first use (a small call's
-    time is mostly this module's)."""
+def _torch_tables():
     import torch
-    if not _ROW_DTYPES:
-        _ROW_DTYPES.update({torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32})
-        _ID_BYTES.update({torch.int32: 4, torch.int64: 8})
-    return torch
+    _ROW_DTYPES.update({torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32})
+    _ID_BYTES.update({torch.int32: 4, torch.int64: 8})
+    # the current stream's address without an object for the stream (0.1 us
+    # instead of 1.2), where this torch offers it
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _NOW[:] = [torch.cuda.current_device,
+               raw or (lambda device: torch.cuda.current_stream(device).cuda_stream)]
 
 
 def _row_dtype(where, t):
+    if not _NOW:
+        _torch_tables()
     code = _ROW_DTYPES.get(t.dtype)
     if code is None:
-        _torch()
-        code = _ROW_DTYPES.get(t.dtype)
-        if code is None:
-            raise ValueError(f"{where}: unsupported dtype {t.dtype}")
+        raise ValueError(f"{where}: unsupported dtype {t.dtype}")
     return code
 
 
@@ -757,30 +759,36 @@ def _vector(where, t, n, dtype=None):
 def _on_gpu(where, stream, *tensors):
     """Kernels run on the current device: the stream to launch on, with every
     tensor (None entries and addresses skipped) on that device."""
-    cuda = _torch().cuda
+    if not _NOW:
+        _torch_tables()
     current = None
     for t in tensors:
         if t is None or isinstance(t, int):
             continue
+        device = t.get_device()
         if current is None:
-            current = cuda.current_device() if t.is_cuda else -1
-        if not t.is_cuda or t.get_device() != current:
+            current = _NOW[0]() if device >= 0 else -2
+        if device != current:
             raise ValueError(f"{where}: buffers on {t.device}, not on the current GPU")
     if stream is None:
-        return cuda.current_stream(current).cuda_stream
+        return _NOW[1](_NOW[0]() if current is None else current)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _ids(where, ids):
+    if not _NOW:
+        _torch_tables()
     size = _ID_BYTES.get(ids.dtype)
     if size is None:
-        _torch()
-        size = _ID_BYTES.get(ids.dtype)
-        if size is None:
-            raise ValueError(f"{where}: ids are int32 or int64, not {ids.dtype}")
+        raise ValueError(f"{where}: ids are int32 or int64, not {ids.dtype}")
     if not ids.is_contiguous():
         raise ValueError(f"{where}: ids must be contiguous")
     return size
+
+
+def _at(t):
+    """A tensor's address, or None."""
+    return None if t is None else t.data_ptr()
 
 
 def _accumulate(flag):
@@ -806,7 +814,7 @@ def embedding(table, ids, out, scale=1.0, stream=None):
     n = ids.numel()
     dtype, ld = _matrix(where, out, n, cols)
     args = EmbeddingArgs(_vector(where, table, vocab * cols), dtype, _ids(where, ids),
-                         float(scale), n, vocab, cols, _ptr(ids), _ptr(table), _ptr(out), ld)
+                         float(scale), n, vocab, cols, ids.data_ptr(), table.data_ptr(), out.data_ptr(), ld)
     _check(lib.zf_embedding(C.byref(args), s), where)
 
 
@@ -829,8 +837,8 @@ def embedding_grad(dout, ids, grad, workspace, scale=1.0, accumulate=False, stre
     n = ids.numel()
     dtype, ld = _matrix(where, dout, n, cols)
     args = EmbeddingGradArgs(dtype, _vector(where, grad, vocab * cols), _ids(where, ids),
-                             _accumulate(accumulate), float(scale), 0, n, vocab, cols, _ptr(ids),
-                             _ptr(dout), ld, _ptr(grad), _ptr(workspace),
+                             _accumulate(accumulate), float(scale), 0, n, vocab, cols,
+                             ids.data_ptr(), dout.data_ptr(), ld, grad.data_ptr(), _ptr(workspace),
                              _nbytes(workspace, workspace_size))
     _check(lib.zf_embedding_grad(C.byref(args), s), where)
 
@@ -873,7 +881,7 @@ def act8_store(a, x, stream=None):
     where = "zf_act8_store"
     s = _on_gpu(where, stream, a.codes, x)
     dtype, ld = _matrix(where, x, *a.shape)
-    _check(lib.zf_act8_store(C.byref(a.struct), dtype, _ptr(x), ld, s), where)
+    _check(lib.zf_act8_store(C.byref(a.struct), dtype, x.data_ptr(), ld, s), where)
 
 
 def act8_load(a, x, stream=None):
@@ -881,7 +889,7 @@ def act8_load(a, x, stream=None):
     where = "zf_act8_load"
     s = _on_gpu(where, stream, a.codes, x)
     dtype, ld = _matrix(where, x, *a.shape)
-    _check(lib.zf_act8_load(C.byref(a.struct), dtype, _ptr(x), ld, s), where)
+    _check(lib.zf_act8_load(C.byref(a.struct), dtype, x.data_ptr(), ld, s), where)
 
 
 def _kept(where, a, rows, cols):
@@ -893,11 +901,11 @@ def _kept(where, a, rows, cols):
 
 
 def _statistics(where, kind, rows, mean, rstd):
-    if kind == NORM_LAYER and mean is None:
-        raise ValueError(f"{where}: layer norm has means")
-    for t in (mean if kind == NORM_LAYER else None, rstd):
-        if t is not None:
-            _vector(where, t, rows, F32)
+    if rstd is None or (kind == NORM_LAYER and mean is None):
+        raise ValueError(f"{where}: rstd is needed, and mean for layer norm")
+    _vector(where, rstd, rows, F32)
+    if kind == NORM_LAYER:
+        _vector(where, mean, rows, F32)
 
 
 def layer_norm(kind, x, weight, bias, eps, y, mean, rstd, x8=None, y8=None, stream=None):
@@ -918,8 +926,8 @@ def layer_norm(kind, x, weight, bias, eps, y, mean, rstd, x8=None, y8=None, stre
     if bias is not None:
         _vector(where, bias, cols, wdt)
     _statistics(where, kind, rows, mean, rstd)
-    args = LayerNormArgs(int(kind), dtype, wdt, 0, float(eps), rows, cols, _ptr(x), x_ld,
-                         _ptr(weight), _ptr(bias), _ptr(y), y_ld, _ptr(mean), _ptr(rstd),
+    args = LayerNormArgs(int(kind), dtype, wdt, 0, float(eps), rows, cols, x.data_ptr(), x_ld,
+                         weight.data_ptr(), _at(bias), y.data_ptr(), y_ld, _at(mean), rstd.data_ptr(),
                          _kept(where, x8, rows, cols), _kept(where, y8, rows, cols))
     _check(lib.zf_layer_norm(C.byref(args), s), where)
 
@@ -954,9 +962,10 @@ def layer_norm_grad(kind, dy, x, weight, mean, rstd, dx, weight_grad, bias_grad,
     wdt = _vector(where, weight, cols)
     _statistics(where, kind, rows, mean, rstd)
     args = LayerNormGradArgs(int(kind), dtype, wdt, gdt, _accumulate(accumulate), 0, rows, cols,
-                             _ptr(dy), dy_ld, None if x8 else _ptr(x), x_ld,
-                             _kept(where, x8, rows, cols), _ptr(weight), _ptr(mean), _ptr(rstd),
-                             _ptr(dx), dx_ld, _ptr(weight_grad), _ptr(bias_grad), _ptr(workspace),
+                             dy.data_ptr(), dy_ld, None if x8 else x.data_ptr(), x_ld,
+                             _kept(where, x8, rows, cols), weight.data_ptr(), _at(mean),
+                             rstd.data_ptr(), dx.data_ptr(), dx_ld, _at(weight_grad), _at(bias_grad),
+                             _ptr(workspace),
                              _nbytes(workspace, workspace_size))
     _check(lib.zf_layer_norm_grad(C.byref(args), s), where)
 
@@ -981,6 +990,6 @@ def weight_grad(dy, x8, grad, workspace, accumulate=False, stream=None, workspac
     if tuple(grad.shape) != (outs, ins):
         raise ValueError(f"{where}: a gradient of {outs} x {ins} was expected")
     args = WeightGradArgs(dtype, _vector(where, grad, outs * ins), _accumulate(accumulate), 0,
-                          rows, outs, ins, _ptr(dy), ld, _kept(where, x8, rows, ins), _ptr(grad),
+                          rows, outs, ins, dy.data_ptr(), ld, _kept(where, x8, rows, ins), grad.data_ptr(),
                           _ptr(workspace), _nbytes(workspace, workspace_size))
     _check(lib.zf_weight_grad(C.byref(args), s), where)
