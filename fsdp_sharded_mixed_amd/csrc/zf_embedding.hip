@@ -311,10 +311,16 @@ __device__ __forceinline__ Raw<GDT> old_row(const RunArgs& a, uint32_t v, int64_
 }
 
 // A group of lanes adds the rows of a span, kU of them and, where runs end,
-// the rows that they are added to on their way together.  WAVE: groups are
-// whole waves, which hold the span's keys and places a lane each and read them
-// as scalars, so that a row's address and every branch are the wave's.
-constexpr int kU = 4, kLongest = 32;
+// the rows that they are added to on their way together.
+//
+// WAVE: groups are whole waves, which hold keys and places a lane each and read
+// them as scalars, so that a row's address and every branch are the wave's.  Such
+// a group also takes the rest of a run that begins in its span and ends in the
+// next one, whose group leaves it out; only runs over three spans and more are
+// cut.  (32768 tokens by word frequency, 2048 columns added to fp32: spans of 32,
+// cut at both ends, 75 us and 13 for the join of 700 cut runs.)
+constexpr int kU = 4, kLongest = 16;
+static_assert(2 * kLongest + kU < 64, "a wave holds two spans and what is read behind them");
 template <int DT, int GDT, bool WHOLE, bool WAVE>
 __global__ __launch_bounds__(kThreads) void zf_run_sums(RunArgs a) {
   const int lanes = 1 << a.log_lanes, per = kThreads >> a.log_lanes, lane = threadIdx.x & 63;
@@ -323,28 +329,42 @@ __global__ __launch_bounds__(kThreads) void zf_run_sums(RunArgs a) {
   if (!WAVE && n <= 0) return;
   int group = threadIdx.x >> a.log_lanes;
   if constexpr (WAVE) group = __builtin_amdgcn_readfirstlane(group);
+  const uint32_t none = a.vocab + 1;  // the key of no token
   int64_t span = (int64_t)blockIdx.x * per + group;
   for (; span < a.spans; span += (int64_t)gridDim.x * per) {
     const int64_t p0 = span * a.length;
     const int count = (int)min((int64_t)a.length, a.tokens - p0);
-    uint32_t held_key = 0, held_place = 0;
-    if constexpr (WAVE) {
-      held_key = p0 + lane < a.tokens && lane <= kLongest ? a.keys[p0 + lane] : a.vocab + 1;
-      held_place = lane < count ? a.places[p0 + lane] : 0;
+    uint32_t held_key = none, held_place = 0;
+    if constexpr (WAVE) {  // of this span and the next one, and the key behind them
+      if (lane <= 2 * a.length && p0 + lane < a.tokens) {
+        held_key = a.keys[p0 + lane];
+        held_place = a.places[p0 + lane];
+      }
     }
     auto key_at = [&](int i) -> uint32_t {
       if constexpr (WAVE) return __builtin_amdgcn_readlane(held_key, i);
-      else return p0 + i < a.tokens ? a.keys[p0 + i] : a.vocab + 1;
+      else return p0 + i < a.tokens ? a.keys[p0 + i] : none;
     };
     auto place_at = [&](int i) -> uint32_t {
       if constexpr (WAVE) return __builtin_amdgcn_readlane(held_place, i);
       else return a.places[p0 + i];
     };
-    bool head = p0 > 0 && a.keys[p0 - 1] == key_at(0);
+    const uint32_t key0 = key_at(0);
+    bool head = p0 > 0 && a.keys[p0 - 1] == key0;
+    int begin = 0, stop = count;
+    if constexpr (WAVE) {
+      const uint32_t last = key_at(count - 1);
+      if (key_at(count) == last && !(head && key0 == last) && key_at(2 * count) != last)
+        stop += __builtin_ctzll(~(__ballot(held_key == last) >> count));
+      if (head && key_at(count) != key0 && (p0 == a.length || a.keys[p0 - a.length - 1] != key0)) {
+        begin = __builtin_ctzll(~__ballot(held_key == key0));
+        head = false;
+      }
+    }
     float sum[kChunk];
 #pragma unroll
     for (int k = 0; k < kChunk; ++k) sum[k] = 0;
-    for (int i = 0; i < count; i += kU) {
+    for (int i = begin; i < stop; i += kU) {
       Raw<DT> r[kU];
       Raw<GDT> old[kU];
       uint32_t key[kU + 1];
@@ -352,18 +372,18 @@ __global__ __launch_bounds__(kThreads) void zf_run_sums(RunArgs a) {
       for (int u = 0; u <= kU; ++u) key[u] = key_at(i + u);
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
-        if (key[u] >= a.vocab) break;
+        if (key[u] >= a.vocab || i + u >= stop) break;
         r[u] = load_raw<DT, true, WHOLE>(a.dout, (int64_t)place_at(i + u) * a.dout_ld + j, n);
         if (key[u] != key[u + 1]) old[u] = old_row<GDT, WHOLE>(a, key[u], j, n);
       }
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
-        if (key[u] >= a.vocab) break;
+        if (key[u] >= a.vocab || i + u >= stop) break;
         float x[kChunk];
         widen8<DT>(r[u], x);
 #pragma unroll
         for (int k = 0; k < kChunk; ++k) sum[k] += x[k];
-        const bool ends = key[u] != key[u + 1], tail = !ends && i + u + 1 == count;
+        const bool ends = key[u] != key[u + 1], tail = !ends && i + u + 1 == stop;
         if (!ends && !tail) continue;
         if (head || tail) {
           store8<ZF_F32, false, WHOLE>(a.partial + (span * 2 + (head ? 0 : 1)) * a.cols, j, n, sum);
