@@ -28,7 +28,6 @@ using zf::kThreads;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 #define ZF_LDS __attribute__((address_space(3)))
 
@@ -40,8 +39,11 @@ struct Tile {
   static constexpr int BM = BM_, BN = BN_, kThreads = WI * WJ * 64, kWavesJ = WJ;
   static constexpr int TI = BM / WI, TJ = BN / WJ, FI = TI / 16, FJ = TJ / 16;
   static constexpr int kShared = kStages * kDepth * (BM + BN) * 2;  // operands, or squares of results
-  static_assert(kShared >= WI * WJ * 16384, "squares fit");
+  static constexpr int kSquare = TI < 64 ? TI : 64;  // rows of a square of results, 64 columns wide
+  static_assert(kShared >= WI * WJ * kSquare * 256, "squares fit");
+  static_assert(TJ % 64 == 0 && TI % kSquare == 0, "squares");
 };
+typedef Tile<64, 128, 2, 2> Little;
 typedef Tile<128, 128, 2, 2> Middle;
 typedef Tile<256, 256, 2, 4> Big;
 typedef f32x4 f32x4_any __attribute__((aligned(4)));
@@ -84,36 +86,35 @@ __device__ __forceinline__ f32x4 mma(s16x8 a, s16x8 b, f32x4 c) {
                                                   __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-// Results leave by whole lines: a wave's squares of 64 x 64 go to shared memory
-// (16 KiB a wave; 16-byte pieces permuted by the row, for the banks) and out
+// Results leave by whole lines: a wave's squares of 64 x 64 (or 32 x 64) go to
+// shared memory (16-byte pieces permuted by the row, for the banks) and out
 // again 8 columns a lane, with one piece of code for every type.
 // acc[i][j][r] is row l, column 4 g + r of a 16 x 16 square.
 template <typename T>
 __device__ __forceinline__ void write_tile(const GradArgs& a, const f32x4 (&acc)[T::FI][T::FJ], char* shared,
                                            int i0, int j0, int split) {
-  static_assert(T::TJ % 64 == 0 && T::TI % 64 == 0, "squares");
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
-  ZF_LDS float* square = (ZF_LDS float*)shared + wave * 4096;
+  ZF_LDS float* square = (ZF_LDS float*)shared + wave * T::kSquare * 64;
   float* partial = a.partial ? a.partial + (int64_t)split * a.out * a.in : nullptr;
   const int32_t gdt = partial ? (int32_t)ZF_F32 : a.gdt;
   void* to = partial ? partial : a.grad;
   const bool add = a.accumulate && !partial;
   const int c = lane & 7;
 #pragma unroll
-  for (int q = 0; q < T::TI / 64 * (T::TJ / 64); ++q) {
+  for (int q = 0; q < T::TI / T::kSquare * (T::TJ / 64); ++q) {
     const int qi = q / (T::TJ / 64), qj = q % (T::TJ / 64);
     const int j = j0 + wave % T::kWavesJ * T::TJ + qj * 64 + c * 8, n = a.in - j;
 #pragma unroll
-    for (int f = 0; f < 4; ++f)
+    for (int f = 0; f < T::kSquare / 16; ++f)
 #pragma unroll
       for (int fj = 0; fj < 4; ++fj)
         *(ZF_LDS f32x4*)(square + (f * 16 + l) * 64 + ((fj * 4 + g) ^ (l & 7)) * 4) =
-            acc[qi * 4 + f][qj * 4 + fj];
+            acc[qi * (T::kSquare / 16) + f][qj * 4 + fj];
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    const int o0 = i0 + wave / T::kWavesJ * T::TI + qi * 64;
+    const int o0 = i0 + wave / T::kWavesJ * T::TI + qi * T::kSquare;
 #pragma unroll 1
-    for (int r = lane >> 3; r < 64; r += 8) {
+    for (int r = lane >> 3; r < T::kSquare; r += 8) {
       if (o0 + r >= a.out || n <= 0) break;
       const int64_t at = (int64_t)(o0 + r) * a.in + j;
       float v[kChunk], old[kChunk];
@@ -324,7 +325,7 @@ struct Pipe {
   }
   // Fragment f of 8 tokens a lane.  Its pieces lie at the first one's place ^ 32
   // f: those bits of the piece's number are zero in the first (a wave's columns
-  // begin at a multiple of 64 or 128).
+  // begin at a multiple of 32, 64 or 128).
   template <int COLS>
   __device__ __forceinline__ s16x8 read(const char* __restrict buf, int first, int f) const {
     const ZF_LDS char* at = (const ZF_LDS char*)buf + (first ^ (f * 32));
@@ -380,7 +381,8 @@ __device__ __forceinline__ void stage(Pipe<T, DT, DIRECT>& o, const char* __rest
 #pragma unroll
     for (int j = 0; j < T::FJ; ++j) acc[i][j] = mma<DT>(q[j], p[i], acc[i][j]);
     p[i] = o.template read<T::BM>(next, rp, i);
-    if (i < T::FJ) q_next[i] = o.template read<T::BN>(next, rq, i);
+#pragma unroll
+    for (int j = i; j < T::FJ; j += T::FI) q_next[j] = o.template read<T::BN>(next, rq, j);
   }
   o.put(fill, held);
   o.fetch(held);
@@ -392,7 +394,8 @@ __device__ __forceinline__ void stage(Pipe<T, DT, DIRECT>& o, const char* __rest
     for (int i = 0; i < T::FI; ++i) {
       __builtin_amdgcn_sched_group_barrier(0x8, T::FJ, 0);
       __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-      if (i < T::FJ) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+#pragma unroll
+      for (int j = i; j < T::FJ; j += T::FI) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
       if (i >= T::FI - 2) __builtin_amdgcn_sched_group_barrier(0x2, 6, 0);
     }
     __builtin_amdgcn_sched_group_barrier(0x200, 2, 0);
@@ -481,8 +484,9 @@ __global__ __launch_bounds__(kThreads) void zf_weight_grad_join(JoinArgs a) {
   }
 }
 
+enum Form { kBig, kMiddle, kLittle };
 struct Plan {
-  bool big;
+  Form form;
   int32_t splits;
   int64_t split_rows;
 };
@@ -506,17 +510,26 @@ int plan(int64_t rows, int64_t out, int64_t in, bool whole, Plan& g) {
   int rc = shape_ok(rows, in);
   if (rc == ZF_OK) rc = shape_ok(0, out);
   if (rc != ZF_OK) return rc;
-  auto tiles_of = [&](int64_t side) { return ((out + side - 1) / side) * ((in + side - 1) / side); };
-  const int64_t middle = tiles_of(Middle::BM), big = tiles_of(Big::BM);
+  auto tiles_of = [&](int64_t bm, int64_t bn) { return ((out + bm - 1) / bm) * ((in + bn - 1) / bn); };
+  const int64_t big = tiles_of(Big::BM, Big::BN), middle = tiles_of(Middle::BM, Middle::BN);
+  const int64_t little = tiles_of(Little::BM, Little::BN);
   if (middle > kMaxBlocks) return ZF_ESIZE;
-  // A compute unit holds one block of 256 x 256 or two of 128 x 128.  8192
-  // tokens of 2048 x 2048: 84 us in large tiles, 89 in small ones; 16384 of 1024 x
-  // 1024: 56 and 52.  Parts of 1024 tokens at least (4096 of 1024 x 1024: parts of
-  // 512 30.8 us, of 1024 29.9, of 4096 50); without whole pieces a stage takes
-  // longer, and 256 are enough (1000 tokens of 128 x 40: 13 us, in one part 27).
-  const int64_t sb = splits_of(rows, big, 256, 1024), sm = splits_of(rows, middle, 512, whole ? 1024 : 256);
-  g.big = whole && cost(rows, out * in, big, sb, 256, 0.92, 10) < cost(rows, out * in, middle, sm, 512, 0.57, 5);
-  const int64_t stages = (rows + kDepth - 1) / kDepth, splits = g.big ? sb : sm;
+  // A compute unit holds one block of 256 x 256 or two of 128 x 128; blocks of 64 x
+  // 128 are best alone.  8192 tokens of 2048 x 2048: 84 us in large tiles, 89 in
+  // middle ones; 16384 of 1024 x 1024: 56, 52 and 73 in little ones; 333 of 776 x
+  // 1008: 9.8 in middle ones, 7.3 in little ones, and 333 of 777 x 1000 12.6 and 9.2.
+  // Middle tiles have parts of 1024 tokens at least (4096 of 1024 x 1024: parts of
+  // 512 30.8 us, of 1024 29.9, of 4096 50), little ones of 512 (2048 of 512 x 512:
+  // 12.4, parts of 1024 15.0); without whole pieces a stage takes longer, and 256
+  // are enough (1000 tokens of 128 x 40 in little tiles: 11.1 us, of 512 15.9).
+  const int64_t sb = splits_of(rows, big, 256, 1024), sm = splits_of(rows, middle, 512, whole ? 1024 : 256),
+                sl = splits_of(rows, little, 256, whole ? 512 : 256);
+  const double cb = cost(rows, out * in, big, sb, 256, 0.92, 10),
+               cm = cost(rows, out * in, middle, sm, 512, 0.57, 5),
+               cl = cost(rows, out * in, little, sl, 256, 0.30, 3.5);
+  g.form = cl < cm ? kLittle : kMiddle;
+  if (whole && cb < std::min(cl, cm)) g.form = kBig;
+  const int64_t stages = (rows + kDepth - 1) / kDepth, splits = g.form == kBig ? sb : g.form == kMiddle ? sm : sl;
   const int64_t per = std::max<int64_t>((stages + splits - 1) / splits, 1);
   g.split_rows = per * kDepth;
   g.splits = (int32_t)std::max<int64_t>((stages + per - 1) / per, 1);
@@ -593,9 +606,9 @@ extern "C" int zf_weight_grad(const zf_weight_grad_args* args, void* stream) {
   a.partial = g.splits > 1 ? static_cast<float*>(p.workspace) : nullptr;
   hipStream_t s = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();
-  if (!whole) launch<Middle, false>(a, p.dtype, s);
-  else if (g.big) launch<Big, true>(a, p.dtype, s);
-  else launch<Middle, true>(a, p.dtype, s);
+  if (g.form == kBig) launch<Big, true>(a, p.dtype, s);
+  else if (g.form == kMiddle) whole ? launch<Middle, true>(a, p.dtype, s) : launch<Middle, false>(a, p.dtype, s);
+  else whole ? launch<Little, true>(a, p.dtype, s) : launch<Little, false>(a, p.dtype, s);
   if (g.splits > 1) {
     const JoinArgs j{a.partial, p.grad, p.out_features * p.in_features, g.splits, p.grad_dtype,
                      p.accumulate};

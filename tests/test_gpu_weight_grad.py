@@ -73,6 +73,22 @@ def test_whole_numbers_are_exact(zf, dtype):
         assert torch.equal(grad.double(), dy.double().t().contiguous() @ x.double())
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("rows,outs,ins", [(40, 2056, 2320), (70, 2049, 2051), (1, 2200, 2000), (600, 2100, 2064),
+                                           (8200, 1104, 1200), (8200, 1101, 1201), (6200, 2056, 2064), (6200, 2049, 2062)])
+def test_whole_numbers_are_exact_in_large_tiles(zf, dtype, rows, outs, ins):
+    """Sizes that larger tiles take, with and without whole pieces and with tokens split over blocks: sums stay below
+    2^24, so every place holds the exact number."""
+    g = R.generator(10)
+    x = torch.randint(-8, 9, (rows, ins), generator=g, device="cuda").to(dtype)
+    dy = torch.randint(-8, 9, (rows, outs), generator=g, device="cuda").to(dtype)
+    grad = torch.ones(outs, ins, device="cuda")
+    ws = R.bytes_buffer(max(1, zf.weight_grad_bytes(rows, outs, ins)))
+    zf.weight_grad(dy, R.kept(zf, x), grad, ws, accumulate=True)
+    want = dy.float().t().contiguous().double() @ x.double() + 1
+    assert torch.equal(grad.double(), want)
+
+
 def test_scales_far_apart(zf):
     """Groups whose scales differ by many powers of two, tiny and huge ones among them."""
     g = R.generator(10)
