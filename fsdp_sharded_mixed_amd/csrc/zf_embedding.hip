@@ -47,9 +47,10 @@ struct LookupArgs {
   int32_t wide, log_lanes;
 };
 
-// A group of lanes takes kRows tokens at a time, all their rows on their way
-// together.
-constexpr int kRows = 4;
+// A group of lanes takes kTogether tokens at a time, their rows on their way
+// together.  32768 tokens of 2048 bf16 columns: one at a time 31.4 us, two 31.5,
+// four 32.6; 8192 of 4096 fp32 columns, all different: 52.8, 50.7 and 49.2.
+constexpr int kTogether = 2;
 template <int TDT, int DT, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void zf_embedding_kernel(LookupArgs a) {
   const int lanes = 1 << a.log_lanes, per = kThreads >> a.log_lanes;
@@ -58,17 +59,17 @@ __global__ __launch_bounds__(kThreads) void zf_embedding_kernel(LookupArgs a) {
   if (n <= 0) return;
   const int64_t step = (int64_t)gridDim.x * per;
   int64_t t = (int64_t)blockIdx.x * per + (threadIdx.x >> a.log_lanes);
-  for (; t < a.tokens; t += step * kRows) {
-    Raw<TDT> r[kRows];
-    uint32_t v[kRows];
+  for (; t < a.tokens; t += step * kTogether) {
+    Raw<TDT> r[kTogether];
+    uint32_t v[kTogether];
 #pragma unroll
-    for (int u = 0; u < kRows; ++u)
+    for (int u = 0; u < kTogether; ++u)
       v[u] = t + u * step < a.tokens ? key_of(a.ids, a.wide, t + u * step, a.vocab) : a.vocab;
 #pragma unroll
-    for (int u = 0; u < kRows; ++u)
+    for (int u = 0; u < kTogether; ++u)
       r[u] = load_raw<TDT, false, WHOLE>(a.table, (int64_t)v[u] * a.cols + j, v[u] < a.vocab ? n : 0);
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) {
+    for (int u = 0; u < kTogether; ++u) {
       if (t + u * step >= a.tokens) break;
       float x[kChunk];
       widen8<TDT>(r[u], x);
@@ -529,7 +530,7 @@ extern "C" int zf_embedding(const zf_embedding_args* args, void* stream) {
   const bool whole = p.cols % kChunk == 0;
   // a block for each set of rows up to 2048 blocks, then several sets a block
   int64_t blocks = (p.tokens + per - 1) / per;
-  if (blocks > 2048) blocks = std::max<int64_t>(2048, (blocks + kRows - 1) / kRows);
+  if (blocks > 2048) blocks = std::max<int64_t>(2048, (blocks + kTogether - 1) / kTogether);
   const dim3 grid((uint32_t)std::min<int64_t>(blocks, kMaxBlocks), (uint32_t)((p.cols + span - 1) / span));
   hipStream_t s = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();
