@@ -65,6 +65,16 @@ __device__ __forceinline__ void widen_x(const RawX<DT, KEPT>& r, float (&x)[kChu
   else widen8<DT>(r.r, x);
 }
 
+// x to xh, and zeros past the row's n elements, where -mean rstd may be infinite.
+template <bool LAYER, bool WHOLE>
+__device__ __forceinline__ void normalize(float (&x)[kChunk], int n, float mean, float rstd) {
+#pragma unroll
+  for (int k = 0; k < kChunk; ++k) {
+    const float from = (WHOLE ? n > 0 : k < n) ? mean : 0.0f;
+    x[k] = (LAYER ? x[k] - from : x[k]) * rstd;
+  }
+}
+
 // A group of G lanes takes a row at a time, 8 V elements a lane; its parameters
 // and the columns' sums stay in registers, and the next row is on its way while
 // this one is worked on.  Rows of more than 512 elements take a block and its
@@ -72,8 +82,8 @@ __device__ __forceinline__ void widen_x(const RawX<DT, KEPT>& r, float (&x)[kChu
 // operands are 40 V registers beside the loads, and with V = 4 (2048 columns a
 // wave) they spill.  32768 rows of 2048 from a checkpoint: 70 us with V = 1,
 // 4.8 TB/s (two rows at a time 80, a wave a row 90).
-// Elements past the row's end have dy = 0 and add nothing (where rstd is not
-// finite, the row's own elements are not either).
+// Elements past the row's end have dy = 0 and xh = 0, so they add nothing (where
+// rstd is not finite, the row's own elements are not either).
 template <int DT, bool KEPT, bool LAYER, int T, int G, int V, bool WHOLE>
 __global__ __launch_bounds__(T) void zf_norm_grad_kernel(NormGradArgs a) {
   constexpr int N = LAYER ? 2 : 1;  // sums of a row: h xh, and h
@@ -118,16 +128,18 @@ __global__ __launch_bounds__(T) void zf_norm_grad_kernel(NormGradArgs a) {
 #pragma unroll
     for (int k = 0; k < N; ++k) sums[k] = 0;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+    for (int v = 0; v < V; ++v) {
+      const int n = a.cols - (v * G + lane) * kChunk;
+      normalize<LAYER, WHOLE>(xh[v], n, mean, rstd);
 #pragma unroll
       for (int k = 0; k < kChunk; ++k) {
-        xh[v][k] = (LAYER ? xh[v][k] - mean : xh[v][k]) * rstd;
         dw[v][k] = __builtin_fmaf(h[v][k], xh[v][k], dw[v][k]);
         db[v][k] += h[v][k];
         h[v][k] *= w[v][k];
         sums[0] = __builtin_fmaf(h[v][k], xh[v][k], sums[0]);
         if constexpr (LAYER) sums[N - 1] += h[v][k];
       }
+    }
     row_sums<G, T, N>(sums, slots, turn);
     const float c2 = sums[0] * a.inv_cols, c1 = LAYER ? sums[N - 1] * a.inv_cols : 0;
 #pragma unroll
@@ -188,11 +200,9 @@ __global__ __launch_bounds__(kThreads) void zf_norm_grad_long(NormGradArgs a) {
       load8<DT>(a.dy, i * a.dy_ld + j, n, h);
       widen_x<DT, KEPT>(load_x<DT, KEPT, false, false>(a, i, j, n), xh);
       load8_of(a.wdt, a.w, j, n, w);
+      normalize<LAYER, false>(xh, n, mean, rstd);
 #pragma unroll
-      for (int k = 0; k < kChunk; ++k) {
-        xh[k] = (LAYER ? xh[k] - mean : xh[k]) * rstd;
-        h[k] *= w[k];
-      }
+      for (int k = 0; k < kChunk; ++k) h[k] *= w[k];
     };
     for (int j = threadIdx.x * kChunk; j < a.cols; j += kSpan) {
       take(j, a.cols - j);
@@ -228,9 +238,10 @@ __global__ __launch_bounds__(kThreads) void zf_norm_grad_columns(NormGradArgs a)
     const float mean = LAYER ? a.mean[i] : 0;
     load8<DT>(a.dy, i * a.dy_ld + j, n, dy);
     widen_x<DT, KEPT>(load_x<DT, KEPT, false, false>(a, i, j, n), xh);
+    normalize<LAYER, false>(xh, n, mean, rstd);
 #pragma unroll
     for (int k = 0; k < kChunk; ++k) {
-      dw[k] += dy[k] * ((LAYER ? xh[k] - mean : xh[k]) * rstd);
+      dw[k] += dy[k] * xh[k];
       db[k] += dy[k];
     }
   }

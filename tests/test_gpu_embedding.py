@@ -115,6 +115,44 @@ def test_one_token_that_fills_a_long_batch(zf):
     check_grad(zf, ids, d, 300001, F32, False, 1.0)
 
 
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("kind", ["even", "often", "one", "none", "each", "runs"])
+@pytest.mark.parametrize("n,cols", [(1, 512), (7, 520), (8, 512), (9, 2048), (17, 1024), (100, 512), (1000, 2056),
+                                    (4096, 512), (4100, 1024), (8192, 2048), (9001, 2048)])
+def test_whole_numbers_in_rows_of_whole_waves(zf, accumulate, kind, n, cols):
+    """Small whole numbers, so that every sum is exact: the sums of runs that end anywhere in and behind their spans."""
+    g = R.generator(n + cols)
+    vocab = 700
+    d = torch.randint(-8, 9, (n, cols), generator=g, device="cuda").to(BF16)
+    if kind == "runs":  # run lengths 1, 2, .. 60, again and again, in a random order
+        lengths = torch.arange(n, device="cuda") % 60 + 1
+        ids = torch.arange(n, device="cuda").repeat_interleave(lengths)[:n] % vocab
+        ids = ids[torch.randperm(n, generator=g, device="cuda")]
+    else:
+        ids = some_ids(g, n, vocab, torch.int64, kind)
+    grad = torch.ones(vocab, cols, device="cuda")
+    zf.embedding_grad(d, ids, grad, R.bytes_buffer(zf.embedding_grad_bytes(n, vocab, cols)), scale=2.0,
+                      accumulate=accumulate)
+    fine = real(ids, vocab)
+    want = torch.zeros(vocab, cols, dtype=torch.float64, device="cuda").index_add_(0, ids[fine].long(), d[fine].double())
+    assert torch.equal(grad.double(), want * 2 + (1 if accumulate else 0))
+
+
+@pytest.mark.parametrize("n", [5, 5000])
+def test_a_vocabulary_of_many_rows(zf, n):
+    """2^27 and more rows of one element: what clears the gradient looks after 2^18 of them at a time, and the sort
+    takes four passes."""
+    vocab = (1 << 27) + 5
+    g = R.generator(n)
+    grad = torch.ones(vocab, 1, dtype=BF16, device="cuda")
+    ids = torch.randint(0, vocab, (n,), generator=g, device="cuda")
+    ids[0], ids[1] = vocab - 1, 0
+    d = torch.randint(1, 9, (n, 1), generator=g, device="cuda").to(BF16)
+    zf.embedding_grad(d, ids, grad, R.bytes_buffer(zf.embedding_grad_bytes(n, vocab, 1)))
+    want = torch.zeros(vocab, device="cuda").index_add_(0, ids, d[:, 0].float())
+    assert torch.equal(grad[:, 0], want.to(BF16))
+
+
 def test_the_same_call_gives_the_same_bits(zf):
     g = R.generator(8)
     d = R.normal(g, 12345, 130).to(BF16)

@@ -95,6 +95,29 @@ def test_forward(zf, kind, dtype, wdtype, bias, keep, rows, cols, gap, skew):
     check_forward(zf, kind, x, w, b, keep, None, gap, skew)
 
 
+@pytest.mark.parametrize("kept", [False, True])
+@pytest.mark.parametrize("cols", [3, 60, 64, 100, 520, 300, 1032, 2000, 2056, 4104, 4100, 9000, 9001, 16392, 17000])
+def test_a_mean_whose_product_with_rstd_no_number_holds(zf, kept, cols):
+    """x = mean = 2^120 in every element and rstd = 1000: x - mean is 0 and -mean * rstd is not finite, so lanes behind a
+    row's end may not take part.  dx = rstd (h - avg(h)), weight_grad = 0, bias_grad = the sum of dy."""
+    g = R.generator(cols)
+    rows = 9
+    x = torch.full((rows, cols), 2.0 ** 120, device="cuda")
+    mean, rstd = torch.full((rows,), 2.0 ** 120, device="cuda"), torch.full((rows,), 1000.0, device="cuda")
+    dy, w = R.filled(R.normal(g, rows, cols), F32), vector(g, cols, F32, 0, 1.0)
+    dx = R.buffer(rows, cols, F32)
+    dw, db = torch.empty(cols, device="cuda"), torch.empty(cols, device="cuda")
+    ws = R.bytes_buffer(zf.layer_norm_grad_bytes(rows, cols))
+    zf.layer_norm_grad(zf.NORM_LAYER, dy, R.kept(zf, x) if kept else x, w, mean, rstd, dx, dw, db, ws)
+    h = dy.double() * w.double()
+    want = 1000.0 * (h - h.mean(1, keepdim=True))
+    # h one rounding, its sum a chain, the mean and the difference one each, and the product
+    off = (depth(cols) + 3) * U * h.abs().mean(1, keepdim=True) + 3 * U * (h.abs() + h.mean(1, keepdim=True).abs())
+    R.assert_within(dx, want, 1000.0 * off * 1.01 + U * want.abs(), "dx")
+    assert bool((dw == 0).all())
+    R.assert_within(db, dy.double().sum(0), rows * U * dy.double().abs().sum(0), "bias_grad")
+
+
 @pytest.mark.parametrize("cols", [100, 2048, 6000, 20000])
 def test_a_mean_far_from_zero(zf, cols):
     """Rows around 1000 with unit deviation: the variance is that of the distances, not a difference of sums."""
