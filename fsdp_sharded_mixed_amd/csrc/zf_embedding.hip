@@ -13,6 +13,13 @@
 // written) once.  The sort moves 16 bytes a token and pass.  Where the
 // gradient is stored, the rows without tokens are cleared by blocks of the
 // first launch, beside the sort's first pass.
+//
+// 32768 tokens by word frequency, 2048 columns of bf16 added to an fp32 table of
+// 40960 rows (296 MB at least): 97 us, of which the runs' sums take 69, the sort
+// 22 in four launches (its passes wait for memory, with 32 blocks) and the join of
+// cut runs 10.  1000 tokens of 1024: 16.7 us, three launches of 4-6 each.  The
+// lookup of 32768 rows of 2048 from fp32: 46 us, 4.7 TB/s of what it cannot do
+// without; rows that come again are read again, from the caches.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

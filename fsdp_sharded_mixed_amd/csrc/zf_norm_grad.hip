@@ -8,6 +8,8 @@
 // groups in shared memory, and a second launch adds the blocks' sums in order.
 //
 // Bound by HBM: a row of dy and of x is read once and one of dx written once.
+// 32768 rows of 2048 bf16 from a checkpoint (338 MB): 64.7 us, of which the join
+// takes 5.9 and the pass 5.6 TB/s; 1000 rows of 1024: two launches of 6.0 and 4.8 us.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -80,8 +82,8 @@ __device__ __forceinline__ void normalize(float (&x)[kChunk], int n, float mean,
 // this one is worked on.  Rows of more than 512 elements take a block and its
 // barrier instead of a wave: parameters, two columns' sums and a row's
 // operands are 40 V registers beside the loads, and with V = 4 (2048 columns a
-// wave) they spill.  32768 rows of 2048 from a checkpoint: 70 us with V = 1,
-// 4.8 TB/s (two rows at a time 80, a wave a row 90).
+// wave) they spill.  32768 rows of 2048 from a checkpoint: 70 us with V = 1 (two
+// rows at a time 80, a wave a row 90; before later steps took it to 64.7).
 // Elements past the row's end have dy = 0 and xh = 0, so they add nothing (where
 // rstd is not finite, the row's own elements are not either).
 template <int DT, bool KEPT, bool LAYER, int T, int G, int V, bool WHOLE>
@@ -300,8 +302,8 @@ void by_grad_shape(int64_t cols, F f) {
 }
 
 // Blocks of the backward pass, each with a partial sum: 1024 threads for each
-// compute unit (32768 rows of 2048 from a checkpoint: 70 us; half or twice as
-// many threads 90 and 76), and 4 rows at least for each group of lanes.
+// compute unit (32768 rows of 2048 from a checkpoint, at the time 70 us; half or
+// twice as many threads 90 and 76), and 4 rows at least for each group of lanes.
 int grad_blocks(int64_t rows, int64_t cols) {
   int64_t per = 4, most = 1024;
   if (cols <= kMostCols)
