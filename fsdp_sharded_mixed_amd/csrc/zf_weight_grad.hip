@@ -171,14 +171,17 @@ struct Place {
   }
 };
 
-// Where a matrix's next stage lies: the address of its first row in this tile's
-// columns, and the rows that are left.  Loads past the matrix's end give zeros
-// (in shared memory too), so tokens behind the last one add nothing; loads past
-// a row's end give elements of columns that are not written.
+// Where a matrix's next kStages stages lie: the address of their first row in this
+// tile's columns, and the rows that are left.  Loads past the matrix's end give
+// zeros (in shared memory too), so tokens behind the last one add nothing; loads
+// past a row's end give elements of columns that are not written.  A turn of
+// kStages has one buffer, so that a stage computes no addresses: with one for
+// each stage, its scalar arithmetic is a third of a small tile's instructions.
 struct Walk {
   const char* at;
   int64_t ld;          // bytes of a stride
   int32_t left, tail;  // rows; bytes of a row from here on
+  uint32_t n;          // bytes of the turn's buffer
 
   __device__ __forceinline__ Walk(const void* base, int64_t row, int64_t rows, int64_t row_bytes, int64_t skip,
                                   int64_t width) {
@@ -186,21 +189,19 @@ struct Walk {
     left = (int32_t)rows;
     ld = row_bytes;
     tail = (int32_t)(width - skip);
+    n = extent();
   }
-  // A stage's buffer.  128 rows are as good as more: it has 32, and its tile's
-  // columns reach 32 further rows at most past the rows' ends.  All of it is 32-bit
-  // scalar arithmetic without branches, which would part the
-  // stage's instructions.
   __device__ __forceinline__ uint32_t extent() const {
-    const int32_t rows = min(left, 128);
+    const int32_t rows = min(left, kStages * kDepth);
     return rows > 0 ? (uint32_t)(rows - 1) * (uint32_t)ld + (uint32_t)tail : 0u;
   }
-  __device__ __forceinline__ Rsrc buffer(uint32_t n) const {
+  __device__ __forceinline__ Rsrc buffer() const {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(at), 0, n, 0x00020000);
   }
-  __device__ __forceinline__ void next() {
-    at += kDepth * ld;
-    left -= kDepth;
+  __device__ __forceinline__ void turn() {
+    at += kStages * kDepth * ld;
+    left -= kStages * kDepth;
+    n = extent();
   }
 };
 // An offset that all lanes share, clamped: the hardware compares a lane's own
@@ -269,24 +270,30 @@ struct Pipe {
     rq = kPBytes + place<T::BN / 8>(frow, wj / 8 + half) + (l & 1) * 8;
   }
 
-  // gradients of the next stage into `buf`
-  __device__ __forceinline__ void fetch_p(char* __restrict buf) {
+  // the turn's next kStages stages
+  __device__ __forceinline__ void turn() {
+    if constexpr (DIRECT) {
+      p.turn();
+      q.turn();
+      s.turn();
+    }
+  }
+  // gradients of the turn's stage e into `buf`
+  __device__ __forceinline__ void fetch_p(char* __restrict buf, int e) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const uint32_t n = p.extent();
-    const Rsrc from = p.buffer(n);
+    const Rsrc from = p.buffer();
     ZF_LDS char* to = (ZF_LDS char*)buf + wave * 1024;
 #pragma unroll
     for (int h = 0; h < kPLoads; ++h)
-      to_shared(from, to + h * T::kThreads * 16, vp, within(h * kPRows * (uint32_t)p.ld, n));
-    p.next();
+      to_shared(from, to + h * T::kThreads * 16, vp, within((e * kDepth + h * kPRows) * (uint32_t)p.ld, p.n));
   }
-  // codes (!DIRECT: and gradients) of the next stage into registers
-  __device__ __forceinline__ void fetch(Held& r) {
+  // codes of the turn's stage e (!DIRECT: codes and gradients of the next stage)
+  // into registers
+  __device__ __forceinline__ void fetch(Held& r, int e) {
     if constexpr (DIRECT) {
-      r.c = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(q.buffer(q.extent()), vq, 0, 0));
-      r.scale = __builtin_amdgcn_raw_buffer_load_b8(s.buffer(s.extent()), vs, 0, 0);
-      q.next();
-      s.next();
+      r.c = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+          q.buffer(), vq, within(e * kDepth * (uint32_t)q.ld, q.n), 0));
+      r.scale = __builtin_amdgcn_raw_buffer_load_b8(s.buffer(), vs, within(e * kDepth * (uint32_t)s.ld, s.n), 0);
     } else {
       // A piece that ends past its row holds the next row's first elements, for
       // columns that are not written; only one that ends past the matrix is
@@ -363,7 +370,7 @@ __device__ __forceinline__ void arrive() {
   asm volatile("" ::: "memory");
 }
 
-// Stage k, whose fragments p and q are in registers: its products, while the
+// Stage k = e (mod kStages), whose fragments p and q are in registers: its products, while the
 // next stage's fragments are read from `next`, the codes of stage k + 2 are
 // written to `fill` and the gradients of stage k + 4 are on their way to the
 // buffer `left` that stage k has left (!DIRECT: gradients go as the codes do).
@@ -372,7 +379,7 @@ template <typename T, int DT, bool DIRECT>
 __device__ __forceinline__ void stage(Pipe<T, DT, DIRECT>& o, const char* __restrict next, char* __restrict fill,
                                       char* __restrict left, s16x8 (&p)[T::FI], const s16x8 (&q)[T::FJ],
                                       s16x8 (&q_next)[T::FJ], typename Pipe<T, DT, DIRECT>::Held& held,
-                                      f32x4 (&acc)[T::FI][T::FJ]) {
+                                      f32x4 (&acc)[T::FI][T::FJ], int e) {
   typedef Pipe<T, DT, DIRECT> P;
   // stage k + 1 is complete: its gradients were followed by the codes of the
   // same stage and by all loads of two more
@@ -383,7 +390,7 @@ __device__ __forceinline__ void stage(Pipe<T, DT, DIRECT>& o, const char* __rest
   int rp = o.rp, rq = o.rq;
   asm volatile("" : "+v"(rp), "+v"(rq));
   if constexpr (DIRECT) {
-    o.fetch_p(left);
+    o.fetch_p(left, e);
     loads_in_order();
   }
 #pragma unroll
@@ -395,7 +402,7 @@ __device__ __forceinline__ void stage(Pipe<T, DT, DIRECT>& o, const char* __rest
     for (int j = i; j < T::FJ; j += T::FI) q_next[j] = o.template read<T::BN>(next, rq, j);
   }
   o.put(fill, held);
-  o.fetch(held);
+  o.fetch(held, e);
   if constexpr (DIRECT) {
     // the order: gradients' loads; a row of products and the reads that may
     // follow it, again and again; the codes' conversion with the last rows
@@ -431,21 +438,21 @@ __global__ __launch_bounds__(T::kThreads, 2) void zf_weight_grad_kernel(GradArgs
   typename P::Held h0, h1;
   s16x8 p[T::FI], qa[T::FJ], qb[T::FJ];
   if constexpr (DIRECT) {
-    o.fetch_p(s0);
-    o.fetch_p(s1);
+    o.fetch_p(s0, 0);
+    o.fetch_p(s1, 1);
   }
-  o.fetch(h0);
-  o.fetch(h1);
+  o.fetch(h0, 0);
+  o.fetch(h1, 1);
   o.put(s0, h0);
   o.put(s1, h1);
   arrive<0>();
-  if constexpr (DIRECT) o.fetch_p(s2);
+  if constexpr (DIRECT) o.fetch_p(s2, 2);
   loads_in_order();
-  o.fetch(h0);
+  o.fetch(h0, 2);
   loads_in_order();
-  if constexpr (DIRECT) o.fetch_p(s3);
+  if constexpr (DIRECT) o.fetch_p(s3, 3);
   loads_in_order();
-  o.fetch(h1);
+  o.fetch(h1, 3);
   loads_in_order();
 #pragma unroll
   for (int i = 0; i < T::FI; ++i) p[i] = o.template read<T::BM>(s0, o.rp, i);
@@ -454,10 +461,11 @@ __global__ __launch_bounds__(T::kThreads, 2) void zf_weight_grad_kernel(GradArgs
   // stages past the last one are zeros
 #pragma unroll 1
   for (int k = 0; k < stages; k += kStages) {
-    stage<T, DT>(o, s1, s2, s0, p, qa, qb, h0, acc);
-    stage<T, DT>(o, s2, s3, s1, p, qb, qa, h1, acc);
-    stage<T, DT>(o, s3, s0, s2, p, qa, qb, h0, acc);
-    stage<T, DT>(o, s0, s1, s3, p, qb, qa, h1, acc);
+    o.turn();
+    stage<T, DT>(o, s1, s2, s0, p, qa, qb, h0, acc, 0);
+    stage<T, DT>(o, s2, s3, s1, p, qb, qa, h1, acc, 1);
+    stage<T, DT>(o, s3, s0, s2, p, qa, qb, h0, acc, 2);
+    stage<T, DT>(o, s0, s1, s3, p, qb, qa, h1, acc, 3);
   }
   arrive<0>();
   write_tile<T>(a, acc, shared, i0, j0, split);
