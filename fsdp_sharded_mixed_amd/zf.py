@@ -846,14 +846,15 @@ def embedding_grad(dout, ids, grad, workspace, scale=1.0, accumulate=False, stre
 @dataclass
 class Act8:
     """An activation checkpoint in 8 bits: its buffers and their C record.
-    Holds the tensors, so the addresses stay good."""
+    Holds the tensors, so the addresses stay good.  (The record's pointer is
+    made once: that takes longer than the rest of a call's look at it.)"""
     struct: Act8Struct
     codes: object
     scales: object
 
-    @property
-    def shape(self):
-        return self.struct.rows, self.struct.cols
+    def __post_init__(self):
+        self.shape = self.struct.rows, self.struct.cols
+        self.pointer = C.pointer(self.struct)
 
 
 def act8(codes, scales):
@@ -897,7 +898,7 @@ def _kept(where, a, rows, cols):
         return None
     if a.shape != (rows, cols):
         raise ValueError(f"{where}: a checkpoint of {rows} x {cols} was expected, got {a.shape}")
-    return C.pointer(a.struct)
+    return a.pointer
 
 
 def _statistics(where, kind, rows, mean, rstd):
