@@ -480,7 +480,10 @@ GradPlan grad_plan(int64_t tokens, int64_t vocab, int64_t cols) {
   g.bits = (width + g.passes - 1) / g.passes;
   g.items = (int32_t)(std::max<int64_t>(1, (tokens + (1 << 20) - 1) >> 20) * kSortThreads);
   g.blocks = (int32_t)((tokens + g.items - 1) / g.items);
-  // spans of 16 tokens, of 8 where those would be under 2048 waves
+  // Spans of 16 tokens, of 8 where those would be under 2048 waves (16384 tokens of
+  // 1024 columns: 46.5 us, in spans of 8 48.7).  Spans of 24: 98 us become 92 for
+  // 32768 tokens of 2048 columns with ids even over their logarithm, but 129 become
+  // 133 for even ids, and 97 become 104 for shuffled ids by word frequency.
   const int log = log_lanes_of(cols);
   const int64_t waves = std::max<int64_t>(1, ((int64_t)1 << log) / 64);
   g.length = kLongest;

@@ -118,7 +118,7 @@ def test_one_token_that_fills_a_long_batch(zf):
 @pytest.mark.parametrize("accumulate", [False, True])
 @pytest.mark.parametrize("kind", ["even", "often", "one", "none", "each", "runs"])
 @pytest.mark.parametrize("n,cols", [(1, 512), (7, 520), (8, 512), (9, 2048), (17, 1024), (100, 512), (1000, 2056),
-                                    (4096, 512), (4100, 1024), (8192, 2048), (9001, 2048)])
+                                    (4096, 512), (4100, 1024), (8192, 2048), (9001, 2048), (12288, 2048), (16385, 2048)])
 def test_whole_numbers_in_rows_of_whole_waves(zf, accumulate, kind, n, cols):
     """Small whole numbers, so that every sum is exact: the sums of runs that end anywhere in and behind their spans."""
     g = R.generator(n + cols)
