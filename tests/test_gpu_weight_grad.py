@@ -89,6 +89,20 @@ def test_whole_numbers_are_exact_in_large_tiles(zf, dtype, rows, outs, ins):
     assert torch.equal(grad.double(), want)
 
 
+@pytest.mark.parametrize("gap,skew", [(0, 0), (1, 1), (5, 3)])
+@pytest.mark.parametrize("rows,outs,ins", [(700, 1, 1), (3000, 5, 3), (5001, 63, 127), (5001, 64, 128), (2500, 65, 129),
+                                           (1025, 129, 500), (2500, 2051, 2053)])
+def test_whole_numbers_are_exact_in_odd_rows(zf, rows, outs, ins, gap, skew):
+    """Rows shorter and longer than a tile, at any alignment: pieces that end past their row, and past the matrix."""
+    g = R.generator(11)
+    x = torch.randint(-8, 9, (rows, ins), generator=g, device="cuda").to(F16)
+    dy = R.filled(torch.randint(-8, 9, (rows, outs), generator=g, device="cuda"), F16, gap, skew, "dy")
+    grad = torch.empty(outs, ins, device="cuda")
+    ws = R.bytes_buffer(max(1, zf.weight_grad_bytes(rows, outs, ins)))
+    zf.weight_grad(dy, R.kept(zf, x, gap, skew), grad, ws)
+    assert torch.equal(grad.double(), dy.float().t().contiguous().double() @ x.double())
+
+
 def test_scales_far_apart(zf):
     """Groups whose scales differ by many powers of two, tiny and huge ones among them."""
     g = R.generator(10)
