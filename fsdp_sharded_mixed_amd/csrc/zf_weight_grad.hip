@@ -13,12 +13,12 @@
 // results a second launch adds in order.
 //
 // Bound by the matrix cores where the result is large: 16384 tokens, 8192 x 2048,
-// bf16 added to fp32: 470 us, 1170 TFLOP/s (the library's product of the same
+// bf16 added to fp32: 448 us, 1228 TFLOP/s (the library's product of the same
 // operands in bf16, without their decoding, 556 us; its best, 8192^3, 1228
-// TFLOP/s).  Where it is small, by what a stage costs beside its products: a
-// barrier, addresses and conversions take 0.3 us a stage and block, with one wave a
-// SIMD 700 cycles for 128 of products.  16384 tokens, 256 x 1024: 24.7 us, the join
-// 4.3 of them (the library's 100); 333 tokens, 777 x 1000: 9.1.
+// TFLOP/s).  Where it is small, by a stage's instructions, of which one wave a SIMD
+// issues one in four cycles: 0.28 us a stage and block, for 128 cycles of products.
+// 16384 tokens, 256 x 1024: 23.5 us, the join 4.1 of them (the library's 100); 333
+// tokens, 777 x 1000: 8.6.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
