@@ -843,7 +843,8 @@ int64_t zf_weight_grad_bytes(int64_t rows, int64_t out_features, int64_t in_feat
  *   grad[o][i] = sum over rows t of dy[t][o] * x8[t][i],
  * on the matrix cores, with x8's numbers in dy's type (exact for a checkpoint
  * stored from that type, and always for ZF_BF16), products exact and sums in
- * binary32.  out_features and in_features are at most ZF_MAX_COLS. */
+ * binary32.  out_features and in_features are at most ZF_MAX_COLS, and the
+ * gradient's tiles of 128 x 128 at most 2^22 (ZF_ESIZE). */
 int zf_weight_grad(const zf_weight_grad_args* args, void* stream);
 
 /* Text for a status code (static storage). */
