@@ -842,8 +842,9 @@ int64_t zf_weight_grad_bytes(int64_t rows, int64_t out_features, int64_t in_feat
 /* Weight gradient of a Linear whose input was kept as a checkpoint:
  *   grad[o][i] = sum over rows t of dy[t][o] * x8[t][i],
  * on the matrix cores, with x8's numbers in dy's type (exact for a checkpoint
- * stored from that type, and always for ZF_BF16), products exact and sums in
- * binary32.  out_features and in_features are at most ZF_MAX_COLS, and the
+ * stored from that type, and always for ZF_BF16; from another type to ZF_F16
+ * rounded to nearest even, past its largest number an infinity), products exact
+ * and sums in binary32.  out_features and in_features are at most ZF_MAX_COLS, and the
  * gradient's tiles of 128 x 128 at most 2^22 (ZF_ESIZE). */
 int zf_weight_grad(const zf_weight_grad_args* args, void* stream);
 
