@@ -352,7 +352,7 @@ inline int rows_ok(const void* p, int32_t dt, int64_t rows, int64_t cols, int64_
   if (rows > 1 && stride < cols) return ZF_EINVAL;
   if (rows > 0 && !p) return ZF_EINVAL;
   if (!aligned_to(p, dt)) return ZF_EALIGN;
-  if (rows > 1 && stride > (int64_t)1 << 31) return ZF_ESIZE;
+  if (rows > 1 && stride > ZF_MAX_STRIDE) return ZF_ESIZE;
   return ZF_OK;
 }
 inline int act8_ok(const zf_act8* a, int64_t rows, int64_t cols) {
@@ -360,8 +360,7 @@ inline int act8_ok(const zf_act8* a, int64_t rows, int64_t cols) {
   const int64_t groups = (cols + ZF_ACT8_GROUP - 1) / ZF_ACT8_GROUP;
   if (rows > 0 && (!a->codes || !a->scales)) return ZF_EINVAL;
   if (rows > 1 && (a->code_stride < cols || a->scale_stride < groups)) return ZF_EINVAL;
-  if (rows > 1 && (a->code_stride > (int64_t)1 << 31 || a->scale_stride > (int64_t)1 << 31))
-    return ZF_ESIZE;
+  if (rows > 1 && (a->code_stride > ZF_MAX_STRIDE || a->scale_stride > ZF_MAX_STRIDE)) return ZF_ESIZE;
   return ZF_OK;
 }
 inline Act8 act8_of(const zf_act8* a) {

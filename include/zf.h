@@ -692,9 +692,10 @@ int zf_muon_step(const zf_muon* muon, const zf_hparams* hp, const zf_muon_hparam
  * flag that is not 0 or 1), ZF_EDTYPE, ZF_EALIGN (a pointer that is not
  * aligned to its element size, or a workspace to 16 bytes), ZF_ESIZE (rows or
  * tokens above ZF_MAX_ROWS, cols above ZF_MAX_COLS, a vocabulary above
- * ZF_MAX_ROWS, a workspace too small), ZF_EHIP. */
+ * ZF_MAX_ROWS, a stride above ZF_MAX_STRIDE, a workspace too small), ZF_EHIP. */
 #define ZF_MAX_ROWS ((1ll << 30))
 #define ZF_MAX_COLS ((1ll << 20))
+#define ZF_MAX_STRIDE ((1ll << 31))  /* elements from a row to the next */
 
 typedef struct {
   int32_t table_dtype;   /* of the table */
