@@ -583,12 +583,14 @@ int64_t partial_bytes(const Plan& g, int64_t out, int64_t in) {
   return g.splits > 1 ? (g.splits * out * in * 4 + 15) / 16 * 16 : 0;
 }
 
-// Whole 16-byte pieces at 16-byte alignment, and 64 rows within an offset of
-// 31 bits.
+// Whole 16-byte pieces at 16-byte alignment, and a turn's rows within an offset of
+// 31 bits: a turn's buffer is kStages * kDepth - 1 strides and a row long, and a row
+// is no longer than its stride.
+constexpr int64_t kTurnStride = ((int64_t)1 << 31) / (kStages * kDepth);  // bytes
 bool whole_pieces(const GradArgs& a) {
   const uintptr_t at = reinterpret_cast<uintptr_t>(a.dy) | reinterpret_cast<uintptr_t>(a.x.codes);
   return (at & 15) == 0 && ((a.dy_ld | a.out) & 7) == 0 && ((a.x.code_ld | a.in) & 15) == 0 &&
-         a.dy_ld < 1 << 23 && a.x.code_ld < 1 << 24 && a.x.scale_ld < 1 << 24;
+         a.dy_ld * 2 < kTurnStride && a.x.code_ld < kTurnStride && a.x.scale_ld < kTurnStride;
 }
 
 template <typename T, bool DIRECT>

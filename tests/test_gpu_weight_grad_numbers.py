@@ -67,3 +67,29 @@ def test_every_gradient(zf, dtype, scale):
     grad = one_token(zf, codes.to(torch.uint8), scales.to(torch.uint8), dy, 0)
     want = (dy.double().t() * 2.0 ** (scale - 127)).expand(65536, 40)
     same(grad, want.float())
+
+
+def whole(g, rows, cols, dtype, stride):
+    """Whole numbers from -8 to 8 in rows that lie `stride` elements apart, the elements between them never written."""
+    full = torch.empty((rows - 1) * stride + cols, dtype=dtype, device="cuda")
+    t = torch.as_strided(full, (rows, cols), (stride, 1))
+    return t.copy_(torch.randint(-8, 9, (rows, cols), generator=g, device="cuda"))
+
+
+@pytest.mark.parametrize("dy_bytes,code_bytes", [(0, 0), (-16, 0), (0, -16), (-16, -16)])
+def test_the_longest_strides_of_whole_pieces(zf, dy_bytes, code_bytes):
+    """Rows of gradients and of codes 2^24 bytes apart, and 16 bytes less: 128 of the latter fit an offset of 31 bits,
+    so they go straight to shared memory, and the former through registers."""
+    g = R.generator(20)
+    rows, outs, ins = 161, 200, 272
+    dy = whole(g, rows, outs, BF16, (2 ** 24 + dy_bytes) // 2)
+    x = whole(g, rows, ins, BF16, ins)
+    codes, scales = R.keep(x)
+    far = torch.as_strided(torch.empty((rows - 1) * (2 ** 24 + code_bytes) + ins, dtype=torch.uint8, device="cuda"),
+                           (rows, ins), (2 ** 24 + code_bytes, 1)).copy_(codes)
+    grad = R.buffer(outs, ins, F32, what="grad")
+    zf.weight_grad(dy, zf.act8(far, scales), grad, R.bytes_buffer(max(1, zf.weight_grad_bytes(rows, outs, ins))))
+    assert torch.equal(grad.double(), dy.double().t().contiguous() @ x.double())
+    del dy, far
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
