@@ -91,12 +91,13 @@ __global__ __launch_bounds__(kThreads) void zf_embedding_kernel(LookupArgs a) {
 // Sort of the tokens by id: by 9 bits or fewer a pass, from the lowest.  Up to
 // 4096 tokens are sorted by one block in shared memory, all passes in one launch.
 // For more, a block takes 1024 consecutive tokens (more where that would be
-// over 1024 blocks), a wave consecutive parts of them; a pass needs how many of
+// over kSortBlocks blocks), a wave consecutive parts of them; a pass needs how many of
 // each digit every block holds, which a launch of its own counts (counted while
 // the pass before writes, by atomics: 6 us more for 32768 tokens, since many
 // tokens are the same, and 3 less for the launch).
 
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
+constexpr int kSortBlocks = 1024;
 constexpr int kBins = 512;
 constexpr int kSmall = 4096;
 
@@ -469,7 +470,7 @@ int log_lanes_of(int64_t cols) {
 struct GradPlan {
   int32_t blocks, items, bits, passes, length;
   int64_t spans, clear_blocks, clear_rows;
-  int64_t keys, places, counts, cut, partial, bytes;  // offsets
+  int64_t keys, places, counts, cut, partial, bytes;  // offsets; enough for fewer tokens too
 };
 
 GradPlan grad_plan(int64_t tokens, int64_t vocab, int64_t cols) {
@@ -478,7 +479,8 @@ GradPlan grad_plan(int64_t tokens, int64_t vocab, int64_t cols) {
   while (vocab >> width) ++width;
   g.passes = (width + 8) / 9;
   g.bits = (width + g.passes - 1) / g.passes;
-  g.items = (int32_t)(std::max<int64_t>(1, (tokens + (1 << 20) - 1) >> 20) * kSortThreads);
+  const int64_t all = (int64_t)kSortBlocks * kSortThreads;
+  g.items = (int32_t)(std::max<int64_t>(1, (tokens + all - 1) / all) * kSortThreads);
   g.blocks = (int32_t)((tokens + g.items - 1) / g.items);
   // Spans of 16 tokens, of 8 where those would be under 2048 waves (16384 tokens of
   // 1024 columns: 46.5 us, in spans of 8 48.7).  Spans of 24: 98 us become 92 for
@@ -486,9 +488,11 @@ GradPlan grad_plan(int64_t tokens, int64_t vocab, int64_t cols) {
   // 133 for even ids, and 97 become 104 for shuffled ids by word frequency.
   const int log = log_lanes_of(cols);
   const int64_t waves = std::max<int64_t>(1, ((int64_t)1 << log) / 64);
+  const int64_t short_spans = (2048 + waves - 1) / waves * (kLongest / 8);  // the most of 8 tokens
   g.length = kLongest;
   if (tokens / g.length * waves < 2048) g.length = 8;
   g.spans = (tokens + g.length - 1) / g.length;
+  const int64_t most_spans = g.length == 8 ? g.spans : std::max(g.spans, short_spans);
   // up to 512 clearing blocks, of 16384 elements and more, with a bit of shared
   // memory a row (32 KiB at most)
   g.clear_blocks = std::max<int64_t>(1, std::min<int64_t>(512, vocab * cols >> 14));
@@ -502,9 +506,10 @@ GradPlan grad_plan(int64_t tokens, int64_t vocab, int64_t cols) {
   g.bytes = 0;
   g.keys = place(tokens * 8);
   g.places = place(tokens * 8);
-  g.counts = place(tokens > kSmall ? (int64_t)g.blocks * 4 << g.bits : 0);
-  g.cut = place(tokens > 0 ? (1 + g.spans) * 4 : 0);
-  g.partial = place(g.spans > 1 ? g.spans * 2 * cols * 4 : 0);
+  const int64_t most_blocks = std::min<int64_t>((tokens + kSortThreads - 1) / kSortThreads, kSortBlocks);
+  g.counts = place(tokens > kSmall ? most_blocks * 4 << g.bits : 0);
+  g.cut = place(tokens > 0 ? (1 + most_spans) * 4 : 0);
+  g.partial = place(most_spans > 1 ? most_spans * 2 * cols * 4 : 0);
   return g;
 }
 

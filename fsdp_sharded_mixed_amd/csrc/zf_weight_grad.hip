@@ -533,6 +533,7 @@ struct Plan {
   Form form;
   int32_t splits;
   int64_t split_rows;
+  int64_t most_splits;  // of any form, for as many tokens or fewer
 };
 
 // The tokens are split where a form's tiles leave places of the GPU free, into
@@ -576,11 +577,12 @@ int plan(int64_t rows, int64_t out, int64_t in, bool whole, Plan& g) {
   const int64_t stages = (rows + kDepth - 1) / kDepth, splits = g.form == kBig ? sb : g.form == kMiddle ? sm : sl;
   const int64_t per = std::max<int64_t>((stages + splits - 1) / splits, 1);
   g.split_rows = per * kDepth;
+  g.most_splits = std::max({sm, sl, whole ? sb : 1});
   g.splits = (int32_t)std::max<int64_t>((stages + per - 1) / per, 1);
   return ZF_OK;
 }
 int64_t partial_bytes(const Plan& g, int64_t out, int64_t in) {
-  return g.splits > 1 ? (g.splits * out * in * 4 + 15) / 16 * 16 : 0;
+  return g.most_splits > 1 ? (g.most_splits * out * in * 4 + 15) / 16 * 16 : 0;
 }
 
 // Whole 16-byte pieces at 16-byte alignment, and a turn's rows within an offset of

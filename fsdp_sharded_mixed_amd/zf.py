@@ -819,7 +819,8 @@ def embedding(table, ids, out, scale=1.0, stream=None):
 
 
 def embedding_grad_bytes(tokens, vocab, cols):
-    """zf_embedding_grad_bytes: the workspace of embedding_grad."""
+    """zf_embedding_grad_bytes: the workspace of embedding_grad, for as many
+    tokens or fewer."""
     return _bytes(lib.zf_embedding_grad_bytes(int(tokens), int(vocab), int(cols)),
                   "zf_embedding_grad_bytes")
 
@@ -934,7 +935,8 @@ def layer_norm(kind, x, weight, bias, eps, y, mean, rstd, x8=None, y8=None, stre
 
 
 def layer_norm_grad_bytes(rows, cols):
-    """zf_layer_norm_grad_bytes: the workspace of layer_norm_grad."""
+    """zf_layer_norm_grad_bytes: the workspace of layer_norm_grad, for as many
+    rows or fewer."""
     return _bytes(lib.zf_layer_norm_grad_bytes(int(rows), int(cols)), "zf_layer_norm_grad_bytes")
 
 
@@ -972,7 +974,8 @@ def layer_norm_grad(kind, dy, x, weight, mean, rstd, dx, weight_grad, bias_grad,
 
 
 def weight_grad_bytes(rows, out_features, in_features):
-    """zf_weight_grad_bytes: the workspace of weight_grad."""
+    """zf_weight_grad_bytes: the workspace of weight_grad, for as many rows or
+    fewer."""
     return _bytes(lib.zf_weight_grad_bytes(int(rows), int(out_features), int(in_features)),
                   "zf_weight_grad_bytes")
 

@@ -686,7 +686,8 @@ int zf_muon_step(const zf_muon* muon, const zf_hparams* hp, const zf_muon_hparam
  *     (pointers, sizes and scalars are those of the capture).  A workspace is
  *     caller-owned device memory, 16-byte aligned, that each call writes
  *     before it reads; calls that may overlap in time (two streams, two
- *     graphs) need workspaces of their own.
+ *     graphs) need workspaces of their own.  One made for the longest batch is
+ *     enough for every shorter one.
  *   - Buffers of a call do not overlap unless it says so.
  * Errors: ZF_EINVAL (NULL, a count or size out of range, a stride < cols, a
  * flag that is not 0 or 1), ZF_EDTYPE, ZF_EALIGN (a pointer that is not
@@ -729,7 +730,7 @@ typedef struct {
   int64_t workspace_size;  /* >= zf_embedding_grad_bytes */
 } zf_embedding_grad_args;
 
-/* Device workspace of zf_embedding_grad.  < 0 on error. */
+/* Device workspace of zf_embedding_grad, for as many tokens or fewer.  < 0 on error. */
 int64_t zf_embedding_grad_bytes(int64_t tokens, int64_t vocab, int64_t cols);
 
 /* Gradient of zf_embedding's table: grad[v] = scale * (sum of dout[t] over the
@@ -813,7 +814,7 @@ typedef struct {
   int64_t workspace_size;  /* >= zf_layer_norm_grad_bytes */
 } zf_layer_norm_grad_args;
 
-/* Device workspace of zf_layer_norm_grad.  < 0 on error. */
+/* Device workspace of zf_layer_norm_grad, for as many rows or fewer.  < 0 on error. */
 int64_t zf_layer_norm_grad_bytes(int64_t rows, int64_t cols);
 
 /* Gradients of zf_layer_norm from mean and rstd as it left them, with
@@ -837,7 +838,7 @@ typedef struct {
   int64_t workspace_size;  /* >= zf_weight_grad_bytes */
 } zf_weight_grad_args;
 
-/* Device workspace of zf_weight_grad.  < 0 on error. */
+/* Device workspace of zf_weight_grad, for as many rows or fewer.  < 0 on error. */
 int64_t zf_weight_grad_bytes(int64_t rows, int64_t out_features, int64_t in_features);
 
 /* Weight gradient of a Linear whose input was kept as a checkpoint:

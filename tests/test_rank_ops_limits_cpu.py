@@ -38,3 +38,21 @@ def test_strides_of_checkpoints(zf, key):
         assert zf.STATUS[fn(C.byref(a), zf.BF16, calls.BASE, 64, None)] == "ZF_ESIZE"
     assert calls.layer_norm(zf, x8=a) == calls.layer_norm(zf, y8=a) == "ZF_ESIZE"
     assert calls.layer_norm_grad(zf, x=None, x8=a) == calls.weight_grad(zf, x8=a) == "ZF_ESIZE"
+
+
+@pytest.mark.parametrize("name,sizes", [
+    ("embedding_grad_bytes", [(40960, 1024), (32000, 2048), (1, 8), (300001, 24), (511, 65), (1000, 8192), (97, 1 << 20)]),
+    ("layer_norm_grad_bytes", [(1024,), (40,), (2049,), (10000,), (16385,)]),
+    ("weight_grad_bytes", [(256, 1024), (1024, 1024), (2048, 2048), (777, 1000), (1, 1), (8192, 2048), (2049, 2047),
+                           (4, 1 << 20)])])
+def test_a_longer_batch_has_a_workspace_for_every_shorter_one(zf, name, sizes):
+    """A program keeps one workspace for its longest batch: sizes never fall as batches grow."""
+    fn = getattr(zf.lib, "zf_" + name)
+    for size in sizes:
+        most = 0
+        batches = list(range(0, 40000, 7)) + [k << e for e in range(15, 29) for k in (1, 3)]
+        batches = sorted(set(batches + [b + d for b in batches[-30:] for d in (-1, 1)]))
+        for rows in batches:
+            need = fn(rows, *size)
+            assert need >= most, f"{size}: {rows} rows need {need} bytes, fewer {most}"
+            most = need
