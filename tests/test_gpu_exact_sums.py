@@ -107,3 +107,15 @@ def test_one_token_that_fills_a_long_batch(zf, cols):
     ids = torch.full((70001,), 3000, device="cuda")
     ids[::1000] = torch.randint(0, 3001, (71,), generator=g, device="cuda")
     table_gradient(zf, ids, whole(g, 8, 70001, cols, BF16), 3001, False)
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("n,vocab", [((1 << 20) + 77, 300001), ((1 << 20) + 77, 500), ((1 << 21) + 1025, 40960)])
+def test_tables_of_batches_past_a_sort_blocks_thousand(zf, n, vocab, accumulate):
+    """Above 2^20 tokens a block of the sort takes 2048 tokens and more: one to three passes, half of the tokens one of
+    three ids, a tenth outside."""
+    g = R.generator(n + vocab)
+    ids = torch.randint(0, vocab, (n,), generator=g, device="cuda")
+    ids = torch.where(torch.rand(n, generator=g, device="cuda") < 0.5, ids % 3, ids)
+    ids = torch.where(torch.rand(n, generator=g, device="cuda") < 0.1, -1, ids).to(torch.int32)
+    table_gradient(zf, ids, whole(g, 4, n, 8, BF16), vocab, accumulate)
