@@ -13,12 +13,13 @@
 // results a second launch adds in order.
 //
 // Bound by the matrix cores where the result is large: 16384 tokens, 8192 x 2048,
-// bf16 added to fp32: 448 us, 1228 TFLOP/s (the library's product of the same
-// operands in bf16, without their decoding, 556 us; its best, 8192^3, 1228
+// bf16 added to fp32: 448 to 507 us, by the card and its clock, 1228 to 1084
+// TFLOP/s (the library's product of 16-bit operands, without decoding or adding, on
+// the cards where this takes 456 to 472 us: 462 to 485; its best, 8192^3, 1385
 // TFLOP/s).  Where it is small, by a stage's instructions, of which one wave a SIMD
 // issues one in four cycles: 0.28 us a stage and block, for 128 cycles of products.
-// 16384 tokens, 256 x 1024: 23.5 us, the join 4.1 of them (the library's 100); 333
-// tokens, 777 x 1000: 8.6.
+// 16384 tokens, 256 x 1024: 23.5 to 26 us, the join 4.1 of them (the library's 98);
+// 333 tokens, 777 x 1000: 8.6.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
