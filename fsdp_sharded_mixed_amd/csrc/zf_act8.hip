@@ -6,7 +6,12 @@
 // that products can take the numbers exactly in 16 bits and a scale is one
 // byte.  Bound by HBM: 2 + 1 + 1/32 bytes an element of bf16 each way.  8192 rows
 // of 8192: kept in 35.8 us (5.7 TB/s), read back in 29.4 (6.9, the codes partly
-// from the Infinity Cache).
+// from the Infinity Cache; 35.5 without it).  As many elements in rows of 40 to 16384
+// that are whole 8s: kept in 36 to 49, read back in 35 to 46; in rows of 2050 58 and
+// 50, of 300 68 and 65.  To and from fp32 58 to 65 and 89 to
+// 108 in rows of whole lines (134 MB more each way).
+//
+// What is read back is stored non-temporally: rows of 2048 35.5 us, plainly 37.1.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -20,6 +20,11 @@
 // cut runs 10.  1000 tokens of 1024: 16.7 us, three launches of 4-6 each.  The
 // lookup of 32768 rows of 2048 from fp32: 46 us, 4.7 TB/s of what it cannot do
 // without; rows that come again are read again, from the caches.
+// Stored instead of added: 65536 tokens of 2048 into a bf16 table of 32000 rows 119 to
+// 139 us by the kind of ids (62 at the rate of a copy), 131072 of 64 into 50000 rows of
+// fp32 112 to 136 (5): every clearing block reads all ids.
+// The lookup stores non-temporally: 32768 rows of 2048 bf16 with ids that are even
+// over 40960 rows 39.9 us, plainly 46.3; of 2049 49.6 and 63.8.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

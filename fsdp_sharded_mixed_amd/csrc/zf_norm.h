@@ -48,6 +48,8 @@ struct Shape {
   static constexpr int T = T_, G = G_, V = V_;
   static constexpr bool WHOLE = WHOLE_;
 };
+// 512 threads with 16 elements a lane for rows of 4104 to 8192: 67M bf16 elements in
+// rows of 5120 and 8192 57 and 47 us, 1024 threads 93 and 70.
 template <typename F>
 inline void by_shape(int64_t cols, F f) {
   if (cols % kChunk != 0) {

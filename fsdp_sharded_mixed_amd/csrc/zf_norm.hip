@@ -6,6 +6,14 @@
 // once and written once; rows of more than 16384 elements are read again for
 // each of their sums.  32768 rows of 2048 bf16 with both checkpoints (407 MB): 73.6
 // us, 5.5 TB/s, where a copy reaches 6.4; 333 rows of 1000: 4.3 us, a launch's time.
+// So it is for rows of 128 to 8192 that are multiples of 128 bytes: 67M bf16
+// elements without checkpoints in rows of 128 to 8192 46 to 57 us.  Of 1000 they take
+// 57, of 10000 67, of 40 107, of 2050 112 (and 112 with both checkpoints), of 4100
+// 121: rows begin inside a line, and lanes behind a row's end idle.
+//
+// Stores are non-temporal.  67M bf16 elements in rows of 2048, of 1000 and of 2050:
+// y alone 48.4, 57.2 and 111.4 us, with plain stores 50.5, 61.4 and 117.5; y and both
+// checkpoints 73.8, 95.7 and 111.1, with plain stores 66.6, 75.3 and 112.5.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
