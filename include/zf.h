@@ -769,7 +769,7 @@ typedef struct {
   int32_t dtype;         /* of x and y */
   int32_t weight_dtype;  /* of weight and bias */
   int32_t reserved;      /* must be 0 */
-  double eps;            /* >= 0, finite */
+  double eps;            /* >= 0, finite; taken in binary32 */
   int64_t rows, cols;
   const void* x;         /* rows x cols */
   int64_t x_stride;
@@ -787,7 +787,10 @@ typedef struct {
 /* Layer norm or RMS norm of every row, and checkpoints of its input and its
  * output from the same pass:
  *   mean = avg(x) (ZF_NORM_RMS: 0),  rstd = 1 / sqrt(avg((x - mean)^2) + eps),
- *   y = (x - mean) * rstd * weight + bias. */
+ *   y = (x - mean) * rstd * weight + bias.
+ * The squares' sum is binary32: a row whose sum passes its largest number (all
+ * magnitudes above 2^64, say) has rstd = 0, as a row without variance has an
+ * infinite rstd and NaN in y where eps is 0 in binary32. */
 int zf_layer_norm(const zf_layer_norm_args* args, void* stream);
 
 typedef struct {
