@@ -622,15 +622,11 @@ extern "C" int zf_weight_grad(const zf_weight_grad_args* args, void* stream) {
   if (!args || args->reserved != 0 || !flag(args->accumulate)) return ZF_EINVAL;
   const zf_weight_grad_args& p = *args;
   if (!valid_dtype(p.dtype) || !row_dtype(p.grad_dtype)) return ZF_EDTYPE;
-  const int64_t need = zf_weight_grad_bytes(p.rows, p.out_features, p.in_features);
-  int rc = need < 0 ? (int)need : ZF_OK;
+  const int64_t most = zf_weight_grad_bytes(p.rows, p.out_features, p.in_features);
+  int rc = most < 0 ? (int)most : ZF_OK;
   if (rc == ZF_OK) rc = rows_ok(p.dy, p.dtype, p.rows, p.out_features, p.dy_stride);
   if (rc == ZF_OK) rc = act8_ok(p.x8, p.rows, p.in_features);
   if (rc != ZF_OK) return rc;
-  if (!p.grad || (need > 0 && !p.workspace)) return ZF_EINVAL;
-  if (!aligned_to(p.grad, p.grad_dtype) || !aligned16(p.workspace)) return ZF_EALIGN;
-  if (p.workspace_size < need) return ZF_ESIZE;
-  if (p.rows == 0 && p.accumulate) return ZF_OK;
   GradArgs a;
   a.dy = p.dy;
   a.x = act8_of(p.x8);
@@ -650,6 +646,11 @@ extern "C" int zf_weight_grad(const zf_weight_grad_args* args, void* stream) {
   Plan g;
   rc = plan(p.rows, p.out_features, p.in_features, whole, g);
   if (rc != ZF_OK) return rc;
+  const int64_t need = g.splits > 1 ? most : 0;  // a call without splits takes any
+  if (!p.grad || (need > 0 && !p.workspace)) return ZF_EINVAL;
+  if (!aligned_to(p.grad, p.grad_dtype) || !aligned16(p.workspace)) return ZF_EALIGN;
+  if (p.workspace_size < need) return ZF_ESIZE;
+  if (p.rows == 0 && p.accumulate) return ZF_OK;
   a.splits = g.splits;
   a.split_rows = g.split_rows;
   a.partial = g.splits > 1 ? static_cast<float*>(p.workspace) : nullptr;

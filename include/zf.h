@@ -838,7 +838,7 @@ typedef struct {
   const zf_act8* x8;     /* rows x in_features */
   void* grad;            /* out_features x in_features, rows end to end */
   void* workspace;       /* may be NULL if zf_weight_grad_bytes is 0 */
-  int64_t workspace_size;  /* >= zf_weight_grad_bytes */
+  int64_t workspace_size;  /* >= zf_weight_grad_bytes (not looked at by a call that needs none) */
 } zf_weight_grad_args;
 
 /* Device workspace of zf_weight_grad, for as many rows or fewer.  < 0 on error. */

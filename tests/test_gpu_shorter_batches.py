@@ -3,6 +3,7 @@ import pytest
 import torch
 
 from tests import rank_ops as R
+from tests import weight_grad_plan as plan
 
 pytestmark = pytest.mark.gpu
 BF16, F32 = torch.bfloat16, torch.float32
@@ -50,3 +51,14 @@ def test_weight_gradients(zf, outs, ins, batches):
         grad = torch.empty(outs, ins, device="cuda")
         zf.weight_grad(dy[:rows], zf.act8(codes[:rows], scales[:rows]), grad, ws)
         assert torch.equal(grad.double(), dy[:rows].double().t().contiguous() @ x[:rows].double()), rows
+
+
+def test_a_weight_gradient_without_splits_takes_no_workspace(zf):
+    """512 tokens of 2048 x 1536 are not split, though the size asked for is that of smaller tiles with two splits."""
+    rows, outs, ins = 512, 2048, 1536
+    assert plan.chosen(rows, outs, ins)[1] == 1
+    g = R.generator(3)
+    dy, x = whole(g, rows, outs), whole(g, rows, ins)
+    grad = torch.empty(outs, ins, device="cuda")
+    zf.weight_grad(dy, zf.act8(*R.keep(x)), grad, None)
+    assert torch.equal(grad.double(), dy.double().t().contiguous() @ x.double())
