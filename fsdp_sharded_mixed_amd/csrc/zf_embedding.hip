@@ -22,7 +22,8 @@
 // without; rows that come again are read again, from the caches.
 // Stored instead of added: 65536 tokens of 2048 into a bf16 table of 32000 rows 119 to
 // 139 us by the kind of ids (62 at the rate of a copy), 131072 of 64 into 50000 rows of
-// fp32 112 to 136 (5): every clearing block reads all ids.
+// fp32 112 to 136 (5): the first count takes 36 and 52 of them instead of 5, since
+// every clearing block reads all ids.
 // The lookup stores non-temporally: 32768 rows of 2048 bf16 with ids that are even
 // over 40960 rows 39.9 us, plainly 46.3; of 2049 49.6 and 63.8.
 #include <hip/hip_runtime.h>
